@@ -72,7 +72,8 @@ enum {
     RMSNORM_ERR_CAPACITY = -10,   /* plan build: output buffer too small */
     RMSNORM_ERR_CUDA = -11,       /* a CUDA runtime call or kernel launch failed */
     RMSNORM_ERR_DEVICE = -12,     /* the current device is not sm_103 */
-    RMSNORM_ERR_VALUE = -13       /* grad_scale is NaN or infinite */
+    RMSNORM_ERR_VALUE = -13,      /* grad_scale is NaN or infinite (layernorm_bi.h: or eps, p out of range) */
+    RMSNORM_ERR_DTYPE = -14       /* unknown element type code (layernorm_bi.h) */
 };
 
 /* Device status word bits (rmsnorm_dweight_status). */

@@ -1,6 +1,7 @@
-"""Batch-invariant RMSNorm forward/backward for GB300 (sm_103a).
+"""Batch-invariant RMSNorm, layer norm and dropout for GB300 (sm_103a).
 
-Thin Python binding over the C ABI in include/rmsnorm_bi.h: every function
+Thin Python binding over the C ABI in include/rmsnorm_bi.h and
+include/layernorm_bi.h (the latter in layernorm.py): every function
 here marshals arguments and calls the library; every step of the computation
 runs in the library's CUDA kernels.  There is no CPU path: if the library is
 missing and cannot be built, importing the binding's functions raises.
@@ -23,6 +24,7 @@ OK = 0
 ERR_NAMES = {
     -1: "NULL", -2: "HIDDEN", -3: "ALIGN", -4: "STRIDE", -5: "LAYOUT", -6: "WORKSPACE",
     -7: "PLAN", -8: "ID", -9: "DUPLICATE", -10: "CAPACITY", -11: "CUDA", -12: "DEVICE", -13: "VALUE",
+    -14: "DTYPE",
 }
 STATUS_DOUBLE, STATUS_MISSING, STATUS_HEADER, STATUS_PLAN, STATUS_TIMEOUT = 1, 2, 4, 8, 16
 PLAN_ITEM_BYTES = 528
@@ -88,6 +90,8 @@ def _load():
         "rmsnorm_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "rmsnorm_kernel_launches": ([], I64),
     }
+    from . import layernorm
+    sig.update(layernorm.signatures(LP))
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -498,3 +502,18 @@ def rmsnorm_bwd_noalloc(x, weight, dy, lay: CallLayout, eps: float, dx=None, dwe
     _check(_load().rmsnorm_bwd_noalloc(_ptr(x), _ptr(weight), _ptr(dy), H, eps, ctypes.byref(L), _ptr(dx),
                                        _ptr(dweight), _ptr(status), _stream(stream)), "rmsnorm_bwd_noalloc")
     return dx, dweight
+
+
+# The layer norm and dropout binding imports torch when it loads; this package
+# does not until one of its functions is called, so these names resolve lazily.
+_LAYERNORM = ("Dropout", "LayerNormWorkspace", "dropout_bwd", "dropout_fwd", "layernorm_add_bwd", "layernorm_add_fwd",
+              "layernorm_bwd", "layernorm_fwd")
+
+
+def __getattr__(name):
+    if name in _LAYERNORM:
+        from . import layernorm
+        for n in _LAYERNORM:
+            globals()[n] = getattr(layernorm, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -21,7 +21,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fno-strict-aliasing", f"-I{INCLUDE}"]
 SOURCES = ["rmsnorm_bi.cu", "rows_fwd.cu", "rows_dx.cu", "rows_dxdw.cu", "rows_adddxdw.cu", "gemm_dw.cu",
-           "plan.cpp"]
+           "layernorm.cu", "ln_rows_bf16.cu", "ln_rows_fp16.cu", "ln_rows_fp32.cu", "plan.cpp"]
 
 
 def nvcc() -> str:
@@ -32,7 +32,7 @@ def nvcc() -> str:
 
 
 def _deps():
-    out = [os.path.join(INCLUDE, "rmsnorm_bi.h"), __file__]
+    out = [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
     out += [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     return out
 

@@ -344,7 +344,8 @@ extern "C" const char *rmsnorm_strerror(int code) {
         case RMSNORM_ERR_CAPACITY: return "plan buffer too small";
         case RMSNORM_ERR_CUDA: return "CUDA runtime error";
         case RMSNORM_ERR_DEVICE: return "device is not sm_103";
-        case RMSNORM_ERR_VALUE: return "grad_scale is not finite";
+        case RMSNORM_ERR_VALUE: return "grad_scale is not finite, or eps or a dropout probability is out of range";
+        case RMSNORM_ERR_DTYPE: return "element type not supported";
         default: return "unknown error";
     }
 }

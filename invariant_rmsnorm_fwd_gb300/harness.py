@@ -35,6 +35,8 @@ class LayoutRun:
     spill_rows: int = 0
     untouched_padding: bool = True
     h: object = None            # residual-add chain: h = bf16(x + r), logical order
+    dh: object = None           # layer-norm chain: gradient of h, logical order
+    dbias: object = None        # layer-norm chain: torch float32 [H]
 
 
 @dataclass
@@ -83,7 +85,7 @@ class InvarianceReport:
 
 def _bits(t):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype in (torch.bfloat16, torch.float16):
         return t.contiguous().view(torch.int16)
     if t.dtype == torch.float32:
         return t.contiguous().view(torch.int32)
@@ -221,6 +223,50 @@ def run_layout_chain(lay: layout_mod.Layout, x_log, r_log, dy_log, dres_log, wei
                      whole, spill, untouched, h=outs["h"])
 
 
+def run_layout_layernorm(lay: layout_mod.Layout, x_log, r_log, dy_log, dres_log, weight, bias, eps: float,
+                         grad_scale: float = 1.0, dropout=None, rows_per_token: int = 1, device="cuda",
+                         stream=None) -> LayoutRun:
+    """Dropout, residual add and layer norm forward, and their backward with both
+    parameter gradients, through the library, for one layout; outputs in logical order.
+    `dropout` is an rb.Dropout or None.  Padding is filled with NaN and the outputs
+    with a sentinel that must survive there."""
+    import torch
+    import invariant_rmsnorm_fwd_gb300 as rb
+    H = x_log.shape[-1]
+    R = rows_per_token
+    views = [t.reshape(-1, R, H) for t in (x_log, r_log, dy_log, dres_log)]
+    n_tok, dtype = views[0].shape[0], x_log.dtype
+    word = torch.int32 if dtype == torch.float32 else torch.int16
+    ws = rb.LayerNormWorkspace(n_tok * R, H, device=device)
+    names = ("h", "y", "dh") + (("dx",) if dropout is not None else ())
+    outs = {k: torch.empty_like(views[0]) for k in names}
+    ws.begin(stream)
+    whole = spill = 0
+    untouched = True
+    for tok in lay.calls:
+        cl = rb.call_layout(tok, R, lay.n_logical_tokens, device=device)
+        whole += cl.whole_blocks
+        spill += cl.spill_rows
+        tid = cl.tok_id.long()
+        act = tid >= 0
+        phys = []
+        for v in views:
+            t = torch.full((tok.size, R, H), float("nan"), dtype=dtype, device=device)
+            t[act] = v[tid[act]]
+            phys.append(t)
+        xp, rp, dp, drp = phys
+        bufs = {k: torch.full((tok.size, R, H), SENTINEL_BITS, dtype=word, device=device).view(dtype) for k in names}
+        rb.layernorm_add_fwd(xp, rp, weight, bias, cl, eps, h=bufs["h"], y=bufs["y"], dropout=dropout, stream=stream)
+        rb.layernorm_add_bwd(bufs["h"], weight, dp, cl, eps, dres=drp, grad_scale=grad_scale, dropout=dropout,
+                             dh=bufs["dh"], dx=bufs.get("dx"), workspace=ws, stream=stream)
+        for k in names:
+            outs[k][tid[act]] = bufs[k][act]
+            untouched &= bool((bufs[k][~act].view(word) == SENTINEL_BITS).all())
+    dw, db = ws.finalize(stream=stream, grad_scale=grad_scale)
+    return LayoutRun(lay.name, outs["y"], outs.get("dx", outs["dh"]), dw, ws.status(stream), len(lay.calls),
+                     lay.rows_per_call, whole, spill, untouched, h=outs["h"], dh=outs["dh"], dbias=db)
+
+
 def run_layout_gemm(lay: layout_mod.Layout, x_log, dy_log, device="cuda", stream=None) -> LayoutRun:
     """The linear layer's deterministic weight gradient for one layout: every call
     places its tokens, one finalize forms dW.  dW is returned as the run's
@@ -254,7 +300,7 @@ def assert_batch_invariant(runs: dict, layouts: dict, reference: str = "full") -
         if name == reference:
             continue
         rep.distinct[name] = layouts_differ(layouts[reference], layouts[name])
-        for t in ("y", "dx", "dweight", "h"):
+        for t in ("y", "dx", "dweight", "h", "dh", "dbias"):
             a, b = getattr(run, t), getattr(ref, t)
             if a is None and b is None:
                 continue
