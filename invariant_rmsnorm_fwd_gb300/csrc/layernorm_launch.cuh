@@ -1,33 +1,122 @@
 // Launcher of the layer-norm row kernels, instantiated per element type.
 #pragma once
+#include <mutex>
+
 #include "host.cuh"
 #include "layernorm_host.cuh"
+#include "layernorm_stream.cuh"
 
 namespace rbi {
 
-template <class E, int NV>
-int ln_launch(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
-    const int V = p.hidden / 8, per = (V + NV - 1) / NV, threads = (per + 31) / 32 * 32;
+// ----------------------------------------------------------------- rows of at most 256 columns
+
+template <class E>
+int ln_launch_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
+    const int V = p.hidden / 8, threads = (V + 31) / 32 * 32;
     const int64_t grid = grads ? p.n_items * kGroups : p.n_rows;
     if (grid == 0) return RMSNORM_OK;
     if (grid >= (int64_t(1) << 31)) return RMSNORM_ERR_LAYOUT;
-    if (grads) ln_rows_kernel<E, NV, true, true><<<unsigned(grid), threads, 0, stream>>>(p);
-    else if (bwd) ln_rows_kernel<E, NV, true, false><<<unsigned(grid), threads, 0, stream>>>(p);
-    else ln_rows_kernel<E, NV, false, false><<<unsigned(grid), threads, 0, stream>>>(p);
+    if (grads) ln_rows_kernel<E, 1, true, true><<<unsigned(grid), threads, 0, stream>>>(p);
+    else if (bwd) ln_rows_kernel<E, 1, true, false><<<unsigned(grid), threads, 0, stream>>>(p);
+    else ln_rows_kernel<E, 1, false, false><<<unsigned(grid), threads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
+}
+
+// ----------------------------------------------------------------- wider rows
+
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // an SM's shared memory; what the system takes per CTA
+
+template <class E, int NV, int MODE, bool DROP, bool GRADS, int MAXT, int MINB>
+int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cudaStream_t stream) {
+    auto kern = ln_stream_kernel<E, NV, MODE, DROP, GRADS, MAXT, MINB>;
+    // registers of this kernel, and its shared-memory limit raised once per device
+    static std::mutex mu;
+    static uint64_t ready = 0;
+    static int regs = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RMSNORM_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!((ready >> dev) & 1)) {
+            cudaFuncAttributes a;
+            if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) return RMSNORM_ERR_CUDA;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem) != cudaSuccess)
+                return RMSNORM_ERR_CUDA;
+            regs = a.numRegs;
+            ready |= uint64_t(1) << dev;
+        }
+    }
+    // Resident CTAs by registers and threads; then as many stages as their share
+    // of the shared memory holds (fewer CTAs where that leaves less than `least`).
+    // Backward, row i + 1 arrives while row i is in use and the stage of row
+    // i - 1 is being refilled: three stages at least.
+    const int row = p.hidden * int(sizeof(E)), least = MODE == kLnBwd ? 3 : 2;
+    int nt = MODE == kLnFwd ? 1 : MODE == kLnAdd ? 2 : p.res ? 3 : 2;
+    if (MODE == kLnBwd && nt == 3 && kFixedBytes + least * nt * row > d.max_smem) nt = 2;
+    const int block = GRADS ? int(align256(int64_t(p.hidden) * 8)) : 0;
+    int ctas = 65536 / ((regs + 7) / 8 * 8 * threads);
+    if (ctas > 2048 / threads) ctas = 2048 / threads;
+    if (ctas > 32) ctas = 32;
+    if (ctas < 1) return RMSNORM_ERR_HIDDEN;
+    int S = 0, use_block = 0;
+    for (; ctas >= 1; --ctas) {
+        int room = kSmemPerSm / ctas - kSmemPerCta;
+        if (room > d.max_smem) room = d.max_smem;
+        room -= kFixedBytes;
+        use_block = GRADS && (room - block) / (nt * row) >= least ? 1 : 0;
+        S = (room - (use_block ? block : 0)) / (nt * row);
+        if (S >= least + 1 || (ctas == 1 && S >= least)) break;
+    }
+    if (ctas < 1) return RMSNORM_ERR_HIDDEN;
+    if (S > kMaxStages) S = kMaxStages;
+    const int smem = kFixedBytes + (use_block ? block : 0) + S * nt * row;
+    const int64_t units = GRADS ? p.n_items * kGroups : p.n_rows;
+    if (units == 0) return RMSNORM_OK;
+    int64_t grid = int64_t(ctas) * d.sms;
+    if (grid > units) grid = units;
+    kern<<<unsigned(grid), threads, smem, stream>>>(p, S, nt, use_block);
+    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
+    count_launch();
+    return RMSNORM_OK;
+}
+
+template <class E, int NV, int MODE, bool DROP, bool GRADS>
+int ln_launch_stream(const LnParams &p, const DeviceInfo &d, cudaStream_t stream) {
+    const int V = p.hidden / Lane<E>::kE, per = (V + NV - 1) / NV, threads = (per + 31) / 32 * 32;
+    if constexpr (NV * Lane<E>::kE <= 16) {              // wider threads: rows of more than 8192 columns only
+        if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, 2>(p, threads, d, stream);
+        if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
+    }
+    return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);
+}
+
+template <class E, int NV>
+int ln_launch_mode(const LnParams &p, bool bwd, bool grads, const DeviceInfo &d, cudaStream_t s) {
+    const bool drop = p.drop.state != nullptr;
+    if (!bwd) {
+        if (!p.res) return ln_launch_stream<E, NV, kLnFwd, false, false>(p, d, s);
+        return drop ? ln_launch_stream<E, NV, kLnAdd, true, false>(p, d, s)
+                    : ln_launch_stream<E, NV, kLnAdd, false, false>(p, d, s);
+    }
+    if (grads) return drop ? ln_launch_stream<E, NV, kLnBwd, true, true>(p, d, s)
+                           : ln_launch_stream<E, NV, kLnBwd, false, true>(p, d, s);
+    return drop ? ln_launch_stream<E, NV, kLnBwd, true, false>(p, d, s)
+                : ln_launch_stream<E, NV, kLnBwd, false, false>(p, d, s);
 }
 
 template <class E>
 int ln_run_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
-    const int V = p.hidden / 8;
-    if (V <= 512) return ln_launch<E, 1>(p, bwd, grads, stream);
-    if (V <= 1024) return ln_launch<E, 2>(p, bwd, grads, stream);
-    if constexpr (sizeof(E) == 2) return ln_launch<E, 4>(p, bwd, grads, stream);
-    return RMSNORM_ERR_HIDDEN;
+    if (p.hidden <= 256) return ln_launch_rows<E>(p, bwd, grads, stream);
+    if constexpr (sizeof(E) == 4) {
+        return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
+    } else {
+        if (p.hidden <= 8192) return ln_launch_mode<E, 2>(p, bwd, grads, *d, stream);
+        return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
+    }
 }
 
 }  // namespace rbi
