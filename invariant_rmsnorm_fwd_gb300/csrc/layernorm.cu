@@ -214,16 +214,21 @@ extern "C" int layernorm_finalize(void *workspace, int64_t n_logical_rows, int64
         if (dbias && cudaMemsetAsync(dbias, 0, size_t(hidden) * 4, s) != cudaSuccess) return RMSNORM_ERR_CUDA;
         return RMSNORM_OK;
     }
-    const unsigned gy = unsigned((2 * hidden + 31) / 32);
+    const unsigned gy = unsigned((2 * hidden + kLnTreeCols - 1) / kLnTreeCols);
     const float *in = nullptr;
     float *scratch[2] = {ws.scratch_a, ws.scratch_b};
     int flip = 0;
     for (int64_t n = ws.n_blocks;;) {
-        const int64_t groups = (n + 31) / 32;
+        // One launch where four rounds of a CTA hold all inputs; else as many
+        // rounds as still leave two CTAs per SM.
+        int rounds = 4;
+        if (n > 4 * kLnTreeBlocks)
+            while (rounds > 1 && (n + rounds * kLnTreeBlocks - 1) / (rounds * kLnTreeBlocks) * gy < 2 * int64_t(d->sms)) rounds /= 2;
+        const int64_t groups = (n + rounds * kLnTreeBlocks - 1) / (rounds * kLnTreeBlocks);
         const bool last = groups == 1;
         float *dst = scratch[flip];
         ln_tree_kernel<<<dim3(unsigned(groups), gy), 1024, 0, s>>>(
-            ws, in, last ? dweight : dst, last ? dbias : dst + hidden, last ? 0 : 2 * hidden, n,
+            ws, in, last ? dweight : dst, last ? dbias : dst + hidden, last ? 0 : 2 * hidden, n, rounds,
             last ? grad_scale : 1.f);
         if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
         count_launch();

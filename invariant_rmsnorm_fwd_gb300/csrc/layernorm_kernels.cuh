@@ -13,15 +13,16 @@ constexpr int kGroupRows = 8;                            // rows of one group of
 constexpr int kGroups = kBlockRows / kGroupRows;         // groups of a logical block
 constexpr uint64_t kLnMagic = 0x3149422d4e4c3352ull;
 
-// State of a group: nothing yet, a group partial in its slot, or part of a
-// whole-block partial (in the block's slot 0).
-constexpr uint8_t kGroupNone = 0, kGroupPartial = 1, kGroupWhole = 2;
+// State byte of a group: 0 nothing, c > 0 a partial in its slot that covers the
+// group and the c - 1 behind it (a fold from the block's first group on, c up
+// to 8; other groups are stored alone).
 
 struct LnWs {
     WsHeader *hdr;
-    uint8_t *state;                  // [nb][8]
+    uint8_t *state;                  // [nb][8], see above
     uint8_t *flag;                   // [N] 1 = row spilled
-    float *partial;                  // [nb][8][2][H]: dweight and dbias of a group; slot 0 holds a whole block's
+    float *partial;                  // [nb][8][2][H]: dweight and dbias of a group, or of the fold that
+                                     //   starts there
     float *scratch_a, *scratch_b;    // [ceil(nb/32)][2][H]
     float *spill;                    // [N][2][H]: xhat and dy of spilled rows
     int64_t n_rows, hidden, n_blocks;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(512) ln_rows_kernel(const __grid_constant__ Ln
             }
             if constexpr (GRADS) {
                 if (!partial && threadIdx.x == 0) {
-                    if (p.ws.flag[g] || p.ws.state[g / kGroupRows] != kGroupNone) set_status(p.ws.hdr, kStDouble);
+                    if (p.ws.flag[g] || p.ws.state[g / kGroupRows] != 0) set_status(p.ws.hdr, kStDouble);
                     p.ws.flag[g] = 1;
                 }
             }
@@ -386,8 +387,8 @@ __global__ void __launch_bounds__(512) ln_rows_kernel(const __grid_constant__ Ln
                 }
             }
             if (threadIdx.x == 0) {
-                if (p.ws.state[grp] != kGroupNone) set_status(p.ws.hdr, kStDouble);
-                p.ws.state[grp] = kGroupPartial;
+                if (p.ws.state[grp] != 0) set_status(p.ws.hdr, kStDouble);
+                p.ws.state[grp] = 1;
             }
         }
     }

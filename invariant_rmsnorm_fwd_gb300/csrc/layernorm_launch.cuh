@@ -52,7 +52,7 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
     // of the shared memory holds (fewer CTAs where that leaves less than `least`).
     // Backward, row i + 1 arrives while row i is in use and the stage of row
     // i - 1 is being refilled: three stages at least.
-    const int row = p.hidden * int(sizeof(E)), least = MODE == kLnBwd ? 3 : 2;
+    const int row = NV * threads * 16, least = MODE == kLnBwd ? 3 : 2;   // a staged row, padded to whole vectors of the CTA
     int nt = MODE == kLnFwd ? 1 : MODE == kLnAdd ? 2 : p.res ? 3 : 2;
     if (MODE == kLnBwd && nt == 3 && kFixedBytes + least * nt * row > d.max_smem) nt = 2;
     const int block = GRADS ? int(align256(int64_t(p.hidden) * 8)) : 0;

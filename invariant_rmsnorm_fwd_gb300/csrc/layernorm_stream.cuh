@@ -28,10 +28,15 @@ constexpr int kMaxStages = 16;
 
 struct LnEntry {                     // one row of a CTA's list
     int64_t off;                     // element offset of the row
-    uint32_t lrow;                   // logical row; bit 31: its group goes into a whole-block partial
-    uint32_t prow;                   // physical row; bit 31: a row of a cut group (spilled)
+    uint32_t lrow;                   // logical row
+    uint32_t tag;                    // forward, dx alone: physical row; parameter gradients: kTag* bits
 };
 static_assert(sizeof(LnEntry) == 16, "one 16-byte shared-memory load");
+// What the last row of a group does with the group's sums: they join the fold
+// of the block's first groups (kTagFold) or are stored on their own; kTagStore
+// ends the fold (the block's last group, or the last one of this CTA's share).
+// kTagSpill: a row of a group that the call holds only partly.
+constexpr uint32_t kTagSpill = 1, kTagClose = 2, kTagFold = 4, kTagStore = 8;
 
 template <class E>
 struct Lane {                        // a 16-byte vector: kE elements, kP FP32 pairs
@@ -157,18 +162,50 @@ __device__ __forceinline__ void cta_sums(float (&v)[K], float *red, int warps) {
     for (int k = 0; k < K; ++k) v[k] = __shfl_sync(kFull, m, k * (32 / K));
 }
 
-template <int P, int NV>
-__device__ __forceinline__ float pair_total(const f2_t (&s)[P][NV]) {
-    f2_t t = s[0][0];
+template <int P>
+__device__ __forceinline__ float pair_total(const f2_t (&s)[P]) {
+    f2_t t = s[0];
 #pragma unroll
-    for (int i = 1; i < P * NV; ++i) t = f2_add(t, s[i / NV][i % NV]);
+    for (int i = 1; i < P; ++i) t = f2_add(t, s[i]);
     return __fadd_rn(f2_lo(t), f2_hi(t));
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ LnEntry lds_entry(uint32_t addr) {
+    LnEntry e;
+    asm volatile("{\n\t.reg .b32 a, b;\n\tld.shared.v4.u32 {a,b,%1,%2}, [%3];\n\tmov.b64 %0, {a,b};\n\t}"
+                 : "=l"(e.off), "=r"(e.lrow), "=r"(e.tag)
+                 : "r"(addr));
+    return e;
+}
+// P pairs to or from consecutive floats, 16 bytes at a time.
+template <int P>
+__device__ __forceinline__ void pairs_store(float *p, const f2_t (&f)[P]) {
+#pragma unroll
+    for (int j = 0; j < P; j += 2) *reinterpret_cast<ulonglong2 *>(p + 2 * j) = make_ulonglong2(f[j], f[j + 1]);
+}
+template <int P>
+__device__ __forceinline__ void pairs_load(const float *p, f2_t (&f)[P]) {
+#pragma unroll
+    for (int j = 0; j < P; j += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p + 2 * j);
+        f[j] = v.x;
+        f[j + 1] = v.y;
+    }
 }
 
 enum LnMode : int { kLnFwd = 0, kLnAdd = 1, kLnBwd = 2 };
 
 // p.res in kLnBwd: dres, staged as the third tensor when nt is 3 (rows too wide
 // for three stages of three tensors read it directly).
+//
+// A staged tensor takes NV * T vectors; those past the row's end are zeroed
+// once and never written again, and their weights and the mean taken off them
+// are zero, so that the passes need no bounds checks, only the stores do.
 template <class E, int NV, int MODE, bool DROP, bool GRADS, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_constant__ LnParams p, int S, int nt,
                                                                int use_block) {
@@ -178,14 +215,18 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);
     float *red = reinterpret_cast<float *>(smem + kRedOff);
-    int *count = reinterpret_cast<int *>(smem + kCountOff);      // [0..15] warps, [16, 17] a copy did not arrive (alternating like red)
+    volatile int *count = reinterpret_cast<volatile int *>(smem + kCountOff);   // [0..15] warps; [16, 17] a copy
+                                                         // did not arrive (alternating like red)
     LnEntry *list = reinterpret_cast<LnEntry *>(smem + kListOff);
     const int tid = threadIdx.x, T = blockDim.x, warps = T >> 5;
     const int V = p.hidden / kE;
     const uint32_t row_bytes = uint32_t(p.hidden) * uint32_t(sizeof(E));
-    const uint32_t stage_bytes = row_bytes * uint32_t(nt);
+    const uint32_t pitch = uint32_t(NV * T) * 16u, stage_pitch = pitch * uint32_t(nt);
     float *block_acc = reinterpret_cast<float *>(smem + kFixedBytes);
-    uint8_t *stages = smem + kFixedBytes + (use_block ? uint32_t(align256(int64_t(p.hidden) * 8)) : 0u);
+    const uint32_t stage0 = kFixedBytes + (use_block ? uint32_t(align256(int64_t(p.hidden) * 8)) : 0u);
+    const uint32_t my0 = smem_addr(smem) + stage0 + uint32_t(tid) * 16u;        // this thread's vectors of stage 0
+    const uint32_t list0 = smem_addr(list);
+    const uint32_t step = uint32_t(T) * 16u;
 
     if constexpr (GRADS) {
         if (!ln_header_ok(p.ws)) {
@@ -201,10 +242,11 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     for (int i = tid; i < 128; i += T) red[i] = 0.f;
     const DropKey key = DROP ? drop_key(p.drop) : DropKey{0, 0, 0, 0};
 
-    f2_t w[NV][P], b[kFwd ? NV : 1][P];
+    f2_t w[NV][P], b[kFwd ? NV : 1][P], in_row[NV];      // in_row: 1 inside the row, 0 past its end
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = tid + k * T;
+        in_row[k] = v < V ? f2_both(1.f) : 0;
         if (v < V) {
             param_pairs<E>(p.w, p.params_f32, v, 1.f, w[k]);
             if constexpr (kFwd) param_pairs<E>(p.b, p.params_f32, v, 0.f, b[k]);
@@ -214,6 +256,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 w[k][i] = 0;
                 if constexpr (kFwd) b[k][i] = 0;
             }
+            for (int s = 0; s < S; ++s)
+                for (int t = 0; t < nt; ++t)
+                    *reinterpret_cast<uint4 *>(smem + stage0 + s * stage_pitch + t * pitch + v * 16) = make_uint4(0, 0, 0, 0);
         }
     }
     f2_t dw[GRADS ? NV : 1][P], db[GRADS ? NV : 1][P];
@@ -255,26 +300,33 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     const int kind = it.kind, blk = it.block;
                     const int32_t prow = it.prow[slot], lrow = it.lrow[slot];
                     if (prow >= 0) {
+                        // whole blocks and quarters hold each row at its place, so a
+                        // group ends at its last row
                         valid = prow < p.n_rows && lrow >= 0 && lrow < p.ws.n_rows &&
                                 (kind == kItemSpill ||
                                  ((kind == kItemWhole || kind == kItemQuarters) && lrow == int64_t(blk) * kBlockRows + slot));
                         if (!valid) set_status(p.ws.hdr, kStPlan);
+                        const bool block_end = slot == kBlockRows - 1 || lrow == p.ws.n_rows - 1;
+                        if (kind == kItemSpill) {
+                            e.tag = kTagSpill;
+                        } else if (slot % kGroupRows == kGroupRows - 1 || block_end) {
+                            e.tag = kTagClose | kTagStore;
+                            if (use_block && kind == kItemWhole && item * kGroups >= share_lo) {
+                                e.tag = kTagClose | kTagFold;
+                                if (block_end || (q >> 3) == share_hi - 1) e.tag |= kTagStore;
+                            }
+                        }
                     }
-                    const int64_t rows = p.ws.n_rows - int64_t(blk) * kBlockRows;
-                    const int groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
-                    const bool whole = use_block && kind == kItemWhole && item * kGroups >= share_lo &&
-                                       item * kGroups + groups <= share_hi;
                     const uint32_t tok = uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - tok * uint32_t(p.rpt);
                     e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
-                    e.lrow = uint32_t(lrow) | (whole ? 0x80000000u : 0u);
-                    e.prow = uint32_t(prow) | (kind == kItemSpill ? 0x80000000u : 0u);
+                    e.lrow = uint32_t(lrow);
                 } else {
                     const uint32_t tok = uint32_t(q) / uint32_t(p.rpt), head = uint32_t(q) - tok * uint32_t(p.rpt);
                     const int32_t id = p.tok_id[tok];
                     valid = id >= 0;
                     e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
                     e.lrow = uint32_t(id) * uint32_t(p.rpt) + head;
-                    e.prow = uint32_t(q);
+                    e.tag = uint32_t(q);
                 }
             }
             const uint32_t bits = __ballot_sync(kFull, valid);
@@ -295,13 +347,13 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
         auto issue = [&](int i) {                        // thread 0
             const uint32_t r = done + uint32_t(i), s = r % uint32_t(S);
             const int64_t off = list[i].off;
-            uint8_t *dst = stages + s * stage_bytes;
-            mbar_arrive_expect_tx(&bars[s], stage_bytes);
+            uint8_t *dst = smem + stage0 + s * stage_pitch;
+            mbar_arrive_expect_tx(&bars[s], row_bytes * uint32_t(nt));
             bulk_copy_g2s(dst, static_cast<const E *>(p.x) + off, row_bytes, &bars[s]);
-            if constexpr (MODE == kLnAdd) bulk_copy_g2s(dst + row_bytes, static_cast<const E *>(p.res) + off, row_bytes, &bars[s]);
+            if constexpr (MODE == kLnAdd) bulk_copy_g2s(dst + pitch, static_cast<const E *>(p.res) + off, row_bytes, &bars[s]);
             if constexpr (MODE == kLnBwd) {
-                bulk_copy_g2s(dst + row_bytes, static_cast<const E *>(p.dy) + off, row_bytes, &bars[s]);
-                if (nt == 3) bulk_copy_g2s(dst + 2 * row_bytes, static_cast<const E *>(p.res) + off, row_bytes, &bars[s]);
+                bulk_copy_g2s(dst + pitch, static_cast<const E *>(p.dy) + off, row_bytes, &bars[s]);
+                if (nt == 3) bulk_copy_g2s(dst + 2 * pitch, static_cast<const E *>(p.res) + off, row_bytes, &bars[s]);
             }
         };
         int issued = 0;
@@ -309,99 +361,92 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
             for (; issued < S && issued < n; ++issued) issue(issued);
 
         uint4 cur[kFwd ? NV : 1], nxt[kFwd ? NV : 1];
-        uint32_t s_cur = done % uint32_t(S), s_nxt = s_cur, par_nxt = (done / uint32_t(S)) & 1u;
+        uint32_t s_nxt = done % uint32_t(S), par_nxt = (done / uint32_t(S)) & 1u;
+        uint32_t st_nxt = my0 + s_nxt * stage_pitch, st_cur = st_nxt;
 
         // Sum of row i (the next one), which has to have arrived; forward: the
         // row moves into registers (residual add: it is formed and stored here).
-        auto first_pass = [&](int i, float &sum) {
+        auto first_pass = [&](int i) -> float {
             if (!mbar_wait_spin_bounded(&bars[s_nxt], par_nxt)) count[16 + (turn & 1)] = 1;
-            const uint8_t *st = stages + s_nxt * stage_bytes;
-            f2_t acc[P][1];
-#pragma unroll
-            for (int j = 0; j < P; ++j) acc[j][0] = 0;
+            f2_t acc[P];
+            LnEntry en;
+            if constexpr (MODE == kLnAdd) en = lds_entry(list0 + uint32_t(i) * 16u);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int v = tid + k * T;
-                if (v < V) {
-                    uint4 u = ld_shared_v4(st + v * 16);
-                    f2_t f[P];
-                    if constexpr (MODE == kLnAdd) {
-                        f2_t r[P];
-                        up<E>(ld_shared_v4(st + row_bytes + v * 16), r);
-                        up<E>(u, f);
-                        if constexpr (DROP) {
-                            const uint32_t keep = lane_keep<E>(v, list[i].lrow, key, p.drop.t);
-#pragma unroll
-                            for (int j = 0; j < P; ++j) {
-                                const float lo = __fmaf_rn(f2_lo(f[j]), p.drop.scale, f2_lo(r[j]));
-                                const float hi = __fmaf_rn(f2_hi(f[j]), p.drop.scale, f2_hi(r[j]));
-                                f[j] = f2_make((keep >> (2 * j)) & 1 ? lo : f2_lo(r[j]),
-                                               (keep >> (2 * j + 1)) & 1 ? hi : f2_hi(r[j]));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < P; ++j) f[j] = f2_add(f[j], r[j]);
-                        }
-                        u = down<E>(f);
-                        st_global_v4(static_cast<E *>(p.out2) + list[i].off + v * kE, u);
-                    }
+                uint4 u = lds_v4(st_nxt + k * step);
+                f2_t f[P];
+                if constexpr (MODE == kLnAdd) {
+                    const int v = tid + k * T;
+                    f2_t r[P];
+                    up<E>(lds_v4(st_nxt + pitch + k * step), r);
                     up<E>(u, f);
-                    if constexpr (kFwd) nxt[k] = u;
+                    if constexpr (DROP) {
+                        const uint32_t keep = lane_keep<E>(v, en.lrow, key, p.drop.t);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) acc[j][0] = f2_add(acc[j][0], f[j]);
+                        for (int j = 0; j < P; ++j) {
+                            const float lo = __fmaf_rn(f2_lo(f[j]), p.drop.scale, f2_lo(r[j]));
+                            const float hi = __fmaf_rn(f2_hi(f[j]), p.drop.scale, f2_hi(r[j]));
+                            f[j] = f2_make((keep >> (2 * j)) & 1 ? lo : f2_lo(r[j]),
+                                           (keep >> (2 * j + 1)) & 1 ? hi : f2_hi(r[j]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) f[j] = f2_add(f[j], r[j]);
+                    }
+                    u = down<E>(f);
+                    if (v < V) st_global_v4(static_cast<E *>(p.out2) + en.off + v * kE, u);
                 }
+                up<E>(u, f);
+                if constexpr (kFwd) nxt[k] = u;
+#pragma unroll
+                for (int j = 0; j < P; ++j) acc[j] = k == 0 ? f[j] : f2_add(acc[j], f[j]);
             }
-            sum = pair_total(acc);
-            s_cur = s_nxt;
+            st_cur = st_nxt;
+            st_nxt += stage_pitch;
             if (++s_nxt == uint32_t(S)) {
                 s_nxt = 0;
+                st_nxt = my0;
                 par_nxt ^= 1u;
             }
+            return pair_total(acc);
         };
 
         constexpr int K = kFwd ? 2 : 4;
         float mean;
         {
             float v[K] = {};
-            first_pass(0, v[0]);
+            v[0] = first_pass(0);
             cta_sums<K>(v, red + (turn & 1) * 64, warps);
             dead = count[16 + (turn & 1)] != 0;          // the same for every thread
             ++turn;
             mean = __fmul_rn(v[0], p.inv_h);
         }
         for (int i = 0; i < n && !dead; ++i) {
-            const uint32_t s_row = s_cur;
+            const uint32_t st = st_cur;
             if constexpr (kFwd) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) cur[k] = nxt[k];
             }
             float v[K] = {};
-            if (i + 1 < n) first_pass(i + 1, v[0]);
+            if (i + 1 < n) v[0] = first_pass(i + 1);
             // ------------------------------------------------ second pass: deviations
-            const uint8_t *st = stages + s_row * stage_bytes;
             const f2_t neg = f2_both(-mean);
-            const LnEntry e = list[i];
             f2_t d[kHold ? NV : 1][P], g[kHold && !kFwd ? NV : 1][P];
-            f2_t m2[P][1], sa[P][1], sc[P][1];
-#pragma unroll
-            for (int j = 0; j < P; ++j) m2[j][0] = sa[j][0] = sc[j][0] = 0;
+            f2_t m2[P], sa[P], sc[P];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int vec = tid + k * T;
                 const int kk = kHold ? k : 0;
-                if (vec < V) {
-                    if constexpr (kFwd) up<E>(cur[k], d[kk]);
-                    else up<E>(ld_shared_v4(st + vec * 16), d[kk]);
-                    if constexpr (!kFwd) up<E>(ld_shared_v4(st + row_bytes + vec * 16), g[kk]);
+                if constexpr (kFwd) up<E>(cur[k], d[kk]);
+                else up<E>(lds_v4(st + k * step), d[kk]);
+                if constexpr (!kFwd) up<E>(lds_v4(st + pitch + k * step), g[kk]);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        d[kk][j] = f2_add(d[kk][j], neg);
-                        m2[j][0] = f2_fma(d[kk][j], d[kk][j], m2[j][0]);
-                        if constexpr (!kFwd) {
-                            const f2_t a = f2_mul(g[kk][j], w[k][j]);
-                            sa[j][0] = f2_add(sa[j][0], a);
-                            sc[j][0] = f2_fma(a, d[kk][j], sc[j][0]);
-                        }
+                for (int j = 0; j < P; ++j) {
+                    d[kk][j] = k == 0 ? f2_add(d[kk][j], neg) : f2_fma(in_row[k], neg, d[kk][j]);
+                    m2[j] = k == 0 ? f2_mul(d[kk][j], d[kk][j]) : f2_fma(d[kk][j], d[kk][j], m2[j]);
+                    if constexpr (!kFwd) {
+                        const f2_t a = f2_mul(g[kk][j], w[k][j]);
+                        sa[j] = k == 0 ? a : f2_add(sa[j], a);
+                        sc[j] = k == 0 ? f2_mul(a, d[kk][j]) : f2_fma(a, d[kk][j], sc[j]);
                     }
                 }
             }
@@ -416,130 +461,129 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
             if (dead) break;
             // every thread has read the stage of row i + 1 (forward) or i - 1 (backward)
             if (tid == 0 && issued < n && (kFwd || i >= 1)) issue(issued++);
+            const LnEntry e = lds_entry(list0 + uint32_t(i) * 16u);
             const float rstd = rsqrtf(__fmaf_rn(v[1], p.inv_h, p.eps));
+            const f2_t r2 = f2_both(rstd);
             if constexpr (kFwd) {
                 if (tid == 0) {
-                    if (p.mean) p.mean[e.prow] = mean;
-                    if (p.rstd) p.rstd[e.prow] = rstd;
+                    if (p.mean) p.mean[e.tag] = mean;
+                    if (p.rstd) p.rstd[e.tag] = rstd;
                 }
-                const f2_t r2 = f2_both(rstd);
+                E *out = static_cast<E *>(p.out) + e.off + tid * kE;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int vec = tid + k * T;
                     const int kk = kHold ? k : 0;
-                    if (vec < V) {
-                        if constexpr (!kHold) {
-                            up<E>(cur[k], d[0]);
+                    if constexpr (!kHold) {
+                        up<E>(cur[k], d[0]);
 #pragma unroll
-                            for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
-                        }
-                        f2_t o[P];
-#pragma unroll
-                        for (int j = 0; j < P; ++j) o[j] = f2_fma(f2_mul(d[kk][j], r2), w[k][j], b[k][j]);
-                        st_global_v4(static_cast<E *>(p.out) + e.off + vec * kE, down<E>(o));
+                        for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
                     }
+                    f2_t o[P];
+#pragma unroll
+                    for (int j = 0; j < P; ++j) o[j] = f2_fma(f2_mul(d[kk][j], r2), w[k][j], b[k][j]);
+                    const uint4 u = down<E>(o);
+                    if (tid + k * T < V) st_global_v4(out + k * T * kE, u);
                 }
             } else {
-                const float ma = __fmul_rn(v[2], p.inv_h), mc = __fmul_rn(__fmul_rn(v[3], p.inv_h), rstd);
-                const f2_t r2 = f2_both(rstd), nma = f2_both(-ma), nmc = f2_both(-mc);
-                const f2_t s2 = f2_both(__fmul_rn(rstd, p.grad_scale));
-                const bool spill = GRADS && (e.prow >> 31);
-                const uint32_t lrow = e.lrow & 0x7fffffffu;
+                // o = s (a - mean(a) - xhat mean(a xhat)) as a s + (d c1 + c0)
+                const float s1 = __fmul_rn(rstd, p.grad_scale), ma = __fmul_rn(v[2], p.inv_h);
+                const float mc = __fmul_rn(__fmul_rn(v[3], p.inv_h), rstd);
+                const f2_t s2 = f2_both(s1), c0 = f2_both(-__fmul_rn(s1, ma));
+                const f2_t c1 = f2_both(-__fmul_rn(s1, __fmul_rn(mc, rstd)));
+                const bool write = !GRADS || p.out;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int vec = tid + k * T;
                     const int kk = kHold ? k : 0;
-                    if (vec < V) {
-                        if constexpr (!kHold) {
-                            up<E>(ld_shared_v4(st + vec * 16), d[0]);
-                            up<E>(ld_shared_v4(st + row_bytes + vec * 16), g[0]);
+                    if constexpr (!kHold) {
+                        up<E>(lds_v4(st + k * step), d[0]);
+                        up<E>(lds_v4(st + pitch + k * step), g[0]);
 #pragma unroll
-                            for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
-                        }
-                        f2_t xh[P], o[P];
+                        for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
+                    }
+                    f2_t o[P];
 #pragma unroll
-                        for (int j = 0; j < P; ++j) {
-                            xh[j] = f2_mul(d[kk][j], r2);
-                            o[j] = f2_add(f2_fma(xh[j], nmc, f2_mul(g[kk][j], w[k][j])), nma);
-                        }
+                    for (int j = 0; j < P; ++j) {
+                        o[j] = f2_fma(f2_mul(g[kk][j], w[k][j]), s2, f2_fma(d[kk][j], c1, c0));
                         if constexpr (GRADS) {
-                            if (!spill) {
-#pragma unroll
-                                for (int j = 0; j < P; ++j) {
-                                    dw[k][j] = f2_fma(g[kk][j], xh[j], dw[k][j]);
-                                    db[k][j] = f2_add(db[k][j], g[kk][j]);
-                                }
-                            } else {
-                                float *sp = p.ws.spill + int64_t(lrow) * 2 * p.hidden + vec * kE;
-#pragma unroll
-                                for (int j = 0; j < P; ++j) {
-                                    *reinterpret_cast<f2_t *>(sp + 2 * j) = xh[j];
-                                    *reinterpret_cast<f2_t *>(sp + p.hidden + 2 * j) = g[kk][j];
-                                }
-                            }
+                            dw[k][j] = f2_fma(g[kk][j], f2_mul(d[kk][j], r2), dw[k][j]);
+                            db[k][j] = f2_add(db[k][j], g[kk][j]);
                         }
-                        if (!GRADS || p.out) {
-                            if (p.res) {
-                                f2_t q[P];
-                                if (nt == 3) up<E>(ld_shared_v4(st + 2 * row_bytes + vec * 16), q);
-                                else up<E>(*reinterpret_cast<const uint4 *>(static_cast<const E *>(p.res) + e.off + vec * kE), q);
+                    }
+                    if (write) {
+                        const int64_t at = e.off + (tid + k * T) * kE;
+                        const bool in = tid + k * T < V;
+                        if (p.res) {
+                            f2_t q[P];
+                            if (nt == 3) up<E>(lds_v4(st + 2 * pitch + k * step), q);
+                            else up<E>(in ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(p.res) + at) : make_uint4(0, 0, 0, 0), q);
 #pragma unroll
-                                for (int j = 0; j < P; ++j) o[j] = f2_fma(o[j], s2, q[j]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < P; ++j) o[j] = f2_mul(o[j], s2);
-                            }
-                            st_global_v4(static_cast<E *>(p.out) + e.off + vec * kE, down<E>(o));
-                            if constexpr (DROP) {
-                                drop_pairs(o, lane_keep<E>(vec, lrow, key, p.drop.t), p.drop.scale);
-                                st_global_v4(static_cast<E *>(p.out2) + e.off + vec * kE, down<E>(o));
-                            }
+                            for (int j = 0; j < P; ++j) o[j] = f2_add(o[j], q[j]);
+                        }
+                        const uint4 u = down<E>(o);
+                        if (in) st_global_v4(static_cast<E *>(p.out) + at, u);
+                        if constexpr (DROP) {
+                            drop_pairs(o, lane_keep<E>(tid + k * T, e.lrow, key, p.drop.t), p.drop.scale);
+                            const uint4 u2 = down<E>(o);
+                            if (in) st_global_v4(static_cast<E *>(p.out2) + at, u2);
                         }
                     }
                 }
                 if constexpr (GRADS) {
-                    const LnEntry nx = i + 1 < n ? list[i + 1] : LnEntry{0, 0xffffffffu, 0x80000000u};
-                    const uint32_t nx_row = nx.prow >> 31 ? 0xffffffffu : nx.lrow & 0x7fffffffu;
-                    if (spill) {
-                        if (tid == 0) {
-                            if (p.ws.flag[lrow] || p.ws.state[lrow / kGroupRows] != kGroupNone) set_status(p.ws.hdr, kStDouble);
-                            p.ws.flag[lrow] = 1;
-                        }
-                    } else if (nx_row / kGroupRows != lrow / kGroupRows) {
-                        // the group is complete
-                        const bool whole = e.lrow >> 31;
-                        const bool first = lrow % kBlockRows < kGroupRows, last = nx_row / kBlockRows != lrow / kBlockRows;
-                        const int64_t slot = whole ? int64_t(lrow / kBlockRows) * kGroups : int64_t(lrow / kGroupRows);
-                        float *dst = p.ws.partial + slot * 2 * p.hidden;
+                    if (e.tag) {
+                        // the end of a group, or a row of a cut one (between groups: the
+                        // sums hold that row alone and are dropped)
+                        const bool spill = e.tag & kTagSpill, fold = e.tag & kTagFold, store = e.tag & kTagStore;
+                        const uint32_t group = e.lrow / kGroupRows, place = group % kGroups;
+                        const int64_t slot = fold ? int64_t(group - place) : int64_t(group);
+                        float *dst = spill ? p.ws.spill + int64_t(e.lrow) * 2 * p.hidden : p.ws.partial + slot * 2 * p.hidden;
 #pragma unroll
                         for (int k = 0; k < NV; ++k) {
-                            const int vec = tid + k * T;
-                            if (vec < V) {
-                                float *a = whole && !last ? block_acc : dst;
-                                f2_t *aw = reinterpret_cast<f2_t *>(a + vec * kE), *ab = reinterpret_cast<f2_t *>(a + p.hidden + vec * kE);
-                                const f2_t *pw = reinterpret_cast<const f2_t *>(block_acc + vec * kE);
-                                const f2_t *pb = reinterpret_cast<const f2_t *>(block_acc + p.hidden + vec * kE);
+                            const int col = (tid + k * T) * kE;
+                            if (tid + k * T < V) {
+                                if (spill) {             // xhat and dy
+                                    const int kk = kHold ? k : 0;
+                                    if constexpr (!kHold) {
+                                        up<E>(lds_v4(st + k * step), d[0]);
+                                        up<E>(lds_v4(st + pitch + k * step), g[0]);
 #pragma unroll
-                                for (int j = 0; j < P; ++j) {
-                                    if (whole && !first) {
-                                        dw[k][j] = f2_add(pw[j], dw[k][j]);
-                                        db[k][j] = f2_add(pb[j], db[k][j]);
+                                        for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
                                     }
-                                    aw[j] = dw[k][j];
-                                    ab[j] = db[k][j];
-                                    dw[k][j] = db[k][j] = 0;
+                                    f2_t xh[P];
+#pragma unroll
+                                    for (int j = 0; j < P; ++j) xh[j] = f2_mul(d[kk][j], r2);
+                                    pairs_store(dst + col, xh);
+                                    pairs_store(dst + p.hidden + col, g[kk]);
+                                } else {
+                                    if (fold && place != 0) {
+                                        f2_t t[P];
+                                        pairs_load(block_acc + col, t);
+#pragma unroll
+                                        for (int j = 0; j < P; ++j) dw[k][j] = f2_add(t[j], dw[k][j]);
+                                        pairs_load(block_acc + p.hidden + col, t);
+#pragma unroll
+                                        for (int j = 0; j < P; ++j) db[k][j] = f2_add(t[j], db[k][j]);
+                                    }
+                                    if (store) {
+                                        pairs_store(dst + col, dw[k]);
+                                        pairs_store(dst + p.hidden + col, db[k]);
+                                    } else {
+                                        pairs_store(block_acc + col, dw[k]);
+                                        pairs_store(block_acc + p.hidden + col, db[k]);
+                                    }
                                 }
                             }
+#pragma unroll
+                            for (int j = 0; j < P; ++j) dw[k][j] = db[k][j] = 0;
                         }
-                        if (tid == 0 && (last || !whole)) {
-                            if (whole) {
-                                uint64_t *state = reinterpret_cast<uint64_t *>(p.ws.state) + lrow / kBlockRows;
-                                if (*state != 0) set_status(p.ws.hdr, kStDouble);
-                                *state = 0x0101010101010101ull * kGroupWhole;
+                        if (tid == 0) {
+                            if (spill) {
+                                if (p.ws.flag[e.lrow] || p.ws.state[group] != 0) set_status(p.ws.hdr, kStDouble);
+                                p.ws.flag[e.lrow] = 1;
                             } else {
-                                uint8_t *state = p.ws.state + lrow / kGroupRows;
-                                if (*state != kGroupNone) set_status(p.ws.hdr, kStDouble);
-                                *state = kGroupPartial;
+                                // state of a group: 1 + the number of groups behind it in its partial
+                                if (p.ws.state[group] != 0) set_status(p.ws.hdr, kStDouble);
+                                if (!fold) p.ws.state[group] = 1;
+                                else p.ws.state[group - place] = uint8_t(place + 1);
                             }
                         }
                     }
