@@ -219,16 +219,11 @@ extern "C" int layernorm_finalize(void *workspace, int64_t n_logical_rows, int64
     float *scratch[2] = {ws.scratch_a, ws.scratch_b};
     int flip = 0;
     for (int64_t n = ws.n_blocks;;) {
-        // One launch where four rounds of a CTA hold all inputs; else as many
-        // rounds as still leave two CTAs per SM.
-        int rounds = 4;
-        if (n > 4 * kLnTreeBlocks)
-            while (rounds > 1 && (n + rounds * kLnTreeBlocks - 1) / (rounds * kLnTreeBlocks) * gy < 2 * int64_t(d->sms)) rounds /= 2;
-        const int64_t groups = (n + rounds * kLnTreeBlocks - 1) / (rounds * kLnTreeBlocks);
+        const int64_t groups = (n + kLnTreeBlocks - 1) / kLnTreeBlocks;
         const bool last = groups == 1;
         float *dst = scratch[flip];
-        ln_tree_kernel<<<dim3(unsigned(groups), gy), 1024, 0, s>>>(
-            ws, in, last ? dweight : dst, last ? dbias : dst + hidden, last ? 0 : 2 * hidden, n, rounds,
+        ln_tree_kernel<<<dim3(unsigned(groups), gy), 256, 0, s>>>(
+            ws, in, last ? dweight : dst, last ? dbias : dst + hidden, last ? 0 : 2 * hidden, n,
             last ? grad_scale : 1.f);
         if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
         count_launch();

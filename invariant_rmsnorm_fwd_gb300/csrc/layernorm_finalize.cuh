@@ -19,8 +19,8 @@ __global__ void ln_begin_kernel(LnWs ws) {
     }
 }
 
-constexpr int kLnTreeCols = 32;                          // columns of [dweight | dbias] per CTA
-constexpr int kLnTreeBlocks = 128;                       // blocks per round: 8 lanes (4 columns each) per block
+constexpr int kLnTreeCols = 32;                          // columns of [dweight | dbias] per CTA: 8 lanes of 4
+constexpr int kLnTreeBlocks = 32;                        // inputs per CTA
 
 __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
@@ -28,8 +28,10 @@ __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
 
 // Four columns of block b from column col of [dweight | dbias]: the groups from
 // the first to the last, each from a stored partial or folded from its spilled
-// rows.  All stored partials are requested before any is used.
-__device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int64_t col, uint64_t state, int &bad) {
+// rows.  All stored partials are requested before any is used.  check: report
+// rows that are missing or arrived twice (one CTA per block does).
+__device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int64_t col, uint64_t state, bool check,
+                                                 int &bad) {
     const int64_t H2 = 2 * ws.hidden;
     const float *part = ws.partial + b * kGroups * H2 + col;
     const int64_t left = ws.n_rows - b * kBlockRows;
@@ -45,7 +47,7 @@ __device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int6
     for (int j = 0; j < kGroups; ++j) {
         const int c = int((state >> (8 * j)) & 0xff);
         if (j < next) {                                  // inside the fold of the block's first groups
-            if (c || flags[j]) bad |= kStDouble;
+            if (check && (c || flags[j])) bad |= kStDouble;
             continue;
         }
         if (j >= groups) continue;
@@ -53,7 +55,7 @@ __device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int6
         if (c) {
             g = v[j];
             next = j + c;
-            if (flags[j]) bad |= kStDouble;
+            if (check && flags[j]) bad |= kStDouble;
         } else {
             next = j + 1;
             g = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -80,74 +82,58 @@ __device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int6
     return acc;
 }
 
-// Pairwise tree with odd carry over n_in inputs (block values, or the results
-// of an earlier pass): CTA (g, c) reduces inputs [g m, (g + 1) m), m = rounds *
-// 128 a power of two, so each result is one node of the tree over all inputs.
-// Eight lanes hold the 32 columns of a block; the four blocks of a warp meet by
-// shuffles, the warps and the rounds through shared memory.
-__global__ void __launch_bounds__(1024) ln_tree_kernel(LnWs ws, const float *in, float *out_w, float *out_b,
-                                                       int64_t out_stride, int64_t n_in, int rounds, float scale) {
-    __shared__ float4 val[32][8];
-    __shared__ float node[4][kLnTreeCols];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7;
+// One pass of the pairwise tree with odd carry over n_in inputs (block values in
+// the first pass, then the results of the one before): CTA (g, c) reduces inputs
+// [32 g, 32 g + 32) of 32 columns to one node.  Eight lanes hold the columns of
+// an input, a warp four inputs, which meet by shuffles; the eight warps through
+// shared memory.  All loads of a pass are in flight at once; what bounds the
+// first pass is reading the partials (mostly from L2), the others are latency.
+__global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, float *out_w, float *out_b,
+                                                      int64_t out_stride, int64_t n_in, float scale) {
+    __shared__ float4 val[8][8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7, i = tid >> 3;
     const int64_t H2 = 2 * ws.hidden, col = int64_t(blockIdx.y) * kLnTreeCols + part * 4;
-    const int64_t base = int64_t(blockIdx.x) * rounds * kLnTreeBlocks;
+    const int64_t first = int64_t(blockIdx.x) * kLnTreeBlocks;
     if (!in && !ln_header_ok(ws)) {
         if (tid == 0) set_status(ws.hdr, kStHeader);
         return;
     }
-    int used = 0;
-    for (int r = 0; r < rounds; ++r) {
-        const int64_t first = base + r * kLnTreeBlocks;
-        if (first >= n_in) break;
-        used = r + 1;
-        const int m = n_in - first < kLnTreeBlocks ? int(n_in - first) : kLnTreeBlocks;
-        const int i = tid >> 3;                          // input of this thread within the round
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        int bad = 0;
-        if (i < m && col < H2) {
-            if (in) v = *reinterpret_cast<const float4 *>(in + (first + i) * H2 + col);
-            else v = ln_block_value(ws, first + i, col, reinterpret_cast<const uint64_t *>(ws.state)[first + i], bad);
-        }
-        if (bad) set_status(ws.hdr, bad);
-#pragma unroll
-        for (int o = 8; o <= 16; o <<= 1) {              // inputs 1, then 2 apart
-            float4 u;
-            u.x = __shfl_down_sync(kFull, v.x, o);
-            u.y = __shfl_down_sync(kFull, v.y, o);
-            u.z = __shfl_down_sync(kFull, v.z, o);
-            u.w = __shfl_down_sync(kFull, v.w, o);
-            if (i + (o >> 3) < m) v = add4(v, u);
-        }
-        if (lane < 8) val[warp][part] = v;
-        __syncthreads();
-        if (warp == 0) {                                 // one column per lane: the warps' quadruples
-            float x[32];
-            const float *f = reinterpret_cast<const float *>(val);
-            const int n = (m + 3) / 4;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = f[k * kLnTreeCols + lane];
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-                for (int k = 0; k + s < 32; k += 2 * s)
-                    if (k + s < n) x[k] = __fadd_rn(x[k], x[k + s]);
-            node[r][lane] = x[0];
-        }
-        __syncthreads();
+    const int m = n_in - first < kLnTreeBlocks ? int(n_in - first) : kLnTreeBlocks;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    int bad = 0;
+    if (i < m && col < H2) {
+        if (in) v = *reinterpret_cast<const float4 *>(in + (first + i) * H2 + col);
+        else v = ln_block_value(ws, first + i, col, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
+                                blockIdx.y == 0, bad);
     }
-    if (warp == 0) {
-        float x[4];
+    if (bad) set_status(ws.hdr, bad);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = k < used ? node[k][lane] : 0.f;
-        if (used > 1) x[0] = __fadd_rn(x[0], x[1]);
-        if (used > 3) x[2] = __fadd_rn(x[2], x[3]);
-        if (used > 2) x[0] = __fadd_rn(x[0], x[2]);
+    for (int o = 8; o <= 16; o <<= 1) {                  // inputs 1, then 2 apart
+        float4 u;
+        u.x = __shfl_down_sync(kFull, v.x, o);
+        u.y = __shfl_down_sync(kFull, v.y, o);
+        u.z = __shfl_down_sync(kFull, v.z, o);
+        u.w = __shfl_down_sync(kFull, v.w, o);
+        if (i + (o >> 3) < m) v = add4(v, u);
+    }
+    if (lane < 8) val[warp][part] = v;
+    __syncthreads();
+    if (warp == 0) {                                     // one column per lane: the warps' quadruples
+        float x[8];
+        const float *f = reinterpret_cast<const float *>(val);
+        const int n = (m + 3) / 4;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = f[k * kLnTreeCols + lane];
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+            for (int k = 0; k + s < 8; k += 2 * s)
+                if (k + s < n) x[k] = __fadd_rn(x[k], x[k + s]);
         const int64_t c = int64_t(blockIdx.y) * kLnTreeCols + lane;
-        const float v = scale != 1.f ? __fmul_rn(x[0], scale) : x[0];   // scaled only at the root
+        const float r = scale != 1.f ? __fmul_rn(x[0], scale) : x[0];   // scaled only at the root
         if (c < H2) {
             float *dst = c < ws.hidden ? out_w : out_b;
-            if (dst) dst[blockIdx.x * out_stride + (c < ws.hidden ? c : c - ws.hidden)] = v;
+            if (dst) dst[blockIdx.x * out_stride + (c < ws.hidden ? c : c - ws.hidden)] = r;
         }
     }
 }
