@@ -21,7 +21,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fno-strict-aliasing", f"-I{INCLUDE}"]
 SOURCES = ["rmsnorm_bi.cu", "rows_fwd.cu", "rows_dx.cu", "rows_dxdw.cu", "rows_adddxdw.cu", "gemm_dw.cu",
-           "layernorm.cu", "ln_rows_bf16.cu", "ln_rows_fp16.cu", "ln_rows_fp32.cu", "plan.cpp"]
+           "layernorm.cu", "ln_rows_bf16.cu", "ln_rows_fp16.cu", "ln_rows_fp32.cu",
+           "ln_narrow_bf16.cu", "ln_narrow_fp16.cu", "ln_narrow_fp32.cu", "plan.cpp"]
 
 
 def nvcc() -> str:

@@ -1,4 +1,4 @@
-// Launcher of the layer-norm row kernels, instantiated per element type.
+// Launcher of the streaming layer-norm kernel, instantiated per element type.
 #pragma once
 #include <mutex>
 
@@ -7,24 +7,6 @@
 #include "layernorm_stream.cuh"
 
 namespace rbi {
-
-// ----------------------------------------------------------------- rows of at most 256 columns
-
-template <class E>
-int ln_launch_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
-    const int V = p.hidden / 8, threads = (V + 31) / 32 * 32;
-    const int64_t grid = grads ? p.n_items * kGroups : p.n_rows;
-    if (grid == 0) return RMSNORM_OK;
-    if (grid >= (int64_t(1) << 31)) return RMSNORM_ERR_LAYOUT;
-    if (grads) ln_rows_kernel<E, 1, true, true><<<unsigned(grid), threads, 0, stream>>>(p);
-    else if (bwd) ln_rows_kernel<E, 1, true, false><<<unsigned(grid), threads, 0, stream>>>(p);
-    else ln_rows_kernel<E, 1, false, false><<<unsigned(grid), threads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
-    count_launch();
-    return RMSNORM_OK;
-}
-
-// ----------------------------------------------------------------- wider rows
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // an SM's shared memory; what the system takes per CTA
 
@@ -110,7 +92,7 @@ template <class E>
 int ln_run_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
-    if (p.hidden <= 256) return ln_launch_rows<E>(p, bwd, grads, stream);
+    if (p.hidden <= 256) return ln_run_narrow<E>(p, bwd, grads, stream);
     if constexpr (sizeof(E) == 4) {
         return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
     } else {

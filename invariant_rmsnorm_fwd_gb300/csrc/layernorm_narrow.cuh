@@ -1,0 +1,365 @@
+// Row kernel of the layer norm for rows of at most 256 columns (per-head norms).
+//
+// A row is held by a team of P lanes, 8 columns a lane, so a warp works on 32 / P
+// rows at once and a row's sums need only shuffles.  A team takes the 8 slots of
+// one group one after the other (in logical order where parameter gradients are
+// wanted), kB rows at a time: their loads are issued together, which keeps enough
+// bytes on their way with a few warps per SM.  Empty slots are computed as zeros
+// and store nothing, so the shuffles of a warp stay together.
+//
+// Parameter gradients: a lane's columns add up in its registers over the group;
+// the groups of a block are in one CTA, which folds them through shared memory
+// (from the first to the last) and writes one partial per block.
+#pragma once
+#include "host.cuh"
+#include "layernorm_host.cuh"
+#include "layernorm_stream.cuh"
+
+namespace rbi {
+
+template <class E>
+struct Oct {                         // 8 packed elements
+    static constexpr int kQ = int(sizeof(E)) / 2;        // 16-byte words
+    uint4 q[kQ];
+};
+template <class E>
+__device__ __forceinline__ Oct<E> oct_load(const void *base, int64_t elem) {
+    Oct<E> v;
+#pragma unroll
+    for (int i = 0; i < Oct<E>::kQ; ++i) v.q[i] = reinterpret_cast<const uint4 *>(static_cast<const E *>(base) + elem)[i];
+    return v;
+}
+template <class E>
+__device__ __forceinline__ void oct_store(void *base, int64_t elem, const f2_t (&f)[4]) {
+    E *p = static_cast<E *>(base) + elem;
+    if constexpr (sizeof(E) == 4) {
+        st_global_f2x4(reinterpret_cast<float *>(p), f);
+    } else {
+        st_global_v4(p, down<E>(f));
+    }
+}
+template <class E>
+__device__ __forceinline__ void oct_up(const Oct<E> &v, f2_t (&f)[4]) {
+    if constexpr (sizeof(E) == 4) {
+        f2_t a[2], b[2];
+        up<E>(v.q[0], a);
+        up<E>(v.q[1], b);
+        f[0] = a[0];
+        f[1] = a[1];
+        f[2] = b[0];
+        f[3] = b[1];
+    } else {
+        up<E>(v.q[0], f);
+    }
+}
+template <class E>
+__device__ __forceinline__ void oct_param(const void *p, int f32, int v, float none, f2_t (&f)[4]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = f2_both(none);
+    } else if (f32) {
+        oct_up<float>(oct_load<float>(p, v * 8), f);
+    } else {
+        oct_up<E>(oct_load<E>(p, v * 8), f);
+    }
+}
+
+// Sum over a team of P lanes; every lane gets it.
+template <int P>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+    for (int o = P / 2; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+constexpr int kNarrowThreads = 256;
+
+// RES: dres is added (kLnBwd).  The slots of a group are read once, slot j by
+// lane j % P of the team, and handed round row by row.
+template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES, int KB, int MINB>
+__global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const __grid_constant__ LnParams p) {
+    constexpr bool kFwd = MODE != kLnBwd, kRes = MODE == kLnAdd || RES;
+    constexpr int kB = KB;                               // rows side by side
+    constexpr int kOwn = P >= kGroupRows ? 1 : kGroupRows / P;   // slots of a lane
+    __shared__ float sums[GRADS ? kNarrowThreads * 16 : 1];   // [team][dweight, dbias][8 P]
+    const int tid = threadIdx.x, team = tid / P, l = tid % P, V = p.hidden >> 3;
+    const bool col = l < V;                              // this lane has columns
+    if constexpr (GRADS) {
+        if (!ln_header_ok(p.ws)) {
+            if (tid == 0) set_status(p.ws.hdr, kStHeader);
+            return;
+        }
+    }
+    const DropKey key = DROP ? drop_key(p.drop) : DropKey{0, 0, 0, 0};
+    const int64_t group = int64_t(blockIdx.x) * (kNarrowThreads / P) + team;     // 8 slots of the call or plan
+    int kind = 0, block = -1, slot0 = 0;
+    bool partial = false;
+    int64_t own_off[kOwn];
+    uint32_t own_row[kOwn], on = 0;                      // on: the team's slots that hold a row
+    if constexpr (GRADS) {
+        slot0 = int(group % kGroups) * kGroupRows;
+        if (group < p.n_items * kGroups) {
+            const PlanItem &it = p.items[group / kGroups];
+            kind = it.kind;
+            block = it.block;
+            // the item's groups that hold all their rows
+            partial = kind == kItemWhole || (kind == kItemQuarters && ((it.quarters >> (slot0 / 16)) & 1));
+        }
+    }
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int j = l + o * P;
+        int64_t prow = -1;
+        bool valid = false;
+        own_off[o] = 0;
+        own_row[o] = 0;
+        if (j < kGroupRows) {
+            if constexpr (GRADS) {
+                if (group < p.n_items * kGroups) {
+                    const PlanItem &it = p.items[group / kGroups];
+                    prow = it.prow[slot0 + j];
+                    const int32_t lr = it.lrow[slot0 + j];
+                    if (prow >= 0) {
+                        valid = prow < p.n_rows && lr >= 0 && lr < p.ws.n_rows &&
+                                (kind == kItemSpill ||
+                                 ((kind == kItemWhole || kind == kItemQuarters) && lr == int64_t(block) * kBlockRows + slot0 + j));
+                        if (!valid) set_status(p.ws.hdr, kStPlan);
+                        own_row[o] = uint32_t(lr);
+                    }
+                }
+            } else {
+                prow = group * kGroupRows + j;
+                if (prow < p.n_rows) {
+                    const uint32_t t = uint32_t(prow) / uint32_t(p.rpt);
+                    const int32_t id = p.tok_id[t];
+                    valid = id >= 0;
+                    own_row[o] = uint32_t(id) * uint32_t(p.rpt) + uint32_t(prow) - t * uint32_t(p.rpt);
+                }
+            }
+            if (valid) {
+                const uint32_t t = uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - t * uint32_t(p.rpt);
+                own_off[o] = int64_t(t) * p.token_stride + int64_t(head) * p.hidden;
+            }
+        }
+        const uint32_t all = __ballot_sync(kFull, valid) >> ((tid & 31) - l);
+        on |= (all & ((1u << (P < kGroupRows ? P : kGroupRows)) - 1u)) << (o * P);
+    }
+    f2_t w[4], b[4], dw[4], db[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = b[j] = dw[j] = db[j] = 0;
+    if (col) {
+        oct_param<E>(p.w, p.params_f32, l, 1.f, w);
+        if constexpr (kFwd) oct_param<E>(p.b, p.params_f32, l, 0.f, b);
+    }
+    float own_mean[kFwd ? kOwn : 1], own_rstd[kFwd ? kOwn : 1];
+#pragma unroll
+    for (int s = 0; s < kGroupRows; s += kB) {
+        int64_t off[kB];
+        Oct<E> xo[kB], ro[kRes ? kB : 1], go[kFwd ? 1 : kB];
+#pragma unroll
+        for (int r = 0; r < kB; ++r) {
+            const int j = s + r;
+            off[r] = __shfl_sync(kFull, own_off[j / P], j % P, P) + l * 8;
+            const bool ld = ((on >> j) & 1) && col;
+#pragma unroll
+            for (int q = 0; q < Oct<E>::kQ; ++q) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                xo[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.x) + off[r])[q] : z;
+                if constexpr (!kFwd) go[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.dy) + off[r])[q] : z;
+                if constexpr (kRes) ro[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.res) + off[r])[q] : z;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kB; ++r) {
+            const int j0 = s + r;
+            const bool row = (on >> j0) & 1, st = row && col;
+            uint32_t lrow = 0;
+            if constexpr (DROP || GRADS) lrow = __shfl_sync(kFull, own_row[j0 / P], j0 % P, P);
+            f2_t x[4], g[4];
+            oct_up<E>(xo[r], x);
+            if constexpr (MODE == kLnAdd) {
+                f2_t q[4];
+                oct_up<E>(ro[r], q);
+                if constexpr (DROP) {
+                    const uint32_t keep = keep_bits(uint32_t(l), lrow, key, p.drop.t);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = __fmaf_rn(f2_lo(x[j]), p.drop.scale, f2_lo(q[j]));
+                        const float c = __fmaf_rn(f2_hi(x[j]), p.drop.scale, f2_hi(q[j]));
+                        x[j] = f2_make((keep >> (2 * j)) & 1 ? a : f2_lo(q[j]), (keep >> (2 * j + 1)) & 1 ? c : f2_hi(q[j]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = f2_add(x[j], q[j]);
+                }
+                if (st) oct_store<E>(p.out2, off[r], x);
+                if constexpr (sizeof(E) == 2) {          // the norm takes the stored h
+                    const uint4 h = down<E>(x);
+                    up<E>(h, x);
+                }
+            }
+            f2_t t = f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3]));
+            const float mean = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(t), f2_hi(t))), p.inv_h);
+            const f2_t neg = col ? f2_both(-mean) : 0;
+            f2_t m2, sa, sc;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = f2_add(x[j], neg);
+                m2 = j == 0 ? f2_mul(x[0], x[0]) : f2_fma(x[j], x[j], m2);
+            }
+            if constexpr (kFwd) {
+                const float var = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(m2), f2_hi(m2))), p.inv_h);
+                const float rstd = rsqrtf(__fadd_rn(var, p.eps));
+                if (l == j0 % P) {
+                    own_mean[j0 / P] = mean;
+                    own_rstd[j0 / P] = rstd;
+                }
+                const f2_t r2 = f2_both(rstd);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = f2_fma(f2_mul(x[j], r2), w[j], b[j]);
+                if (st) oct_store<E>(p.out, off[r], x);
+            } else {
+                // the three sums of the row side by side (independent shuffles)
+                oct_up<E>(go[r], g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2_t a = f2_mul(g[j], w[j]);
+                    sa = j == 0 ? a : f2_add(sa, a);
+                    sc = j == 0 ? f2_mul(a, x[0]) : f2_fma(a, x[j], sc);
+                }
+                const float var = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(m2), f2_hi(m2))), p.inv_h);
+                const float ma = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(sa), f2_hi(sa))), p.inv_h);
+                const float md = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(sc), f2_hi(sc))), p.inv_h);
+                // (an empty slot adds zeros, also where eps is 0)
+                const float rstd = row ? rsqrtf(__fadd_rn(var, p.eps)) : 0.f;
+                const f2_t r2 = f2_both(rstd);
+                // s (a - mean(a) - xhat mean(a xhat)) as a s + (d c1 + c0)
+                const float s1 = __fmul_rn(rstd, p.grad_scale), mc = __fmul_rn(md, rstd);
+                const f2_t s2 = f2_both(s1), c0 = f2_both(-__fmul_rn(s1, ma)), c1 = f2_both(-__fmul_rn(s1, __fmul_rn(mc, rstd)));
+                f2_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[j] = f2_fma(f2_mul(g[j], w[j]), s2, f2_fma(x[j], c1, c0));
+                    if constexpr (GRADS) {
+                        x[j] = f2_mul(x[j], r2);
+                        dw[j] = f2_fma(g[j], x[j], dw[j]);
+                        db[j] = f2_add(db[j], g[j]);
+                    }
+                }
+                if constexpr (GRADS) {
+                    if (row && !partial) {               // a row of a cut group
+                        if (col) {
+                            float *sp = p.ws.spill + int64_t(lrow) * 2 * p.hidden + l * 8;
+                            st_global_f2x4(sp, x);
+                            st_global_f2x4(sp + p.hidden, g);
+                        }
+                        if (l == 0) {
+                            if (p.ws.flag[lrow] || p.ws.state[lrow / kGroupRows] != 0) set_status(p.ws.hdr, kStDouble);
+                            p.ws.flag[lrow] = 1;
+                        }
+                    }
+                }
+                if constexpr (RES) {
+                    f2_t q[4];
+                    oct_up<E>(ro[r], q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], q[j]);
+                }
+                if (st && (!GRADS || p.out)) {
+                    oct_store<E>(p.out, off[r], o);
+                    if constexpr (DROP) {
+                        drop_pairs(o, keep_bits(uint32_t(l), lrow, key, p.drop.t), p.drop.scale);
+                        oct_store<E>(p.out2, off[r], o);
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (kFwd) {
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int j = l + o * P;
+            if (j < kGroupRows && ((on >> j) & 1)) {
+                const int64_t prow = group * kGroupRows + j;
+                if (p.mean) p.mean[prow] = own_mean[o];
+                if (p.rstd) p.rstd[prow] = own_rstd[o];
+            }
+        }
+    }
+    if constexpr (GRADS) {
+        float *mine = sums + team * 16 * P + l * 8;
+        pairs_store(mine, dw);
+        pairs_store(mine + 8 * P, db);
+        if (kind == kItemQuarters && partial && col) {   // groups of a cut block stand alone
+            float *dst = p.ws.partial + (int64_t(block) * kGroups + slot0 / kGroupRows) * 2 * p.hidden + l * 8;
+            st_global_f2x4(dst, dw);
+            st_global_f2x4(dst + p.hidden, db);
+        }
+        if (partial && l == 0) {
+            const int64_t rows = p.ws.n_rows - int64_t(block) * kBlockRows;
+            uint8_t *state = p.ws.state + int64_t(block) * kGroups + slot0 / kGroupRows;
+            if (slot0 < rows) {
+                if (*state != 0) set_status(p.ws.hdr, kStDouble);
+                const int groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
+                if (kind == kItemQuarters) *state = 1;
+                else if (slot0 == 0) *state = uint8_t(groups);
+            }
+        }
+        __syncthreads();
+        if (kind == kItemWhole && partial) {
+            // lane (team of the block, l): two of the 16 P sums of the block
+            const int64_t rows = p.ws.n_rows - int64_t(block) * kBlockRows;
+            const int groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
+            const int at = (slot0 / kGroupRows * P + l) * 2, half = at / (8 * P), c = at - half * 8 * P;
+            const f2_t *from = reinterpret_cast<const f2_t *>(sums + (team / kGroups) * kGroups * 16 * P + at);
+            f2_t v[kGroups];
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) v[j] = from[j * 8 * P];
+#pragma unroll
+            for (int j = 1; j < kGroups; ++j)
+                if (j < groups) v[0] = f2_add(v[0], v[j]);
+            if (c < p.hidden)
+                *reinterpret_cast<f2_t *>(p.ws.partial + int64_t(block) * kGroups * 2 * p.hidden + half * p.hidden + c) = v[0];
+        }
+    }
+}
+
+template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
+int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
+    const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
+    constexpr int kTeams = kNarrowThreads / P;
+    const int64_t grid = (groups + kTeams - 1) / kTeams;
+    if (grid == 0) return RMSNORM_OK;
+    constexpr int kB = sizeof(E) == 4 || (RES && GRADS) ? 4 : 8;
+    ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES, kB, 2><<<unsigned(grid), kNarrowThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
+    count_launch();
+    return RMSNORM_OK;
+}
+
+// Lanes per row: the next power of two of hidden / 8, at least 4.
+template <class E, int MODE, bool DROP, bool GRADS, bool RES>
+int ln_launch_narrow(const LnParams &p, cudaStream_t s) {
+    if (p.hidden <= 32) return ln_launch_narrow_t<E, 4, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 64) return ln_launch_narrow_t<E, 8, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 128) return ln_launch_narrow_t<E, 16, MODE, DROP, GRADS, RES>(p, s);
+    return ln_launch_narrow_t<E, 32, MODE, DROP, GRADS, RES>(p, s);
+}
+
+template <class E>
+int ln_run_narrow(const LnParams &p, bool bwd, bool grads, cudaStream_t s) {
+    const bool drop = p.drop.state != nullptr;
+    if (!bwd) {
+        if (!p.res) return ln_launch_narrow<E, kLnFwd, false, false, false>(p, s);
+        return drop ? ln_launch_narrow<E, kLnAdd, true, false, false>(p, s)
+                    : ln_launch_narrow<E, kLnAdd, false, false, false>(p, s);
+    }
+    if (p.res) {
+        if (grads) return drop ? ln_launch_narrow<E, kLnBwd, true, true, true>(p, s) : ln_launch_narrow<E, kLnBwd, false, true, true>(p, s);
+        return drop ? ln_launch_narrow<E, kLnBwd, true, false, true>(p, s) : ln_launch_narrow<E, kLnBwd, false, false, true>(p, s);
+    }
+    if (grads) return drop ? ln_launch_narrow<E, kLnBwd, true, true, false>(p, s) : ln_launch_narrow<E, kLnBwd, false, true, false>(p, s);
+    return drop ? ln_launch_narrow<E, kLnBwd, true, false, false>(p, s) : ln_launch_narrow<E, kLnBwd, false, false, false>(p, s);
+}
+
+}  // namespace rbi
