@@ -2,10 +2,37 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "layernorm_kernels.cuh"
 #include "layernorm_bi.h"
 
 namespace rbi {
+
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // an SM's shared memory; what the system takes per CTA
+
+// What a launcher needs of its kernel, asked for once per device: the registers
+// per thread; the kernel's shared-memory limit is raised on the way.
+struct KernelInfo {
+    std::mutex mu;
+    uint64_t ready = 0;
+    int regs = 0;
+    int get(const void *kern, int max_smem, int *out) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RMSNORM_ERR_CUDA;
+        std::lock_guard<std::mutex> lk(mu);
+        if (!((ready >> dev) & 1)) {
+            cudaFuncAttributes a;
+            if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) return RMSNORM_ERR_CUDA;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess)
+                return RMSNORM_ERR_CUDA;
+            regs = a.numRegs;
+            ready |= uint64_t(1) << dev;
+        }
+        *out = regs;
+        return RMSNORM_OK;
+    }
+};
 
 // Launches the rows of one call for element type E (ln_rows_*.cu instantiate it).
 // Rows of at most 256 columns take ln_run_narrow (ln_narrow_*.cu).

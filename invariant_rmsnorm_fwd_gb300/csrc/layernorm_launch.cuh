@@ -1,35 +1,17 @@
 // Launcher of the streaming layer-norm kernel, instantiated per element type.
 #pragma once
-#include <mutex>
-
 #include "host.cuh"
 #include "layernorm_host.cuh"
 #include "layernorm_stream.cuh"
 
 namespace rbi {
 
-constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // an SM's shared memory; what the system takes per CTA
-
 template <class E, int NV, int MODE, bool DROP, bool GRADS, int MAXT, int MINB>
 int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cudaStream_t stream) {
     auto kern = ln_stream_kernel<E, NV, MODE, DROP, GRADS, MAXT, MINB>;
-    // registers of this kernel, and its shared-memory limit raised once per device
-    static std::mutex mu;
-    static uint64_t ready = 0;
-    static int regs = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RMSNORM_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!((ready >> dev) & 1)) {
-            cudaFuncAttributes a;
-            if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) return RMSNORM_ERR_CUDA;
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem) != cudaSuccess)
-                return RMSNORM_ERR_CUDA;
-            regs = a.numRegs;
-            ready |= uint64_t(1) << dev;
-        }
-    }
+    static KernelInfo info;
+    int regs = 0;
+    if (int rc = info.get(reinterpret_cast<const void *>(kern), d.max_smem, &regs)) return rc;
     // Resident CTAs by registers and threads; then as many stages as their share
     // of the shared memory holds (fewer CTAs where that leaves less than `least`).
     // Backward, row i + 1 arrives while row i is in use and the stage of row

@@ -3,9 +3,11 @@
 // A row is held by a team of P lanes, 8 columns a lane, so a warp works on 32 / P
 // rows at once and a row's sums need only shuffles.  A team takes the 8 slots of
 // one group one after the other (in logical order where parameter gradients are
-// wanted), kB rows at a time: their loads are issued together, which keeps enough
-// bytes on their way with a few warps per SM.  Empty slots are computed as zeros
-// and store nothing, so the shuffles of a warp stay together.
+// wanted) and goes on to its next group; each lane keeps the next kDepth rows'
+// pieces on their way into shared-memory places of its own (cp.async), across
+// groups, and reads the slots of a group while it works on the one before, so
+// memory does not wait for a group's end.  Empty slots are computed as zeros and
+// store nothing, so the shuffles of a warp stay together.
 //
 // Parameter gradients: a lane's columns add up in its registers over the group;
 // the groups of a block are in one CTA, which folds them through shared memory
@@ -73,16 +75,112 @@ __device__ __forceinline__ float team_sum(float v) {
 }
 
 constexpr int kNarrowThreads = 256;
+constexpr int kDepth = 4;                                // rows of a team on their way
 
-// RES: dres is added (kLnBwd).  The slots of a group are read once, slot j by
-// lane j % P of the team, and handed round row by row.
-template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES, int KB, int MINB>
-__global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const __grid_constant__ LnParams p) {
+template <class E, int MODE, bool RES>
+constexpr int kNarrowPieces = (MODE == kLnFwd ? 1 : 2 + (RES ? 1 : 0)) * Oct<E>::kQ;   // 16-byte pieces of a lane's row
+
+// The slots of a team's group: slot j belongs to lane j % P.
+template <int P>
+struct TeamSlots {
+    static constexpr int kOwn = P >= kGroupRows ? 1 : kGroupRows / P;
+    int64_t off[kOwn];               // element offset of the row
+    uint32_t row[kOwn];              // logical row
+    uint32_t on;                     // the team's slots that hold a row
+    int32_t kind, block;             // of the plan item
+    int32_t slot0;
+    bool partial;                    // the group holds all its rows
+};
+
+// What is read of a group before its slots are worked out.
+template <int P>
+struct TeamRaw {
+    int32_t prow[TeamSlots<P>::kOwn], lrow[TeamSlots<P>::kOwn];   // without a plan: lrow is the token's id
+    int32_t kind, block, quarters;
+};
+
+template <int P, bool GRADS>
+__device__ __forceinline__ void team_read(const LnParams &p, int64_t group, TeamRaw<P> &raw) {
+    const int l = threadIdx.x % P;
+    if constexpr (GRADS) {
+        raw.kind = raw.block = -1;
+        raw.quarters = 0;
+        const bool have = group < p.n_items * kGroups;
+        const PlanItem *it = p.items + (have ? group / kGroups : 0);
+        if (have) {
+            raw.kind = it->kind;
+            raw.block = it->block;
+            raw.quarters = it->quarters;
+        }
+#pragma unroll
+        for (int o = 0; o < TeamSlots<P>::kOwn; ++o) {
+            const int j = l + o * P;
+            raw.prow[o] = raw.lrow[o] = -1;
+            if (have && j < kGroupRows) {
+                raw.prow[o] = it->prow[int(group % kGroups) * kGroupRows + j];
+                raw.lrow[o] = it->lrow[int(group % kGroups) * kGroupRows + j];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int o = 0; o < TeamSlots<P>::kOwn; ++o) {
+            const int j = l + o * P;
+            const int64_t prow = group * kGroupRows + j;
+            raw.prow[o] = raw.lrow[o] = -1;
+            if (j < kGroupRows && prow < p.n_rows) {
+                raw.prow[o] = int32_t(prow);
+                raw.lrow[o] = p.tok_id[p.rpt == 1 ? uint32_t(prow) : uint32_t(prow) / uint32_t(p.rpt)];
+            }
+        }
+    }
+}
+
+template <int P, bool GRADS>
+__device__ __forceinline__ void team_slots(const LnParams &p, int64_t group, const TeamRaw<P> &raw, TeamSlots<P> &s) {
+    const int l = threadIdx.x % P;
+    s.on = 0;
+    s.slot0 = int(group % kGroups) * kGroupRows;
+    if constexpr (GRADS) {
+        s.kind = raw.kind;
+        s.block = raw.block;
+        s.partial = raw.kind == kItemWhole || (raw.kind == kItemQuarters && ((raw.quarters >> (s.slot0 / 16)) & 1));
+    }
+#pragma unroll
+    for (int o = 0; o < TeamSlots<P>::kOwn; ++o) {
+        const int64_t prow = raw.prow[o], lr = raw.lrow[o];
+        bool valid = prow >= 0;
+        if constexpr (GRADS) {
+            if (valid) {
+                valid = prow < p.n_rows && lr >= 0 && lr < p.ws.n_rows &&
+                        (raw.kind == kItemSpill || ((raw.kind == kItemWhole || raw.kind == kItemQuarters) &&
+                                                    lr == int64_t(raw.block) * kBlockRows + s.slot0 + l + o * P));
+                if (!valid) set_status(p.ws.hdr, kStPlan);
+            }
+        } else {
+            valid = valid && lr >= 0;
+        }
+        s.off[o] = 0;
+        s.row[o] = 0;
+        if (valid) {
+            const uint32_t t = p.rpt == 1 ? uint32_t(prow) : uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - t * uint32_t(p.rpt);
+            s.off[o] = int64_t(t) * p.token_stride + int64_t(head) * p.hidden;
+            s.row[o] = GRADS ? uint32_t(lr) : uint32_t(lr) * uint32_t(p.rpt) + head;
+        }
+        const uint32_t all = __ballot_sync(kFull, valid) >> ((threadIdx.x & 31) - l);
+        s.on |= (all & ((1u << (P < kGroupRows ? P : kGroupRows)) - 1u)) << (o * P);
+    }
+}
+
+// RES: dres is added (kLnBwd).
+template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
+__global__ void __launch_bounds__(kNarrowThreads, 2) ln_narrow_kernel(const __grid_constant__ LnParams p) {
     constexpr bool kFwd = MODE != kLnBwd, kRes = MODE == kLnAdd || RES;
-    constexpr int kB = KB;                               // rows side by side
-    constexpr int kOwn = P >= kGroupRows ? 1 : kGroupRows / P;   // slots of a lane
-    __shared__ float sums[GRADS ? kNarrowThreads * 16 : 1];   // [team][dweight, dbias][8 P]
+    constexpr int kPieces = kNarrowPieces<E, MODE, RES>, kQ = Oct<E>::kQ, kTeams = kNarrowThreads / P;
+    constexpr int kOwn = TeamSlots<P>::kOwn;
+    extern __shared__ __align__(128) uint8_t smem[];     // [kDepth][kPieces][256 threads], then the block sums
+    float *sums = reinterpret_cast<float *>(smem + kDepth * kPieces * kNarrowThreads * 16);   // [team][dweight, dbias][8 P]
     const int tid = threadIdx.x, team = tid / P, l = tid % P, V = p.hidden >> 3;
+    const uint32_t mine = smem_addr(smem) + uint32_t(tid) * 16u;
     const bool col = l < V;                              // this lane has columns
     if constexpr (GRADS) {
         if (!ln_header_ok(p.ws)) {
@@ -91,59 +189,8 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
         }
     }
     const DropKey key = DROP ? drop_key(p.drop) : DropKey{0, 0, 0, 0};
-    const int64_t group = int64_t(blockIdx.x) * (kNarrowThreads / P) + team;     // 8 slots of the call or plan
-    int kind = 0, block = -1, slot0 = 0;
-    bool partial = false;
-    int64_t own_off[kOwn];
-    uint32_t own_row[kOwn], on = 0;                      // on: the team's slots that hold a row
-    if constexpr (GRADS) {
-        slot0 = int(group % kGroups) * kGroupRows;
-        if (group < p.n_items * kGroups) {
-            const PlanItem &it = p.items[group / kGroups];
-            kind = it.kind;
-            block = it.block;
-            // the item's groups that hold all their rows
-            partial = kind == kItemWhole || (kind == kItemQuarters && ((it.quarters >> (slot0 / 16)) & 1));
-        }
-    }
-#pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-        const int j = l + o * P;
-        int64_t prow = -1;
-        bool valid = false;
-        own_off[o] = 0;
-        own_row[o] = 0;
-        if (j < kGroupRows) {
-            if constexpr (GRADS) {
-                if (group < p.n_items * kGroups) {
-                    const PlanItem &it = p.items[group / kGroups];
-                    prow = it.prow[slot0 + j];
-                    const int32_t lr = it.lrow[slot0 + j];
-                    if (prow >= 0) {
-                        valid = prow < p.n_rows && lr >= 0 && lr < p.ws.n_rows &&
-                                (kind == kItemSpill ||
-                                 ((kind == kItemWhole || kind == kItemQuarters) && lr == int64_t(block) * kBlockRows + slot0 + j));
-                        if (!valid) set_status(p.ws.hdr, kStPlan);
-                        own_row[o] = uint32_t(lr);
-                    }
-                }
-            } else {
-                prow = group * kGroupRows + j;
-                if (prow < p.n_rows) {
-                    const uint32_t t = uint32_t(prow) / uint32_t(p.rpt);
-                    const int32_t id = p.tok_id[t];
-                    valid = id >= 0;
-                    own_row[o] = uint32_t(id) * uint32_t(p.rpt) + uint32_t(prow) - t * uint32_t(p.rpt);
-                }
-            }
-            if (valid) {
-                const uint32_t t = uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - t * uint32_t(p.rpt);
-                own_off[o] = int64_t(t) * p.token_stride + int64_t(head) * p.hidden;
-            }
-        }
-        const uint32_t all = __ballot_sync(kFull, valid) >> ((tid & 31) - l);
-        on |= (all & ((1u << (P < kGroupRows ? P : kGroupRows)) - 1u)) << (o * P);
-    }
+    const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
+    const int64_t stride = int64_t(gridDim.x) * kTeams;
     f2_t w[4], b[4], dw[4], db[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = b[j] = dw[j] = db[j] = 0;
@@ -151,35 +198,58 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
         oct_param<E>(p.w, p.params_f32, l, 1.f, w);
         if constexpr (kFwd) oct_param<E>(p.b, p.params_f32, l, 0.f, b);
     }
-    float own_mean[kFwd ? kOwn : 1], own_rstd[kFwd ? kOwn : 1];
+    TeamSlots<P> cur, nxt;
+    int64_t off[kDepth];                                 // element offset of this lane's piece of the rows on their way
+    // Requests row j of the group into place j % kDepth.
+    auto request = [&](const TeamSlots<P> &s, int j) {
+        const int64_t at = __shfl_sync(kFull, s.off[j / P], j % P, P) + l * 8;
+        off[j % kDepth] = at;
+        const uint32_t bytes = ((s.on >> j) & 1) && col ? 16u : 0u;
+        const uint32_t to = mine + uint32_t(j % kDepth) * uint32_t(kPieces * kNarrowThreads * 16);
+        const int64_t from = bytes ? at : 0;
 #pragma unroll
-    for (int s = 0; s < kGroupRows; s += kB) {
-        int64_t off[kB];
-        Oct<E> xo[kB], ro[kRes ? kB : 1], go[kFwd ? 1 : kB];
-#pragma unroll
-        for (int r = 0; r < kB; ++r) {
-            const int j = s + r;
-            off[r] = __shfl_sync(kFull, own_off[j / P], j % P, P) + l * 8;
-            const bool ld = ((on >> j) & 1) && col;
-#pragma unroll
-            for (int q = 0; q < Oct<E>::kQ; ++q) {
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                xo[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.x) + off[r])[q] : z;
-                if constexpr (!kFwd) go[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.dy) + off[r])[q] : z;
-                if constexpr (kRes) ro[r].q[q] = ld ? reinterpret_cast<const uint4 *>(static_cast<const E *>(p.res) + off[r])[q] : z;
-            }
+        for (int q = 0; q < kQ; ++q) {
+            cp_async_zfill(to + q * (kNarrowThreads * 16), static_cast<const E *>(p.x) + from + q * 4, bytes);
+            if constexpr (!kFwd) cp_async_zfill(to + (kQ + q) * (kNarrowThreads * 16), static_cast<const E *>(p.dy) + from + q * 4, bytes);
+            if constexpr (kRes)
+                cp_async_zfill(to + ((kFwd ? 1 : 2) * kQ + q) * (kNarrowThreads * 16), static_cast<const E *>(p.res) + from + q * 4, bytes);
         }
+        cp_async_commit();
+    };
+    int64_t unit = int64_t(blockIdx.x) * kTeams;         // first group of this CTA's teams
+    {
+        TeamRaw<P> raw;
+        team_read<P, GRADS>(p, unit + team, raw);
+        team_slots<P, GRADS>(p, unit + team, raw, cur);
+    }
 #pragma unroll
-        for (int r = 0; r < kB; ++r) {
-            const int j0 = s + r;
-            const bool row = (on >> j0) & 1, st = row && col;
+    for (int j = 0; j < kDepth; ++j) request(cur, j);
+#pragma unroll 1
+    for (; unit < groups; unit += stride) {
+        const int64_t group = unit + team;
+        TeamRaw<P> raw;
+        team_read<P, GRADS>(p, group + stride, raw);
+        float own_mean[kFwd ? kOwn : 1], own_rstd[kFwd ? kOwn : 1];
+#pragma unroll
+        for (int j0 = 0; j0 < kGroupRows; ++j0) {
+            cp_async_wait<kDepth - 1>();                 // row j0 has arrived (in this lane's own places)
+            const uint32_t at = mine + uint32_t(j0 % kDepth) * uint32_t(kPieces * kNarrowThreads * 16);
+            Oct<E> xo, go, ro;
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                ld_shared_vec(at + q * (kNarrowThreads * 16), xo.q[q]);
+                if constexpr (!kFwd) ld_shared_vec(at + (kQ + q) * (kNarrowThreads * 16), go.q[q]);
+                if constexpr (kRes) ld_shared_vec(at + ((kFwd ? 1 : 2) * kQ + q) * (kNarrowThreads * 16), ro.q[q]);
+            }
+            const int64_t here = off[j0 % kDepth];
+            const bool row = (cur.on >> j0) & 1, st = row && col;
             uint32_t lrow = 0;
-            if constexpr (DROP || GRADS) lrow = __shfl_sync(kFull, own_row[j0 / P], j0 % P, P);
+            if constexpr (DROP || GRADS) lrow = __shfl_sync(kFull, cur.row[j0 / P], j0 % P, P);
             f2_t x[4], g[4];
-            oct_up<E>(xo[r], x);
+            oct_up<E>(xo, x);
             if constexpr (MODE == kLnAdd) {
                 f2_t q[4];
-                oct_up<E>(ro[r], q);
+                oct_up<E>(ro, q);
                 if constexpr (DROP) {
                     const uint32_t keep = keep_bits(uint32_t(l), lrow, key, p.drop.t);
 #pragma unroll
@@ -192,7 +262,7 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = f2_add(x[j], q[j]);
                 }
-                if (st) oct_store<E>(p.out2, off[r], x);
+                if (st) oct_store<E>(p.out2, here, x);
                 if constexpr (sizeof(E) == 2) {          // the norm takes the stored h
                     const uint4 h = down<E>(x);
                     up<E>(h, x);
@@ -217,10 +287,10 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 const f2_t r2 = f2_both(rstd);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = f2_fma(f2_mul(x[j], r2), w[j], b[j]);
-                if (st) oct_store<E>(p.out, off[r], x);
+                if (st) oct_store<E>(p.out, here, x);
             } else {
                 // the three sums of the row side by side (independent shuffles)
-                oct_up<E>(go[r], g);
+                oct_up<E>(go, g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f2_t a = f2_mul(g[j], w[j]);
@@ -247,7 +317,7 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                     }
                 }
                 if constexpr (GRADS) {
-                    if (row && !partial) {               // a row of a cut group
+                    if (row && !cur.partial) {           // a row of a cut group
                         if (col) {
                             float *sp = p.ws.spill + int64_t(lrow) * 2 * p.hidden + l * 8;
                             st_global_f2x4(sp, x);
@@ -261,77 +331,96 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 }
                 if constexpr (RES) {
                     f2_t q[4];
-                    oct_up<E>(ro[r], q);
+                    oct_up<E>(ro, q);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], q[j]);
                 }
                 if (st && (!GRADS || p.out)) {
-                    oct_store<E>(p.out, off[r], o);
+                    oct_store<E>(p.out, here, o);
                     if constexpr (DROP) {
                         drop_pairs(o, keep_bits(uint32_t(l), lrow, key, p.drop.t), p.drop.scale);
-                        oct_store<E>(p.out2, off[r], o);
+                        oct_store<E>(p.out2, here, o);
                     }
                 }
             }
-        }
-    }
-    if constexpr (kFwd) {
-#pragma unroll
-        for (int o = 0; o < kOwn; ++o) {
-            const int j = l + o * P;
-            if (j < kGroupRows && ((on >> j) & 1)) {
-                const int64_t prow = group * kGroupRows + j;
-                if (p.mean) p.mean[prow] = own_mean[o];
-                if (p.rstd) p.rstd[prow] = own_rstd[o];
+            // the row's place is free again: the next row but kDepth - 1 goes there
+            if (j0 + kDepth < kGroupRows) {
+                request(cur, j0 + kDepth);
+            } else {
+                if (j0 + kDepth == kGroupRows) team_slots<P, GRADS>(p, group + stride, raw, nxt);
+                request(nxt, j0 + kDepth - kGroupRows);
             }
         }
-    }
-    if constexpr (GRADS) {
-        float *mine = sums + team * 16 * P + l * 8;
-        pairs_store(mine, dw);
-        pairs_store(mine + 8 * P, db);
-        if (kind == kItemQuarters && partial && col) {   // groups of a cut block stand alone
-            float *dst = p.ws.partial + (int64_t(block) * kGroups + slot0 / kGroupRows) * 2 * p.hidden + l * 8;
-            st_global_f2x4(dst, dw);
-            st_global_f2x4(dst + p.hidden, db);
+        if constexpr (kFwd) {
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) {
+                const int j = l + o * P;
+                if (j < kGroupRows && ((cur.on >> j) & 1)) {
+                    const int64_t prow = group * kGroupRows + j;
+                    if (p.mean) p.mean[prow] = own_mean[o];
+                    if (p.rstd) p.rstd[prow] = own_rstd[o];
+                }
+            }
         }
-        if (partial && l == 0) {
-            const int64_t rows = p.ws.n_rows - int64_t(block) * kBlockRows;
-            uint8_t *state = p.ws.state + int64_t(block) * kGroups + slot0 / kGroupRows;
-            if (slot0 < rows) {
+        if constexpr (GRADS) {
+            float *to = sums + team * 16 * P + l * 8;
+            pairs_store(to, dw);
+            pairs_store(to + 8 * P, db);
+            if (cur.kind == kItemQuarters && cur.partial && col) {   // groups of a cut block stand alone
+                float *dst = p.ws.partial + (int64_t(cur.block) * kGroups + cur.slot0 / kGroupRows) * 2 * p.hidden + l * 8;
+                st_global_f2x4(dst, dw);
+                st_global_f2x4(dst + p.hidden, db);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dw[j] = db[j] = 0;
+            const int64_t rows = p.ws.n_rows - int64_t(cur.block) * kBlockRows;
+            const int n_groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
+            if (cur.partial && l == 0 && cur.slot0 < rows && cur.block >= 0 && cur.block < p.ws.n_blocks) {
+                uint8_t *state = p.ws.state + int64_t(cur.block) * kGroups + cur.slot0 / kGroupRows;
                 if (*state != 0) set_status(p.ws.hdr, kStDouble);
-                const int groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
-                if (kind == kItemQuarters) *state = 1;
-                else if (slot0 == 0) *state = uint8_t(groups);
+                if (cur.kind == kItemQuarters) *state = 1;
+                else if (cur.slot0 == 0) *state = uint8_t(n_groups);
             }
-        }
-        __syncthreads();
-        if (kind == kItemWhole && partial) {
-            // lane (team of the block, l): two of the 16 P sums of the block
-            const int64_t rows = p.ws.n_rows - int64_t(block) * kBlockRows;
-            const int groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
-            const int at = (slot0 / kGroupRows * P + l) * 2, half = at / (8 * P), c = at - half * 8 * P;
-            const f2_t *from = reinterpret_cast<const f2_t *>(sums + (team / kGroups) * kGroups * 16 * P + at);
-            f2_t v[kGroups];
+            __syncthreads();
+            if (cur.kind == kItemWhole && cur.block >= 0 && cur.block < p.ws.n_blocks) {
+                // lane (team of the block, l): two of the 16 P sums of the block
+                const int at = (cur.slot0 / kGroupRows * P + l) * 2, half = at / (8 * P), c = at - half * 8 * P;
+                const f2_t *from = reinterpret_cast<const f2_t *>(sums + (team / kGroups) * kGroups * 16 * P + at);
+                f2_t v[kGroups];
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) v[j] = from[j * 8 * P];
+                for (int j = 0; j < kGroups; ++j) v[j] = from[j * 8 * P];
 #pragma unroll
-            for (int j = 1; j < kGroups; ++j)
-                if (j < groups) v[0] = f2_add(v[0], v[j]);
-            if (c < p.hidden)
-                *reinterpret_cast<f2_t *>(p.ws.partial + int64_t(block) * kGroups * 2 * p.hidden + half * p.hidden + c) = v[0];
+                for (int j = 1; j < kGroups; ++j)
+                    if (j < n_groups) v[0] = f2_add(v[0], v[j]);
+                if (c < p.hidden)
+                    *reinterpret_cast<f2_t *>(p.ws.partial + int64_t(cur.block) * kGroups * 2 * p.hidden + half * p.hidden + c) = v[0];
+            }
+            __syncthreads();                             // the sums are read
         }
+        cur = nxt;
     }
+    cp_async_wait<0>();
 }
 
 template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
 int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
+    auto kern = ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES>;
+    constexpr int smem = kDepth * kNarrowPieces<E, MODE, RES> * kNarrowThreads * 16 + (GRADS ? kNarrowThreads * 64 : 0);
+    DeviceInfo *d = nullptr;
+    if (int rc = device_info(&d)) return rc;
     const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
     constexpr int kTeams = kNarrowThreads / P;
-    const int64_t grid = (groups + kTeams - 1) / kTeams;
+    static KernelInfo info;
+    int regs = 0;
+    if (int rc = info.get(reinterpret_cast<const void *>(kern), smem, &regs)) return rc;
+    int ctas = 65536 / ((regs + 7) / 8 * 8 * kNarrowThreads);
+    if (ctas > 8) ctas = 8;
+    if (ctas > kSmemPerSm / (smem + kSmemPerCta)) ctas = kSmemPerSm / (smem + kSmemPerCta);
+    if (ctas < 1) return RMSNORM_ERR_HIDDEN;
+    int64_t grid = (groups + kTeams - 1) / kTeams;
     if (grid == 0) return RMSNORM_OK;
-    constexpr int kB = sizeof(E) == 4 || (RES && GRADS) ? 4 : 8;
-    ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES, kB, 2><<<unsigned(grid), kNarrowThreads, 0, stream>>>(p);
+    if (grid > int64_t(ctas) * d->sms) grid = int64_t(ctas) * d->sms;
+    kern<<<unsigned(grid), kNarrowThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
