@@ -172,8 +172,8 @@ __device__ __forceinline__ void team_slots(const LnParams &p, int64_t group, con
 }
 
 // RES: dres is added (kLnBwd).
-template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
-__global__ void __launch_bounds__(kNarrowThreads, 2) ln_narrow_kernel(const __grid_constant__ LnParams p) {
+template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES, int MINB>
+__global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const __grid_constant__ LnParams p) {
     constexpr bool kFwd = MODE != kLnBwd, kRes = MODE == kLnAdd || RES;
     constexpr int kPieces = kNarrowPieces<E, MODE, RES>, kQ = Oct<E>::kQ, kTeams = kNarrowThreads / P;
     constexpr int kOwn = TeamSlots<P>::kOwn;
@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) ln_narrow_kernel(const __gr
 
 template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
 int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
-    auto kern = ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES>;
+    constexpr int kMinB = 3;
+    auto kern = ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES, kMinB>;
     constexpr int smem = kDepth * kNarrowPieces<E, MODE, RES> * kNarrowThreads * 16 + (GRADS ? kNarrowThreads * 64 : 0);
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
