@@ -19,78 +19,98 @@ __global__ void ln_begin_kernel(LnWs ws) {
     }
 }
 
-constexpr int kLnTreeCols = 32;                          // columns of [dweight | dbias] per CTA: 8 lanes of 4
+constexpr int kLnTreeCols = 64;                          // columns of [dweight | dbias] per CTA: 8 lanes, twice 4 each
 constexpr int kLnTreeBlocks = 32;                        // inputs per CTA
 
+struct Cols {                        // a lane's columns: c .. c + 3 and c + 32 .. c + 35
+    float4 a, b;
+};
 __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
+__device__ __forceinline__ float4 fma4(const float4 &a, const float4 &b, const float4 &c) {
+    return make_float4(__fmaf_rn(a.x, b.x, c.x), __fmaf_rn(a.y, b.y, c.y), __fmaf_rn(a.z, b.z, c.z), __fmaf_rn(a.w, b.w, c.w));
+}
+__device__ __forceinline__ Cols add_cols(const Cols &x, const Cols &y) { return {add4(x.a, y.a), add4(x.b, y.b)}; }
+__device__ __forceinline__ float4 down4(const float4 &v, int o) {
+    return make_float4(__shfl_down_sync(kFull, v.x, o), __shfl_down_sync(kFull, v.y, o), __shfl_down_sync(kFull, v.z, o),
+                       __shfl_down_sync(kFull, v.w, o));
+}
+// two: the second four columns are inside [dweight | dbias]
+__device__ __forceinline__ Cols load_cols(const float *p, bool two) {
+    Cols v;
+    v.a = *reinterpret_cast<const float4 *>(p);
+    v.b = two ? *reinterpret_cast<const float4 *>(p + 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return v;
+}
 
-// Four columns of block b from column col of [dweight | dbias]: the groups from
-// the first to the last, each from a stored partial or folded from its spilled
-// rows.  All stored partials are requested before any is used.  check: report
-// rows that are missing or arrived twice (one CTA per block does).
-__device__ __forceinline__ float4 ln_block_value(const LnWs &ws, int64_t b, int64_t col, uint64_t state, bool check,
-                                                 int &bad) {
+// A group's sums for four columns from its spilled rows.
+__device__ __forceinline__ float4 spilled4(const LnWs &ws, int64_t row0, int rows, int64_t col, int &bad) {
+    const int64_t H2 = 2 * ws.hidden;
+    const bool is_w = col < ws.hidden;
+    const int64_t c = is_w ? col : col - ws.hidden;
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < rows; ++r) {
+        const int64_t row = row0 + r;
+        if (!ws.flag[row]) {
+            bad |= kStMissing;
+            continue;
+        }
+        const float4 dy = *reinterpret_cast<const float4 *>(ws.spill + row * H2 + ws.hidden + c);
+        if (is_w) g = fma4(dy, *reinterpret_cast<const float4 *>(ws.spill + row * H2 + c), g);
+        else g = add4(g, dy);
+    }
+    return g;
+}
+
+// Eight columns of block b: the groups from the first to the last, each from a
+// stored partial or folded from its spilled rows.  All stored partials are
+// requested before any is used.  check: report rows that are missing or arrived
+// twice (one CTA per block does).
+__device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_t col, bool two, uint64_t state, bool check,
+                                               int &bad) {
     const int64_t H2 = 2 * ws.hidden;
     const float *part = ws.partial + b * kGroups * H2 + col;
     const int64_t left = ws.n_rows - b * kBlockRows;
     const int rows = left < kBlockRows ? int(left) : kBlockRows, groups = (rows + kGroupRows - 1) / kGroupRows;
-    float4 v[kGroups];
+    Cols v[kGroups];
 #pragma unroll
     for (int j = 0; j < kGroups; ++j)
-        if ((state >> (8 * j)) & 0xff) v[j] = *reinterpret_cast<const float4 *>(part + j * H2);
+        if ((state >> (8 * j)) & 0xff) v[j] = load_cols(part + j * H2, two);
     const uint64_t *flags = reinterpret_cast<const uint64_t *>(ws.flag) + b * kGroups;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    Cols acc = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     int next = 0;                                        // first group not yet taken
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
         const int c = int((state >> (8 * j)) & 0xff);
+        if (check && c && flags[j]) bad |= kStDouble;    // a group that arrived as a partial has no spilled rows
         if (j < next) {                                  // inside the fold of the block's first groups
             if (check && (c || flags[j])) bad |= kStDouble;
             continue;
         }
         if (j >= groups) continue;
-        float4 g;
         if (c) {
-            g = v[j];
             next = j + c;
-            if (check && flags[j]) bad |= kStDouble;
         } else {
             next = j + 1;
-            g = make_float4(0.f, 0.f, 0.f, 0.f);
-            const bool is_w = col < ws.hidden;
-            const int64_t c0 = is_w ? col : col - ws.hidden;
-            for (int r = j * kGroupRows; r < (j + 1) * kGroupRows && r < rows; ++r) {
-                const int64_t row = b * kBlockRows + r;
-                if (!ws.flag[row]) {
-                    bad |= kStMissing;
-                    continue;
-                }
-                const float4 dy = *reinterpret_cast<const float4 *>(ws.spill + row * H2 + ws.hidden + c0);
-                if (is_w) {
-                    const float4 xh = *reinterpret_cast<const float4 *>(ws.spill + row * H2 + c0);
-                    g = make_float4(__fmaf_rn(dy.x, xh.x, g.x), __fmaf_rn(dy.y, xh.y, g.y), __fmaf_rn(dy.z, xh.z, g.z),
-                                    __fmaf_rn(dy.w, xh.w, g.w));
-                } else {
-                    g = add4(g, dy);
-                }
-            }
+            const int n = rows - j * kGroupRows < kGroupRows ? rows - j * kGroupRows : kGroupRows;
+            v[j].a = spilled4(ws, b * kBlockRows + j * kGroupRows, n, col, bad);
+            v[j].b = two ? spilled4(ws, b * kBlockRows + j * kGroupRows, n, col + 32, bad) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        acc = j == 0 ? g : add4(acc, g);
+        acc = j == 0 ? v[j] : add_cols(acc, v[j]);
     }
     return acc;
 }
 
 // One pass of the pairwise tree with odd carry over n_in inputs (block values in
 // the first pass, then the results of the one before): CTA (g, c) reduces inputs
-// [32 g, 32 g + 32) of 32 columns to one node.  Eight lanes hold the columns of
+// [32 g, 32 g + 32) of 64 columns to one node.  Eight lanes hold the columns of
 // an input, a warp four inputs, which meet by shuffles; the eight warps through
 // shared memory.  All loads of a pass are in flight at once; what bounds the
-// first pass is reading the partials (mostly from L2), the others are latency.
+// first pass is reading the partials, the others are latency.
 __global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, float *out_w, float *out_b,
                                                       int64_t out_stride, int64_t n_in, float scale) {
-    __shared__ float4 val[8][8];
+    __shared__ float4 val[8][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7, i = tid >> 3;
     const int64_t H2 = 2 * ws.hidden, col = int64_t(blockIdx.y) * kLnTreeCols + part * 4;
     const int64_t first = int64_t(blockIdx.x) * kLnTreeBlocks;
@@ -99,37 +119,37 @@ __global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, 
         return;
     }
     const int m = n_in - first < kLnTreeBlocks ? int(n_in - first) : kLnTreeBlocks;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    Cols v = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     int bad = 0;
     if (i < m && col < H2) {
-        if (in) v = *reinterpret_cast<const float4 *>(in + (first + i) * H2 + col);
-        else v = ln_block_value(ws, first + i, col, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
+        const bool two = col + 32 < H2;
+        if (in) v = load_cols(in + (first + i) * H2 + col, two);
+        else v = ln_block_value(ws, first + i, col, two, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
                                 blockIdx.y == 0, bad);
     }
     if (bad) set_status(ws.hdr, bad);
 #pragma unroll
     for (int o = 8; o <= 16; o <<= 1) {                  // inputs 1, then 2 apart
-        float4 u;
-        u.x = __shfl_down_sync(kFull, v.x, o);
-        u.y = __shfl_down_sync(kFull, v.y, o);
-        u.z = __shfl_down_sync(kFull, v.z, o);
-        u.w = __shfl_down_sync(kFull, v.w, o);
-        if (i + (o >> 3) < m) v = add4(v, u);
+        const Cols u = {down4(v.a, o), down4(v.b, o)};
+        if (i + (o >> 3) < m) v = add_cols(v, u);
     }
-    if (lane < 8) val[warp][part] = v;
+    if (lane < 8) {
+        val[warp][part] = v.a;
+        val[warp][8 + part] = v.b;
+    }
     __syncthreads();
-    if (warp == 0) {                                     // one column per lane: the warps' quadruples
+    if (warp < 2) {                                      // one column per lane: the warps' quadruples
         float x[8];
         const float *f = reinterpret_cast<const float *>(val);
         const int n = (m + 3) / 4;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = f[k * kLnTreeCols + lane];
+        for (int k = 0; k < 8; ++k) x[k] = f[k * kLnTreeCols + warp * 32 + lane];
 #pragma unroll
         for (int s = 1; s < 8; s <<= 1)
 #pragma unroll
             for (int k = 0; k + s < 8; k += 2 * s)
                 if (k + s < n) x[k] = __fadd_rn(x[k], x[k + s]);
-        const int64_t c = int64_t(blockIdx.y) * kLnTreeCols + lane;
+        const int64_t c = int64_t(blockIdx.y) * kLnTreeCols + warp * 32 + lane;
         const float r = scale != 1.f ? __fmul_rn(x[0], scale) : x[0];   // scaled only at the root
         if (c < H2) {
             float *dst = c < ws.hidden ? out_w : out_b;
