@@ -9,7 +9,6 @@ type per call), weight and bias have that type or float32.
 from __future__ import annotations
 
 import ctypes
-import math
 from dataclasses import dataclass
 
 import torch
@@ -42,6 +41,24 @@ def signatures(layout_ptr) -> dict:
     }
 
 
+def _index(t) -> int:
+    """Device index of a CUDA tensor, -1 for a host tensor."""
+    return t.get_device()
+
+
+def _is_cuda(t) -> bool:
+    return t.is_cuda
+
+
+def _current() -> int:
+    return torch.cuda.current_device()
+
+
+# The raw handle of the current stream, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 @dataclass
 class Dropout:
     """Dropout with probability p whose mask is a function of the state and the
@@ -52,12 +69,12 @@ class Dropout:
     p: float
     state: object
 
-    def struct(self, device) -> _Dropout:
+    def struct(self, index: int) -> _Dropout:
         s = self.state
         if not isinstance(s, torch.Tensor) or s.dtype != torch.int64:
             raise TypeError("dropout.state: expected an int64 tensor (seed, offset)")
-        if not _is_cuda(s) or s.device != device:
-            raise ValueError(f"dropout.state: must be a CUDA tensor on {device} (got {s.device})")
+        if not _is_cuda(s) or _index(s) != index:
+            raise ValueError(f"dropout.state: must be a CUDA tensor on the call's device (got {s.device})")
         if s.numel() != 2 or not s.is_contiguous():
             raise ValueError("dropout.state: expected a contiguous tensor of two int64 (seed, offset)")
         if not 0.0 <= self.p <= 1.0:
@@ -65,134 +82,148 @@ class Dropout:
         return _Dropout(s.data_ptr(), self.p)
 
 
-def _is_cuda(t) -> bool:
-    return t.is_cuda
+class _Call:
+    """The checks of one call's tensors.  The first one (x, h or dy) fixes the
+    element type, the device, the shape and the token stride; the others are
+    compared with it."""
+    __slots__ = ("lay", "H", "index", "dtype", "shape", "strides", "code", "stream")
 
+    def __init__(self, x, name: str, lay, stream):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
+        if not _is_cuda(x):
+            raise ValueError(f"{name}: must be a CUDA tensor (got {x.device})")
+        self.lay, self.dtype, self.shape, self.strides, self.index = lay, x.dtype, x.shape, x.stride(), _index(x)
+        self.code = _DTYPE.get(x.dtype)
+        if self.code is None:
+            raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {x.dtype}")
+        R, nd = lay.rows_per_token, len(self.shape)
+        self.H = self.shape[2] if nd == 3 else self.shape[1] // R if nd == 2 else 0
+        self._layout_of(name, self.shape, self.strides)
+        if self.index != _current():
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{_current()}")
+        if stream is None:
+            self.stream = _raw_stream(self.index)
+        else:
+            if stream.device_index != self.index:
+                raise ValueError(f"stream: on {stream.device}, the call's rows are on {x.device}")
+            self.stream = stream.cuda_stream
 
-def _rows(t, name: str, lay, H: int, like=None):
-    """Checks a [T, rows_per_token, H] or [T, rows_per_token * H] tensor of the
-    call (T >= n_tokens); `like` is the call's first tensor, whose type, device
-    and token stride the others share."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not _is_cuda(t):
-        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
-    if like is None:
-        if t.dtype not in _DTYPE:
-            raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
-        if lay.n_tokens and lay.tok_id.device != t.device:
-            raise ValueError(f"{name}: on {t.device}, the call's layout is on {lay.tok_id.device}")
-    elif t.dtype != like.dtype:
-        raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
-    elif t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, the call's rows are on {like.device}")
-    R, shape, st = lay.rows_per_token, t.shape, t.stride()
-    if len(shape) == 3:
-        ok = shape[1] == R and shape[2] == H and st[2] == 1 and (st[1] == H or R == 1)
-    else:
-        ok = len(shape) == 2 and shape[1] == R * H and st[1] == 1
-    if not ok:
-        raise ValueError(f"{name}: expected [n_tokens, {R}, {H}] or [n_tokens, {R * H}] with unit column stride, "
-                         f"got shape {tuple(shape)} strides {tuple(st)}")
-    if shape[0] < lay.n_tokens:
-        raise ValueError(f"{name}: {shape[0]} token slots, the call's layout has {lay.n_tokens}")
-    if like is not None and st[0] != like.stride(0) and lay.n_tokens > 1:
-        raise ValueError(f"{name}: token stride {st[0]} differs from {like.stride(0)} (one stride per call)")
+    def _layout_of(self, name, shape, st):
+        R, H = self.lay.rows_per_token, self.H
+        if len(shape) == 3:
+            ok = shape[1] == R and shape[2] == H and st[2] == 1 and (st[1] == H or R == 1)
+        else:
+            ok = len(shape) == 2 and shape[1] == R * H and st[1] == 1
+        if not ok:
+            raise ValueError(f"{name}: expected [n_tokens, {R}, hidden] or [n_tokens, {R} * hidden] with unit column "
+                             f"stride (hidden {H}), got shape {tuple(shape)} strides {tuple(st)}")
+        if shape[0] < self.lay.n_tokens:
+            raise ValueError(f"{name}: {shape[0]} token slots, the call's layout has {self.lay.n_tokens}")
 
-
-def _hidden(x, lay) -> int:
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"x: expected a torch.Tensor, got {type(x).__name__}")
-    if x.dim() == 3:
-        return x.shape[2]
-    if x.dim() == 2 and x.shape[1] % lay.rows_per_token == 0:
-        return x.shape[1] // lay.rows_per_token
-    raise ValueError(f"x: expected [n_tokens, {lay.rows_per_token}, hidden] or [n_tokens, "
-                     f"{lay.rows_per_token} * hidden], got shape {tuple(x.shape)}")
-
-
-def _new(like, lay, H: int):
-    """A new output with the call's token stride (rows past n_tokens and padding are left as they come)."""
-    if like.shape[0] <= 1 or like.is_contiguous():
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    return torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
-
-
-def _params(x, H: int, weight, bias=None) -> int:
-    code = None
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
+    def rows(self, t, name: str) -> int:
+        """Address of another tensor of rows."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-        if t.device != x.device:
-            raise ValueError(f"{name}: on {t.device}, the call's rows are on {x.device}")
-        if t.dtype != x.dtype and t.dtype != torch.float32:
-            raise TypeError(f"{name}: expected {x.dtype} or torch.float32, got {t.dtype}")
-        if t.shape != (H,) or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous [{H}] tensor, got shape {tuple(t.shape)}")
-        if code is not None and code != _DTYPE[t.dtype]:
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
+        if not _is_cuda(t) or _index(t) != self.index:
+            raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {t.device})")
+        shape, st = t.shape, t.stride()
+        if shape != self.shape or st != self.strides:
+            self._layout_of(name, shape, st)
+            if st[0] != self.strides[0] and self.lay.n_tokens > 1:
+                raise ValueError(f"{name}: token stride {st[0]} differs from {self.strides[0]} (one stride per call)")
+        return t.data_ptr()
+
+    def params(self, weight, bias=None) -> int:
+        code = self.code
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+            if t.dtype != self.dtype and t.dtype != torch.float32:
+                raise TypeError(f"{name}: expected {self.dtype} or torch.float32, got {t.dtype}")
+            if _index(t) != self.index or not _is_cuda(t):
+                raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {t.device})")
+            if t.dim() != 1 or t.numel() != self.H or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous [{self.H}] tensor, got shape {tuple(t.shape)}")
+            code = _DTYPE[t.dtype]
+        if weight is not None and bias is not None and weight.dtype != bias.dtype:
             raise TypeError("weight and bias: expected one type")
-        code = _DTYPE[t.dtype]
-    return _DTYPE[x.dtype] if code is None else code
+        return code
+
+    def stat(self, t, name: str):
+        """Address of an optional float32 output of one value per row."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name}: expected a float32 tensor")
+        n = self.lay.n_tokens * self.lay.rows_per_token
+        if not _is_cuda(t) or _index(t) != self.index or not t.is_contiguous() or t.numel() < n:
+            raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {n} elements on the call's device")
+        return t.data_ptr()
+
+    def workspace(self, ws):
+        if ws is None:
+            return None
+        if not isinstance(ws, LayerNormWorkspace):
+            raise TypeError(f"workspace: expected LayerNormWorkspace, got {type(ws).__name__}")
+        if _index(ws.buf) != self.index:
+            raise ValueError(f"workspace: on {ws.buf.device}, the call's rows are on cuda:{self.index}")
+        n = self.lay.n_logical_tokens * self.lay.rows_per_token
+        if ws.n_rows != n or ws.hidden != self.H:
+            raise ValueError(f"workspace: for {ws.n_rows} rows of {ws.hidden}, the call's multiset has {n} rows of {self.H}")
+        return ws.buf.data_ptr()
+
+    def layout(self, plan: bool):
+        """The call's descriptor; the plan only where it is used.  A call of at most
+        one slot does not use its token stride."""
+        lay, n = self.lay, self.lay.n_tokens
+        tok = None
+        if n:
+            t = lay.tok_id
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+                raise TypeError("layout.tok_id: expected an int32 tensor")
+            if not _is_cuda(t) or _index(t) != self.index:
+                raise ValueError(f"layout.tok_id: must be a CUDA tensor on the call's device (got {t.device})")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"layout.tok_id: expected {n} contiguous ids")
+            tok = t.data_ptr()
+        addr, items = None, 0
+        if plan and lay.plan is not None:
+            t, items = lay.plan, lay.plan_items
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+                raise TypeError("layout.plan: expected a uint8 tensor")
+            if not _is_cuda(t) or (items and _index(t) != self.index):
+                raise ValueError(f"layout.plan: must be a CUDA tensor on the call's device (got {t.device})")
+            if items and (t.numel() < items * _rb.PLAN_ITEM_BYTES or not t.is_contiguous()):
+                raise ValueError(f"layout.plan: {items} items need {items * _rb.PLAN_ITEM_BYTES} contiguous bytes")
+            addr = t.data_ptr()
+        stride = self.strides[0] if n > 1 else lay.rows_per_token * self.H
+        return ctypes.byref(_rb._Layout(n, lay.rows_per_token, 0, stride, tok, lay.n_logical_tokens, addr, items))
 
 
-def _layout(x, lay, H: int):
-    """The call's descriptor.  A call of at most one slot does not use its stride."""
-    return ctypes.byref(lay.struct(x.stride(0) if lay.n_tokens > 1 else lay.rows_per_token * H))
-
-
-def _stats(lay, x, mean, rstd):
-    n = lay.n_tokens * lay.rows_per_token
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _rb._f32_out(t, name, n, x.device)
-
-
-def _ws(workspace, lay, H: int, device):
-    if workspace is None:
-        return None
-    if not isinstance(workspace, LayerNormWorkspace):
-        raise TypeError(f"workspace: expected LayerNormWorkspace, got {type(workspace).__name__}")
-    if workspace.buf.device != device:
-        raise ValueError(f"workspace: on {workspace.buf.device}, the call's rows are on {device}")
-    n = lay.n_logical_tokens * lay.rows_per_token
-    if workspace.n_rows != n or workspace.hidden != H:
-        raise ValueError(f"workspace: for {workspace.n_rows} rows of {workspace.hidden}, the call's multiset has "
-                         f"{n} rows of {H}")
-    return workspace.buf.data_ptr()
+def _new(like):
+    """A new output with the shape and strides of `like` (rows past n_tokens and padding are left as they come)."""
+    return torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _s(stream, t):
-    """The stream handle; t's device has to be the stream's, and the current one."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the call's tensors are on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if stream.device != t.device:
-        raise ValueError(f"stream: on {stream.device}, the call's tensors are on {t.device}")
-    return stream.cuda_stream
-
-
 def layernorm_fwd(x, weight, bias, lay, eps: float, y=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * weight + bias on every active row.  weight and bias
     may be None; mean and rstd are optional float32 outputs of one value per row."""
-    H = _hidden(x, lay)
-    _rows(x, "x", lay, H)
-    st = _s(stream, x)
+    c = _Call(x, "x", lay, stream)
     if y is None:
-        y = _new(x, lay, H)
-    _rows(y, "y", lay, H, x)
-    _stats(lay, x, mean, rstd)
-    pd = _params(x, H, weight, bias)
-    _rb._check(_rb._load().layernorm_fwd(x.data_ptr(), _p(weight), _p(bias), H, eps, _DTYPE[x.dtype], pd,
-                                         _layout(x, lay, H), y.data_ptr(), _p(mean), _p(rstd), st),
-               "layernorm_fwd")
+        y = _new(x)
+    rc = _rb._load().layernorm_fwd(x.data_ptr(), _p(weight), _p(bias), c.H, eps, c.code, c.params(weight, bias),
+                                   c.layout(False), c.rows(y, "y"), c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
+    if rc:
+        _rb._check(rc, "layernorm_fwd")
     return y
 
 
@@ -200,39 +231,31 @@ def layernorm_add_fwd(x, residual, weight, bias, lay, eps: float, h=None, y=None
                       dropout: Dropout = None, stream=None):
     """Dropout and residual add fused with the norm: h = round(drop(x) + residual),
     y = layer norm of h.  Returns (h, y); h is what the backward pass takes."""
-    H = _hidden(x, lay)
-    _rows(x, "x", lay, H)
-    st = _s(stream, x)
+    c = _Call(x, "x", lay, stream)
     if h is None:
-        h = _new(x, lay, H)
+        h = _new(x)
     if y is None:
-        y = _new(x, lay, H)
-    for name, t in (("residual", residual), ("h", h), ("y", y)):
-        _rows(t, name, lay, H, x)
-    _stats(lay, x, mean, rstd)
-    pd = _params(x, H, weight, bias)
-    d = None if dropout is None else ctypes.byref(dropout.struct(x.device))
-    _rb._check(_rb._load().layernorm_add_fwd(x.data_ptr(), residual.data_ptr(), _p(weight), _p(bias), H, eps,
-                                             _DTYPE[x.dtype], pd, _layout(x, lay, H), d, h.data_ptr(), y.data_ptr(),
-                                             _p(mean), _p(rstd), st), "layernorm_add_fwd")
+        y = _new(x)
+    d = None if dropout is None else ctypes.byref(dropout.struct(c.index))
+    rc = _rb._load().layernorm_add_fwd(x.data_ptr(), c.rows(residual, "residual"), _p(weight), _p(bias), c.H, eps, c.code,
+                                       c.params(weight, bias), c.layout(False), d, c.rows(h, "h"), c.rows(y, "y"),
+                                       c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
+    if rc:
+        _rb._check(rc, "layernorm_add_fwd")
     return h, y
 
 
 def layernorm_bwd(x, weight, dy, lay, eps: float, dx=None, workspace=None, stream=None, write_dx: bool = True):
     """dx on every active row; with a workspace the same pass adds the call's rows
     to dweight and dbias (the layout needs its plan)."""
-    H = _hidden(x, lay)
-    _rows(x, "x", lay, H)
-    st = _s(stream, x)
-    _rows(dy, "dy", lay, H, x)
+    c = _Call(x, "x", lay, stream)
     if dx is None and write_dx:
-        dx = _new(dy, lay, H)
-    if dx is not None:
-        _rows(dx, "dx", lay, H, x)
-    pd = _params(x, H, weight)
-    ws = _ws(workspace, lay, H, x.device)
-    _rb._check(_rb._load().layernorm_bwd(x.data_ptr(), _p(weight), dy.data_ptr(), H, eps, _DTYPE[x.dtype], pd,
-                                         _layout(x, lay, H), _p(dx), ws, st), "layernorm_bwd")
+        dx = _new(dy)
+    rc = _rb._load().layernorm_bwd(x.data_ptr(), _p(weight), c.rows(dy, "dy"), c.H, eps, c.code, c.params(weight),
+                                   c.layout(workspace is not None), None if dx is None else c.rows(dx, "dx"),
+                                   c.workspace(workspace), c.stream)
+    if rc:
+        _rb._check(rc, "layernorm_bwd")
     return dx
 
 
@@ -242,43 +265,36 @@ def layernorm_add_bwd(h, weight, dy, lay, eps: float, dres=None, grad_scale: flo
     (norm backward) + dres) is the residual's gradient, dx = round(drop(the same
     sum)) is x's.  Returns (dh, dx); without dropout dx is dh.  The workspace's
     terms stay unscaled (scale them at finalize)."""
-    H = _hidden(h, lay)
-    _rows(h, "h", lay, H)
-    st = _s(stream, h)
-    _rows(dy, "dy", lay, H, h)
+    c = _Call(h, "h", lay, stream)
+    at_dy = c.rows(dy, "dy")
     if dh is None:
-        dh = _new(dy, lay, H)
-    _rows(dh, "dh", lay, H, h)
-    if dres is not None:
-        _rows(dres, "dres", lay, H, h)
+        dh = _new(dy)
     d = None
     if dropout is not None:
         if dx is None:
-            dx = _new(dy, lay, H)
-        _rows(dx, "dx", lay, H, h)
-        d = ctypes.byref(dropout.struct(h.device))
+            dx = _new(dy)
+        d = ctypes.byref(dropout.struct(c.index))
     elif dx is not None:
         raise ValueError("dx: only with a dropout (without one it is dh)")
-    pd = _params(h, H, weight)
-    ws = _ws(workspace, lay, H, h.device)
-    _rb._check(_rb._load().layernorm_add_bwd(h.data_ptr(), _p(weight), dy.data_ptr(), _p(dres), H, eps, grad_scale,
-                                             _DTYPE[h.dtype], pd, _layout(h, lay, H), d, dh.data_ptr(), _p(dx), ws,
-                                             st), "layernorm_add_bwd")
+    rc = _rb._load().layernorm_add_bwd(h.data_ptr(), _p(weight), at_dy, None if dres is None else c.rows(dres, "dres"),
+                                       c.H, eps, grad_scale, c.code, c.params(weight), c.layout(workspace is not None), d,
+                                       c.rows(dh, "dh"), None if dx is None else c.rows(dx, "dx"),
+                                       c.workspace(workspace), c.stream)
+    if rc:
+        _rb._check(rc, "layernorm_add_bwd")
     return dh, (dh if dropout is None else dx)
 
 
 def _dropout(fn: str, x, out, in_name: str, out_name: str, lay, dropout, stream):
-    H = _hidden(x, lay)
-    _rows(x, in_name, lay, H)
-    st = _s(stream, x)
+    c = _Call(x, in_name, lay, stream)
     if not isinstance(dropout, Dropout):
         raise TypeError(f"dropout: expected Dropout, got {type(dropout).__name__}")
     if out is None:
-        out = _new(x, lay, H)
-    _rows(out, out_name, lay, H, x)
-    d = dropout.struct(x.device)
-    _rb._check(getattr(_rb._load(), fn)(x.data_ptr(), H, _DTYPE[x.dtype], _layout(x, lay, H), ctypes.byref(d),
-                                        out.data_ptr(), st), fn)
+        out = _new(x)
+    rc = getattr(_rb._load(), fn)(x.data_ptr(), c.H, c.code, c.layout(False), ctypes.byref(dropout.struct(c.index)),
+                                  c.rows(out, out_name), c.stream)
+    if rc:
+        _rb._check(rc, fn)
     return out
 
 
@@ -305,27 +321,41 @@ class LayerNormWorkspace:
         if self.buf.data_ptr() % 256:
             raise RuntimeError("workspace allocation is not 256-byte aligned")
 
+    def _stream(self, stream) -> int:
+        index = _index(self.buf)
+        if index != _current():
+            raise ValueError(f"workspace: on {self.buf.device}, the current device is cuda:{_current()}")
+        if stream is None:
+            return _raw_stream(index)
+        if stream.device_index != index:
+            raise ValueError(f"stream: on {stream.device}, the workspace is on {self.buf.device}")
+        return stream.cuda_stream
+
+    def _gradient(self, t, name: str):
+        if t is None:
+            return torch.empty(self.hidden, dtype=torch.float32, device=self.buf.device)
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name}: expected a float32 tensor")
+        if _index(t) != _index(self.buf) or not t.is_contiguous() or t.numel() < self.hidden:
+            raise ValueError(f"{name}: expected a contiguous tensor of at least {self.hidden} elements on {self.buf.device}")
+        return t
+
     def begin(self, stream=None):
-        _rb._check(_rb._load().layernorm_begin(self.buf.data_ptr(), self.bytes, self.n_rows, self.hidden,
-                                               _s(stream, self.buf)), "layernorm_begin")
+        rc = _rb._load().layernorm_begin(self.buf.data_ptr(), self.bytes, self.n_rows, self.hidden, self._stream(stream))
+        if rc:
+            _rb._check(rc, "layernorm_begin")
 
     def finalize(self, dweight=None, dbias=None, stream=None, grad_scale: float = 1.0):
         """(dweight, dbias) of the reduction, each root multiplied once by grad_scale."""
-        if not math.isfinite(grad_scale):
-            raise _rb.RmsNormError(-13, "layernorm_finalize")
-        if dweight is None:
-            dweight = torch.empty(self.hidden, dtype=torch.float32, device=self.buf.device)
-        if dbias is None:
-            dbias = torch.empty(self.hidden, dtype=torch.float32, device=self.buf.device)
-        _rb._f32_out(dweight, "dweight", self.hidden, self.buf.device)
-        _rb._f32_out(dbias, "dbias", self.hidden, self.buf.device)
-        _rb._check(_rb._load().layernorm_finalize(self.buf.data_ptr(), self.n_rows, self.hidden, grad_scale,
-                                                  dweight.data_ptr(), dbias.data_ptr(), _s(stream, self.buf)),
-                   "layernorm_finalize")
+        dweight, dbias = self._gradient(dweight, "dweight"), self._gradient(dbias, "dbias")
+        rc = _rb._load().layernorm_finalize(self.buf.data_ptr(), self.n_rows, self.hidden, grad_scale,
+                                            dweight.data_ptr(), dbias.data_ptr(), self._stream(stream))
+        if rc:
+            _rb._check(rc, "layernorm_finalize")
         return dweight, dbias
 
     def status(self, stream=None) -> int:
         out = ctypes.c_int32(0)
-        _rb._check(_rb._load().layernorm_status(self.buf.data_ptr(), _s(stream, self.buf), ctypes.byref(out)),
+        _rb._check(_rb._load().layernorm_status(self.buf.data_ptr(), self._stream(stream), ctypes.byref(out)),
                    "layernorm_status")
         return int(out.value)
