@@ -250,16 +250,14 @@ extern "C" int dropout_fwd(const void *x, int64_t hidden, int32_t dtype, const r
     if (bad_align(x) || bad_align(y)) return RMSNORM_ERR_ALIGN;
     DeviceInfo *d = nullptr;
     if ((rc = device_info(&d))) return rc;
-    DropoutParams p = {x, y, drop, layout->tok_id, layout->n_tokens, layout->token_stride,
-                       layout->rows_per_token, int32_t(hidden)};
+    const DropoutParams p = {x, y, drop, layout->tok_id, layout->n_tokens * layout->rows_per_token, layout->token_stride,
+                             layout->rows_per_token, int32_t(hidden)};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case LAYERNORM_BF16: rc = dropout_launch<__nv_bfloat16>(p, d->sms, s); break;
-        case LAYERNORM_FP16: rc = dropout_launch<__half>(p, d->sms, s); break;
-        default: rc = dropout_launch<float>(p, d->sms, s); break;
+        case LAYERNORM_BF16: return dropout_launch<__nv_bfloat16>(p, s);
+        case LAYERNORM_FP16: return dropout_launch<__half>(p, s);
+        default: return dropout_launch<float>(p, s);
     }
-    if (rc == RMSNORM_OK) count_launch();
-    return rc;
 }
 
 extern "C" int dropout_bwd(const void *dy, int64_t hidden, int32_t dtype, const rmsnorm_layout_t *layout,

@@ -251,13 +251,9 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 f2_t q[4];
                 oct_up<E>(ro, q);
                 if constexpr (DROP) {
-                    const uint32_t keep = keep_bits(uint32_t(l), lrow, key, p.drop.t);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a = __fmaf_rn(f2_lo(x[j]), p.drop.scale, f2_lo(q[j]));
-                        const float c = __fmaf_rn(f2_hi(x[j]), p.drop.scale, f2_hi(q[j]));
-                        x[j] = f2_make((keep >> (2 * j)) & 1 ? a : f2_lo(q[j]), (keep >> (2 * j + 1)) & 1 ? c : f2_hi(q[j]));
-                    }
+                    const uint4 u = philox4x32(uint32_t(l), lrow, key);
+                    const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+                    drop_add_pairs(x, q, words, drop_rule(p.drop));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = f2_add(x[j], q[j]);
@@ -338,7 +334,9 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 if (st && (!GRADS || p.out)) {
                     oct_store<E>(p.out, here, o);
                     if constexpr (DROP) {
-                        drop_pairs(o, keep_bits(uint32_t(l), lrow, key, p.drop.t), p.drop.scale);
+                        const uint4 u = philox4x32(uint32_t(l), lrow, key);
+                        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+                        drop_pairs(o, words, drop_rule(p.drop));
                         oct_store<E>(p.out2, here, o);
                     }
                 }

@@ -93,21 +93,40 @@ __device__ __forceinline__ void param_pairs(const void *p, int f32, int v, float
     }
 }
 
-// Keep bits of the elements of 16-byte vector v of logical row g.
+// Random words of the elements of 16-byte vector v of logical row g, one per pair.
 template <class E>
-__device__ __forceinline__ uint32_t lane_keep(int v, uint32_t g, const DropKey &key, uint32_t t) {
-    if constexpr (Lane<E>::kE == 8) return keep_bits(uint32_t(v), g, key, t);
-    return keep_bits(uint32_t(v) >> 1, g, key, t) >> (4 * (v & 1));
+__device__ __forceinline__ void lane_words(int v, uint32_t g, const DropKey &key, uint32_t (&w)[Lane<E>::kP]) {
+    if constexpr (Lane<E>::kE == 8) {
+        const uint4 r = philox4x32(uint32_t(v), g, key);
+        w[0] = r.x;
+        w[1] = r.y;
+        w[2] = r.z;
+        w[3] = r.w;
+    } else {
+        const uint4 r = philox4x32(uint32_t(v) >> 1, g, key);
+        w[0] = v & 1 ? r.z : r.x;
+        w[1] = v & 1 ? r.w : r.y;
+    }
 }
 
 // Pairs times the factor where kept, +0 elsewhere.
 template <int P>
-__device__ __forceinline__ void drop_pairs(f2_t (&f)[P], uint32_t keep, float scale) {
+__device__ __forceinline__ void drop_pairs(f2_t (&f)[P], const uint32_t (&w)[P], const DropRule &rule) {
+    const f2_t s = f2_both(rule.scale);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const float a = (keep >> (2 * i)) & 1 ? __fmul_rn(f2_lo(f[i]), scale) : 0.f;
-        const float b = (keep >> (2 * i + 1)) & 1 ? __fmul_rn(f2_hi(f[i]), scale) : 0.f;
-        f[i] = f2_make(a, b);
+        const f2_t v = f2_mul(f[i], s);
+        f[i] = f2_make(kept_lo(w[i], rule) ? f2_lo(v) : 0.f, kept_hi(w[i], rule) ? f2_hi(v) : 0.f);
+    }
+}
+// f = f times the factor + q where kept, q elsewhere.
+template <int P>
+__device__ __forceinline__ void drop_add_pairs(f2_t (&f)[P], const f2_t (&q)[P], const uint32_t (&w)[P], const DropRule &rule) {
+    const f2_t s = f2_both(rule.scale);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const f2_t v = f2_fma(f[i], s, q[i]);
+        f[i] = f2_make(kept_lo(w[i], rule) ? f2_lo(v) : f2_lo(q[i]), kept_hi(w[i], rule) ? f2_hi(v) : f2_hi(q[i]));
     }
 }
 
@@ -381,14 +400,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     up<E>(lds_v4(st_nxt + pitch + k * step), r);
                     up<E>(u, f);
                     if constexpr (DROP) {
-                        const uint32_t keep = lane_keep<E>(v, en.lrow, key, p.drop.t);
-#pragma unroll
-                        for (int j = 0; j < P; ++j) {
-                            const float lo = __fmaf_rn(f2_lo(f[j]), p.drop.scale, f2_lo(r[j]));
-                            const float hi = __fmaf_rn(f2_hi(f[j]), p.drop.scale, f2_hi(r[j]));
-                            f[j] = f2_make((keep >> (2 * j)) & 1 ? lo : f2_lo(r[j]),
-                                           (keep >> (2 * j + 1)) & 1 ? hi : f2_hi(r[j]));
-                        }
+                        uint32_t words[P];
+                        lane_words<E>(v, en.lrow, key, words);
+                        drop_add_pairs(f, r, words, drop_rule(p.drop));
                     } else {
 #pragma unroll
                         for (int j = 0; j < P; ++j) f[j] = f2_add(f[j], r[j]);
@@ -522,7 +536,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                         const uint4 u = down<E>(o);
                         if (in) st_global_v4(static_cast<E *>(p.out) + at, u);
                         if constexpr (DROP) {
-                            drop_pairs(o, lane_keep<E>(tid + k * T, e.lrow, key, p.drop.t), p.drop.scale);
+                            uint32_t words[P];
+                            lane_words<E>(tid + k * T, e.lrow, key, words);
+                            drop_pairs(o, words, drop_rule(p.drop));
                             const uint4 u2 = down<E>(o);
                             if (in) st_global_v4(static_cast<E *>(p.out2) + at, u2);
                         }

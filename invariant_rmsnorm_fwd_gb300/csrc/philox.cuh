@@ -41,17 +41,16 @@ __device__ __forceinline__ uint4 philox4x32(uint32_t c0, uint32_t c1, const Drop
     return make_uint4(a, b, c, d);
 }
 
-// Bit e set = element e of vector v of logical row g is kept.
-__device__ __forceinline__ uint32_t keep_bits(uint32_t v, uint32_t g, const DropKey &k, uint32_t t) {
-    const uint4 r = philox4x32(v, g, k);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        m |= ((w[e] & 0xffffu) >= t ? 1u : 0u) << (2 * e);
-        m |= ((w[e] >> 16) >= t ? 1u : 0u) << (2 * e + 1);
-    }
-    return m;
-}
+// Which of the 8 elements of a vector are kept: word i of its random words holds
+// elements 2i (low half) and 2i + 1 (high half).  A half is >= t exactly when the
+// half moved to the top of a word (whatever is below it) is >= t << 16.
+struct DropRule {
+    uint32_t limit;                  // t << 16
+    bool any;                        // t < 65536
+    float scale;
+};
+__device__ __forceinline__ DropRule drop_rule(const DropParams &d) { return {d.t << 16, d.t < 65536u, d.scale}; }
+__device__ __forceinline__ bool kept_lo(uint32_t w, const DropRule &r) { return r.any && (w << 16) >= r.limit; }
+__device__ __forceinline__ bool kept_hi(uint32_t w, const DropRule &r) { return r.any && w >= r.limit; }
 
 }  // namespace rbi
