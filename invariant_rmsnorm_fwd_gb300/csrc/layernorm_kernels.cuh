@@ -79,6 +79,7 @@ struct LnParams {
     int64_t n_rows, token_stride;
     const PlanItem *items;
     int64_t n_items;
+    int32_t chunk_shift;             // streaming kernel without a plan: log2 of the slots dealt at a time
     LnWs ws;
 };
 

@@ -36,11 +36,15 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
     if (S > kMaxStages) S = kMaxStages;
     const int smem = kFixedBytes + (use_block ? block : 0) + S * nt * row;
-    const int64_t units = GRADS ? p.n_items * kGroups : p.n_rows;
-    if (units == 0) return RMSNORM_OK;
     int64_t grid = int64_t(ctas) * d.sms;
+    // without a plan slots are dealt eight at a time (their ids are one 32-byte
+    // sector), one at a time where that would leave CTAs without a row
+    LnParams q = p;
+    q.chunk_shift = p.n_rows >= 16 * grid ? 3 : 0;
+    const int64_t units = GRADS ? p.n_items * kGroups : (p.n_rows + (1 << q.chunk_shift) - 1) >> q.chunk_shift;
+    if (units == 0) return RMSNORM_OK;
     if (grid > units) grid = units;
-    kern<<<unsigned(grid), threads, smem, stream>>>(p, S, nt, use_block);
+    kern<<<unsigned(grid), threads, smem, stream>>>(q, S, nt, use_block);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;

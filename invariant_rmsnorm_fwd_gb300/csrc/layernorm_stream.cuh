@@ -288,14 +288,16 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
             for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0;
     }
 
-    // this CTA's share: slots [pos, end)
-    const int64_t units = GRADS ? p.n_items * kGroups : p.n_rows;
-    int64_t pos = units * blockIdx.x / gridDim.x, end = units * (blockIdx.x + 1) / gridDim.x;
-    const int64_t share_lo = pos, share_hi = end;        // in groups (GRADS)
-    if constexpr (GRADS) {
-        pos *= kGroupRows;
-        end *= kGroupRows;
-    }
+    // This CTA's share, positions [pos, end).  Parameter gradients: consecutive slots
+    // of the plan (blocks stay together).  Else position q is slot q % 2^c of chunk
+    // q / 2^c * gridDim + blockIdx of 2^c slots each, so that padding, which comes in
+    // long runs, falls on every CTA alike.
+    const int64_t units = p.n_items * kGroups;
+    const int64_t share_lo = GRADS ? units * blockIdx.x / gridDim.x : 0;         // in groups
+    const int64_t share_hi = GRADS ? units * (blockIdx.x + 1) / gridDim.x : 0;
+    const int64_t chunks = (p.n_rows + (int64_t(1) << p.chunk_shift) - 1) >> p.chunk_shift;
+    int64_t pos = share_lo * kGroupRows;
+    const int64_t end = GRADS ? share_hi * kGroupRows : ((chunks - blockIdx.x + gridDim.x - 1) / gridDim.x) << p.chunk_shift;
     uint32_t done = 0;                                   // rows through the ring so far
     int turn = 0;
     bool dead = false;
@@ -340,12 +342,14 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
                     e.lrow = uint32_t(lrow);
                 } else {
-                    const uint32_t tok = uint32_t(q) / uint32_t(p.rpt), head = uint32_t(q) - tok * uint32_t(p.rpt);
-                    const int32_t id = p.tok_id[tok];
+                    const int64_t slot = ((((q >> p.chunk_shift) * gridDim.x + blockIdx.x) << p.chunk_shift)) +
+                                         (q & ((int64_t(1) << p.chunk_shift) - 1));
+                    const uint32_t tok = uint32_t(slot) / uint32_t(p.rpt), head = uint32_t(slot) - tok * uint32_t(p.rpt);
+                    const int32_t id = slot < p.n_rows ? p.tok_id[tok] : -1;
                     valid = id >= 0;
                     e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
                     e.lrow = uint32_t(id) * uint32_t(p.rpt) + head;
-                    e.tag = uint32_t(q);
+                    e.tag = uint32_t(slot);
                 }
             }
             const uint32_t bits = __ballot_sync(kFull, valid);
