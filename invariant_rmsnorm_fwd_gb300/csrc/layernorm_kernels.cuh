@@ -79,7 +79,7 @@ struct LnParams {
     int64_t n_rows, token_stride;
     const PlanItem *items;
     int64_t n_items;
-    int32_t chunk_shift;             // streaming kernel without a plan: log2 of the slots dealt at a time
+    int32_t share, share_rest;       // streaming kernel: units of a CTA; the first share_rest CTAs have one more
     LnWs ws;
 };
 

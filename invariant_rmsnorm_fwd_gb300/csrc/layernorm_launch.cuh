@@ -19,32 +19,35 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
     const int row = NV * threads * 16, least = MODE == kLnBwd ? 3 : 2;   // a staged row, padded to whole vectors of the CTA
     int nt = MODE == kLnFwd ? 1 : MODE == kLnAdd ? 2 : p.res ? 3 : 2;
     if (MODE == kLnBwd && nt == 3 && kFixedBytes + least * nt * row > d.max_smem) nt = 2;
-    const int block = GRADS ? int(align256(int64_t(p.hidden) * 8)) : 0;
+    // tensor memory of a CTA: the sums and the fold of its warps, four side by side
+    int cols = 0;
+    if (GRADS) {
+        cols = 32;
+        while (cols < (threads + 127) / 128 * 4 * NV * Lane<E>::kE) cols *= 2;
+    }
     int ctas = 65536 / ((regs + 7) / 8 * 8 * threads);
     if (ctas > 2048 / threads) ctas = 2048 / threads;
     if (ctas > 32) ctas = 32;
+    if (GRADS && ctas > 512 / cols) ctas = 512 / cols;
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
-    int S = 0, use_block = 0;
+    int S = 0;
     for (; ctas >= 1; --ctas) {
         int room = kSmemPerSm / ctas - kSmemPerCta;
         if (room > d.max_smem) room = d.max_smem;
-        room -= kFixedBytes;
-        use_block = GRADS && (room - block) / (nt * row) >= least ? 1 : 0;
-        S = (room - (use_block ? block : 0)) / (nt * row);
+        S = (room - kFixedBytes) / (nt * row);
         if (S >= least + 1 || (ctas == 1 && S >= least)) break;
     }
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
     if (S > kMaxStages) S = kMaxStages;
-    const int smem = kFixedBytes + (use_block ? block : 0) + S * nt * row;
+    const int smem = kFixedBytes + S * nt * row;
     int64_t grid = int64_t(ctas) * d.sms;
-    // without a plan slots are dealt eight at a time (their ids are one 32-byte
-    // sector), one at a time where that would leave CTAs without a row
-    LnParams q = p;
-    q.chunk_shift = p.n_rows >= 16 * grid ? 3 : 0;
-    const int64_t units = GRADS ? p.n_items * kGroups : (p.n_rows + (1 << q.chunk_shift) - 1) >> q.chunk_shift;
+    const int64_t units = GRADS ? p.n_items * kGroups : p.n_rows;
     if (units == 0) return RMSNORM_OK;
     if (grid > units) grid = units;
-    kern<<<unsigned(grid), threads, smem, stream>>>(q, S, nt, use_block);
+    LnParams q = p;
+    q.share = int32_t(units / grid);
+    q.share_rest = int32_t(units % grid);
+    kern<<<unsigned(grid), threads, smem, stream>>>(q, S, nt, cols);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
@@ -53,8 +56,9 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
 template <class E, int NV, int MODE, bool DROP, bool GRADS>
 int ln_launch_stream(const LnParams &p, const DeviceInfo &d, cudaStream_t stream) {
     const int V = p.hidden / Lane<E>::kE, per = (V + NV - 1) / NV, threads = (per + 31) / 32 * 32;
+    constexpr int kMinB = 2;
     if constexpr (NV * Lane<E>::kE <= 16) {              // wider threads: rows of more than 8192 columns only
-        if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, 2>(p, threads, d, stream);
+        if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, kMinB>(p, threads, d, stream);
         if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
     }
     return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);

@@ -14,11 +14,14 @@
 // barrier also releases a stage: every thread has read it, so thread 0 refills
 // it without a barrier of its own.
 //
-// Parameter gradients: a thread's columns accumulate in registers over the 8
-// rows of a group (in logical order), and over the groups of a block in shared
-// memory where the CTA holds the whole block.
+// Parameter gradients: the sums of a thread's columns over the 8 rows of a group
+// (in logical order), and the fold of a block's groups from its first one on,
+// live in tensor memory, which nothing else here needs: a row's terms are added
+// on the way through registers.  In registers the sums alone would take 32 of a
+// thread's 80 and cost a third of the warps, in shared memory the stages.
 #pragma once
 #include "layernorm_kernels.cuh"
+#include "umma.cuh"
 
 namespace rbi {
 
@@ -217,6 +220,165 @@ __device__ __forceinline__ void pairs_load(const float *p, f2_t (&f)[P]) {
     }
 }
 
+// The sums of one vector (dweight, then dbias) in tensor memory at `at`, read or
+// written by the whole warp.
+template <int P>
+__device__ __forceinline__ void sums_load(uint32_t at, f2_t (&w)[P], f2_t (&b)[P]) {
+    uint32_t u[8], v[8];
+    umma::ld_32x32_x8(at, u);
+    if constexpr (P == 4) umma::ld_32x32_x8(at + 8, v);
+    umma::wait_ld();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        if constexpr (P == 4) b[i] = f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        else b[i] = f2_make(__uint_as_float(u[4 + 2 * i]), __uint_as_float(u[5 + 2 * i]));
+    }
+}
+template <int P>
+__device__ __forceinline__ void sums_store(uint32_t at, const f2_t (&w)[P], const f2_t (&b)[P]) {
+    uint32_t u[8], v[8];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        u[2 * i] = __float_as_uint(f2_lo(w[i]));
+        u[2 * i + 1] = __float_as_uint(f2_hi(w[i]));
+        uint32_t *to = P == 4 ? v + 2 * i : u + 4 + 2 * i;
+        to[0] = __float_as_uint(f2_lo(b[i]));
+        to[1] = __float_as_uint(f2_hi(b[i]));
+    }
+    umma::st_32x32_x8(at, u);
+    if constexpr (P == 4) umma::st_32x32_x8(at + 8, v);
+}
+
+// The rare parts of the kernel are functions of their own, called: inlined, their
+// registers would count in the row loop's.
+
+// Writes the CTA's list number `turn` and returns its length, -1 behind the last
+// one.  The CTA's share of positions: with parameter gradients consecutive slots
+// of the plan (blocks stay together); else position q is slot q gridDim + blockIdx,
+// so that padding, which comes in long runs, falls on every CTA alike.
+template <class E, bool GRADS>
+__device__ __noinline__ int ln_list(const LnParams &p, uint8_t *smem, int turn) {
+    volatile int *count = reinterpret_cast<volatile int *>(smem + kCountOff);
+    LnEntry *list = reinterpret_cast<LnEntry *>(smem + kListOff);
+    const int tid = threadIdx.x, T = blockDim.x, warps = T >> 5;
+    const int64_t cta = blockIdx.x, more = cta < p.share_rest ? 1 : 0;
+    const int64_t share_lo = GRADS ? cta * p.share + (more ? cta : int64_t(p.share_rest)) : 0, share_hi = share_lo + p.share + more;
+    const int64_t lo = GRADS ? share_lo * kGroupRows : 0, end = GRADS ? share_hi * kGroupRows : share_hi;
+    // whole items after the first list
+    const int64_t base = (GRADS ? lo - lo % kBlockRows : 0) + int64_t(turn) * kListRows;
+    if (base >= end) return -1;
+    const int64_t pos = base < lo ? lo : base, stop = base + kListRows < end ? base + kListRows : end;
+    __syncthreads();                                     // the last list is read, its stages are free
+    int n = 0;
+    for (int64_t q0 = pos; q0 < stop; q0 += T) {
+        const int64_t q = q0 + tid;
+        LnEntry e = {0, 0, 0};
+        bool valid = false;
+        if (q < stop) {
+            if constexpr (GRADS) {
+                const int64_t item = q >> 6;
+                const int slot = int(q & 63);
+                const PlanItem &it = p.items[item];
+                const int kind = it.kind, blk = it.block;
+                const int32_t prow = it.prow[slot], lrow = it.lrow[slot];
+                if (prow >= 0) {
+                    // whole blocks and quarters hold each row at its place, so a
+                    // group ends at its last row
+                    valid = prow < p.n_rows && lrow >= 0 && lrow < p.ws.n_rows &&
+                            (kind == kItemSpill ||
+                             ((kind == kItemWhole || kind == kItemQuarters) && lrow == int64_t(blk) * kBlockRows + slot));
+                    if (!valid) set_status(p.ws.hdr, kStPlan);
+                    const bool block_end = slot == kBlockRows - 1 || lrow == p.ws.n_rows - 1;
+                    if (kind == kItemSpill) {
+                        e.tag = kTagSpill;
+                    } else if (slot % kGroupRows == kGroupRows - 1 || block_end) {
+                        e.tag = kTagClose | kTagStore;
+                        if (kind == kItemWhole && item * kGroups >= share_lo) {
+                            e.tag = kTagClose | kTagFold;
+                            if (block_end || (q >> 3) == share_hi - 1) e.tag |= kTagStore;
+                        }
+                    }
+                }
+                const uint32_t tok = uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - tok * uint32_t(p.rpt);
+                e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
+                e.lrow = uint32_t(lrow);
+            } else {
+                const int64_t slot = q * gridDim.x + blockIdx.x;
+                const uint32_t tok = uint32_t(slot) / uint32_t(p.rpt), head = uint32_t(slot) - tok * uint32_t(p.rpt);
+                const int32_t id = p.tok_id[tok];
+                valid = id >= 0;
+                e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
+                e.lrow = uint32_t(id) * uint32_t(p.rpt) + head;
+                e.tag = uint32_t(slot);
+            }
+        }
+        const uint32_t bits = __ballot_sync(kFull, valid);
+        if ((tid & 31) == 0) count[tid >> 5] = __popc(bits);
+        __syncthreads();
+        int at = n;
+        for (int i = 0; i < warps; ++i) {
+            const int c = count[i];
+            if (i < (tid >> 5)) at += c;
+            n += c;
+        }
+        if (valid) list[at + __popc(bits & ((1u << (tid & 31)) - 1u))] = e;
+        __syncthreads();
+    }
+    return n;
+}
+
+// Ends a group (its sums are in tensor memory at `sums`, the block's fold behind
+// them), or stores a row of a cut one (xhat and dy; the sums held that row alone
+// and are dropped).  st: this thread's vectors of the row in its stage.
+template <class E, int NV>
+__device__ __noinline__ void ln_close(const LnParams &p, uint32_t sums, uint32_t st, uint32_t pitch, float neg_mean, float rstd,
+                                      uint32_t lrow, uint32_t tag) {
+    constexpr int kE = Lane<E>::kE, P = Lane<E>::kP, kSumCols = 2 * NV * kE;
+    const int tid = threadIdx.x, T = blockDim.x, V = p.hidden / kE;
+    const bool spill = tag & kTagSpill, fold = tag & kTagFold, store = tag & kTagStore;
+    const uint32_t group = lrow / kGroupRows, place = group % kGroups;
+    const int64_t slot = fold ? int64_t(group - place) : int64_t(group);
+    float *dst = spill ? p.ws.spill + int64_t(lrow) * 2 * p.hidden : p.ws.partial + slot * 2 * p.hidden;
+    umma::wait_st();
+#pragma unroll 1
+    for (int k = 0; k < NV; ++k) {
+        const int v = tid + k * T;
+        f2_t w[P], b[P];
+        if (spill) {
+            up<E>(lds_v4(st + k * T * 16), w);
+            up<E>(lds_v4(st + pitch + k * T * 16), b);
+#pragma unroll
+            for (int j = 0; j < P; ++j) w[j] = f2_mul(f2_add(w[j], f2_both(neg_mean)), f2_both(rstd));
+        } else {
+            sums_load(sums + k * 2 * kE, w, b);
+            if (fold && place != 0) {
+                f2_t fw[P], fb[P];
+                sums_load(sums + kSumCols + k * 2 * kE, fw, fb);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    w[j] = f2_add(fw[j], w[j]);
+                    b[j] = f2_add(fb[j], b[j]);
+                }
+            }
+        }
+        if (spill || store) {
+            if (v < V) {
+                pairs_store(dst + v * kE, w);
+                pairs_store(dst + p.hidden + v * kE, b);
+            }
+        } else {
+            sums_store(sums + kSumCols + k * 2 * kE, w, b);
+        }
+    }
+    if (tid == 0) {
+        if (p.ws.state[group] != 0 || (spill && p.ws.flag[lrow])) set_status(p.ws.hdr, kStDouble);
+        if (spill) p.ws.flag[lrow] = 1;
+        else if (!fold) p.ws.state[group] = 1;
+        else if (store) p.ws.state[group - place] = uint8_t(place + 1);
+    }
+}
+
 enum LnMode : int { kLnFwd = 0, kLnAdd = 1, kLnBwd = 2 };
 
 // p.res in kLnBwd: dres, staged as the third tensor when nt is 3 (rows too wide
@@ -227,7 +389,7 @@ enum LnMode : int { kLnFwd = 0, kLnAdd = 1, kLnBwd = 2 };
 // are zero, so that the passes need no bounds checks, only the stores do.
 template <class E, int NV, int MODE, bool DROP, bool GRADS, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_constant__ LnParams p, int S, int nt,
-                                                               int use_block) {
+                                                               int tmem_cols) {
     constexpr int kE = Lane<E>::kE, P = Lane<E>::kP;
     constexpr bool kFwd = MODE != kLnBwd;
     constexpr bool kHold = NV * kE <= 16;                // d and dy stay in registers between the two passes
@@ -241,8 +403,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     const int V = p.hidden / kE;
     const uint32_t row_bytes = uint32_t(p.hidden) * uint32_t(sizeof(E));
     const uint32_t pitch = uint32_t(NV * T) * 16u, stage_pitch = pitch * uint32_t(nt);
-    float *block_acc = reinterpret_cast<float *>(smem + kFixedBytes);
-    const uint32_t stage0 = kFixedBytes + (use_block ? uint32_t(align256(int64_t(p.hidden) * 8)) : 0u);
+    constexpr uint32_t stage0 = kFixedBytes;
     const uint32_t my0 = smem_addr(smem) + stage0 + uint32_t(tid) * 16u;        // this thread's vectors of stage 0
     const uint32_t list0 = smem_addr(list);
     const uint32_t step = uint32_t(T) * 16u;
@@ -280,91 +441,31 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     *reinterpret_cast<uint4 *>(smem + stage0 + s * stage_pitch + t * pitch + v * 16) = make_uint4(0, 0, 0, 0);
         }
     }
-    f2_t dw[GRADS ? NV : 1][P], db[GRADS ? NV : 1][P];
+    // Tensor memory: kSumCols columns of a warp's 32 lanes for the group's sums and as
+    // many for the block's fold; warps w, w + 4, ... share a quarter of the lanes.
+    constexpr int kSumCols = 2 * NV * kE;
+    uint32_t sums = 0;
+    bool fresh = true;                                   // the next row begins a group
     if constexpr (GRADS) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0;
+        uint32_t *slot = reinterpret_cast<uint32_t *>(smem + kCountOff + 80);
+        if (tid < 32) {
+            umma::tmem_alloc(slot, uint32_t(tmem_cols));
+            umma::tmem_relinquish();
+        }
+        umma::fence_before();
+        __syncthreads();
+        umma::fence_after();
+        sums = *slot + (uint32_t((tid >> 5) & 3) << 21) + uint32_t(tid >> 7) * uint32_t(2 * kSumCols);
     }
 
-    // This CTA's share, positions [pos, end).  Parameter gradients: consecutive slots
-    // of the plan (blocks stay together).  Else position q is slot q % 2^c of chunk
-    // q / 2^c * gridDim + blockIdx of 2^c slots each, so that padding, which comes in
-    // long runs, falls on every CTA alike.
-    const int64_t units = p.n_items * kGroups;
-    const int64_t share_lo = GRADS ? units * blockIdx.x / gridDim.x : 0;         // in groups
-    const int64_t share_hi = GRADS ? units * (blockIdx.x + 1) / gridDim.x : 0;
-    const int64_t chunks = (p.n_rows + (int64_t(1) << p.chunk_shift) - 1) >> p.chunk_shift;
-    int64_t pos = share_lo * kGroupRows;
-    const int64_t end = GRADS ? share_hi * kGroupRows : ((chunks - blockIdx.x + gridDim.x - 1) / gridDim.x) << p.chunk_shift;
     uint32_t done = 0;                                   // rows through the ring so far
     int turn = 0;
     bool dead = false;
 
-    while (pos < end && !dead) {
-        // ------------------------------------------------ the list of the next rows
-        int64_t stop = pos + kListRows;
-        if constexpr (GRADS) stop -= pos % kBlockRows;   // whole items after the first list
-        if (stop > end) stop = end;
-        __syncthreads();                                 // the last list is read, its stages are free
-        int n = 0;
-        for (int64_t q0 = pos; q0 < stop; q0 += T) {
-            const int64_t q = q0 + tid;
-            LnEntry e = {0, 0, 0};
-            bool valid = false;
-            if (q < stop) {
-                if constexpr (GRADS) {
-                    const int64_t item = q >> 6;
-                    const int slot = int(q & 63);
-                    const PlanItem &it = p.items[item];
-                    const int kind = it.kind, blk = it.block;
-                    const int32_t prow = it.prow[slot], lrow = it.lrow[slot];
-                    if (prow >= 0) {
-                        // whole blocks and quarters hold each row at its place, so a
-                        // group ends at its last row
-                        valid = prow < p.n_rows && lrow >= 0 && lrow < p.ws.n_rows &&
-                                (kind == kItemSpill ||
-                                 ((kind == kItemWhole || kind == kItemQuarters) && lrow == int64_t(blk) * kBlockRows + slot));
-                        if (!valid) set_status(p.ws.hdr, kStPlan);
-                        const bool block_end = slot == kBlockRows - 1 || lrow == p.ws.n_rows - 1;
-                        if (kind == kItemSpill) {
-                            e.tag = kTagSpill;
-                        } else if (slot % kGroupRows == kGroupRows - 1 || block_end) {
-                            e.tag = kTagClose | kTagStore;
-                            if (use_block && kind == kItemWhole && item * kGroups >= share_lo) {
-                                e.tag = kTagClose | kTagFold;
-                                if (block_end || (q >> 3) == share_hi - 1) e.tag |= kTagStore;
-                            }
-                        }
-                    }
-                    const uint32_t tok = uint32_t(prow) / uint32_t(p.rpt), head = uint32_t(prow) - tok * uint32_t(p.rpt);
-                    e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
-                    e.lrow = uint32_t(lrow);
-                } else {
-                    const int64_t slot = ((((q >> p.chunk_shift) * gridDim.x + blockIdx.x) << p.chunk_shift)) +
-                                         (q & ((int64_t(1) << p.chunk_shift) - 1));
-                    const uint32_t tok = uint32_t(slot) / uint32_t(p.rpt), head = uint32_t(slot) - tok * uint32_t(p.rpt);
-                    const int32_t id = slot < p.n_rows ? p.tok_id[tok] : -1;
-                    valid = id >= 0;
-                    e.off = int64_t(tok) * p.token_stride + int64_t(head) * p.hidden;
-                    e.lrow = uint32_t(id) * uint32_t(p.rpt) + head;
-                    e.tag = uint32_t(slot);
-                }
-            }
-            const uint32_t bits = __ballot_sync(kFull, valid);
-            if ((tid & 31) == 0) count[tid >> 5] = __popc(bits);
-            __syncthreads();
-            int at = n;
-            for (int i = 0; i < warps; ++i) {
-                const int c = count[i];
-                if (i < (tid >> 5)) at += c;
-                n += c;
-            }
-            if (valid) list[at + __popc(bits & ((1u << (tid & 31)) - 1u))] = e;
-            __syncthreads();
-        }
-        pos = stop;
+#pragma unroll 1
+    for (int lists = 0; !dead; ++lists) {
+        const int n = ln_list<E, GRADS>(p, smem, lists);
+        if (n < 0) break;
         if (n == 0) continue;
 
         auto issue = [&](int i) {                        // thread 0
@@ -509,6 +610,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 const f2_t s2 = f2_both(s1), c0 = f2_both(-__fmul_rn(s1, ma));
                 const f2_t c1 = f2_both(-__fmul_rn(s1, __fmul_rn(mc, rstd)));
                 const bool write = !GRADS || p.out;
+                if constexpr (GRADS) umma::wait_st();
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int kk = kHold ? k : 0;
@@ -522,10 +624,22 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < P; ++j) {
                         o[j] = f2_fma(f2_mul(g[kk][j], w[k][j]), s2, f2_fma(d[kk][j], c1, c0));
-                        if constexpr (GRADS) {
-                            dw[k][j] = f2_fma(g[kk][j], f2_mul(d[kk][j], r2), dw[k][j]);
-                            db[k][j] = f2_add(db[k][j], g[kk][j]);
+                    }
+                    if constexpr (GRADS) {
+                        f2_t dw[P], db[P];
+                        if (fresh) {
+#pragma unroll
+                            for (int j = 0; j < P; ++j) dw[j] = db[j] = 0;
+                        } else {
+                            sums_load(sums + k * 2 * kE, dw, db);
                         }
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            d[kk][j] = f2_mul(d[kk][j], r2);
+                            dw[j] = f2_fma(g[kk][j], d[kk][j], dw[j]);
+                            db[j] = f2_add(db[j], g[kk][j]);
+                        }
+                        sums_store(sums + k * 2 * kE, dw, db);
                     }
                     if (write) {
                         const int64_t at = e.off + (tid + k * T) * kE;
@@ -549,64 +663,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     }
                 }
                 if constexpr (GRADS) {
-                    if (e.tag) {
-                        // the end of a group, or a row of a cut one (between groups: the
-                        // sums hold that row alone and are dropped)
-                        const bool spill = e.tag & kTagSpill, fold = e.tag & kTagFold, store = e.tag & kTagStore;
-                        const uint32_t group = e.lrow / kGroupRows, place = group % kGroups;
-                        const int64_t slot = fold ? int64_t(group - place) : int64_t(group);
-                        float *dst = spill ? p.ws.spill + int64_t(e.lrow) * 2 * p.hidden : p.ws.partial + slot * 2 * p.hidden;
-#pragma unroll
-                        for (int k = 0; k < NV; ++k) {
-                            const int col = (tid + k * T) * kE;
-                            if (tid + k * T < V) {
-                                if (spill) {             // xhat and dy
-                                    const int kk = kHold ? k : 0;
-                                    if constexpr (!kHold) {
-                                        up<E>(lds_v4(st + k * step), d[0]);
-                                        up<E>(lds_v4(st + pitch + k * step), g[0]);
-#pragma unroll
-                                        for (int j = 0; j < P; ++j) d[0][j] = f2_add(d[0][j], neg);
-                                    }
-                                    f2_t xh[P];
-#pragma unroll
-                                    for (int j = 0; j < P; ++j) xh[j] = f2_mul(d[kk][j], r2);
-                                    pairs_store(dst + col, xh);
-                                    pairs_store(dst + p.hidden + col, g[kk]);
-                                } else {
-                                    if (fold && place != 0) {
-                                        f2_t t[P];
-                                        pairs_load(block_acc + col, t);
-#pragma unroll
-                                        for (int j = 0; j < P; ++j) dw[k][j] = f2_add(t[j], dw[k][j]);
-                                        pairs_load(block_acc + p.hidden + col, t);
-#pragma unroll
-                                        for (int j = 0; j < P; ++j) db[k][j] = f2_add(t[j], db[k][j]);
-                                    }
-                                    if (store) {
-                                        pairs_store(dst + col, dw[k]);
-                                        pairs_store(dst + p.hidden + col, db[k]);
-                                    } else {
-                                        pairs_store(block_acc + col, dw[k]);
-                                        pairs_store(block_acc + p.hidden + col, db[k]);
-                                    }
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < P; ++j) dw[k][j] = db[k][j] = 0;
-                        }
-                        if (tid == 0) {
-                            if (spill) {
-                                if (p.ws.flag[e.lrow] || p.ws.state[group] != 0) set_status(p.ws.hdr, kStDouble);
-                                p.ws.flag[e.lrow] = 1;
-                            } else {
-                                // state of a group: 1 + the number of groups behind it in its partial
-                                if (p.ws.state[group] != 0) set_status(p.ws.hdr, kStDouble);
-                                if (!fold) p.ws.state[group] = 1;
-                                else p.ws.state[group - place] = uint8_t(place + 1);
-                            }
-                        }
-                    }
+                    fresh = e.tag != 0;
+                    if (e.tag) ln_close<E, NV>(p, sums, st, pitch, -mean, rstd, e.lrow, e.tag);
                 }
             }
             mean = __fmul_rn(v[0], p.inv_h);
@@ -626,6 +684,12 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
             __syncthreads();
         }
         done += uint32_t(n);
+    }
+    if constexpr (GRADS) {
+        umma::fence_before();
+        __syncthreads();
+        umma::fence_after();
+        if (tid < 32) umma::tmem_dealloc(sums, uint32_t(tmem_cols));
     }
 }
 
