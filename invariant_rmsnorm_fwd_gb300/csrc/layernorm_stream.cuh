@@ -224,30 +224,38 @@ __device__ __forceinline__ void pairs_load(const float *p, f2_t (&f)[P]) {
 // written by the whole warp.
 template <int P>
 __device__ __forceinline__ void sums_load(uint32_t at, f2_t (&w)[P], f2_t (&b)[P]) {
-    uint32_t u[8], v[8];
-    umma::ld_32x32_x8(at, u);
-    if constexpr (P == 4) umma::ld_32x32_x8(at + 8, v);
-    umma::wait_ld();
+    if constexpr (P == 4) {
+        uint32_t u[16];
+        umma::ld_32x32_x16(at, u);
+        umma::wait_ld();
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-        if constexpr (P == 4) b[i] = f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        else b[i] = f2_make(__uint_as_float(u[4 + 2 * i]), __uint_as_float(u[5 + 2 * i]));
+        for (int i = 0; i < 4; ++i) {
+            w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+            b[i] = f2_make(__uint_as_float(u[8 + 2 * i]), __uint_as_float(u[9 + 2 * i]));
+        }
+    } else {
+        uint32_t u[8];
+        umma::ld_32x32_x8(at, u);
+        umma::wait_ld();
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+            b[i] = f2_make(__uint_as_float(u[4 + 2 * i]), __uint_as_float(u[5 + 2 * i]));
+        }
     }
 }
 template <int P>
 __device__ __forceinline__ void sums_store(uint32_t at, const f2_t (&w)[P], const f2_t (&b)[P]) {
-    uint32_t u[8], v[8];
+    uint32_t u[4 * P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         u[2 * i] = __float_as_uint(f2_lo(w[i]));
         u[2 * i + 1] = __float_as_uint(f2_hi(w[i]));
-        uint32_t *to = P == 4 ? v + 2 * i : u + 4 + 2 * i;
-        to[0] = __float_as_uint(f2_lo(b[i]));
-        to[1] = __float_as_uint(f2_hi(b[i]));
+        u[2 * P + 2 * i] = __float_as_uint(f2_lo(b[i]));
+        u[2 * P + 2 * i + 1] = __float_as_uint(f2_hi(b[i]));
     }
-    umma::st_32x32_x8(at, u);
-    if constexpr (P == 4) umma::st_32x32_x8(at + 8, v);
+    if constexpr (P == 4) umma::st_32x32_x16(at, u);
+    else umma::st_32x32_x8(at, u);
 }
 
 // The rare parts of the kernel are functions of their own, called: inlined, their
@@ -370,6 +378,9 @@ __device__ __noinline__ void ln_close(const LnParams &p, uint32_t sums, uint32_t
         } else {
             sums_store(sums + kSumCols + k * 2 * kE, w, b);
         }
+#pragma unroll
+        for (int j = 0; j < P; ++j) w[j] = 0;            // the next group begins
+        sums_store(sums + k * 2 * kE, w, w);
     }
     if (tid == 0) {
         if (p.ws.state[group] != 0 || (spill && p.ws.flag[lrow])) set_status(p.ws.hdr, kStDouble);
@@ -445,7 +456,6 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     // many for the block's fold; warps w, w + 4, ... share a quarter of the lanes.
     constexpr int kSumCols = 2 * NV * kE;
     uint32_t sums = 0;
-    bool fresh = true;                                   // the next row begins a group
     if constexpr (GRADS) {
         uint32_t *slot = reinterpret_cast<uint32_t *>(smem + kCountOff + 80);
         if (tid < 32) {
@@ -456,6 +466,11 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
         __syncthreads();
         umma::fence_after();
         sums = *slot + (uint32_t((tid >> 5) & 3) << 21) + uint32_t(tid >> 7) * uint32_t(2 * kSumCols);
+        f2_t zero[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) zero[i] = 0;
+#pragma unroll 1
+        for (int k = 0; k < NV; ++k) sums_store(sums + k * 2 * kE, zero, zero);
     }
 
     uint32_t done = 0;                                   // rows through the ring so far
@@ -627,12 +642,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     }
                     if constexpr (GRADS) {
                         f2_t dw[P], db[P];
-                        if (fresh) {
-#pragma unroll
-                            for (int j = 0; j < P; ++j) dw[j] = db[j] = 0;
-                        } else {
-                            sums_load(sums + k * 2 * kE, dw, db);
-                        }
+                        sums_load(sums + k * 2 * kE, dw, db);
 #pragma unroll
                         for (int j = 0; j < P; ++j) {
                             d[kk][j] = f2_mul(d[kk][j], r2);
@@ -663,7 +673,6 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                     }
                 }
                 if constexpr (GRADS) {
-                    fresh = e.tag != 0;
                     if (e.tag) ln_close<E, NV>(p, sums, st, pitch, -mean, rstd, e.lrow, e.tag);
                 }
             }
