@@ -219,7 +219,7 @@ extern "C" int layernorm_finalize(void *workspace, int64_t n_logical_rows, int64
     float *scratch[2] = {ws.scratch_a, ws.scratch_b};
     int flip = 0;
     for (int64_t n = ws.n_blocks;;) {
-        const int64_t groups = (n + kLnTreeBlocks - 1) / kLnTreeBlocks;
+        const int64_t per = in ? kLnTreeNodes : kLnTreeBlocks, groups = (n + per - 1) / per;
         const bool last = groups == 1;
         float *dst = scratch[flip];
         ln_tree_kernel<<<dim3(unsigned(groups), gy), 256, 0, s>>>(

@@ -20,7 +20,8 @@ __global__ void ln_begin_kernel(LnWs ws) {
 }
 
 constexpr int kLnTreeCols = 64;                          // columns of [dweight | dbias] per CTA: 8 lanes, twice 4 each
-constexpr int kLnTreeBlocks = 32;                        // inputs per CTA
+constexpr int kLnTreeBlocks = 32;                        // blocks per CTA in the first pass
+constexpr int kLnTreeNodes = 256;                        // inputs per CTA in the others: 8 per 8 lanes
 
 struct Cols {                        // a lane's columns: c .. c + 3 and c + 32 .. c + 35
     float4 a, b;
@@ -104,26 +105,41 @@ __device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_
 
 // One pass of the pairwise tree with odd carry over n_in inputs (block values in
 // the first pass, then the results of the one before): CTA (g, c) reduces inputs
-// [32 g, 32 g + 32) of 64 columns to one node.  Eight lanes hold the columns of
-// an input, a warp four inputs, which meet by shuffles; the eight warps through
-// shared memory.  All loads of a pass are in flight at once; what bounds the
-// first pass is reading the partials, the others are latency.
+// [m g, m (g + 1)) of 64 columns to one node, m = 32 in the first pass, 256 in the
+// others.  Eight lanes hold the columns of a block (of 8 consecutive inputs), the
+// four of a warp meet by shuffles, the eight warps through shared memory.  All
+// loads of a pass are in flight at once; what bounds the first pass is reading the
+// partials, the others are latency.
 __global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, float *out_w, float *out_b,
                                                       int64_t out_stride, int64_t n_in, float scale) {
     __shared__ float4 val[8][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7, i = tid >> 3;
     const int64_t H2 = 2 * ws.hidden, col = int64_t(blockIdx.y) * kLnTreeCols + part * 4;
-    const int64_t first = int64_t(blockIdx.x) * kLnTreeBlocks;
+    const int64_t first = int64_t(blockIdx.x) * (in ? kLnTreeNodes : kLnTreeBlocks);
     if (!in && !ln_header_ok(ws)) {
         if (tid == 0) set_status(ws.hdr, kStHeader);
         return;
     }
-    const int m = n_in - first < kLnTreeBlocks ? int(n_in - first) : kLnTreeBlocks;
+    // m teams of eight lanes have something; in the first pass one block each
+    const int64_t left = in ? (n_in - first + 7) / 8 : n_in - first;
+    const int m = left < 32 ? int(left) : 32;
     Cols v = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     int bad = 0;
     if (i < m && col < H2) {
         const bool two = col + 32 < H2;
-        if (in) v = load_cols(in + (first + i) * H2 + col, two);
+        if (in) {
+            const int64_t n = n_in - first - i * 8;
+            Cols x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) x[k] = load_cols(in + (first + i * 8 + k) * H2 + col, two);
+#pragma unroll
+            for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+                for (int k = 0; k + s < 8; k += 2 * s)
+                    if (k + s < n) x[k] = add_cols(x[k], x[k + s]);
+            v = x[0];
+        }
         else v = ln_block_value(ws, first + i, col, two, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
                                 blockIdx.y == 0, bad);
     }

@@ -56,12 +56,14 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
 template <class E, int NV, int MODE, bool DROP, bool GRADS>
 int ln_launch_stream(const LnParams &p, const DeviceInfo &d, cudaStream_t stream) {
     const int V = p.hidden / Lane<E>::kE, per = (V + NV - 1) / NV, threads = (per + 31) / 32 * 32;
-    constexpr int kMinB = 2;
     if constexpr (NV * Lane<E>::kE <= 16) {              // wider threads: rows of more than 8192 columns only
-        if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, kMinB>(p, threads, d, stream);
-        if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
+        if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, 2>(p, threads, d, stream);
+        if constexpr (NV * Lane<E>::kE == 16) {
+            if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
+        }
     }
-    return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);
+    if constexpr (NV * Lane<E>::kE >= 16) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);
+    return RMSNORM_ERR_HIDDEN;
 }
 
 template <class E, int NV>
@@ -83,9 +85,16 @@ int ln_run_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
     if (p.hidden <= 256) return ln_run_narrow<E>(p, bwd, grads, stream);
+    // Vectors per thread: two of 8 elements (FP32: four of 4), half of that in the
+    // narrowest rows, whose CTAs would be single warps otherwise (hidden 512, 64 M
+    // elements: backward 162 -> 142 us; at 1024 it loses, 121 -> 128 us), twice that
+    // in the widest.  It depends on the hidden size and type alone, so every call
+    // sums a row in the same order.
     if constexpr (sizeof(E) == 4) {
+        if (p.hidden <= 512) return ln_launch_mode<E, 2>(p, bwd, grads, *d, stream);
         return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
     } else {
+        if (p.hidden <= 512) return ln_launch_mode<E, 1>(p, bwd, grads, *d, stream);
         if (p.hidden <= 8192) return ln_launch_mode<E, 2>(p, bwd, grads, *d, stream);
         return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
     }

@@ -403,7 +403,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                                                                int tmem_cols) {
     constexpr int kE = Lane<E>::kE, P = Lane<E>::kP;
     constexpr bool kFwd = MODE != kLnBwd;
-    constexpr bool kHold = NV * kE <= 16;                // d and dy stay in registers between the two passes
+    // d and dy stay in registers between the two passes (else they are read from the
+    // stage again), where the registers hold them without spills
+    constexpr bool kHold = NV * kE <= 16 && !(GRADS && MAXT == 320);
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);
     float *red = reinterpret_cast<float *>(smem + kRedOff);
@@ -575,7 +577,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 if constexpr (!kFwd) up<E>(lds_v4(st + pitch + k * step), g[kk]);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    d[kk][j] = k == 0 ? f2_add(d[kk][j], neg) : f2_fma(in_row[k], neg, d[kk][j]);
+                    // (a thread's first vector of several is always inside the row)
+                    d[kk][j] = k == 0 && NV > 1 ? f2_add(d[kk][j], neg) : f2_fma(in_row[k], neg, d[kk][j]);
                     m2[j] = k == 0 ? f2_mul(d[kk][j], d[kk][j]) : f2_fma(d[kk][j], d[kk][j], m2[j]);
                     if constexpr (!kFwd) {
                         const f2_t a = f2_mul(g[kk][j], w[k][j]);
