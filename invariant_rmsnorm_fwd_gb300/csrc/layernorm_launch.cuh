@@ -12,11 +12,18 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
     static KernelInfo info;
     int regs = 0;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d.max_smem, &regs)) return rc;
-    // Resident CTAs by registers and threads; then as many stages as their share
-    // of the shared memory holds (fewer CTAs where that leaves less than `least`).
-    // Backward, row i + 1 arrives while row i is in use and the stage of row
-    // i - 1 is being refilled: three stages at least.
-    const int row = NV * threads * 16, least = MODE == kLnBwd ? 3 : 2;   // a staged row, padded to whole vectors of the CTA
+    // Resident CTAs by registers and threads, then as many stages as their share of
+    // the shared memory holds; fewer CTAs where that leaves less than `want`.
+    // Backward, row i + 1 arrives while row i is in use and the stage of row i - 1
+    // is being refilled: three stages at least, and more of them are not worth
+    // warps (residual-add backward of 64 M bf16 elements, three staged tensors,
+    // 3 / 4 stages wanted: hidden 5120 165 / 218 us, 1024 169 / 176; 6 wanted:
+    // hidden 4096 225 against 171).  Forward has more warps than it needs: 5 wanted
+    // against 3 take the FP32 forward of 1024 columns from 60 to 53 us, the
+    // residual-add one in bf16 from 130 to 101, and change nothing else by 2 %;
+    // 7 wanted cost 40 % at hidden 5120.
+    const int row = NV * threads * 16;                   // a staged row, padded to whole vectors of the CTA
+    const int least = MODE == kLnBwd ? 3 : 2, want = MODE == kLnBwd ? 3 : 5;
     int nt = MODE == kLnFwd ? 1 : MODE == kLnAdd ? 2 : p.res ? 3 : 2;
     if (MODE == kLnBwd && nt == 3 && kFixedBytes + least * nt * row > d.max_smem) nt = 2;
     // tensor memory of a CTA: the sums and the fold of its warps, four side by side
@@ -35,7 +42,7 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
         int room = kSmemPerSm / ctas - kSmemPerCta;
         if (room > d.max_smem) room = d.max_smem;
         S = (room - kFixedBytes) / (nt * row);
-        if (S >= least + 1 || (ctas == 1 && S >= least)) break;
+        if (S >= want || (ctas == 1 && S >= least)) break;
     }
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
     if (S > kMaxStages) S = kMaxStages;

@@ -258,15 +258,12 @@ __device__ __forceinline__ void sums_store(uint32_t at, const f2_t (&w)[P], cons
     else umma::st_32x32_x8(at, u);
 }
 
-// The rare parts of the kernel are functions of their own, called: inlined, their
-// registers would count in the row loop's.
-
 // Writes the CTA's list number `turn` and returns its length, -1 behind the last
 // one.  The CTA's share of positions: with parameter gradients consecutive slots
 // of the plan (blocks stay together); else position q is slot q gridDim + blockIdx,
 // so that padding, which comes in long runs, falls on every CTA alike.
 template <class E, bool GRADS>
-__device__ __noinline__ int ln_list(const LnParams &p, uint8_t *smem, int turn) {
+__device__ __forceinline__ int ln_list(const LnParams &p, uint8_t *smem, int turn) {
     volatile int *count = reinterpret_cast<volatile int *>(smem + kCountOff);
     LnEntry *list = reinterpret_cast<LnEntry *>(smem + kListOff);
     const int tid = threadIdx.x, T = blockDim.x, warps = T >> 5;
@@ -334,6 +331,13 @@ __device__ __noinline__ int ln_list(const LnParams &p, uint8_t *smem, int turn) 
         __syncthreads();
     }
     return n;
+}
+
+// With parameter gradients the rare parts are functions of their own, called:
+// inlined, their registers would count in the row loop's.
+template <class E>
+__device__ __noinline__ int ln_list_called(const LnParams &p, uint8_t *smem, int turn) {
+    return ln_list<E, true>(p, smem, turn);
 }
 
 // Ends a group (its sums are in tensor memory at `sums`, the block's fold behind
@@ -481,7 +485,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
 
 #pragma unroll 1
     for (int lists = 0; !dead; ++lists) {
-        const int n = ln_list<E, GRADS>(p, smem, lists);
+        int n;
+        if constexpr (GRADS) n = ln_list_called<E>(p, smem, lists);
+        else n = ln_list<E, false>(p, smem, lists);
         if (n < 0) break;
         if (n == 0) continue;
 
