@@ -1,5 +1,5 @@
 // What the kernels of the batch-invariant layer norm (sm_103a) share: the
-// workspace, the parameters of a call, vectors of 8 elements.
+// workspace and the parameters of a call.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -82,72 +82,5 @@ struct LnParams {
     int32_t share, share_rest;       // streaming kernel: units of a CTA; the first share_rest CTAs have one more
     LnWs ws;
 };
-
-// ----------------------------------------------------------------- vectors of 8 elements
-
-template <class E>
-struct Vec;                          // packed vector of 8 elements of E
-template <>
-struct Vec<__nv_bfloat16> { uint4 q; };
-template <>
-struct Vec<__half> { uint4 q; };
-template <>
-struct Vec<float> { uint4 q, r; };
-
-template <class E>
-__device__ __forceinline__ Vec<E> vload(const void *base, int64_t elem) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const E *>(base) + elem);
-    Vec<E> v;
-    v.q = p[0];
-    if constexpr (sizeof(E) == 4) v.r = p[1];
-    return v;
-}
-template <class E>
-__device__ __forceinline__ void vstore(void *base, int64_t elem, const Vec<E> &v) {
-    uint4 *p = reinterpret_cast<uint4 *>(static_cast<E *>(base) + elem);
-    p[0] = v.q;
-    if constexpr (sizeof(E) == 4) p[1] = v.r;
-}
-
-__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16> &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.q.x, v.q.y, v.q.z, v.q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void unpack(const Vec<__half> &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.q.x, v.q.y, v.q.z, v.q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
-    }
-}
-__device__ __forceinline__ void unpack(const Vec<float> &v, float (&f)[8]) {
-    f[0] = __uint_as_float(v.q.x); f[1] = __uint_as_float(v.q.y); f[2] = __uint_as_float(v.q.z); f[3] = __uint_as_float(v.q.w);
-    f[4] = __uint_as_float(v.r.x); f[5] = __uint_as_float(v.r.y); f[6] = __uint_as_float(v.r.z); f[7] = __uint_as_float(v.r.w);
-}
-__device__ __forceinline__ void pack(const float (&f)[8], Vec<__nv_bfloat16> &v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f2_to_bf16x2(f2_make(f[2 * i], f[2 * i + 1]));
-    v.q = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void pack(const float (&f)[8], Vec<__half> &v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    v.q = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void pack(const float (&f)[8], Vec<float> &v) {
-    v.q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    v.r = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-}
 
 }  // namespace rbi
