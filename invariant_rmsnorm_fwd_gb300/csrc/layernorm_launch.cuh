@@ -63,9 +63,13 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
 template <class E, int NV, int MODE, bool DROP, bool GRADS>
 int ln_launch_stream(const LnParams &p, const DeviceInfo &d, cudaStream_t stream) {
     const int V = p.hidden / Lane<E>::kE, per = (V + NV - 1) / NV, threads = (per + 31) / 32 * 32;
+    // Two CTAs of up to 320 threads fit an SM at 96 registers a thread; FP32's
+    // residual add with dropout needs 119 and is faster alone than spilled (hidden
+    // 5120, 32 M elements: 92 against 112 us).
+    constexpr bool kPair320 = NV * Lane<E>::kE == 16 && !(sizeof(E) == 4 && MODE == kLnAdd && DROP);
     if constexpr (NV * Lane<E>::kE <= 16) {              // wider threads: rows of more than 8192 columns only
         if (threads <= 256) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 256, 2>(p, threads, d, stream);
-        if constexpr (NV * Lane<E>::kE == 16) {
+        if constexpr (kPair320) {
             if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
         }
     }
