@@ -35,7 +35,7 @@ struct KernelInfo {
 };
 
 // Launches the rows of one call for element type E (ln_rows_*.cu instantiate it).
-// Rows of at most 256 columns take ln_run_narrow (ln_narrow_*.cu).
+// Rows of at most 512 columns take ln_run_narrow (ln_narrow_*.cu).
 template <class E>
 int ln_run_narrow(const LnParams &p, bool bwd, bool grads, cudaStream_t stream);
 template <class E>

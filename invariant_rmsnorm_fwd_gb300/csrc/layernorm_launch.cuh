@@ -73,8 +73,7 @@ int ln_launch_stream(const LnParams &p, const DeviceInfo &d, cudaStream_t stream
             if (threads <= 320) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 320, 2>(p, threads, d, stream);
         }
     }
-    if constexpr (NV * Lane<E>::kE >= 16) return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);
-    return RMSNORM_ERR_HIDDEN;
+    return ln_launch_stream_t<E, NV, MODE, DROP, GRADS, 512, 1>(p, threads, d, stream);
 }
 
 template <class E, int NV>
@@ -95,17 +94,16 @@ template <class E>
 int ln_run_rows(const LnParams &p, bool bwd, bool grads, cudaStream_t stream) {
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
-    if (p.hidden <= 256) return ln_run_narrow<E>(p, bwd, grads, stream);
-    // Vectors per thread: two of 8 elements (FP32: four of 4), half of that in the
-    // narrowest rows, whose CTAs would be single warps otherwise (hidden 512, 64 M
-    // elements: backward 162 -> 142 us; at 1024 it loses, 121 -> 128 us), twice that
-    // in the widest.  It depends on the hidden size and type alone, so every call
+    if (p.hidden <= 512) return ln_run_narrow<E>(p, bwd, grads, stream);
+    // Vectors per thread: two of 8 elements (FP32: four of 4), in the widest rows twice
+    // that.  Rows of up to 512 columns are teams of lanes: a CTA of one or two warps
+    // pays its barrier for too few columns (64 M bf16 elements, this kernel against
+    // teams: hidden 512 forward 64 / 50 us, backward 138 / 98; hidden 264 118 / 73
+    // and 235 / 147).  The rule looks at hidden size and type alone, so every call
     // sums a row in the same order.
     if constexpr (sizeof(E) == 4) {
-        if (p.hidden <= 512) return ln_launch_mode<E, 2>(p, bwd, grads, *d, stream);
         return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
     } else {
-        if (p.hidden <= 512) return ln_launch_mode<E, 1>(p, bwd, grads, *d, stream);
         if (p.hidden <= 8192) return ln_launch_mode<E, 2>(p, bwd, grads, *d, stream);
         return ln_launch_mode<E, 4>(p, bwd, grads, *d, stream);
     }

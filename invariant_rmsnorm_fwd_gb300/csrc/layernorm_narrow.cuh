@@ -1,17 +1,22 @@
-// Row kernel of the layer norm for rows of at most 256 columns (per-head norms).
+// Row kernel of the layer norm for rows of at most 512 columns (per-head norms).
 //
-// A row is held by a team of P lanes, 8 columns a lane, so a warp works on 32 / P
-// rows at once and a row's sums need only shuffles.  A team takes the 8 slots of
-// one group one after the other (in logical order where parameter gradients are
-// wanted) and goes on to its next group; each lane keeps the next kDepth rows'
-// pieces on their way into shared-memory places of its own (cp.async), across
-// groups, and reads the slots of a group while it works on the one before, so
-// memory does not wait for a group's end.  Empty slots are computed as zeros and
-// store nothing, so the shuffles of a warp stay together.
+// A row is held by a team of P lanes, 8 columns a lane (16 above 256 columns), so a
+// warp works on 32 / P rows at once and a row's sums need only shuffles.  A team
+// takes the 8 slots of one group one after the other (in logical order where
+// parameter gradients are wanted) and goes on to its next group; each lane keeps
+// the next kDepth rows' pieces on their way into shared-memory places of its own
+// (cp.async), across groups, and reads the slots of a group while it works on the
+// one before, so memory does not wait for a group's end.  Empty slots are computed
+// as zeros and store nothing, so the shuffles of a warp stay together.
 //
-// Parameter gradients: a lane's columns add up in its registers over the group;
-// the groups of a block are in one CTA, which folds them through shared memory
-// (from the first to the last) and writes one partial per block.
+// Parameter gradients: a lane's columns add up over the group; the groups of a
+// block are in one CTA, which folds them through shared memory (from the first to
+// the last) and writes one partial per block.
+//
+// Forward, memory bounds it (hidden 128, 64 M bf16 elements: 46 us, 0.87 of the copy
+// rate); backward, issue does: a row's 16-byte piece costs a lane its share of five
+// shuffles for each of four sums next to the arithmetic (102 us, 0.58).  Widths
+// between powers of two leave lanes idle (hidden 72: 0.6 and 0.37).
 #pragma once
 #include "host.cuh"
 #include "layernorm_host.cuh"
@@ -75,10 +80,12 @@ __device__ __forceinline__ float team_sum(float v) {
 }
 
 constexpr int kNarrowThreads = 256;
-constexpr int kDepth = 4;                                // rows of a team on their way
 
-template <class E, int MODE, bool RES>
-constexpr int kNarrowPieces = (MODE == kLnFwd ? 1 : 2 + (RES ? 1 : 0)) * Oct<E>::kQ;   // 16-byte pieces of a lane's row
+// NO: octets of columns a lane holds (l, l + P).
+template <class E, int NO, int MODE, bool RES>
+constexpr int kNarrowPieces = (MODE == kLnFwd ? 1 : 2 + (RES ? 1 : 0)) * Oct<E>::kQ * NO;   // 16-byte pieces of a lane's row
+template <int NO>
+constexpr int kNarrowDepth = 4 / NO;                     // rows of a team on their way
 
 // The slots of a team's group: slot j belongs to lane j % P.
 template <int P>
@@ -172,16 +179,17 @@ __device__ __forceinline__ void team_slots(const LnParams &p, int64_t group, con
 }
 
 // RES: dres is added (kLnBwd).
-template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES, int MINB>
-__global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const __grid_constant__ LnParams p) {
+template <class E, int P, int NO, int MODE, bool DROP, bool GRADS, bool RES>
+__global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_kernel(const __grid_constant__ LnParams p) {
     constexpr bool kFwd = MODE != kLnBwd, kRes = MODE == kLnAdd || RES;
-    constexpr int kPieces = kNarrowPieces<E, MODE, RES>, kQ = Oct<E>::kQ, kTeams = kNarrowThreads / P;
+    constexpr int kPieces = kNarrowPieces<E, NO, MODE, RES>, kDepth = kNarrowDepth<NO>, kQ = Oct<E>::kQ;
+    constexpr int kTeams = kNarrowThreads / P, kCols = 8 * P * NO, kPiece = kNarrowThreads * 16;
     constexpr int kOwn = TeamSlots<P>::kOwn;
     extern __shared__ __align__(128) uint8_t smem[];     // [kDepth][kPieces][256 threads], then the block sums
-    float *sums = reinterpret_cast<float *>(smem + kDepth * kPieces * kNarrowThreads * 16);   // [team][dweight, dbias][8 P]
+    float *sums = reinterpret_cast<float *>(smem + kDepth * kPieces * kPiece);   // [team][dweight, dbias][kCols]
     const int tid = threadIdx.x, team = tid / P, l = tid % P, V = p.hidden >> 3;
     const uint32_t mine = smem_addr(smem) + uint32_t(tid) * 16u;
-    const bool col = l < V;                              // this lane has columns
+    bool col[NO];                                        // this lane has the columns of octet l + k P
     if constexpr (GRADS) {
         if (!ln_header_ok(p.ws)) {
             if (tid == 0) set_status(p.ws.hdr, kStHeader);
@@ -191,30 +199,69 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
     const DropKey key = DROP ? drop_key(p.drop) : DropKey{0, 0, 0, 0};
     const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
     const int64_t stride = int64_t(gridDim.x) * kTeams;
-    f2_t w[4], b[4], dw[4], db[4];
+    f2_t w[NO][4], b[kFwd ? NO : 1][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = b[j] = dw[j] = db[j] = 0;
-    if (col) {
-        oct_param<E>(p.w, p.params_f32, l, 1.f, w);
-        if constexpr (kFwd) oct_param<E>(p.b, p.params_f32, l, 0.f, b);
+    for (int k = 0; k < NO; ++k) {
+        col[k] = l + k * P < V;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[k][j] = 0;
+            if constexpr (kFwd) b[k][j] = 0;
+        }
+        if (col[k]) {
+            oct_param<E>(p.w, p.params_f32, l + k * P, 1.f, w[k]);
+            if constexpr (kFwd) oct_param<E>(p.b, p.params_f32, l + k * P, 0.f, b[k]);
+        }
+    }
+    // The sums of a lane's columns over its group: in registers, or in tensor memory
+    // (16 columns an octet; warps w and w + 4 share a quarter of the lanes) where
+    // dropout or dres need the registers (64 M bf16 elements, registers / tensor
+    // memory: hidden 128 backward 103 / 108 us, with both 168 / 144; hidden 512
+    // 98 / 102, with both 189 / 160).
+    constexpr bool kTmem = GRADS && (DROP || RES), kRegs = GRADS && !kTmem;
+    constexpr uint32_t kTmemCols = 32 * NO;
+    uint32_t acc = 0;
+    f2_t rw[kRegs ? NO : 1][4] = {}, rb[kRegs ? NO : 1][4] = {};
+    if constexpr (kTmem) {
+        __shared__ uint32_t tmem;
+        if (tid < 32) {
+            umma::tmem_alloc(&tmem, kTmemCols);
+            umma::tmem_relinquish();
+        }
+        umma::fence_before();
+        __syncthreads();
+        umma::fence_after();
+        acc = tmem + (uint32_t((tid >> 5) & 3) << 21) + uint32_t(tid >> 7) * (16 * NO);
+        const f2_t zero[4] = {};
+#pragma unroll
+        for (int k = 0; k < NO; ++k) sums_store(acc + k * 16, zero, zero);
     }
     TeamSlots<P> cur, nxt;
-    int64_t off[kDepth];                                 // element offset of this lane's piece of the rows on their way
     // Requests row j of the group into place j % kDepth.
     auto request = [&](const TeamSlots<P> &s, int j) {
         const int64_t at = __shfl_sync(kFull, s.off[j / P], j % P, P) + l * 8;
-        off[j % kDepth] = at;
-        const uint32_t bytes = ((s.on >> j) & 1) && col ? 16u : 0u;
-        const uint32_t to = mine + uint32_t(j % kDepth) * uint32_t(kPieces * kNarrowThreads * 16);
-        const int64_t from = bytes ? at : 0;
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-            cp_async_zfill(to + q * (kNarrowThreads * 16), static_cast<const E *>(p.x) + from + q * 4, bytes);
-            if constexpr (!kFwd) cp_async_zfill(to + (kQ + q) * (kNarrowThreads * 16), static_cast<const E *>(p.dy) + from + q * 4, bytes);
-            if constexpr (kRes)
-                cp_async_zfill(to + ((kFwd ? 1 : 2) * kQ + q) * (kNarrowThreads * 16), static_cast<const E *>(p.res) + from + q * 4, bytes);
+        for (int k = 0; k < NO; ++k) {
+            const uint32_t bytes = ((s.on >> j) & 1) && col[k] ? 16u : 0u;
+            const uint32_t to = mine + uint32_t((j % kDepth) * kPieces + k) * uint32_t(kPiece);
+            const int64_t from = bytes ? at + k * P * 8 : 0;
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                cp_async_zfill(to + q * NO * kPiece, static_cast<const E *>(p.x) + from + q * 4, bytes);
+                if constexpr (!kFwd) cp_async_zfill(to + (kQ + q) * NO * kPiece, static_cast<const E *>(p.dy) + from + q * 4, bytes);
+                if constexpr (kRes)
+                    cp_async_zfill(to + ((kFwd ? 1 : 2) * kQ + q) * NO * kPiece, static_cast<const E *>(p.res) + from + q * 4, bytes);
+            }
         }
         cp_async_commit();
+    };
+    // A lane's octet k of tensor t (0 x, 1 dy, last the residual) of the row in place j % kDepth.
+    auto fetch = [&](int j, int t, int k) {
+        const uint32_t at = mine + uint32_t((j % kDepth) * kPieces + t * kQ * NO + k) * uint32_t(kPiece);
+        Oct<E> v;
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) ld_shared_vec(at + q * NO * kPiece, v.q[q]);
+        return v;
     };
     int64_t unit = int64_t(blockIdx.x) * kTeams;         // first group of this CTA's teams
     {
@@ -233,45 +280,50 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
 #pragma unroll
         for (int j0 = 0; j0 < kGroupRows; ++j0) {
             cp_async_wait<kDepth - 1>();                 // row j0 has arrived (in this lane's own places)
-            const uint32_t at = mine + uint32_t(j0 % kDepth) * uint32_t(kPieces * kNarrowThreads * 16);
-            Oct<E> xo, go, ro;
+            Oct<E> xo[NO], go[NO];
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                ld_shared_vec(at + q * (kNarrowThreads * 16), xo.q[q]);
-                if constexpr (!kFwd) ld_shared_vec(at + (kQ + q) * (kNarrowThreads * 16), go.q[q]);
-                if constexpr (kRes) ld_shared_vec(at + ((kFwd ? 1 : 2) * kQ + q) * (kNarrowThreads * 16), ro.q[q]);
+            for (int k = 0; k < NO; ++k) {
+                xo[k] = fetch(j0, 0, k);
+                if constexpr (!kFwd) go[k] = fetch(j0, 1, k);
             }
-            const int64_t here = off[j0 % kDepth];
-            const bool row = (cur.on >> j0) & 1, st = row && col;
+            const int64_t here = __shfl_sync(kFull, cur.off[j0 / P], j0 % P, P) + l * 8;
+            const bool row = (cur.on >> j0) & 1;
             uint32_t lrow = 0;
             if constexpr (DROP || GRADS) lrow = __shfl_sync(kFull, cur.row[j0 / P], j0 % P, P);
-            f2_t x[4], g[4];
-            oct_up<E>(xo, x);
-            if constexpr (MODE == kLnAdd) {
-                f2_t q[4];
-                oct_up<E>(ro, q);
-                if constexpr (DROP) {
-                    const uint4 u = philox4x32(uint32_t(l), lrow, key);
-                    const uint32_t words[4] = {u.x, u.y, u.z, u.w};
-                    drop_add_pairs(x, q, words, drop_rule(p.drop));
-                } else {
+            f2_t x[NO][4], g[NO][4], t;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = f2_add(x[j], q[j]);
+            for (int k = 0; k < NO; ++k) {
+                oct_up<E>(xo[k], x[k]);
+                if constexpr (MODE == kLnAdd) {
+                    f2_t q[4];
+                    oct_up<E>(fetch(j0, 1, k), q);
+                    if constexpr (DROP) {
+                        const uint4 u = philox4x32(uint32_t(l + k * P), lrow, key);
+                        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+                        drop_add_pairs(x[k], q, words, drop_rule(p.drop));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[k][j] = f2_add(x[k][j], q[j]);
+                    }
+                    if (row && col[k]) oct_store<E>(p.out2, here + k * P * 8, x[k]);
+                    if constexpr (sizeof(E) == 2) {      // the norm takes the stored h
+                        const uint4 h = down<E>(x[k]);
+                        up<E>(h, x[k]);
+                    }
                 }
-                if (st) oct_store<E>(p.out2, here, x);
-                if constexpr (sizeof(E) == 2) {          // the norm takes the stored h
-                    const uint4 h = down<E>(x);
-                    up<E>(h, x);
-                }
+                const f2_t s = f2_add(f2_add(x[k][0], x[k][1]), f2_add(x[k][2], x[k][3]));
+                t = k == 0 ? s : f2_add(t, s);
             }
-            f2_t t = f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3]));
             const float mean = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(t), f2_hi(t))), p.inv_h);
-            const f2_t neg = col ? f2_both(-mean) : 0;
             f2_t m2, sa, sc;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = f2_add(x[j], neg);
-                m2 = j == 0 ? f2_mul(x[0], x[0]) : f2_fma(x[j], x[j], m2);
+            for (int k = 0; k < NO; ++k) {
+                const f2_t neg = col[k] ? f2_both(-mean) : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[k][j] = f2_add(x[k][j], neg);
+                    m2 = k + j == 0 ? f2_mul(x[0][0], x[0][0]) : f2_fma(x[k][j], x[k][j], m2);
+                }
             }
             if constexpr (kFwd) {
                 const float var = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(m2), f2_hi(m2))), p.inv_h);
@@ -282,16 +334,22 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 }
                 const f2_t r2 = f2_both(rstd);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = f2_fma(f2_mul(x[j], r2), w[j], b[j]);
-                if (st) oct_store<E>(p.out, here, x);
+                for (int k = 0; k < NO; ++k) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[k][j] = f2_fma(f2_mul(x[k][j], r2), w[k][j], b[k][j]);
+                    if (row && col[k]) oct_store<E>(p.out, here + k * P * 8, x[k]);
+                }
             } else {
                 // the three sums of the row side by side (independent shuffles)
-                oct_up<E>(go, g);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f2_t a = f2_mul(g[j], w[j]);
-                    sa = j == 0 ? a : f2_add(sa, a);
-                    sc = j == 0 ? f2_mul(a, x[0]) : f2_fma(a, x[j], sc);
+                for (int k = 0; k < NO; ++k) {
+                    oct_up<E>(go[k], g[k]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f2_t a = f2_mul(g[k][j], w[k][j]);
+                        sa = k + j == 0 ? a : f2_add(sa, a);
+                        sc = k + j == 0 ? f2_mul(a, x[0][0]) : f2_fma(a, x[k][j], sc);
+                    }
                 }
                 const float var = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(m2), f2_hi(m2))), p.inv_h);
                 const float ma = __fmul_rn(team_sum<P>(__fadd_rn(f2_lo(sa), f2_hi(sa))), p.inv_h);
@@ -300,44 +358,52 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
                 const float rstd = row ? rsqrtf(__fadd_rn(var, p.eps)) : 0.f;
                 const f2_t r2 = f2_both(rstd);
                 // s (a - mean(a) - xhat mean(a xhat)) as a s + (d c1 + c0)
+                if constexpr (kTmem) umma::wait_st();
                 const float s1 = __fmul_rn(rstd, p.grad_scale), mc = __fmul_rn(md, rstd);
                 const f2_t s2 = f2_both(s1), c0 = f2_both(-__fmul_rn(s1, ma)), c1 = f2_both(-__fmul_rn(s1, __fmul_rn(mc, rstd)));
-                f2_t o[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    o[j] = f2_fma(f2_mul(g[j], w[j]), s2, f2_fma(x[j], c1, c0));
+                for (int k = 0; k < NO; ++k) {
+                    f2_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[j] = f2_fma(f2_mul(g[k][j], w[k][j]), s2, f2_fma(x[k][j], c1, c0));
+                    }
                     if constexpr (GRADS) {
-                        x[j] = f2_mul(x[j], r2);
-                        dw[j] = f2_fma(g[j], x[j], dw[j]);
-                        db[j] = f2_add(db[j], g[j]);
+                        f2_t (&dw)[4] = rw[kRegs ? k : 0], (&db)[4] = rb[kRegs ? k : 0];
+                        if constexpr (kTmem) sums_load(acc + k * 16, dw, db);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[k][j] = f2_mul(x[k][j], r2);
+                            dw[j] = f2_fma(g[k][j], x[k][j], dw[j]);
+                            db[j] = f2_add(db[j], g[k][j]);
+                        }
+                        if constexpr (kTmem) sums_store(acc + k * 16, dw, db);
+                        if (row && !cur.partial && col[k]) {   // a row of a cut group
+                            float *sp = p.ws.spill + int64_t(lrow) * 2 * p.hidden + (l + k * P) * 8;
+                            st_global_f2x4(sp, x[k]);
+                            st_global_f2x4(sp + p.hidden, g[k]);
+                        }
+                    }
+                    if constexpr (RES) {
+                        f2_t q[4];
+                        oct_up<E>(fetch(j0, 2, k), q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], q[j]);
+                    }
+                    if (row && col[k] && (!GRADS || p.out)) {
+                        oct_store<E>(p.out, here + k * P * 8, o);
+                        if constexpr (DROP) {
+                            const uint4 u = philox4x32(uint32_t(l + k * P), lrow, key);
+                            const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+                            drop_pairs(o, words, drop_rule(p.drop));
+                            oct_store<E>(p.out2, here + k * P * 8, o);
+                        }
                     }
                 }
                 if constexpr (GRADS) {
-                    if (row && !cur.partial) {           // a row of a cut group
-                        if (col) {
-                            float *sp = p.ws.spill + int64_t(lrow) * 2 * p.hidden + l * 8;
-                            st_global_f2x4(sp, x);
-                            st_global_f2x4(sp + p.hidden, g);
-                        }
-                        if (l == 0) {
-                            if (p.ws.flag[lrow] || p.ws.state[lrow / kGroupRows] != 0) set_status(p.ws.hdr, kStDouble);
-                            p.ws.flag[lrow] = 1;
-                        }
-                    }
-                }
-                if constexpr (RES) {
-                    f2_t q[4];
-                    oct_up<E>(ro, q);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], q[j]);
-                }
-                if (st && (!GRADS || p.out)) {
-                    oct_store<E>(p.out, here, o);
-                    if constexpr (DROP) {
-                        const uint4 u = philox4x32(uint32_t(l), lrow, key);
-                        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
-                        drop_pairs(o, words, drop_rule(p.drop));
-                        oct_store<E>(p.out2, here, o);
+                    if (row && !cur.partial && l == 0) {
+                        if (p.ws.flag[lrow] || p.ws.state[lrow / kGroupRows] != 0) set_status(p.ws.hdr, kStDouble);
+                        p.ws.flag[lrow] = 1;
                     }
                 }
             }
@@ -361,16 +427,23 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
             }
         }
         if constexpr (GRADS) {
-            float *to = sums + team * 16 * P + l * 8;
-            pairs_store(to, dw);
-            pairs_store(to + 8 * P, db);
-            if (cur.kind == kItemQuarters && cur.partial && col) {   // groups of a cut block stand alone
-                float *dst = p.ws.partial + (int64_t(cur.block) * kGroups + cur.slot0 / kGroupRows) * 2 * p.hidden + l * 8;
-                st_global_f2x4(dst, dw);
-                st_global_f2x4(dst + p.hidden, db);
-            }
+            if constexpr (kTmem) umma::wait_st();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dw[j] = db[j] = 0;
+            for (int k = 0; k < NO; ++k) {
+                f2_t (&dw)[4] = rw[kRegs ? k : 0], (&db)[4] = rb[kRegs ? k : 0];
+                if constexpr (kTmem) sums_load(acc + k * 16, dw, db);
+                float *to = sums + team * 2 * kCols + (l + k * P) * 8;
+                pairs_store(to, dw);
+                pairs_store(to + kCols, db);
+                if (cur.kind == kItemQuarters && cur.partial && col[k]) {   // groups of a cut block stand alone
+                    float *dst = p.ws.partial + (int64_t(cur.block) * kGroups + cur.slot0 / kGroupRows) * 2 * p.hidden + (l + k * P) * 8;
+                    st_global_f2x4(dst, dw);
+                    st_global_f2x4(dst + p.hidden, db);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dw[j] = db[j] = 0;
+                if constexpr (kTmem) sums_store(acc + k * 16, dw, db);
+            }
             const int64_t rows = p.ws.n_rows - int64_t(cur.block) * kBlockRows;
             const int n_groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
             if (cur.partial && l == 0 && cur.slot0 < rows && cur.block >= 0 && cur.block < p.ws.n_blocks) {
@@ -381,30 +454,38 @@ __global__ void __launch_bounds__(kNarrowThreads, MINB) ln_narrow_kernel(const _
             }
             __syncthreads();
             if (cur.kind == kItemWhole && cur.block >= 0 && cur.block < p.ws.n_blocks) {
-                // lane (team of the block, l): two of the 16 P sums of the block
-                const int at = (cur.slot0 / kGroupRows * P + l) * 2, half = at / (8 * P), c = at - half * 8 * P;
-                const f2_t *from = reinterpret_cast<const f2_t *>(sums + (team / kGroups) * kGroups * 16 * P + at);
-                f2_t v[kGroups];
+                // lane (team of the block, l): NO pairs of the block's 2 kCols sums
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) v[j] = from[j * 8 * P];
+                for (int k = 0; k < NO; ++k) {
+                    const int at = ((k * kGroups + cur.slot0 / kGroupRows) * P + l) * 2, half = at / kCols, c = at - half * kCols;
+                    const f2_t *from = reinterpret_cast<const f2_t *>(sums + (team / kGroups) * kGroups * 2 * kCols + at);
+                    f2_t v[kGroups];
 #pragma unroll
-                for (int j = 1; j < kGroups; ++j)
-                    if (j < n_groups) v[0] = f2_add(v[0], v[j]);
-                if (c < p.hidden)
-                    *reinterpret_cast<f2_t *>(p.ws.partial + int64_t(cur.block) * kGroups * 2 * p.hidden + half * p.hidden + c) = v[0];
+                    for (int j = 0; j < kGroups; ++j) v[j] = from[j * kCols];
+#pragma unroll
+                    for (int j = 1; j < kGroups; ++j)
+                        if (j < n_groups) v[0] = f2_add(v[0], v[j]);
+                    if (c < p.hidden)
+                        *reinterpret_cast<f2_t *>(p.ws.partial + int64_t(cur.block) * kGroups * 2 * p.hidden + half * p.hidden + c) = v[0];
+                }
             }
             __syncthreads();                             // the sums are read
         }
         cur = nxt;
     }
     cp_async_wait<0>();
+    if constexpr (kTmem) {
+        umma::fence_before();
+        __syncthreads();
+        umma::fence_after();
+        if (tid < 32) umma::tmem_dealloc(acc, kTmemCols);
+    }
 }
 
-template <class E, int P, int MODE, bool DROP, bool GRADS, bool RES>
+template <class E, int P, int NO, int MODE, bool DROP, bool GRADS, bool RES>
 int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
-    constexpr int kMinB = 3;
-    auto kern = ln_narrow_kernel<E, P, MODE, DROP, GRADS, RES, kMinB>;
-    constexpr int smem = kDepth * kNarrowPieces<E, MODE, RES> * kNarrowThreads * 16 + (GRADS ? kNarrowThreads * 64 : 0);
+    auto kern = ln_narrow_kernel<E, P, NO, MODE, DROP, GRADS, RES>;
+    constexpr int smem = kNarrowDepth<NO> * kNarrowPieces<E, NO, MODE, RES> * kNarrowThreads * 16 + (GRADS ? kNarrowThreads * 64 * NO : 0);
     DeviceInfo *d = nullptr;
     if (int rc = device_info(&d)) return rc;
     const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
@@ -428,10 +509,11 @@ int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
 // Lanes per row: the next power of two of hidden / 8, at least 4.
 template <class E, int MODE, bool DROP, bool GRADS, bool RES>
 int ln_launch_narrow(const LnParams &p, cudaStream_t s) {
-    if (p.hidden <= 32) return ln_launch_narrow_t<E, 4, MODE, DROP, GRADS, RES>(p, s);
-    if (p.hidden <= 64) return ln_launch_narrow_t<E, 8, MODE, DROP, GRADS, RES>(p, s);
-    if (p.hidden <= 128) return ln_launch_narrow_t<E, 16, MODE, DROP, GRADS, RES>(p, s);
-    return ln_launch_narrow_t<E, 32, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 32) return ln_launch_narrow_t<E, 4, 1, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 64) return ln_launch_narrow_t<E, 8, 1, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 128) return ln_launch_narrow_t<E, 16, 1, MODE, DROP, GRADS, RES>(p, s);
+    if (p.hidden <= 256) return ln_launch_narrow_t<E, 32, 1, MODE, DROP, GRADS, RES>(p, s);
+    return ln_launch_narrow_t<E, 32, 2, MODE, DROP, GRADS, RES>(p, s);
 }
 
 template <class E>

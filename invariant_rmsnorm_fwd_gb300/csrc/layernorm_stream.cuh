@@ -1,4 +1,4 @@
-// Streaming row kernel of the layer norm for rows of more than 256 columns.
+// Streaming row kernel of the layer norm for rows of more than 512 columns.
 //
 // A CTA owns a contiguous share of the call (rows, or 8-row groups of plan
 // items) and keeps all columns of a row: thread i holds the 16-byte vectors
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 if constexpr (!kFwd) up<E>(lds_v4(st + pitch + k * step), g[kk]);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    // (a thread's first vector of several is always inside the row)
-                    d[kk][j] = k == 0 && NV > 1 ? f2_add(d[kk][j], neg) : f2_fma(in_row[k], neg, d[kk][j]);
+                    // (a thread's first vector is always inside the row)
+                    d[kk][j] = k == 0 ? f2_add(d[kk][j], neg) : f2_fma(in_row[k], neg, d[kk][j]);
                     m2[j] = k == 0 ? f2_mul(d[kk][j], d[kk][j]) : f2_fma(d[kk][j], d[kk][j], m2[j]);
                     if constexpr (!kFwd) {
                         const f2_t a = f2_mul(g[kk][j], w[k][j]);
