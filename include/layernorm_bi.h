@@ -38,7 +38,8 @@
  *
  * Supported hidden sizes: multiples of 8 up to 16384 for 16-bit types, up to
  * 8192 for FP32; dropout alone: multiples of 8 up to 2^20.  Data pointers are
- * 16-byte aligned, layout->token_stride is a multiple of 8.
+ * 16-byte aligned, mean, rstd, the ids and the plan to 4 bytes; layout->token_stride
+ * is a multiple of 8.
  */
 #ifndef LAYERNORM_BI_H
 #define LAYERNORM_BI_H

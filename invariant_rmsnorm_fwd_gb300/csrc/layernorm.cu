@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxHidden16 = 16384, kMaxHidden32 = 8192, kMaxHiddenDrop = int64_t(1) << 20;
 
 bool bad_align(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool bad_align4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 int ln_check(const rmsnorm_layout_t *L, int64_t H, int64_t max_hidden) {
     if (H < 8 || H % 8 != 0 || H > max_hidden) return RMSNORM_ERR_HIDDEN;
@@ -23,7 +24,7 @@ int ln_check(const rmsnorm_layout_t *L, int64_t H, int64_t max_hidden) {
         L->plan_items < 0)
         return RMSNORM_ERR_LAYOUT;
     if (L->n_tokens > 0 && !L->tok_id) return RMSNORM_ERR_NULL;
-    if (L->token_stride % 8 != 0) return RMSNORM_ERR_ALIGN;
+    if (L->token_stride % 8 != 0 || bad_align4(L->tok_id) || bad_align4(L->plan)) return RMSNORM_ERR_ALIGN;
     if (L->token_stride < int64_t(L->rows_per_token) * H) return RMSNORM_ERR_STRIDE;
     const int64_t lim = int64_t(1) << 31;
     if (L->n_tokens >= lim || L->n_logical_tokens >= lim || L->n_tokens * L->rows_per_token >= lim ||
@@ -96,7 +97,8 @@ extern "C" int layernorm_fwd(const void *x, const void *weight, const void *bias
     if (rc || (rc = ln_check(layout, hidden, ln_max_hidden(dtype))) || (rc = ln_eps(eps))) return rc;
     if (layout->n_tokens == 0) return RMSNORM_OK;
     if (!x || !y) return RMSNORM_ERR_NULL;
-    if (bad_align(x) || bad_align(weight) || bad_align(bias) || bad_align(y)) return RMSNORM_ERR_ALIGN;
+    if (bad_align(x) || bad_align(weight) || bad_align(bias) || bad_align(y) || bad_align4(mean) || bad_align4(rstd))
+        return RMSNORM_ERR_ALIGN;
     LnParams p = ln_params(layout, hidden, eps, dtype, param_dtype);
     p.x = x;
     p.w = weight;
@@ -118,7 +120,8 @@ extern "C" int layernorm_add_fwd(const void *x, const void *residual, const void
     if (layout->n_tokens == 0) return RMSNORM_OK;
     if (!x || !residual || !h_out || !y) return RMSNORM_ERR_NULL;
     if (h_out == y) return RMSNORM_ERR_LAYOUT;
-    if (bad_align(x) || bad_align(residual) || bad_align(weight) || bad_align(bias) || bad_align(h_out) || bad_align(y))
+    if (bad_align(x) || bad_align(residual) || bad_align(weight) || bad_align(bias) || bad_align(h_out) || bad_align(y) ||
+        bad_align4(mean) || bad_align4(rstd))
         return RMSNORM_ERR_ALIGN;
     LnParams p = ln_params(layout, hidden, eps, dtype, param_dtype);
     p.x = x;

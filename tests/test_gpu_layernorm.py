@@ -488,3 +488,131 @@ def test_gradients_against_differences():
             # truncation: step^2 / 6 times a third derivative of order 10; rounding: 48 terms of
             # order 1, each 2^-22 off, over 2 step
             assert abs(num - float(gf[i])) < 1e-3, (i, num, float(gf[i]))
+
+
+# Both sides of every rule that picks a kernel: lanes and octets of a team, a row's
+# first CTA, one and two CTAs an SM, vectors a thread, packed weights.
+EDGES = [(16, BF), (32, F32), (72, BF), (136, FP16), (248, F32), (504, BF), (512, F32), (520, FP16), (520, F32), (1032, BF),
+         (4096, F32), (5112, BF), (5128, BF), (5128, F32), (6144, FP16), (8184, BF), (8192, FP16), (8200, F32), (10240, FP16),
+         (12288, BF), (16376, FP16)]
+
+
+@pytest.mark.parametrize("H,dtype", [e for e in EDGES if e[1] != F32 or e[0] <= 8192], ids=lambda v: str(v).replace("torch.", ""))
+def test_chain_at_the_edges_of_the_rules(H, dtype):
+    n = 150
+    x, res, dy, dres, w, b = _data(n, H, dtype, param=F32 if H % 3 == 0 else None)
+    for drop in (None, rb.Dropout(0.3, _state())):
+        lays = {k: L.make_layout(k, [n - 20, 20], chunk=37) for k in ("full", "permuted_chunked", "padded_left")}
+        runs = {k: harness.run_layout_layernorm(v, x, res, dy, dres, w, b, EPS, 0.5, drop) for k, v in lays.items()}
+        rep = harness.assert_batch_invariant(runs, lays)
+        assert rep.green, rep.summary()
+        r = runs["full"]
+        assert r.status == 0
+        _check_chain(r.h, r.y, r.dh, r.dx, r.dweight, r.dbias, x, res, dy, dres, w, b, drop, 0.5, dtype)
+
+
+@pytest.mark.parametrize("H", [48, 400, 1040, 12288])
+def test_absent_parameters_are_ones_and_zeros(H):
+    n = 9
+    x, res, dy, dres, w, b = _data(n, H, BF)
+    cl = rb.call_layout(np.arange(n, dtype=np.int32), 1, n)
+    for one, zero in ((torch.ones_like(w), torch.zeros_like(b)), (torch.ones_like(w).float(), torch.zeros_like(b).float())):
+        assert _same(rb.layernorm_fwd(x, None, None, cl, EPS), rb.layernorm_fwd(x, one, zero, cl, EPS))
+        assert _same(rb.layernorm_fwd(x, one, None, cl, EPS), rb.layernorm_fwd(x, one, zero, cl, EPS))
+        assert _same(rb.layernorm_fwd(x, None, zero, cl, EPS), rb.layernorm_fwd(x, one, zero, cl, EPS))
+        assert _same(rb.layernorm_bwd(x, None, dy, cl, EPS), rb.layernorm_bwd(x, one, dy, cl, EPS))
+
+
+@pytest.mark.parametrize("n", [64 * 32 + 1, 64 * 300 + 9, 64 * 8200 + 5])
+def test_final_tree_of_two_and_three_passes(n):
+    """Exact terms (xhat = +-1), sums that round: every order gives another result."""
+    H = 8
+    rng = np.random.default_rng(n)
+    sign = np.where(np.arange(H) % 2 == 0, 1.0, -1.0) * np.where(rng.random((n, 1)) < 0.5, 1.0, -1.0)
+    dy = np.where(rng.random((n, H)) < 0.5, 1.0, 2.0 ** rng.integers(0, 26, size=(n, H))) * np.where(rng.random((n, H)) < 0.5, 1.0, -1.0)
+    xt, dyt = torch.tensor(sign).to("cuda", BF), torch.tensor(dy).to("cuda", BF)
+    cl = rb.call_layout(np.arange(n, dtype=np.int32), 1, n)
+    ws = rb.LayerNormWorkspace(n, H)
+    ws.begin()
+    rb.layernorm_bwd(xt, None, dyt, cl, 0.0, workspace=ws, write_dx=False)
+    dw, db = ws.finalize()
+    assert ws.status() == 0
+    assert np.array_equal(dw.cpu().numpy(), O.grad_replay(dy, sign))
+    assert np.array_equal(db.cpu().numpy(), O.grad_replay(dy))
+
+
+@pytest.mark.parametrize("H,dtype", [(128, BF), (264, F32), (1024, FP16), (9000, BF)], ids=str)
+def test_offsets_past_32_bits(H, dtype):
+    """Six slots 2^30 elements apart, every tensor a view of one buffer: the last offsets
+    are beyond 2^32 elements."""
+    n, pitch = 6, 2 ** 30
+    x, res, dy, dres, w, b = _data(n, H, dtype)
+    cl = rb.call_layout(np.arange(n, dtype=np.int32)[::-1].copy(), 1, n)
+    drop = rb.Dropout(0.4, _state())
+
+    def run(t):
+        x, res, dy, dres, h, y, dh, dx, z = t
+        ws = rb.LayerNormWorkspace(n, H)
+        ws.begin()
+        rb.layernorm_add_fwd(x, res, w, b, cl, EPS, h=h, y=y, dropout=drop)
+        rb.layernorm_add_bwd(h, w, dy, cl, EPS, dres=dres, dropout=drop, dh=dh, dx=dx, workspace=ws)
+        rb.dropout_fwd(x, cl, drop, y=z)
+        dw, db = ws.finalize()
+        assert ws.status() == 0
+        return [t.reshape(n, H).clone() for t in (h, y, dh, dx, z)] + [dw, db]
+
+    ins = [t.reshape(n, H) for t in (x, res, dy, dres)]
+    near = run(ins + [torch.zeros(n, H, dtype=dtype, device="cuda") for _ in range(5)])
+    buf = torch.empty(n, pitch, dtype=dtype, device="cuda")
+    far = [buf[:, i * 16384:i * 16384 + H] for i in range(9)]
+    for v, t in zip(far, ins):
+        v.copy_(t)
+    assert all(_same(a, c) for a, c in zip(near, run(far)))
+
+
+def test_duplicate_ids_in_the_passes_without_gradients():
+    """Two slots may hold the same logical row where nothing is reduced: both get its
+    result and its mask."""
+    for H in (64, 300 * 8):
+        ids = np.asarray([3, 0, 3, -1, 1, 3], dtype=np.int32)
+        x, res, dy, dres, w, b = _data(4, H, BF)
+        cl = rb.call_layout(ids, 1, 4, with_plan=False)
+        drop = rb.Dropout(0.5, _state())
+        at = torch.tensor(np.maximum(ids, 0), device="cuda").long()
+        xs, rs, ds = x[at], res[at], dy[at]
+        out = rb.layernorm_add_fwd(xs, rs, w, b, cl, EPS, dropout=drop) + rb.layernorm_add_bwd(xs, w, ds, cl, EPS, dropout=drop) + \
+            (rb.dropout_fwd(xs, cl, drop), rb.layernorm_fwd(xs, w, b, cl, EPS))
+        for t in out:
+            assert _same(t[0], t[2]) and _same(t[0], t[5])
+            assert not bool((t[0] == t[1]).all())
+
+
+def test_runs_next_to_the_other_norm():
+    """Two kernels that hold tensor memory, on two streams at once: results as when alone."""
+    n, H = 4000, 12296
+    x, res, dy, dres, w, b = _data(n, H, BF)
+    cl = rb.call_layout(np.arange(n, dtype=np.int32), 1, n)
+    R = 10240                                                               # the other norm's widest rows
+    ws, rws = rb.LayerNormWorkspace(n, H), rb.DweightWorkspace(n, R)
+    rx, rw, rdy = res[..., :R].contiguous(), w[:R].contiguous(), dy[..., :R].contiguous()
+
+    def ln(ws):
+        ws.begin()
+        dx = rb.layernorm_bwd(x, w, dy, cl, EPS, workspace=ws)
+        return (dx,) + tuple(ws.finalize())
+
+    def rms():
+        rws.begin()
+        dx = rb.rmsnorm_bwd_dx(rx, rw, rdy, cl, EPS, workspace=rws)
+        return dx, rws.finalize()
+
+    a0, r0 = ln(ws), rms()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        r1 = rms()
+        with torch.cuda.stream(side):
+            a1 = ln(ws)
+        torch.cuda.synchronize()
+        assert all(_same(u, v) for u, v in zip(a0, a1)) and all(_same(u, v) for u, v in zip(r0, r1))
+        assert ws.status() == 0 and rws.status() == 0

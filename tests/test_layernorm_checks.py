@@ -163,3 +163,12 @@ def test_tensors_off_the_current_device_are_refused(as_cuda, monkeypatch):
         rb.layernorm_fwd(x, w, w, lay, 1e-5)
     with pytest.raises(ValueError, match="current device"):
         rb.dropout_bwd(x, lay, rb.Dropout(0.1, torch.zeros(2, dtype=torch.int64)))
+
+
+def test_unaligned_statistics_ids_and_plans_are_refused():
+    lib = rb._load()
+    for mean, rstd in ((P(258), None), (None, P(257))):
+        assert lib.layernorm_fwd(G, G, G, 64, 1e-5, 0, 0, _layout(), G, mean, rstd, None) == -3
+        assert lib.layernorm_add_fwd(G, G, G, G, 64, 1e-5, 0, 0, _layout(), None, G, G2, mean, rstd, None) == -3
+    assert _fwd(lib, lay=_layout(tok=258)) == -3
+    assert lib.layernorm_bwd(G, G, G, 64, 1e-5, 0, 0, _layout(plan=258, items=1), G, G, None) == -3
