@@ -11,6 +11,13 @@ namespace rbi {
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // an SM's shared memory; what the system takes per CTA
 
+// CTAs that an SM's registers and warps hold: a quarter of an SM has 16,384
+// registers, of which a warp takes whole multiples of 256.
+inline int resident_ctas(int regs, int threads) {
+    const int per_warp = (regs * 32 + 255) / 256 * 256, warps = 16384 / per_warp * 4;
+    return (warps < 64 ? warps : 64) / (threads / 32);
+}
+
 // What a launcher needs of its kernel, asked for once per device: the registers
 // per thread; the kernel's shared-memory limit is raised on the way.
 struct KernelInfo {

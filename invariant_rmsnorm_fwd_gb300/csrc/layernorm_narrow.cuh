@@ -493,8 +493,7 @@ int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
     static KernelInfo info;
     int regs = 0;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), smem, &regs)) return rc;
-    int ctas = 65536 / ((regs + 7) / 8 * 8 * kNarrowThreads);
-    if (ctas > 8) ctas = 8;
+    int ctas = resident_ctas(regs, kNarrowThreads);
     if (ctas > kSmemPerSm / (smem + kSmemPerCta)) ctas = kSmemPerSm / (smem + kSmemPerCta);
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
     int64_t grid = (groups + kTeams - 1) / kTeams;
