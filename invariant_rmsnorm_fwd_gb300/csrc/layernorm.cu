@@ -225,7 +225,8 @@ extern "C" int layernorm_finalize(void *workspace, int64_t n_logical_rows, int64
         const int64_t per = in ? kLnTreeNodes : kLnTreeBlocks, groups = (n + per - 1) / per;
         const bool last = groups == 1;
         float *dst = scratch[flip];
-        ln_tree_kernel<<<dim3(unsigned(groups), gy), 256, 0, s>>>(
+        auto kern = in ? ln_tree_kernel<false> : ln_tree_kernel<true>;
+        kern<<<dim3(unsigned(groups), gy), 256, 0, s>>>(
             ws, in, last ? dweight : dst, last ? dbias : dst + hidden, last ? 0 : 2 * hidden, n,
             last ? grad_scale : 1.f);
         if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;

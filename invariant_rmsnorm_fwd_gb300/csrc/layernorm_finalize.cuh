@@ -45,8 +45,10 @@ __device__ __forceinline__ Cols load_cols(const float *p, bool two) {
     return v;
 }
 
-// A group's sums for four columns from its spilled rows.
-__device__ __forceinline__ float4 spilled4(const LnWs &ws, int64_t row0, int rows, int64_t col, int &bad) {
+// A group's sums for four columns from its spilled rows.  A function of its own:
+// inlined for each of a block's groups it would be most of the kernel's code, and
+// fetching that code what the tree waits for.
+__device__ __noinline__ float4 spilled4(const LnWs &ws, int64_t row0, int rows, int64_t col) {
     const int64_t H2 = 2 * ws.hidden;
     const bool is_w = col < ws.hidden;
     const int64_t c = is_w ? col : col - ws.hidden;
@@ -54,7 +56,7 @@ __device__ __forceinline__ float4 spilled4(const LnWs &ws, int64_t row0, int row
     for (int r = 0; r < rows; ++r) {
         const int64_t row = row0 + r;
         if (!ws.flag[row]) {
-            bad |= kStMissing;
+            set_status(ws.hdr, kStMissing);
             continue;
         }
         const float4 dy = *reinterpret_cast<const float4 *>(ws.spill + row * H2 + ws.hidden + c);
@@ -95,8 +97,8 @@ __device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_
         } else {
             next = j + 1;
             const int n = rows - j * kGroupRows < kGroupRows ? rows - j * kGroupRows : kGroupRows;
-            v[j].a = spilled4(ws, b * kBlockRows + j * kGroupRows, n, col, bad);
-            v[j].b = two ? spilled4(ws, b * kBlockRows + j * kGroupRows, n, col + 32, bad) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j].a = spilled4(ws, b * kBlockRows + j * kGroupRows, n, col);
+            v[j].b = two ? spilled4(ws, b * kBlockRows + j * kGroupRows, n, col + 32) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         acc = j == 0 ? v[j] : add_cols(acc, v[j]);
     }
@@ -110,24 +112,27 @@ __device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_
 // four of a warp meet by shuffles, the eight warps through shared memory.  All
 // loads of a pass are in flight at once; what bounds the first pass is reading the
 // partials, the others are latency.
-__global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, float *out_w, float *out_b,
+template <bool FIRST>
+__global__ void __launch_bounds__(256) ln_tree_kernel(const __grid_constant__ LnWs ws, const float *in, float *out_w, float *out_b,
                                                       int64_t out_stride, int64_t n_in, float scale) {
     __shared__ float4 val[8][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7, i = tid >> 3;
     const int64_t H2 = 2 * ws.hidden, col = int64_t(blockIdx.y) * kLnTreeCols + part * 4;
-    const int64_t first = int64_t(blockIdx.x) * (in ? kLnTreeNodes : kLnTreeBlocks);
-    if (!in && !ln_header_ok(ws)) {
-        if (tid == 0) set_status(ws.hdr, kStHeader);
-        return;
+    const int64_t first = int64_t(blockIdx.x) * (FIRST ? kLnTreeBlocks : kLnTreeNodes);
+    if constexpr (FIRST) {
+        if (!ln_header_ok(ws)) {
+            if (tid == 0) set_status(ws.hdr, kStHeader);
+            return;
+        }
     }
     // m teams of eight lanes have something; in the first pass one block each
-    const int64_t left = in ? (n_in - first + 7) / 8 : n_in - first;
+    const int64_t left = FIRST ? n_in - first : (n_in - first + 7) / 8;
     const int m = left < 32 ? int(left) : 32;
     Cols v = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     int bad = 0;
     if (i < m && col < H2) {
         const bool two = col + 32 < H2;
-        if (in) {
+        if constexpr (!FIRST) {
             const int64_t n = n_in - first - i * 8;
             Cols x[8];
 #pragma unroll
@@ -139,9 +144,10 @@ __global__ void __launch_bounds__(256) ln_tree_kernel(LnWs ws, const float *in, 
                 for (int k = 0; k + s < 8; k += 2 * s)
                     if (k + s < n) x[k] = add_cols(x[k], x[k + s]);
             v = x[0];
+        } else {
+            v = ln_block_value(ws, first + i, col, two, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
+                               blockIdx.y == 0, bad);
         }
-        else v = ln_block_value(ws, first + i, col, two, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
-                                blockIdx.y == 0, bad);
     }
     if (bad) set_status(ws.hdr, bad);
 #pragma unroll
