@@ -224,24 +224,14 @@ __device__ __forceinline__ void pairs_load(const float *p, f2_t (&f)[P]) {
 // written by the whole warp.
 template <int P>
 __device__ __forceinline__ void sums_load(uint32_t at, f2_t (&w)[P], f2_t (&b)[P]) {
-    if constexpr (P == 4) {
-        uint32_t u[16];
-        umma::ld_32x32_x16(at, u);
-        umma::wait_ld();
+    uint32_t u[4 * P];
+    if constexpr (P == 4) umma::ld_32x32_x16(at, u);
+    else umma::ld_32x32_x8(at, u);
+    umma::wait_ld(u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-            b[i] = f2_make(__uint_as_float(u[8 + 2 * i]), __uint_as_float(u[9 + 2 * i]));
-        }
-    } else {
-        uint32_t u[8];
-        umma::ld_32x32_x8(at, u);
-        umma::wait_ld();
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-            b[i] = f2_make(__uint_as_float(u[4 + 2 * i]), __uint_as_float(u[5 + 2 * i]));
-        }
+    for (int i = 0; i < P; ++i) {
+        w[i] = f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        b[i] = f2_make(__uint_as_float(u[2 * P + 2 * i]), __uint_as_float(u[2 * P + 2 * i + 1]));
     }
 }
 template <int P>
