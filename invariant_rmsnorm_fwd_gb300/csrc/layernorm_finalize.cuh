@@ -119,15 +119,17 @@ __global__ void __launch_bounds__(256) ln_tree_kernel(const __grid_constant__ Ln
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = tid & 7, i = tid >> 3;
     const int64_t H2 = 2 * ws.hidden, col = int64_t(blockIdx.y) * kLnTreeCols + part * 4;
     const int64_t first = int64_t(blockIdx.x) * (FIRST ? kLnTreeBlocks : kLnTreeNodes);
+    // m teams of eight lanes have something; in the first pass one block each
+    const int64_t left = FIRST ? n_in - first : (n_in - first + 7) / 8;
+    const int m = left < 32 ? int(left) : 32;
+    uint64_t state = 0;
     if constexpr (FIRST) {
+        if (i < m) state = reinterpret_cast<const uint64_t *>(ws.state)[first + i];
         if (!ln_header_ok(ws)) {
             if (tid == 0) set_status(ws.hdr, kStHeader);
             return;
         }
     }
-    // m teams of eight lanes have something; in the first pass one block each
-    const int64_t left = FIRST ? n_in - first : (n_in - first + 7) / 8;
-    const int m = left < 32 ? int(left) : 32;
     Cols v = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     int bad = 0;
     if (i < m && col < H2) {
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(256) ln_tree_kernel(const __grid_constant__ Ln
                     if (k + s < n) x[k] = add_cols(x[k], x[k + s]);
             v = x[0];
         } else {
-            v = ln_block_value(ws, first + i, col, two, reinterpret_cast<const uint64_t *>(ws.state)[first + i],
+            v = ln_block_value(ws, first + i, col, two, state,
                                blockIdx.y == 0, bad);
         }
     }

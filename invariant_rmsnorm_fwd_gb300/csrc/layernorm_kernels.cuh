@@ -58,9 +58,12 @@ inline LnWs ln_ws(void *base, int64_t N, int64_t H) {
     return w;
 }
 
+// (all three fields are loaded at once: small calls wait for each round trip)
 __device__ __forceinline__ bool ln_header_ok(const LnWs &ws) {
     const WsHeader *h = ws.hdr;
-    return h->magic == kLnMagic && h->n_rows == ws.n_rows && h->hidden == ws.hidden;
+    const auto magic = h->magic;
+    const int64_t n_rows = h->n_rows, hidden = h->hidden;
+    return (magic == kLnMagic) & (n_rows == ws.n_rows) & (hidden == ws.hidden);
 }
 
 struct LnParams {

@@ -190,12 +190,8 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
     const int tid = threadIdx.x, team = tid / P, l = tid % P, V = p.hidden >> 3;
     const uint32_t mine = smem_addr(smem) + uint32_t(tid) * 16u;
     bool col[NO];                                        // this lane has the columns of octet l + k P
-    if constexpr (GRADS) {
-        if (!ln_header_ok(p.ws)) {
-            if (tid == 0) set_status(p.ws.hdr, kStHeader);
-            return;
-        }
-    }
+    bool header = true;
+    if constexpr (GRADS) header = ln_header_ok(p.ws);    // used behind the loads of the parameters
     const DropKey key = DROP ? drop_key(p.drop) : DropKey{0, 0, 0, 0};
     const int64_t groups = GRADS ? p.n_items * kGroups : (p.n_rows + kGroupRows - 1) / kGroupRows;
     const int64_t stride = int64_t(gridDim.x) * kTeams;
@@ -211,6 +207,12 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
         if (col[k]) {
             oct_param<E>(p.w, p.params_f32, l + k * P, 1.f, w[k]);
             if constexpr (kFwd) oct_param<E>(p.b, p.params_f32, l + k * P, 0.f, b[k]);
+        }
+    }
+    if constexpr (GRADS) {
+        if (!header) {
+            if (tid == 0) set_status(p.ws.hdr, kStHeader);
+            return;
         }
     }
     // The sums of a lane's columns over its group: in registers, or in tensor memory

@@ -415,12 +415,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     const uint32_t list0 = smem_addr(list);
     const uint32_t step = uint32_t(T) * 16u;
 
-    if constexpr (GRADS) {
-        if (!ln_header_ok(p.ws)) {
-            if (tid == 0) set_status(p.ws.hdr, kStHeader);
-            return;
-        }
-    }
+    bool header = true;
+    if constexpr (GRADS) header = ln_header_ok(p.ws);    // used behind the loads of the parameters
     if (tid == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
@@ -460,6 +456,12 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
             for (int s = 0; s < S; ++s)
                 for (int t = 0; t < nt; ++t)
                     *reinterpret_cast<uint4 *>(smem + stage0 + s * stage_pitch + t * pitch + v * 16) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if constexpr (GRADS) {
+        if (!header) {
+            if (tid == 0) set_status(p.ws.hdr, kStHeader);
+            return;
         }
     }
     // Tensor memory: kSumCols columns of a warp's 32 lanes for the group's sums and as
