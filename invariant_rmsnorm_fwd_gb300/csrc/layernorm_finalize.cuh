@@ -110,8 +110,14 @@ __device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_
 // [m g, m (g + 1)) of 64 columns to one node, m = 32 in the first pass, 256 in the
 // others.  Eight lanes hold the columns of a block (of 8 consecutive inputs), the
 // four of a warp meet by shuffles, the eight warps through shared memory.  All
-// loads of a pass are in flight at once; what bounds the first pass is reading the
-// partials, the others are latency.
+// loads of a pass are in flight at once.
+//
+// What bounds it: latency.  Hidden 4096, 276 blocks, about 40 MB of partials (most
+// of them still in the L2): 13 us, hidden 8192 25 us, in 4 and 8 rounds of CTAs of
+// about 3 us each, a few dependent loads long; a later pass 2 us.  32 inputs in the
+// later passes too: three launches instead of two at hidden 4096; 32 columns a CTA,
+// 4 groups in flight at twice the CTAs, CTAs that walk over the columns: equal or
+// slower.
 template <bool FIRST>
 __global__ void __launch_bounds__(256) ln_tree_kernel(const __grid_constant__ LnWs ws, const float *in, float *out_w, float *out_b,
                                                       int64_t out_stride, int64_t n_in, float scale) {
