@@ -205,9 +205,18 @@ class _Call:
         return ctypes.byref(_rb._Layout(n, lay.rows_per_token, 0, stride, tok, lay.n_logical_tokens, addr, items))
 
 
-def _new(like):
+def _empty(shape, strides, dtype, device, stream):
+    """Memory of a new output: of the stream that writes it, for what the current stream
+    has given back may still be in use there."""
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _new(like, stream):
     """A new output with the shape and strides of `like` (rows past n_tokens and padding are left as they come)."""
-    return torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
+    return _empty(like.shape, like.stride(), like.dtype, like.device, stream)
 
 
 def _p(t):
@@ -219,7 +228,7 @@ def layernorm_fwd(x, weight, bias, lay, eps: float, y=None, mean=None, rstd=None
     may be None; mean and rstd are optional float32 outputs of one value per row."""
     c = _Call(x, "x", lay, stream)
     if y is None:
-        y = _new(x)
+        y = _new(x, stream)
     rc = _rb._load().layernorm_fwd(x.data_ptr(), _p(weight), _p(bias), c.H, eps, c.code, c.params(weight, bias),
                                    c.layout(False), c.rows(y, "y"), c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
     if rc:
@@ -233,9 +242,9 @@ def layernorm_add_fwd(x, residual, weight, bias, lay, eps: float, h=None, y=None
     y = layer norm of h.  Returns (h, y); h is what the backward pass takes."""
     c = _Call(x, "x", lay, stream)
     if h is None:
-        h = _new(x)
+        h = _new(x, stream)
     if y is None:
-        y = _new(x)
+        y = _new(x, stream)
     d = None if dropout is None else ctypes.byref(dropout.struct(c.index))
     rc = _rb._load().layernorm_add_fwd(x.data_ptr(), c.rows(residual, "residual"), _p(weight), _p(bias), c.H, eps, c.code,
                                        c.params(weight, bias), c.layout(False), d, c.rows(h, "h"), c.rows(y, "y"),
@@ -250,7 +259,7 @@ def layernorm_bwd(x, weight, dy, lay, eps: float, dx=None, workspace=None, strea
     to dweight and dbias (the layout needs its plan)."""
     c = _Call(x, "x", lay, stream)
     if dx is None and write_dx:
-        dx = _new(dy)
+        dx = _new(dy, stream)
     rc = _rb._load().layernorm_bwd(x.data_ptr(), _p(weight), c.rows(dy, "dy"), c.H, eps, c.code, c.params(weight),
                                    c.layout(workspace is not None), None if dx is None else c.rows(dx, "dx"),
                                    c.workspace(workspace), c.stream)
@@ -268,11 +277,11 @@ def layernorm_add_bwd(h, weight, dy, lay, eps: float, dres=None, grad_scale: flo
     c = _Call(h, "h", lay, stream)
     at_dy = c.rows(dy, "dy")
     if dh is None:
-        dh = _new(dy)
+        dh = _new(dy, stream)
     d = None
     if dropout is not None:
         if dx is None:
-            dx = _new(dy)
+            dx = _new(dy, stream)
         d = ctypes.byref(dropout.struct(c.index))
     elif dx is not None:
         raise ValueError("dx: only with a dropout (without one it is dh)")
@@ -290,7 +299,7 @@ def _dropout(fn: str, x, out, in_name: str, out_name: str, lay, dropout, stream)
     if not isinstance(dropout, Dropout):
         raise TypeError(f"dropout: expected Dropout, got {type(dropout).__name__}")
     if out is None:
-        out = _new(x)
+        out = _new(x, stream)
     rc = getattr(_rb._load(), fn)(x.data_ptr(), c.H, c.code, c.layout(False), ctypes.byref(dropout.struct(c.index)),
                                   c.rows(out, out_name), c.stream)
     if rc:
@@ -331,9 +340,9 @@ class LayerNormWorkspace:
             raise ValueError(f"stream: on {stream.device}, the workspace is on {self.buf.device}")
         return stream.cuda_stream
 
-    def _gradient(self, t, name: str):
+    def _gradient(self, t, name: str, stream):
         if t is None:
-            return torch.empty(self.hidden, dtype=torch.float32, device=self.buf.device)
+            return _empty((self.hidden,), (1,), torch.float32, self.buf.device, stream)
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
             raise TypeError(f"{name}: expected a float32 tensor")
         if _index(t) != _index(self.buf) or not t.is_contiguous() or t.numel() < self.hidden:
@@ -347,9 +356,10 @@ class LayerNormWorkspace:
 
     def finalize(self, dweight=None, dbias=None, stream=None, grad_scale: float = 1.0):
         """(dweight, dbias) of the reduction, each root multiplied once by grad_scale."""
-        dweight, dbias = self._gradient(dweight, "dweight"), self._gradient(dbias, "dbias")
+        at = self._stream(stream)
+        dweight, dbias = self._gradient(dweight, "dweight", stream), self._gradient(dbias, "dbias", stream)
         rc = _rb._load().layernorm_finalize(self.buf.data_ptr(), self.n_rows, self.hidden, grad_scale,
-                                            dweight.data_ptr(), dbias.data_ptr(), self._stream(stream))
+                                            dweight.data_ptr(), dbias.data_ptr(), at)
         if rc:
             _rb._check(rc, "layernorm_finalize")
         return dweight, dbias

@@ -345,7 +345,7 @@ def test_empty_calls_and_empty_multiset():
     rb.layernorm_fwd(x, w, w, none, EPS, y=y)
     rb.layernorm_bwd(x, w, x, none, EPS, dx=dx, workspace=ws)
     dw, db = ws.finalize()
-    assert ws.status() == 0 and not dw.any() and not db.any()
+    assert ws.status() == 0 and dw.shape == db.shape == (128,) and not dw.any() and not db.any()
     assert bool((y == 3).all()) and bool((dx == 3).all())
 
 
@@ -616,3 +616,29 @@ def test_runs_next_to_the_other_norm():
         torch.cuda.synchronize()
         assert all(_same(u, v) for u, v in zip(a0, a1)) and all(_same(u, v) for u, v in zip(r0, r1))
         assert ws.status() == 0 and rws.status() == 0
+
+
+def test_outputs_of_a_given_stream_belong_to_it():
+    """A block that the current stream has just given back, and may still be writing, is
+    not where a call on another stream puts its new outputs."""
+    n, H = 600, 2048
+    x, res, dy, dres, w, b = _data(n, H, BF)
+    cl = rb.call_layout(np.arange(n, dtype=np.int32), 1, n)
+    drop = rb.Dropout(0.5, _state())
+    side = torch.cuda.Stream()
+    ws = rb.LayerNormWorkspace(n, H)
+    ws.begin()
+    want = (rb.layernorm_fwd(x, w, b, cl, EPS), rb.layernorm_bwd(x, w, dy, cl, EPS, workspace=ws)) + ws.finalize()
+    torch.cuda.synchronize()
+    given = [torch.empty_like(x) for _ in range(8)] + [torch.empty(H, device="cuda") for _ in range(4)]
+    used = {t.data_ptr() for t in given}
+    given.clear()
+    ws.begin(side)
+    outs = (rb.layernorm_fwd(x, w, b, cl, EPS, stream=side), rb.layernorm_bwd(x, w, dy, cl, EPS, workspace=ws, stream=side))
+    outs += ws.finalize(stream=side)
+    outs += rb.layernorm_add_fwd(x, res, w, b, cl, EPS, dropout=drop, stream=side)
+    outs += rb.layernorm_add_bwd(x, w, dy, cl, EPS, dropout=drop, stream=side)
+    outs += (rb.dropout_fwd(x, cl, drop, stream=side), rb.dropout_bwd(x, cl, drop, stream=side))
+    side.synchronize()
+    assert not used & {t.data_ptr() for t in outs}
+    assert all(_same(u, v) for u, v in zip(want, outs))
