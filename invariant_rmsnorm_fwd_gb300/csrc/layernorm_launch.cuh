@@ -33,7 +33,6 @@ int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cuda
         while (cols < (threads + 127) / 128 * 4 * NV * Lane<E>::kE) cols *= 2;
     }
     int ctas = resident_ctas(regs, threads);
-    if (ctas > 32) ctas = 32;
     if (GRADS && ctas > 512 / cols) ctas = 512 / cols;
     if (ctas < 1) return RMSNORM_ERR_HIDDEN;
     int S = 0;

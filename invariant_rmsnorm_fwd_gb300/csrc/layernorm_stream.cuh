@@ -173,26 +173,22 @@ __device__ __forceinline__ void lane_sums(float (&v)[K], float &mine) {
 }
 
 template <int K>
-__device__ __forceinline__ void cta_sums(float (&v)[K], float *red, int warps) {
+__device__ __forceinline__ void cta_sums(float (&v)[K], float *red) {
     const int lane = threadIdx.x & 31;
     float m;
     lane_sums(v, m);
-    if (warps > 1) {
-        constexpr int kLanes = 32 / K;                   // lanes that hold the same value
-        if (lane % kLanes == 0) red[(lane / kLanes) * 16 + (threadIdx.x >> 5)] = m;
-        __syncthreads();
-        if constexpr (K == 4) {
-            m = __fadd_rn(red[(lane >> 3) * 16 + (lane & 7)], red[(lane >> 3) * 16 + (lane & 7) + 8]);
-        } else {
-            m = red[(lane >> 4) * 16 + (lane & 15)];
-            m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 8));
-        }
-        m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 4));
-        m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 2));
-        m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 1));
+    constexpr int kLanes = 32 / K;                       // lanes that hold the same value
+    if (lane % kLanes == 0) red[(lane / kLanes) * 16 + (threadIdx.x >> 5)] = m;
+    __syncthreads();
+    if constexpr (K == 4) {
+        m = __fadd_rn(red[(lane >> 3) * 16 + (lane & 7)], red[(lane >> 3) * 16 + (lane & 7) + 8]);
     } else {
-        __syncwarp();
+        m = red[(lane >> 4) * 16 + (lane & 15)];
+        m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 8));
     }
+    m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 4));
+    m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 2));
+    m = __fadd_rn(m, __shfl_xor_sync(kFull, m, 1));
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = __shfl_sync(kFull, m, k * (32 / K));
 }
@@ -217,20 +213,11 @@ __device__ __forceinline__ LnEntry lds_entry(uint32_t addr) {
                  : "r"(addr));
     return e;
 }
-// P pairs to or from consecutive floats, 16 bytes at a time.
+// P pairs to consecutive floats, 16 bytes at a time.
 template <int P>
 __device__ __forceinline__ void pairs_store(float *p, const f2_t (&f)[P]) {
 #pragma unroll
     for (int j = 0; j < P; j += 2) *reinterpret_cast<ulonglong2 *>(p + 2 * j) = make_ulonglong2(f[j], f[j + 1]);
-}
-template <int P>
-__device__ __forceinline__ void pairs_load(const float *p, f2_t (&f)[P]) {
-#pragma unroll
-    for (int j = 0; j < P; j += 2) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p + 2 * j);
-        f[j] = v.x;
-        f[j + 1] = v.y;
-    }
 }
 
 // The sums of one vector (dweight, then dbias) in tensor memory at `at`, read or
@@ -419,7 +406,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
     volatile int *count = reinterpret_cast<volatile int *>(smem + kCountOff);   // [0..15] warps; [16, 17] a copy
                                                          // did not arrive (alternating like red)
     LnEntry *list = reinterpret_cast<LnEntry *>(smem + kListOff);
-    const int tid = threadIdx.x, T = blockDim.x, warps = T >> 5;
+    const int tid = threadIdx.x, T = blockDim.x;
     const int V = p.hidden / kE;
     const uint32_t row_bytes = uint32_t(p.hidden) * uint32_t(sizeof(E));
     const uint32_t pitch = uint32_t(NV * T) * 16u, stage_pitch = pitch * uint32_t(nt);
@@ -577,7 +564,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
         {
             float v[K] = {};
             v[0] = first_pass(0);
-            cta_sums<K>(v, red + (turn & 1) * 64, warps);
+            cta_sums<K>(v, red + (turn & 1) * 64);
             dead = count[16 + (turn & 1)] != 0;          // the same for every thread
             ++turn;
             mean = __fmul_rn(v[0], p.inv_h);
@@ -617,7 +604,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 v[2] = pair_total(sa);
                 v[3] = pair_total(sc);
             }
-            cta_sums<K>(v, red + (turn & 1) * 64, warps);
+            cta_sums<K>(v, red + (turn & 1) * 64);
             dead = count[16 + (turn & 1)] != 0;
             ++turn;
             if (dead) break;
