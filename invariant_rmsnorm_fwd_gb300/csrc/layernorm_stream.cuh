@@ -22,10 +22,10 @@
 // place (hidden 8192 with dropout and dres: 322 -> 294 us when they moved here).
 //
 // What bounds it (bf16, DRAM floor at the copy rate of 6.78 TB/s in brackets):
-// forward, hidden 4096, 17,620 rows: 51 us (43), 5.7 TB/s; with dropout and
+// forward, hidden 4096, 17,620 rows: 50.5 us (43), 5.7 TB/s; with dropout and
 // residual add, hidden 5120, 17,620 active rows among padding: 118 us (107): memory.
-// Backward with both parameter gradients, hidden 4096: 94 us (64); hidden 8192
-// with dropout and dres, 285 us (213): not memory but the row's chain of
+// Backward with both parameter gradients, hidden 4096: 92.5 us (64); hidden 8192
+// with dropout and dres, 280 us (213): not memory but the row's chain of
 // dependent steps.  A row alone takes about 1,900 cycles (590 of them the
 // exchange, 320 the next row's sum, 300 the stores), 380 instructions a warp, and
 // 16 warps, all that 128 registers allow, hide half of it (issue slots 50 % busy).
@@ -148,8 +148,13 @@ __device__ __forceinline__ void drop_add_pairs(f2_t (&f)[P], const f2_t (&q)[P],
 
 // Sums K values over the CTA: lanes by a butterfly that hands each value to
 // its own lanes on the way (K = 4: 6 shuffles instead of 20), warps through
-// shared memory.  The order of the additions is the same for K = 2 and 4 and
-// depends on the thread count only.  `red` is one of two alternating buffers.
+// shared memory and a second butterfly, or (DIRECT, the most warps of a CTA) by
+// reads of all warps' values in every thread: shorter, but more instructions.
+// Residual add with dropout in 10 warps (32,768 slots of 5120, 17,624 of them rows):
+// butterfly 125 us, reads 119; 8 warps and fewer 92 and 93; 16 warps 92 and 96;
+// forward alone and backward as slow or slower by reads.  The order of the
+// additions is the same in both, warps 8, 4, 2 and 1 apart, and for K = 2 and 4.
+// `red` is one of two alternating buffers, zero behind the CTA's warps.
 template <int K>
 __device__ __forceinline__ void lane_sums(float (&v)[K], float &mine) {
     const int lane = threadIdx.x & 31;
@@ -172,12 +177,28 @@ __device__ __forceinline__ void lane_sums(float (&v)[K], float &mine) {
     mine = __fadd_rn(mine, __shfl_xor_sync(kFull, mine, 1));
 }
 
-template <int K>
+template <int K, int DIRECT>
 __device__ __forceinline__ void cta_sums(float (&v)[K], float *red) {
     const int lane = threadIdx.x & 31;
     float m;
     lane_sums(v, m);
     constexpr int kLanes = 32 / K;                       // lanes that hold the same value
+    if constexpr (DIRECT > 0) {
+        static_assert(K == 2, "pairs of two values");
+        if (lane % kLanes == 0) red[(threadIdx.x >> 5) * K + lane / kLanes] = m;
+        __syncthreads();
+        ulonglong2 q[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) q[w] = 2 * w < DIRECT ? reinterpret_cast<const ulonglong2 *>(red)[w] : make_ulonglong2(0, 0);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1)
+#pragma unroll
+            for (int w = 0; w < o; ++w) q[w] = make_ulonglong2(f2_add(q[w].x, q[w + o].x), f2_add(q[w].y, q[w + o].y));
+        q[0].x = f2_add(q[0].x, q[0].y);
+        v[0] = f2_lo(q[0].x);
+        v[1] = f2_hi(q[0].x);
+        return;
+    }
     if (lane % kLanes == 0) red[(lane / kLanes) * 16 + (threadIdx.x >> 5)] = m;
     __syncthreads();
     if constexpr (K == 4) {
@@ -564,7 +585,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
         {
             float v[K] = {};
             v[0] = first_pass(0);
-            cta_sums<K>(v, red + (turn & 1) * 64);
+            cta_sums<K, MODE == kLnAdd && MAXT == 320 ? MAXT / 32 : 0>(v, red + (turn & 1) * 64);
             dead = count[16 + (turn & 1)] != 0;          // the same for every thread
             ++turn;
             mean = __fmul_rn(v[0], p.inv_h);
@@ -604,7 +625,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
                 v[2] = pair_total(sa);
                 v[3] = pair_total(sc);
             }
-            cta_sums<K>(v, red + (turn & 1) * 64);
+            cta_sums<K, MODE == kLnAdd && MAXT == 320 ? MAXT / 32 : 0>(v, red + (turn & 1) * 64);
             dead = count[16 + (turn & 1)] != 0;
             ++turn;
             if (dead) break;
