@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
     }
     cp_async_wait<0>();
     if constexpr (kTmem) {
+        umma::wait_st();                                 // this warp's last stores have landed before the columns are freed
         umma::fence_before();
         __syncthreads();
         umma::fence_after();

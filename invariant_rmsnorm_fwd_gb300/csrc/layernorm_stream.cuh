@@ -750,6 +750,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_stream_kernel(const __grid_cons
         done += uint32_t(n);
     }
     if constexpr (GRADS) {
+        umma::wait_st();                                 // this warp's last stores (cleared sums) have landed: the
+                                                         // columns may go to another CTA now
         umma::fence_before();
         __syncthreads();
         umma::fence_after();
