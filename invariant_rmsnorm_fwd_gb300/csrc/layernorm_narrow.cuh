@@ -151,6 +151,11 @@ __device__ __forceinline__ void team_slots(const LnParams &p, int64_t group, con
         s.kind = raw.kind;
         s.block = raw.block;
         s.partial = raw.kind == kItemWhole || (raw.kind == kItemQuarters && ((raw.quarters >> (s.slot0 / 16)) & 1));
+        if ((raw.kind == kItemWhole || raw.kind == kItemQuarters) && (raw.block < 0 || raw.block >= p.ws.n_blocks)) {
+            set_status(p.ws.hdr, kStPlan);               // a block that the workspace does not have: contributes nothing
+            s.kind = kBadItem;
+            s.partial = false;
+        }
     }
 #pragma unroll
     for (int o = 0; o < TeamSlots<P>::kOwn; ++o) {
@@ -448,14 +453,14 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
             }
             const int64_t rows = p.ws.n_rows - int64_t(cur.block) * kBlockRows;
             const int n_groups = rows >= kBlockRows ? kGroups : int((rows + kGroupRows - 1) / kGroupRows);
-            if (cur.partial && l == 0 && cur.slot0 < rows && cur.block >= 0 && cur.block < p.ws.n_blocks) {
+            if (cur.partial && l == 0 && cur.slot0 < rows) {
                 uint8_t *state = p.ws.state + int64_t(cur.block) * kGroups + cur.slot0 / kGroupRows;
                 if (*state != 0) set_status(p.ws.hdr, kStDouble);
                 if (cur.kind == kItemQuarters) *state = 1;
                 else if (cur.slot0 == 0) *state = uint8_t(n_groups);
             }
             __syncthreads();
-            if (cur.kind == kItemWhole && cur.block >= 0 && cur.block < p.ws.n_blocks) {
+            if (cur.kind == kItemWhole) {
                 // lane (team of the block, l): NO pairs of the block's 2 kCols sums
 #pragma unroll
                 for (int k = 0; k < NO; ++k) {
