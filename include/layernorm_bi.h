@@ -86,8 +86,8 @@ int layernorm_add_fwd(const void *x, const void *residual, const void *weight, c
 /*
  * Backward: dx on every active row (mean and rstd recomputed bitwise as in the
  * forward).  With a workspace the same pass contributes this call's rows to
- * dweight and dbias (layout->plan required); dx may then be NULL.  dx may
- * alias dy or x.
+ * dweight and dbias (layout->plan required); dx may then be NULL, as for a
+ * call of no slots.  dx may alias dy or x.
  */
 int layernorm_bwd(const void *x, const void *weight, const void *dy, int64_t hidden, float eps, int32_t dtype,
                   int32_t param_dtype, const rmsnorm_layout_t *layout, void *dx, void *workspace,
@@ -101,7 +101,8 @@ int layernorm_bwd(const void *x, const void *weight, const void *dy, int64_t hid
  * dh) and must then be non-NULL.  grad_scale is the loss seed's factor as in
  * rmsnorm_add_bwd; the workspace's terms stay unscaled (layernorm_finalize
  * takes the factor).  dh may be NULL only with a workspace and neither dres
- * nor dropout.  dh and dx may alias dy, dres or h, dh != dx.
+ * nor dropout, or for a call of no slots (n_tokens == 0), whose data pointers
+ * are not looked at.  dh and dx may alias dy, dres or h, dh != dx.
  */
 int layernorm_add_bwd(const void *h, const void *weight, const void *dy, const void *dres, int64_t hidden,
                       float eps, float grad_scale, int32_t dtype, int32_t param_dtype,

@@ -145,7 +145,7 @@ extern "C" int layernorm_add_bwd(const void *h, const void *weight, const void *
     if (!std::isfinite(grad_scale)) return RMSNORM_ERR_VALUE;
     DropParams drop;
     if ((rc = drop_params(dropout, &drop))) return rc;
-    if (!dh && (!workspace || dres || dropout)) return RMSNORM_ERR_NULL;
+    if (!dh && (!workspace || dres || dropout) && layout->n_tokens > 0) return RMSNORM_ERR_NULL;
     if (dropout && !dx && layout->n_tokens > 0) return RMSNORM_ERR_NULL;
     if (dropout && dh == dx && layout->n_tokens > 0) return RMSNORM_ERR_LAYOUT;
     if (workspace && !layout->plan && layout->n_tokens > 0) return RMSNORM_ERR_PLAN;
