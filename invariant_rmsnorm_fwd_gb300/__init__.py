@@ -50,6 +50,10 @@ class _Layout(ctypes.Structure):
     ]
 
 
+class _Dropout(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_double)]
+
+
 def library_path() -> str:
     from . import _build
     return _build.LIB
@@ -64,7 +68,7 @@ def _load():
     path = _build.build()
     lib = ctypes.CDLL(path)
     P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
-    LP = ctypes.POINTER(_Layout)
+    LP, DP = ctypes.POINTER(_Layout), ctypes.POINTER(_Dropout)
     sig = {
         "rmsnorm_fwd": ([P, P, I64, F, LP, P, P, P], ctypes.c_int),
         "rmsnorm_bwd_dx": ([P, P, P, I64, F, LP, P, P, P], ctypes.c_int),
@@ -89,9 +93,17 @@ def _load():
         "gemm_dw_status": ([P, P, ctypes.POINTER(I32)], ctypes.c_int),
         "rmsnorm_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "rmsnorm_kernel_launches": ([], I64),
+        "layernorm_fwd": ([P, P, P, I64, F, I32, I32, LP, P, P, P, P], ctypes.c_int),
+        "layernorm_add_fwd": ([P, P, P, P, I64, F, I32, I32, LP, DP, P, P, P, P, P], ctypes.c_int),
+        "layernorm_bwd": ([P, P, P, I64, F, I32, I32, LP, P, P, P], ctypes.c_int),
+        "layernorm_add_bwd": ([P, P, P, P, I64, F, F, I32, I32, LP, DP, P, P, P, P], ctypes.c_int),
+        "layernorm_workspace_bytes": ([I64, I64], ctypes.c_size_t),
+        "layernorm_begin": ([P, ctypes.c_size_t, I64, I64, P], ctypes.c_int),
+        "layernorm_finalize": ([P, I64, I64, F, P, P, P], ctypes.c_int),
+        "layernorm_status": ([P, P, ctypes.POINTER(I32)], ctypes.c_int),
+        "dropout_fwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
+        "dropout_bwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
     }
-    from . import layernorm
-    sig.update(layernorm.signatures(LP))
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args

@@ -15,30 +15,8 @@ import torch
 
 import invariant_rmsnorm_fwd_gb300 as _rb
 
+_Dropout = _rb._Dropout
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-
-
-class _Dropout(ctypes.Structure):
-    _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_double)]
-
-
-def signatures(layout_ptr) -> dict:
-    """Argument and result types of the library's functions (filled in by the package's loader)."""
-    P, I64, I32, F, D, S = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
-                            ctypes.POINTER(_Dropout), ctypes.c_size_t)
-    L, R = layout_ptr, ctypes.c_int
-    return {
-        "layernorm_fwd": ([P, P, P, I64, F, I32, I32, L, P, P, P, P], R),
-        "layernorm_add_fwd": ([P, P, P, P, I64, F, I32, I32, L, D, P, P, P, P, P], R),
-        "layernorm_bwd": ([P, P, P, I64, F, I32, I32, L, P, P, P], R),
-        "layernorm_add_bwd": ([P, P, P, P, I64, F, F, I32, I32, L, D, P, P, P, P], R),
-        "layernorm_workspace_bytes": ([I64, I64], S),
-        "layernorm_begin": ([P, S, I64, I64, P], R),
-        "layernorm_finalize": ([P, I64, I64, F, P, P, P], R),
-        "layernorm_status": ([P, P, ctypes.POINTER(I32)], R),
-        "dropout_fwd": ([P, I64, I32, L, D, P, P], R),
-        "dropout_bwd": ([P, I64, I32, L, D, P, P], R),
-    }
 
 
 def _index(t) -> int:
