@@ -60,6 +60,13 @@ class Dropout:
         return _Dropout(s.data_ptr(), self.p)
 
 
+def _drop(dropout, index: int):
+    """The call's dropout for the library."""
+    if not isinstance(dropout, Dropout):
+        raise TypeError(f"dropout: expected Dropout, got {type(dropout).__name__}")
+    return ctypes.byref(dropout.struct(index))
+
+
 class _Call:
     """The checks of one call's tensors.  The first one (x, h or dy) fixes the
     element type, the device, the shape and the token stride; the others are
@@ -207,8 +214,9 @@ def layernorm_fwd(x, weight, bias, lay, eps: float, y=None, mean=None, rstd=None
     c = _Call(x, "x", lay, stream)
     if y is None:
         y = _new(x, stream)
-    rc = _rb._load().layernorm_fwd(x.data_ptr(), _p(weight), _p(bias), c.H, eps, c.code, c.params(weight, bias),
-                                   c.layout(False), c.rows(y, "y"), c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
+    params = c.params(weight, bias)
+    rc = _rb._load().layernorm_fwd(x.data_ptr(), _p(weight), _p(bias), c.H, eps, c.code, params, c.layout(False),
+                                   c.rows(y, "y"), c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
     if rc:
         _rb._check(rc, "layernorm_fwd")
     return y
@@ -223,9 +231,10 @@ def layernorm_add_fwd(x, residual, weight, bias, lay, eps: float, h=None, y=None
         h = _new(x, stream)
     if y is None:
         y = _new(x, stream)
-    d = None if dropout is None else ctypes.byref(dropout.struct(c.index))
+    d = None if dropout is None else _drop(dropout, c.index)
+    params = c.params(weight, bias)
     rc = _rb._load().layernorm_add_fwd(x.data_ptr(), c.rows(residual, "residual"), _p(weight), _p(bias), c.H, eps, c.code,
-                                       c.params(weight, bias), c.layout(False), d, c.rows(h, "h"), c.rows(y, "y"),
+                                       params, c.layout(False), d, c.rows(h, "h"), c.rows(y, "y"),
                                        c.stat(mean, "mean"), c.stat(rstd, "rstd"), c.stream)
     if rc:
         _rb._check(rc, "layernorm_add_fwd")
@@ -236,9 +245,11 @@ def layernorm_bwd(x, weight, dy, lay, eps: float, dx=None, workspace=None, strea
     """dx on every active row; with a workspace the same pass adds the call's rows
     to dweight and dbias (the layout needs its plan)."""
     c = _Call(x, "x", lay, stream)
+    at_dy = c.rows(dy, "dy")
     if dx is None and write_dx:
         dx = _new(dy, stream)
-    rc = _rb._load().layernorm_bwd(x.data_ptr(), _p(weight), c.rows(dy, "dy"), c.H, eps, c.code, c.params(weight),
+    params = c.params(weight)
+    rc = _rb._load().layernorm_bwd(x.data_ptr(), _p(weight), at_dy, c.H, eps, c.code, params,
                                    c.layout(workspace is not None), None if dx is None else c.rows(dx, "dx"),
                                    c.workspace(workspace), c.stream)
     if rc:
@@ -260,11 +271,12 @@ def layernorm_add_bwd(h, weight, dy, lay, eps: float, dres=None, grad_scale: flo
     if dropout is not None:
         if dx is None:
             dx = _new(dy, stream)
-        d = ctypes.byref(dropout.struct(c.index))
+        d = _drop(dropout, c.index)
     elif dx is not None:
         raise ValueError("dx: only with a dropout (without one it is dh)")
+    params = c.params(weight)
     rc = _rb._load().layernorm_add_bwd(h.data_ptr(), _p(weight), at_dy, None if dres is None else c.rows(dres, "dres"),
-                                       c.H, eps, grad_scale, c.code, c.params(weight), c.layout(workspace is not None), d,
+                                       c.H, eps, grad_scale, c.code, params, c.layout(workspace is not None), d,
                                        c.rows(dh, "dh"), None if dx is None else c.rows(dx, "dx"),
                                        c.workspace(workspace), c.stream)
     if rc:
@@ -274,12 +286,10 @@ def layernorm_add_bwd(h, weight, dy, lay, eps: float, dres=None, grad_scale: flo
 
 def _dropout(fn: str, x, out, in_name: str, out_name: str, lay, dropout, stream):
     c = _Call(x, in_name, lay, stream)
-    if not isinstance(dropout, Dropout):
-        raise TypeError(f"dropout: expected Dropout, got {type(dropout).__name__}")
+    d = _drop(dropout, c.index)
     if out is None:
         out = _new(x, stream)
-    rc = getattr(_rb._load(), fn)(x.data_ptr(), c.H, c.code, c.layout(False), ctypes.byref(dropout.struct(c.index)),
-                                  c.rows(out, out_name), c.stream)
+    rc = getattr(_rb._load(), fn)(x.data_ptr(), c.H, c.code, c.layout(False), d, c.rows(out, out_name), c.stream)
     if rc:
         _rb._check(rc, fn)
     return out
