@@ -19,7 +19,10 @@ inline int resident_ctas(int regs, int threads) {
 }
 
 // What a launcher needs of its kernel, asked for once per device: the registers
-// per thread; the kernel's shared-memory limit is raised on the way.
+// per thread; the kernel's shared-memory limit is raised on the way.  The launchers
+// that keep one have internal linkage: a static of a function template with external
+// linkage is one object for the whole process, so a second copy of the library in it
+// would take the first one's kernels for its own.
 struct KernelInfo {
     std::mutex mu;
     uint64_t ready = 0;

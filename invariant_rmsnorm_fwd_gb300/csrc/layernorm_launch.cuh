@@ -7,7 +7,7 @@
 namespace rbi {
 
 template <class E, int NV, int MODE, bool DROP, bool GRADS, int MAXT, int MINB>
-int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cudaStream_t stream) {
+static int ln_launch_stream_t(const LnParams &p, int threads, const DeviceInfo &d, cudaStream_t stream) {
     auto kern = ln_stream_kernel<E, NV, MODE, DROP, GRADS, MAXT, MINB>;
     static KernelInfo info;
     int regs = 0;

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
 }
 
 template <class E, int P, int NO, int MODE, bool DROP, bool GRADS, bool RES>
-int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
+static int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
     auto kern = ln_narrow_kernel<E, P, NO, MODE, DROP, GRADS, RES>;
     constexpr int smem = kNarrowDepth<NO> * kNarrowPieces<E, NO, MODE, RES> * kNarrowThreads * 16 + (GRADS ? kNarrowThreads * 64 * NO : 0);
     DeviceInfo *d = nullptr;
