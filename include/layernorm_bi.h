@@ -36,6 +36,12 @@
  * statistics and parameter gradients are FP32; each output element is rounded
  * to its type once.  A dropped element is +0 whatever it was (NaN included).
  *
+ * Lost copies.  Rows of more than 512 columns wait for asynchronous copies, at
+ * most about one second each; a wait that runs out ends the CTA with the rest of
+ * its rows unwritten.  With a workspace RMSNORM_STATUS_TIMEOUT is set.  Calls
+ * without one (forward, dx alone) have no device-side report, of this or
+ * anything else: their outputs then keep what was there.
+ *
  * Supported hidden sizes: multiples of 8 up to 16384 for 16-bit types, up to
  * 8192 for FP32; dropout alone: multiples of 8 up to 2^20.  Data pointers are
  * 16-byte aligned, mean, rstd, the ids and the plan to 4 bytes; layout->token_stride
