@@ -135,14 +135,14 @@ __device__ __forceinline__ void drop_pairs(f2_t (&f)[P], const uint32_t (&w)[P],
         f[i] = f2_make(kept_lo(w[i], rule) ? f2_lo(v) : 0.f, kept_hi(w[i], rule) ? f2_hi(v) : 0.f);
     }
 }
-// f = f times the factor + q where kept, q elsewhere.
+// f = f times the factor + q, with f = +0 where dropped (so that -0 in q becomes +0 there, as in the sum).
 template <int P>
 __device__ __forceinline__ void drop_add_pairs(f2_t (&f)[P], const f2_t (&q)[P], const uint32_t (&w)[P], const DropRule &rule) {
     const f2_t s = f2_both(rule.scale);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const f2_t v = f2_fma(f[i], s, q[i]);
-        f[i] = f2_make(kept_lo(w[i], rule) ? f2_lo(v) : f2_lo(q[i]), kept_hi(w[i], rule) ? f2_hi(v) : f2_hi(q[i]));
+        const f2_t kept = f2_make(kept_lo(w[i], rule) ? f2_lo(f[i]) : 0.f, kept_hi(w[i], rule) ? f2_hi(f[i]) : 0.f);
+        f[i] = f2_fma(kept, s, q[i]);
     }
 }
 
