@@ -150,12 +150,11 @@ __device__ __forceinline__ void team_slots(const LnParams &p, int64_t group, con
     if constexpr (GRADS) {
         s.kind = raw.kind;
         s.block = raw.block;
-        s.partial = raw.kind == kItemWhole || (raw.kind == kItemQuarters && ((raw.quarters >> (s.slot0 / 16)) & 1));
-        if ((raw.kind == kItemWhole || raw.kind == kItemQuarters) && (raw.block < 0 || raw.block >= p.ws.n_blocks)) {
-            set_status(p.ws.hdr, kStPlan);               // a block that the workspace does not have: contributes nothing
-            s.kind = kBadItem;
-            s.partial = false;
-        }
+        // an item of a block that the workspace does not have contributes nothing
+        const bool blocked = raw.kind == kItemWhole || raw.kind == kItemQuarters;
+        const bool known = uint32_t(raw.block) < uint32_t(p.ws.n_blocks);
+        s.partial = known && (raw.kind == kItemWhole || (raw.kind == kItemQuarters && ((raw.quarters >> (s.slot0 / 16)) & 1)));
+        if (blocked && !known) set_status(p.ws.hdr, kStPlan);
     }
 #pragma unroll
     for (int o = 0; o < TeamSlots<P>::kOwn; ++o) {
@@ -460,7 +459,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NO == 1 ? 3 : 2) ln_narrow_ker
                 else if (cur.slot0 == 0) *state = uint8_t(n_groups);
             }
             __syncthreads();
-            if (cur.kind == kItemWhole) {
+            if (cur.kind == kItemWhole && cur.partial) {
                 // lane (team of the block, l): NO pairs of the block's 2 kCols sums
 #pragma unroll
                 for (int k = 0; k < NO; ++k) {
