@@ -19,7 +19,16 @@
  * numbers: as easy as 1, 2, 3", SC 2011) with key = seed (low word first) and
  * counter = (h / 8, g, offset low word, offset high word).  The mask is never
  * stored: whoever has the seed and the offset has it again, so dropout's
- * backward pass is the same function of dy.  p acts in steps of 2^-16.
+ * backward pass is the same function of dy.  p acts in steps of 2^-16 (below
+ * 2^-17 nothing is dropped).
+ *
+ * The row in the counter is the call's own logical row, tok_id * rows_per_token
+ * + head.  Ranks that number their rows locally therefore draw the SAME masks
+ * from one state, each those of rows 0, 1, 2, ...: give such ranks different
+ * seeds or offsets.  For one device's masks on several ranks, give the calls
+ * with a dropout the rows' global ids (they need no plan, and ids are not
+ * compared with n_logical_tokens there), and take the parameter gradients from
+ * layernorm_bwd under local ids, with dx NULL.
  *
  * The guarantee.  y, dx, dweight, dbias and the mask are bitwise identical for
  * the same logical token multiset whatever its physical layout.  Row sums use

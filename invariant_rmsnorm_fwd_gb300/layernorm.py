@@ -43,7 +43,9 @@ class Dropout:
     logical row and column alone.  state: CUDA int64 tensor (seed, offset), read
     when the kernel runs; a captured graph that is replayed after the state was
     changed in place draws a new mask.  Give each layer and step an offset of
-    its own.  p acts in steps of 2^-16."""
+    its own.  The logical row is the call's own (tok_id): ranks that number their
+    rows locally need different states, or calls with global ids.  p acts in
+    steps of 2^-16; below 2^-17 nothing is dropped."""
     p: float
     state: object
 
@@ -306,7 +308,9 @@ def dropout_bwd(dy, lay, dropout: Dropout, dx=None, stream=None):
 
 
 class LayerNormWorkspace:
-    """Device workspace of one reduction of dweight and dbias (allocated by PyTorch)."""
+    """Device workspace of one reduction of dweight and dbias (allocated by PyTorch).
+    It has no nodes over ranges of blocks: the sharded reduction is the RMSNorm
+    workspace's."""
 
     def __init__(self, n_logical_rows: int, hidden: int, device="cuda"):
         self.n_rows = int(n_logical_rows)
