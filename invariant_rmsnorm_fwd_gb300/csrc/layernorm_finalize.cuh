@@ -112,8 +112,8 @@ __device__ __forceinline__ Cols ln_block_value(const LnWs &ws, int64_t b, int64_
 // four of a warp meet by shuffles, the eight warps through shared memory.  All
 // loads of a pass are in flight at once.
 //
-// What bounds it: latency.  Hidden 4096, 276 blocks, about 40 MB of partials (most
-// of them still in the L2): 13 us, hidden 8192 25 us, in 4 and 8 rounds of CTAs of
+// What bounds it: latency.  Hidden 4096, 276 blocks, 1,055 partials of 304 shares, 35 MB
+// (most of them still in the L2): 13 us, hidden 8192 25 us, in 4 and 8 rounds of CTAs of
 // about 3 us each, a few dependent loads long; a later pass 2 us.  32 inputs in the
 // later passes too: three launches instead of two at hidden 4096; 32 columns a CTA,
 // 4 groups in flight at twice the CTAs, CTAs that walk over the columns: equal or

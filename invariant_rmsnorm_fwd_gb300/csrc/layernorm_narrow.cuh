@@ -14,9 +14,12 @@
 // the last) and writes one partial per block.
 //
 // Forward, memory bounds it (hidden 128, 64 M bf16 elements: 46 us, 0.87 of the copy
-// rate); backward, issue does: a row's 16-byte piece costs a lane its share of five
-// shuffles for each of four sums next to the arithmetic (102 us, 0.58).  Widths
-// between powers of two leave lanes idle (hidden 72: 0.6 and 0.37).
+// rate); backward, issue does: a row's 16-byte piece costs a lane its share of up to five
+// shuffles for each of four sums next to the arithmetic (102 us, 0.58), and nearly all
+// instances with parameter gradients spill a few registers at the 80 that three CTAs
+// leave (8 to 108 bytes of local stores and loads in bf16).  A call's last round of
+// groups may be half empty (264,960 rows of 128: 4.5 rounds).  Widths between powers of
+// two leave lanes idle (hidden 72: 0.6 and 0.37).
 #pragma once
 #include "host.cuh"
 #include "layernorm_host.cuh"
@@ -512,7 +515,8 @@ static int ln_launch_narrow_t(const LnParams &p, cudaStream_t stream) {
     return RMSNORM_OK;
 }
 
-// Lanes per row: the next power of two of hidden / 8, at least 4.
+// Lanes per row: the next power of two of hidden / 8, at least 4; rows of 257 to 512
+// columns take 32 lanes with two octets each.
 template <class E, int MODE, bool DROP, bool GRADS, bool RES>
 int ln_launch_narrow(const LnParams &p, cudaStream_t s) {
     if (p.hidden <= 32) return ln_launch_narrow_t<E, 4, 1, MODE, DROP, GRADS, RES>(p, s);

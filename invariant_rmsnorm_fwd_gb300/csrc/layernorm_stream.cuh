@@ -24,11 +24,17 @@
 // What bounds it (bf16, DRAM floor at the copy rate of 6.78 TB/s in brackets):
 // forward, hidden 4096, 17,620 rows: 50.5 us (43), 5.7 TB/s; with dropout and
 // residual add, hidden 5120, 17,620 active rows among padding: 118 us (107): memory.
+// FP32 forward of 1000 columns, 17,163 rows: 28.4 us (20): two warps a CTA, 105 registers
+// (16 warps an SM), and a ring that works as one stage less than it has, since nothing
+// is issued behind the first exchange, where the first row's stage is free already.
 // Backward with both parameter gradients, hidden 4096: 92.5 us (64); hidden 8192
 // with dropout and dres, 280 us (213): not memory but the row's chain of
 // dependent steps.  A row alone takes about 1,900 cycles (590 of them the
 // exchange, 320 the next row's sum, 300 the stores), 380 instructions a warp, and
-// 16 warps, all that 128 registers allow, hide half of it (issue slots 50 % busy).
+// 16 warps, all that 128 registers allow, hide half of it (issue slots 50 % busy);
+// CTAs of 6 or 12 warps leave 12 an SM.  Next to that the shares are uneven (hidden 4096:
+// 80 CTAs have 64 rows, 224 have 56, and the longer ones end alone), and one that starts
+// inside a block stores each of its groups there (1,055 partials for 276 blocks).
 // Fewer registers (spills), two rows at a time, a copying warp, the outputs put
 // off behind the next row and the sums asked for ahead of dx were all measured
 // slower or equal.
@@ -152,7 +158,8 @@ __device__ __forceinline__ void drop_add_pairs(f2_t (&f)[P], const f2_t (&q)[P],
 // reads of all warps' values in every thread: shorter, but more instructions.
 // Residual add with dropout in 10 warps (32,768 slots of 5120, 17,624 of them rows):
 // butterfly 125 us, reads 119; 8 warps and fewer 92 and 93; 16 warps 92 and 96;
-// forward alone and backward as slow or slower by reads.  The order of the
+// forward alone and backward as slow or slower by reads.  (CTAs of 9 warps take the
+// reads too and were not measured.)  The order of the
 // additions is the same in both, warps 8, 4, 2 and 1 apart, and for K = 2 and 4.
 // `red` is one of two alternating buffers, zero behind the CTA's warps.
 template <int K>

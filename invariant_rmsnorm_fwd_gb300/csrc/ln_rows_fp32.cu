@@ -1,4 +1,4 @@
-// Layer-norm row kernels of more than 256 columns for fp32 rows.
+// Layer-norm row kernels of more than 512 columns for fp32 rows.
 #include "layernorm_launch.cuh"
 
 template int rbi::ln_run_rows<float>(const rbi::LnParams &, bool, bool, cudaStream_t);
