@@ -68,9 +68,7 @@ def draw(rng):
     q_heads = max(1, round(_log(rng, 1, 64)))
     k_heads = rng.choice((1, q_heads, max(1, q_heads // 4), max(1, q_heads // 8)))
     pairs = rng.choice(("half", "interleaved"))
-    step = 4 if pairs == "half" else 2
-    r = rng.choice((D, D, D // 2, D // 4, step * rng.randint(1, D // step)))
-    r = max(step, r // step * step)
+    r = max(4, rng.choice((D, D, D // 2, D // 4, rng.randint(4, D))) // 4 * 4)
     most = (64 if dtype == "fp32" else 128) * 2 ** 20                 # elements in all slots
     slots = int(_log(rng, 1, max(2, min(2 ** 18, most // ((q_heads + k_heads) * D)))))
     samples = min(slots, int(_log(rng, 1, 300)))
