@@ -1,8 +1,8 @@
-"""Batch-invariant RMSNorm, layer norm and dropout for GB300 (sm_103a).
+"""Batch-invariant RMSNorm, layer norm, dropout and rotary positions for GB300 (sm_103a).
 
-Thin Python binding over the C ABI in include/rmsnorm_bi.h and
-include/layernorm_bi.h (the latter in layernorm.py): every function
-here marshals arguments and calls the library; every step of the computation
+Thin Python binding over the C ABI in include/rmsnorm_bi.h,
+include/layernorm_bi.h (in layernorm.py) and include/rotary_bi.h (in rotary.py):
+every function here marshals arguments and calls the library; every step of the computation
 runs in the library's CUDA kernels.  There is no CPU path: if the library is
 missing and cannot be built, importing the binding's functions raises.
 
@@ -54,6 +54,26 @@ class _Dropout(ctypes.Structure):
     _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_double)]
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [
+        ("position", ctypes.c_void_p),
+        ("turns", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [
+        ("input", ctypes.c_void_p), ("in_token", ctypes.c_int64), ("in_head", ctypes.c_int64),
+        ("dy", ctypes.c_void_p), ("dy_token", ctypes.c_int64), ("dy_head", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+    ]
+
+
 def library_path() -> str:
     from . import _build
     return _build.LIB
@@ -69,6 +89,7 @@ def _load():
     lib = ctypes.CDLL(path)
     P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     LP, DP = ctypes.POINTER(_Layout), ctypes.POINTER(_Dropout)
+    RP, HP = ctypes.POINTER(_Rotary), ctypes.POINTER(_Heads)
     sig = {
         "rmsnorm_fwd": ([P, P, I64, F, LP, P, P, P], ctypes.c_int),
         "rmsnorm_bwd_dx": ([P, P, P, I64, F, LP, P, P, P], ctypes.c_int),
@@ -103,6 +124,15 @@ def _load():
         "layernorm_status": ([P, P, ctypes.POINTER(I32)], ctypes.c_int),
         "dropout_fwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
         "dropout_bwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
+        "rotary_turns": ([P, I32, P], ctypes.c_int),
+        "rotary_fwd": ([HP, HP, I64, I32, LP, RP, P], ctypes.c_int),
+        "rotary_bwd": ([HP, HP, I64, I32, LP, RP, P], ctypes.c_int),
+        "qk_norm_rotary_fwd": ([HP, HP, I64, F, I32, I32, LP, RP, P], ctypes.c_int),
+        "qk_norm_rotary_bwd": ([HP, HP, I64, F, I32, I32, LP, RP, P, P], ctypes.c_int),
+        "qk_norm_workspace_bytes": ([I64, I32, I32, I64], ctypes.c_size_t),
+        "qk_norm_begin": ([P, ctypes.c_size_t, I64, I32, I32, I64, P], ctypes.c_int),
+        "qk_norm_finalize": ([P, I64, I32, I32, I64, F, P, P, P], ctypes.c_int),
+        "qk_norm_status": ([P, P, ctypes.POINTER(I32)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -516,16 +546,22 @@ def rmsnorm_bwd_noalloc(x, weight, dy, lay: CallLayout, eps: float, dx=None, dwe
     return dx, dweight
 
 
-# The layer norm and dropout binding imports torch when it loads; this package
-# does not until one of its functions is called, so these names resolve lazily.
-_LAYERNORM = ("Dropout", "LayerNormWorkspace", "dropout_bwd", "dropout_fwd", "layernorm_add_bwd", "layernorm_add_fwd",
-              "layernorm_bwd", "layernorm_fwd")
+# The bindings of these names import torch when they load; this package does not
+# until one of its functions is called, so the names resolve lazily.
+_LAZY = {
+    "layernorm": ("Dropout", "LayerNormWorkspace", "dropout_bwd", "dropout_fwd", "layernorm_add_bwd", "layernorm_add_fwd",
+                  "layernorm_bwd", "layernorm_fwd"),
+    "rotary": ("QkNormWorkspace", "Rotary", "qk_norm_rotary_bwd", "qk_norm_rotary_fwd", "rotary_bwd", "rotary_frequencies",
+               "rotary_fwd"),
+}
 
 
 def __getattr__(name):
-    if name in _LAYERNORM:
-        from . import layernorm
-        for n in _LAYERNORM:
-            globals()[n] = getattr(layernorm, n)
-        return globals()[name]
+    for module, names in _LAZY.items():
+        if name in names:
+            import importlib
+            mod = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(mod, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

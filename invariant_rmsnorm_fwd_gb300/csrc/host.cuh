@@ -18,6 +18,18 @@ struct DeviceInfo {
 int device_info(DeviceInfo **out);   // cached per device; RMSNORM_ERR_DEVICE unless sm_103
 void count_launch();                 // one more kernel of this library enqueued
 
+// Division of n < 2^31 by a divisor that the host knows: floor(n m / 2^(31+s)) with
+// s = ceil(log2 d), m = ceil(2^(31+s) / d).  m d exceeds 2^(31+s) by less than
+// d <= 2^s, so the quotient is too large by less than 2^-s <= 1 / d.
+struct Divisor {
+    uint32_t d, m, s;
+    explicit Divisor(uint32_t div) : d(div), s(0) {
+        while ((uint64_t(1) << s) < d) ++s;
+        m = uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return uint32_t((uint64_t(n) * m) >> (31 + s)); }
+};
+
 // ---------------------------------------------------------------- shapes
 
 struct Shape {

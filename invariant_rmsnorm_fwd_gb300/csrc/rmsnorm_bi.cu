@@ -335,7 +335,7 @@ extern "C" const char *rmsnorm_strerror(int code) {
         case RMSNORM_ERR_NULL: return "a required pointer is NULL";
         case RMSNORM_ERR_HIDDEN: return "hidden size not supported";
         case RMSNORM_ERR_ALIGN: return "pointer not 16-byte aligned or stride not a multiple of 8";
-        case RMSNORM_ERR_STRIDE: return "token_stride smaller than rows_per_token * hidden";
+        case RMSNORM_ERR_STRIDE: return "token_stride smaller than rows_per_token * hidden, or strides with which rows overlap";
         case RMSNORM_ERR_LAYOUT: return "invalid layout sizes";
         case RMSNORM_ERR_WORKSPACE: return "workspace too small";
         case RMSNORM_ERR_PLAN: return "dweight contribution needs a plan";

@@ -1,0 +1,300 @@
+// C-ABI entry points of the rotary operators (sm_103a), the workspace of the
+// weight gradients of the norms in front of them, and its final reduction.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "rotary_kernels.cuh"
+
+using namespace rbi;
+
+namespace {
+
+constexpr int64_t kMaxHeadDim = 512, kMaxHeads = 65535;
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// A tensor's strides.  A stride that is never taken (one slot, one head) is set to 0.
+struct Strides {
+    int64_t token, head;
+};
+Strides taken(int64_t token, int64_t head, int64_t n, int32_t heads) { return {n > 1 ? token : 0, heads > 1 ? head : 0}; }
+
+int stride_check(const Strides &s) {
+    if (s.token % 8 != 0 || s.head % 8 != 0) return RMSNORM_ERR_ALIGN;
+    return s.token < 0 || s.head < 0 ? RMSNORM_ERR_STRIDE : RMSNORM_OK;
+}
+
+// Rows of an output must not overlap: heads inside token slots or slots inside heads.
+int output_check(const Strides &s, int64_t n, int32_t heads, int64_t D) {
+    const bool heads_inside = (heads == 1 || s.head >= D) && (n == 1 || s.token >= (heads - 1) * s.head + D);
+    const bool slots_inside = (n == 1 || s.token >= D) && (heads == 1 || s.head >= (n - 1) * s.token + D);
+    return heads_inside || slots_inside ? RMSNORM_OK : RMSNORM_ERR_STRIDE;
+}
+
+bool same(const Strides &a, const Strides &b) { return a.token == b.token && a.head == b.head; }
+
+int side_check(const rmsnorm_heads_t *h, int64_t n, int64_t D, bool norm, bool bwd) {
+    if (h->heads < 1 || h->heads > kMaxHeads || h->reserved0 != 0) return RMSNORM_ERR_LAYOUT;
+    if (n == 0) return RMSNORM_OK;
+    if (!h->in || !h->out || (bwd && !h->dy)) return RMSNORM_ERR_NULL;
+    if (off16(h->in) || off16(h->out) || (bwd && off16(h->dy)) || (norm && off16(h->weight))) return RMSNORM_ERR_ALIGN;
+    const Strides in = taken(h->in_token, h->in_head, n, h->heads), out = taken(h->out_token, h->out_head, n, h->heads),
+                  dy = taken(h->dy_token, h->dy_head, n, h->heads);
+    int rc;
+    if ((rc = stride_check(in)) || (rc = stride_check(out)) || (rc = output_check(out, n, h->heads, D))) return rc;
+    if (bwd && (rc = stride_check(dy))) return rc;
+    if (h->out == h->in && !same(in, out)) return RMSNORM_ERR_STRIDE;
+    if (bwd && h->out == h->dy && !same(dy, out)) return RMSNORM_ERR_STRIDE;
+    return RMSNORM_OK;
+}
+
+HeadsParams side_params(const rmsnorm_heads_t *h, int64_t n, int chunks) {
+    HeadsParams s = {};
+    const Strides in = taken(h->in_token, h->in_head, n, h->heads), out = taken(h->out_token, h->out_head, n, h->heads),
+                  dy = taken(h->dy_token, h->dy_head, n, h->heads);
+    s.in = h->in;
+    s.dy = h->dy;
+    s.w = h->weight;
+    s.out = h->out;
+    s.in_t = in.token;
+    s.in_h = in.head;
+    s.dy_t = dy.token;
+    s.dy_h = dy.head;
+    s.out_t = out.token;
+    s.out_h = out.head;
+    s.heads = h->heads;
+    s.per = (h->heads + chunks - 1) / chunks;
+    return s;
+}
+
+int ws_sizes_check(int64_t N, int32_t hq, int32_t hk, int64_t D) {
+    if (D < 8 || D % 8 != 0 || D > kMaxHeadDim) return RMSNORM_ERR_HIDDEN;
+    if (N < 0 || N >= (int64_t(1) << 31) || hq < 1 || hk < 0 || hq > kMaxHeads || hk > kMaxHeads) return RMSNORM_ERR_LAYOUT;
+    return RMSNORM_OK;
+}
+int ws_check(const void *ws, int64_t N, int32_t hq, int32_t hk, int64_t D) {
+    if (!ws) return RMSNORM_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return RMSNORM_ERR_ALIGN;
+    return ws_sizes_check(N, hq, hk, D);
+}
+
+// mode as in rotary_run; back: turn the other way.
+int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float eps, int32_t dtype, int32_t param_dtype,
+         const rmsnorm_layout_t *L, const rmsnorm_rotary_t *r, void *workspace, int mode, bool back, rmsnorm_stream_t stream) {
+    if (dtype < LAYERNORM_BF16 || dtype > LAYERNORM_FP32 || (param_dtype != dtype && param_dtype != LAYERNORM_FP32))
+        return RMSNORM_ERR_DTYPE;
+    if (D < 8 || D % 8 != 0 || D > kMaxHeadDim) return RMSNORM_ERR_HIDDEN;
+    if (!q || !L || !r) return RMSNORM_ERR_NULL;
+    if (L->n_tokens < 0 || L->rows_per_token != 1 || L->reserved0 != 0 || L->n_logical_tokens < 0 ||
+        L->n_logical_tokens >= (int64_t(1) << 31))
+        return RMSNORM_ERR_LAYOUT;
+    if (r->rotary_dim < 4 || r->rotary_dim % 4 != 0 || r->rotary_dim > D || r->first < 0 || r->first % 2 != 0 ||
+        r->first > D - r->rotary_dim)
+        return RMSNORM_ERR_HIDDEN;
+    if (r->interleaved != 0 && r->interleaved != 1) return RMSNORM_ERR_LAYOUT;
+    if (!std::isfinite(r->scale) || !(std::isfinite(eps) && eps >= 0.f)) return RMSNORM_ERR_VALUE;
+    const int64_t n = L->n_tokens, lim = int64_t(1) << 31;
+    const bool norm = mode > 0, bwd = mode > 1;
+    int rc;
+    if ((rc = side_check(q, n, D, norm, bwd)) || (k && (rc = side_check(k, n, D, norm, bwd)))) return rc;
+    if (n >= lim || n * (q->heads + (k ? k->heads : 0)) >= lim) return RMSNORM_ERR_LAYOUT;
+    if (workspace && (rc = ws_check(workspace, L->n_logical_tokens, q->heads, k ? k->heads : 0, D))) return rc;
+    if (n == 0) return RMSNORM_OK;
+    if (!L->tok_id || !r->position || !r->turns) return RMSNORM_ERR_NULL;
+    if (off4(L->tok_id) || off4(r->position) || off16(r->turns)) return RMSNORM_ERR_ALIGN;
+    // no tensor of one side is written while the other side may still read or write it
+    if (k && (k->out == q->out || k->out == q->in || q->out == k->in || (bwd && (k->out == q->dy || q->out == k->dy))))
+        return RMSNORM_ERR_LAYOUT;
+    DeviceInfo *d = nullptr;
+    if ((rc = device_info(&d))) return rc;
+
+    RotaryParams p = {};
+    p.chunks_q = qk_chunks(q->heads);
+    p.chunks = p.chunks_q + (k ? qk_chunks(k->heads) : 0);
+    p.side[0] = side_params(q, n, p.chunks_q);
+    if (k) p.side[1] = side_params(k, n, p.chunks - p.chunks_q);
+    p.most = p.side[0].per > p.side[1].per ? p.side[0].per : p.side[1].per;
+    p.by_chunks = Divisor(uint32_t(p.chunks));
+    p.tok_id = L->tok_id;
+    p.position = r->position;
+    p.turns = r->turns;
+    p.n_tokens = n;
+    p.D = int32_t(D);
+    p.rot = r->rotary_dim;
+    p.first = r->first;
+    p.params_f32 = param_dtype == LAYERNORM_FP32 ? 1 : 0;
+    p.in_place = mode == 0 && q->out == q->in && (!k || k->out == k->in) ? 1 : 0;
+    p.scale = r->scale;
+    p.sign = back ? -1.f : 1.f;
+    p.eps = eps;
+    p.inv_d = (D & (D - 1)) == 0 ? float(1.0 / double(D)) : 0.f;
+    if (workspace) p.ws = qk_ws(workspace, L->n_logical_tokens, q->heads, k ? k->heads : 0, D);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (dtype) {
+        case LAYERNORM_BF16: return rotary_run<__nv_bfloat16>(p, mode, r->interleaved, s);
+        case LAYERNORM_FP16: return rotary_run<__half>(p, mode, r->interleaved, s);
+        default: return rotary_run<float>(p, mode, r->interleaved, s);
+    }
+}
+
+// ----------------------------------------------------------------- workspace kernels
+
+__global__ void qk_begin_kernel(QkWs ws) {
+    const int64_t tid = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, n = int64_t(gridDim.x) * blockDim.x;
+    const int64_t n16 = (reinterpret_cast<uint8_t *>(ws.partial) - reinterpret_cast<uint8_t *>(ws.flag)) / 16;
+    uint4 *f = reinterpret_cast<uint4 *>(ws.flag);
+    for (int64_t i = tid; i < n16; i += n) f[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+        ws.hdr->n_rows = ws.n;
+        ws.hdr->hidden = ws.sizes;
+        ws.hdr->n_blocks = ws.groups;
+        ws.hdr->status = 0;
+        ws.hdr->magic = kQkMagic;
+    }
+}
+
+constexpr int kFinalCtas = 8, kFinalWarps = 16;
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Both weight gradients in one launch: a cluster takes 32 columns of one of them, its
+// CTAs consecutive shares of the groups, a CTA's warps every 16th group of the share.
+// Chunks of a group from the first to the last, groups of a warp likewise, then the
+// warps, then the CTAs: an order that depends on the sizes alone.
+__global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps * 32)
+    qk_finalize_kernel(const __grid_constant__ QkWs ws, float scale, float *dq, float *dk, int slices) {
+    __shared__ float part[kFinalWarps][32];
+    __shared__ float whole[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!qk_header_ok(ws)) {                             // the same for the whole cluster
+        if (threadIdx.x == 0) qk_report(ws, kStHeader);
+        return;
+    }
+    const bool keys = int(blockIdx.x) >= slices;
+    const int col = (int(blockIdx.x) - (keys ? slices : 0)) * 32 + lane;
+    const int chunk0 = keys ? ws.chunks_q : 0, chunks = keys ? ws.chunks_k : ws.chunks_q;
+    const int64_t per = (ws.groups + kFinalCtas - 1) / kFinalCtas, g0 = blockIdx.y * per;
+    const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
+    const bool mine = col < ws.D, check = blockIdx.x == 0;
+    float acc = 0.f;
+    for (int64_t g = g0 + warp; g < g1; g += kFinalWarps) {
+        const int64_t t = g * kQkGroup + lane;
+        const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup;
+        const int32_t f = lane < n ? ws.flag[t] : 0;
+        const uint32_t in_partial = __ballot_sync(kFull, f == 1), stored = __ballot_sync(kFull, f == 2);
+        if (check && lane == 0 && (in_partial | stored) != (1u << n) - 1u) qk_report(ws, kStMissing);
+        if (!mine) continue;
+        float v = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+            float u = 0.f;
+            if (in_partial) {
+                u = ws.partial[(int64_t(chunk0 + c) * ws.groups + g) * ws.D + col];
+            } else {
+                bool first = true;
+                for (int i = 0; i < n; ++i) {
+                    if (!((stored >> i) & 1)) continue;
+                    const float x = ws.spill[(int64_t(chunk0 + c) * ws.n + g * kQkGroup + i) * ws.D + col];
+                    u = first ? x : __fadd_rn(u, x);
+                    first = false;
+                }
+            }
+            v = c ? __fadd_rn(v, u) : u;
+        }
+        acc = __fadd_rn(acc, v);
+    }
+    part[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0) {
+        float v = part[0][lane];
+#pragma unroll
+        for (int i = 1; i < kFinalWarps; ++i) v = __fadd_rn(v, part[i][lane]);
+        whole[lane] = v;
+    }
+    cluster_barrier();
+    if (blockIdx.y == 0 && warp == 0) {
+        const uint32_t at = smem_addr(&whole[lane]);
+        float v = whole[lane];
+#pragma unroll
+        for (int i = 1; i < kFinalCtas; ++i) v = __fadd_rn(v, ld_cluster_f32(map_to_rank(at, uint32_t(i))));
+        float *dst = keys ? dk : dq;
+        if (dst && mine) dst[col] = scale != 1.f ? __fmul_rn(v, scale) : v;
+    }
+    cluster_barrier();                                   // the sums stay until they are read
+}
+
+}  // namespace
+
+extern "C" int rotary_fwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t head_dim, int32_t dtype,
+                          const rmsnorm_layout_t *layout, const rmsnorm_rotary_t *rotary, rmsnorm_stream_t stream) {
+    return call(q, k, head_dim, 0.f, dtype, dtype, layout, rotary, nullptr, 0, false, stream);
+}
+
+extern "C" int rotary_bwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t head_dim, int32_t dtype,
+                          const rmsnorm_layout_t *layout, const rmsnorm_rotary_t *rotary, rmsnorm_stream_t stream) {
+    return call(q, k, head_dim, 0.f, dtype, dtype, layout, rotary, nullptr, 0, true, stream);
+}
+
+extern "C" int qk_norm_rotary_fwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t head_dim, float eps,
+                                  int32_t dtype, int32_t param_dtype, const rmsnorm_layout_t *layout,
+                                  const rmsnorm_rotary_t *rotary, rmsnorm_stream_t stream) {
+    return call(q, k, head_dim, eps, dtype, param_dtype, layout, rotary, nullptr, 1, false, stream);
+}
+
+extern "C" int qk_norm_rotary_bwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t head_dim, float eps,
+                                  int32_t dtype, int32_t param_dtype, const rmsnorm_layout_t *layout,
+                                  const rmsnorm_rotary_t *rotary, void *workspace, rmsnorm_stream_t stream) {
+    return call(q, k, head_dim, eps, dtype, param_dtype, layout, rotary, workspace, workspace ? 3 : 2, true, stream);
+}
+
+extern "C" size_t qk_norm_workspace_bytes(int64_t n_logical_tokens, int32_t q_heads, int32_t k_heads, int64_t head_dim) {
+    if (ws_sizes_check(n_logical_tokens, q_heads, k_heads, head_dim)) return 0;
+    return size_t(QkWsLayout(n_logical_tokens, q_heads, k_heads, head_dim).total);
+}
+
+extern "C" int qk_norm_begin(void *workspace, size_t bytes, int64_t n_logical_tokens, int32_t q_heads, int32_t k_heads,
+                             int64_t head_dim, rmsnorm_stream_t stream) {
+    int rc = ws_check(workspace, n_logical_tokens, q_heads, k_heads, head_dim);
+    if (rc) return rc;
+    if (bytes < qk_norm_workspace_bytes(n_logical_tokens, q_heads, k_heads, head_dim)) return RMSNORM_ERR_WORKSPACE;
+    DeviceInfo *d = nullptr;
+    if ((rc = device_info(&d))) return rc;
+    int64_t blocks = (n_logical_tokens / 4 + 255) / 256;
+    if (blocks > int64_t(d->sms) * 4) blocks = int64_t(d->sms) * 4;
+    if (blocks < 1) blocks = 1;
+    qk_begin_kernel<<<unsigned(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        qk_ws(workspace, n_logical_tokens, q_heads, k_heads, head_dim));
+    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
+    count_launch();
+    return RMSNORM_OK;
+}
+
+extern "C" int qk_norm_finalize(void *workspace, int64_t n_logical_tokens, int32_t q_heads, int32_t k_heads,
+                                int64_t head_dim, float grad_scale, float *dq_weight, float *dk_weight,
+                                rmsnorm_stream_t stream) {
+    if (!std::isfinite(grad_scale)) return RMSNORM_ERR_VALUE;
+    int rc = ws_check(workspace, n_logical_tokens, q_heads, k_heads, head_dim);
+    if (rc) return rc;
+    if (!dq_weight && !dk_weight) return RMSNORM_ERR_NULL;
+    if (dk_weight && k_heads == 0) return RMSNORM_ERR_LAYOUT;
+    if (off4(dq_weight) || off4(dk_weight)) return RMSNORM_ERR_ALIGN;
+    DeviceInfo *d = nullptr;
+    if ((rc = device_info(&d))) return rc;
+    const int slices = int(head_dim + 31) / 32;
+    qk_finalize_kernel<<<dim3(unsigned(slices * (k_heads ? 2 : 1)), kFinalCtas), kFinalWarps * 32, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(
+        qk_ws(workspace, n_logical_tokens, q_heads, k_heads, head_dim), grad_scale, dq_weight, dk_weight, slices);
+    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
+    count_launch();
+    return RMSNORM_OK;
+}
+
+extern "C" int qk_norm_status(const void *workspace, rmsnorm_stream_t stream, int32_t *status) {
+    return rmsnorm_dweight_status(workspace, stream, status);
+}

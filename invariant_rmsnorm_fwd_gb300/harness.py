@@ -37,6 +37,9 @@ class LayoutRun:
     h: object = None            # residual-add chain: h = bf16(x + r), logical order
     dh: object = None           # layer-norm chain: gradient of h, logical order
     dbias: object = None        # layer-norm chain: torch float32 [H]
+    k: object = None            # queries and keys: the keys' y, dx and weight gradient (the queries' are y, dx, dweight)
+    dk: object = None
+    dk_weight: object = None
 
 
 @dataclass
@@ -267,6 +270,52 @@ def run_layout_layernorm(lay: layout_mod.Layout, x_log, r_log, dy_log, dres_log,
                      lay.rows_per_call, whole, spill, untouched, h=outs["h"], dh=outs["dh"], dbias=db)
 
 
+def run_layout_qk_norm_rotary(lay: layout_mod.Layout, q_log, k_log, dq_log, dk_log, q_weight, k_weight, position, rotary,
+                              eps: float, grad_scale: float = 1.0, device="cuda", stream=None) -> LayoutRun:
+    """Norms of queries and keys with the rotation, and their backward pass with both weight gradients, through the
+    library, for one layout; outputs in logical order.  Tensors are [N_tok, heads, D] in logical order (k_log and what
+    belongs to it may be None), position int32 [N_tok].  Padding is filled with NaN and the outputs with a sentinel that
+    must survive there."""
+    import torch
+    import invariant_rmsnorm_fwd_gb300 as rb
+    dtype = q_log.dtype
+    word = torch.int32 if dtype == torch.float32 else torch.int16
+    n_tok, hq, D = q_log.shape
+    ws = rb.QkNormWorkspace(n_tok, hq, 0 if k_log is None else k_log.shape[1], D, device=device)
+    outs = {"y": torch.empty_like(q_log), "dx": torch.empty_like(q_log)}
+    if k_log is not None:
+        outs.update(k=torch.empty_like(k_log), dk=torch.empty_like(k_log))
+    ws.begin(stream)
+    untouched = True
+    for tok in lay.calls:
+        cl = rb.call_layout(tok, 1, lay.n_logical_tokens, device=device, with_plan=False)
+        tid = cl.tok_id.long()
+        act = tid >= 0
+
+        def place(v):
+            if v is None:
+                return None
+            t = torch.full((tok.size,) + v.shape[1:], float("nan"), dtype=dtype, device=device)
+            t[act] = v[tid[act]]
+            return t
+
+        qp, kp, dqp, dkp = (place(v) for v in (q_log, k_log, dq_log, dk_log))
+        pos = torch.full((tok.size,), -2 ** 31, dtype=torch.int32, device=device)
+        pos[act] = position[tid[act]]
+        bufs = {n: torch.full((tok.size,) + v.shape[1:], SENTINEL_BITS, dtype=word, device=device).view(dtype)
+                for n, v in outs.items()}
+        rb.qk_norm_rotary_fwd(qp, kp, q_weight, k_weight, cl, pos, rotary, eps, q_out=bufs["y"], k_out=bufs.get("k"),
+                              stream=stream)
+        rb.qk_norm_rotary_bwd(qp, kp, q_weight, k_weight, dqp, dkp, cl, pos, rotary, eps, dq=bufs["dx"],
+                              dk=bufs.get("dk"), workspace=ws, stream=stream)
+        for n in outs:
+            outs[n][tid[act]] = bufs[n][act]
+            untouched &= bool((bufs[n][~act].view(word) == SENTINEL_BITS).all())
+    dw, dkw = ws.finalize(stream=stream, grad_scale=grad_scale)
+    return LayoutRun(lay.name, outs["y"], outs["dx"], dw, ws.status(stream), len(lay.calls), lay.rows_per_call,
+                     untouched_padding=untouched, k=outs.get("k"), dk=outs.get("dk"), dk_weight=dkw)
+
+
 def run_layout_gemm(lay: layout_mod.Layout, x_log, dy_log, device="cuda", stream=None) -> LayoutRun:
     """The linear layer's deterministic weight gradient for one layout: every call
     places its tokens, one finalize forms dW.  dW is returned as the run's
@@ -300,7 +349,7 @@ def assert_batch_invariant(runs: dict, layouts: dict, reference: str = "full") -
         if name == reference:
             continue
         rep.distinct[name] = layouts_differ(layouts[reference], layouts[name])
-        for t in ("y", "dx", "dweight", "h", "dh", "dbias"):
+        for t in ("y", "dx", "dweight", "h", "dh", "dbias", "k", "dk", "dk_weight"):
             a, b = getattr(run, t), getattr(ref, t)
             if a is None and b is None:
                 continue

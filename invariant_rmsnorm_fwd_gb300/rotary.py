@@ -1,0 +1,356 @@
+"""Rotary positions of queries and keys, alone and behind an RMS norm of every head:
+binding of include/rotary_bi.h.
+
+The functions stand beside the per-head norms and take the same CallLayout, one
+row per token slot (rows_per_token = 1, no plan); queries and keys are
+[n_tokens, heads, head_dim] tensors with any token and head stride, so slices of a
+joined projection and head-major tensors need no copy.  y, dx and the weight
+gradients are bitwise the same for every physical layout of a logical token
+multiset.  Heads are bfloat16, float16 or float32 (one type per call), weights
+have that type or float32.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import torch
+
+import invariant_rmsnorm_fwd_gb300 as _rb
+
+_Heads = _rb._Heads
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _index(t) -> int:
+    """Device index of a CUDA tensor, -1 for a host tensor."""
+    return t.get_device()
+
+
+def _is_cuda(t) -> bool:
+    return t.is_cuda
+
+
+def _current() -> int:
+    return torch.cuda.current_device()
+
+
+# The raw handle of the current stream, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: float = None,
+                       low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """Radians per position of the rotary_dim / 2 pairs: base^(-2i / rotary_dim), in float64.
+
+    factor > 1 stretches the positions for contexts longer than the trained one: all
+    pairs alike (f / factor), or, with the original length, by how many turns a pair
+    makes over it: pairs of at least `high` turns keep their speed, those of at most
+    `low` are stretched in full, in between the two are mixed in proportion."""
+    if rotary_dim < 4 or rotary_dim % 4:
+        raise ValueError(f"rotary_dim: expected a positive multiple of 4, got {rotary_dim}")
+    if not (base > 0 and factor > 0):
+        raise ValueError(f"base and factor must be positive, got {base} and {factor}")
+    f = float(base) ** (-np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim)
+    if original_length is None:
+        return f / factor
+    if not (original_length > 0 and high > low):
+        raise ValueError("original_length must be positive and high above low")
+    keep = np.clip((original_length * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+    return f * keep + f * (1 - keep) / factor
+
+
+class Rotary:
+    """A rotation that a program keeps: the frequencies on the device, which columns of a
+    head turn (rotary_dim of them from `first` on) and which belong together: halves
+    (i and i + rotary_dim / 2) or neighbours (interleaved).  inv_freq: radians per position
+    of the rotary_dim / 2 pairs (rotary_frequencies by default); scale multiplies cosine
+    and sine."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, first: int = 0, inv_freq=None,
+                 scale: float = 1.0, device="cuda"):
+        self.rotary_dim, self.first, self.interleaved, self.scale = int(rotary_dim), int(first), bool(interleaved), float(scale)
+        if self.rotary_dim < 4 or self.rotary_dim % 4:
+            raise ValueError(f"rotary_dim: expected a positive multiple of 4, got {rotary_dim}")
+        if self.first < 0 or self.first % 2:
+            raise ValueError(f"first: expected an even column, got {first}")
+        if inv_freq is None:
+            inv_freq = rotary_frequencies(self.rotary_dim, base)
+        f = np.ascontiguousarray(inv_freq.cpu() if isinstance(inv_freq, torch.Tensor) else inv_freq, dtype=np.float64)
+        if f.shape != (self.rotary_dim // 2,):
+            raise ValueError(f"inv_freq: expected {self.rotary_dim // 2} frequencies, got shape {f.shape}")
+        turns = np.empty(f.size, dtype=np.uint64)
+        _rb._check(_rb._load().rotary_turns(f.ctypes.data, f.size, turns.ctypes.data), "rotary_turns")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+
+    def struct(self, position, n: int, index: int):
+        """The library's descriptor for a call of n slots on device `index`."""
+        if not isinstance(position, torch.Tensor) or position.dtype != torch.int32:
+            raise TypeError("position: expected an int32 tensor")
+        if not _is_cuda(position) or _index(position) != index:
+            raise ValueError(f"position: must be a CUDA tensor on the call's device (got {position.device})")
+        if position.dim() != 1 or position.numel() < n or not position.is_contiguous():
+            raise ValueError(f"position: expected a contiguous tensor of at least {n} positions, one per token slot")
+        if not _is_cuda(self.turns) or _index(self.turns) != index:
+            raise ValueError(f"rotary: on {self.turns.device}, the call's heads are on cuda:{index}")
+        return ctypes.byref(_rb._Rotary(position.data_ptr(), self.turns.data_ptr(), self.rotary_dim, self.first,
+                                        self.interleaved, self.scale))
+
+
+class _Call:
+    """The checks of one call's tensors.  The first one (the queries') fixes the element
+    type, the device and the head width; the others are compared with it."""
+    __slots__ = ("lay", "n", "D", "index", "dtype", "code", "param", "stream")
+
+    def __init__(self, q, name: str, lay, stream):
+        if not isinstance(lay, _rb.CallLayout):
+            raise TypeError(f"layout: expected CallLayout, got {type(lay).__name__}")
+        if not isinstance(q, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(q).__name__}")
+        if not _is_cuda(q):
+            raise ValueError(f"{name}: must be a CUDA tensor (got {q.device})")
+        if lay.rows_per_token != 1:
+            raise ValueError(f"layout: one row per token slot expected (heads are a dimension of the tensors), got "
+                             f"rows_per_token {lay.rows_per_token}")
+        self.lay, self.n, self.dtype, self.index = lay, lay.n_tokens, q.dtype, _index(q)
+        self.code = self.param = _DTYPE.get(q.dtype)
+        if self.code is None:
+            raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {q.dtype}")
+        if q.dim() != 3:
+            raise ValueError(f"{name}: expected [n_tokens, heads, head_dim], got shape {tuple(q.shape)}")
+        self.D = q.shape[2]
+        if self.index != _current():
+            raise ValueError(f"{name}: on {q.device}, the current device is cuda:{_current()}")
+        if stream is None:
+            self.stream = _raw_stream(self.index)
+        else:
+            if stream.device_index != self.index:
+                raise ValueError(f"stream: on {stream.device}, the call's heads are on {q.device}")
+            self.stream = stream.cuda_stream
+
+    def heads(self, t, name: str, heads=None):
+        """(address, token stride, head stride) of a tensor of heads."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
+        if not _is_cuda(t) or _index(t) != self.index:
+            raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {t.device})")
+        shape, st = t.shape, t.stride()
+        if len(shape) != 3 or shape[2] != self.D or st[2] != 1 or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name}: expected [n_tokens, {'heads' if heads is None else heads}, {self.D}] with unit "
+                             f"column stride, got shape {tuple(shape)} strides {tuple(st)}")
+        if shape[0] < self.n:
+            raise ValueError(f"{name}: {shape[0]} token slots, the call's layout has {self.n}")
+        return t.data_ptr(), st[0], st[1]
+
+    def weight(self, w, name: str):
+        if w is None:
+            return None
+        if not isinstance(w, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(w).__name__}")
+        if w.dtype != self.dtype and w.dtype != torch.float32:
+            raise TypeError(f"{name}: expected {self.dtype} or torch.float32, got {w.dtype}")
+        if not _is_cuda(w) or _index(w) != self.index:
+            raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {w.device})")
+        if w.dim() != 1 or w.numel() != self.D or not w.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous [{self.D}] tensor, got shape {tuple(w.shape)}")
+        self.param = _DTYPE[w.dtype]
+        return w.data_ptr()
+
+    def side(self, x, x_name, out, out_name, dy=None, dy_name="", w=None):
+        """The library's descriptor of one tensor's heads."""
+        at, ts, hs = self.heads(x, x_name)
+        heads = x.shape[1]
+        o_at, o_ts, o_hs = self.heads(out, out_name, heads)
+        d_at, d_ts, d_hs = self.heads(dy, dy_name, heads) if dy_name else (None, 0, 0)
+        return ctypes.byref(_Heads(at, ts, hs, d_at, d_ts, d_hs, o_at, o_ts, o_hs, w, heads, 0))
+
+    def layout(self):
+        n, tok = self.n, None
+        if n:
+            t = self.lay.tok_id
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+                raise TypeError("layout.tok_id: expected an int32 tensor")
+            if not _is_cuda(t) or _index(t) != self.index:
+                raise ValueError(f"layout.tok_id: must be a CUDA tensor on the call's device (got {t.device})")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"layout.tok_id: expected {n} contiguous ids")
+            tok = t.data_ptr()
+        return ctypes.byref(_rb._Layout(n, 1, 0, 0, tok, self.lay.n_logical_tokens, None, 0))
+
+    def rotary(self, rotary, position):
+        if not isinstance(rotary, Rotary):
+            raise TypeError(f"rotary: expected Rotary, got {type(rotary).__name__}")
+        return rotary.struct(position, self.n, self.index)
+
+
+def _new(like, stream):
+    """A new contiguous output with the shape of `like`, allocated on the stream that writes it, for what the
+    current stream has given back may still be in use there (rows past n_tokens and padding are left as they come)."""
+    if stream is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _tensor(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+
+
+def _rotate(fn: str, q, k, lay, position, rotary, q_out, k_out, names, stream):
+    c = _Call(q, names[0], lay, stream)
+    if k is None and k_out is not None:
+        raise ValueError(f"{names[3]}: only with {names[1]}")
+    if k is not None:
+        _tensor(k, names[1])
+    if q_out is None:
+        q_out = _new(q, stream)
+    if k_out is None and k is not None:
+        k_out = _new(k, stream)
+    qs = c.side(q, names[0], q_out, names[2])
+    ks = None if k is None else c.side(k, names[1], k_out, names[3])
+    rc = getattr(_rb._load(), fn)(qs, ks, c.D, c.code, c.layout(), c.rotary(rotary, position), c.stream)
+    if rc:
+        _rb._check(rc, fn)
+    return q_out, k_out
+
+
+def rotary_fwd(q, k, lay, position, rotary: Rotary, q_out=None, k_out=None, stream=None):
+    """Turns the heads of q and k (None: q alone) by their tokens' positions; position: int32, one per token slot.
+    Returns (q_out, k_out); in place (q_out is q) only the rotated columns are touched."""
+    return _rotate("rotary_fwd", q, k, lay, position, rotary, q_out, k_out, ("q", "k", "q_out", "k_out"), stream)
+
+
+def rotary_bwd(dq_out, dk_out, lay, position, rotary: Rotary, dq=None, dk=None, stream=None):
+    """Gradients of rotary_fwd's inputs from those of its outputs: the heads turned back (times scale)."""
+    return _rotate("rotary_bwd", dq_out, dk_out, lay, position, rotary, dq, dk, ("dq_out", "dk_out", "dq", "dk"), stream)
+
+
+def _pair_weights(c, q_weight, k_weight):
+    """Addresses of both weights, which have one type where both are given."""
+    qw, kw = c.weight(q_weight, "q_weight"), c.weight(k_weight, "k_weight")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight: expected one type")
+    return qw, kw
+
+
+def qk_norm_rotary_fwd(q, k, q_weight, k_weight, lay, position, rotary: Rotary, eps: float, q_out=None, k_out=None,
+                       stream=None):
+    """RMS norm of every head of q and k (None: q alone) with its weight (None: ones), and the rotation, in one pass
+    with one rounding.  Returns (q_out, k_out)."""
+    c = _Call(q, "q", lay, stream)
+    if k is None and (k_out is not None or k_weight is not None):
+        raise ValueError("k_out and k_weight: only with k")
+    if k is not None:
+        _tensor(k, "k")
+    if q_out is None:
+        q_out = _new(q, stream)
+    if k_out is None and k is not None:
+        k_out = _new(k, stream)
+    qw, kw = _pair_weights(c, q_weight, k_weight)
+    qs = c.side(q, "q", q_out, "q_out", w=qw)
+    ks = None if k is None else c.side(k, "k", k_out, "k_out", w=kw)
+    rc = _rb._load().qk_norm_rotary_fwd(qs, ks, c.D, eps, c.code, c.param, c.layout(), c.rotary(rotary, position), c.stream)
+    if rc:
+        _rb._check(rc, "qk_norm_rotary_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rotary_bwd(q, k, q_weight, k_weight, dq_out, dk_out, lay, position, rotary: Rotary, eps: float, dq=None,
+                       dk=None, workspace=None, stream=None):
+    """Backward of qk_norm_rotary_fwd (q and k are its inputs).  With a workspace the same pass adds the call's tokens
+    to both weight gradients.  Returns (dq, dk); dq may be q or dq_out, dk likewise."""
+    c = _Call(q, "q", lay, stream)
+    if k is None and (dk is not None or dk_out is not None or k_weight is not None):
+        raise ValueError("dk, dk_out and k_weight: only with k")
+    if k is not None:
+        _tensor(k, "k")
+    if dq is None:
+        dq = _new(q, stream)
+    if dk is None and k is not None:
+        dk = _new(k, stream)
+    qw, kw = _pair_weights(c, q_weight, k_weight)
+    qs = c.side(q, "q", dq, "dq", dq_out, "dq_out", qw)
+    ks = None if k is None else c.side(k, "k", dk, "dk", dk_out, "dk_out", kw)
+    ws = None
+    if workspace is not None:
+        if not isinstance(workspace, QkNormWorkspace):
+            raise TypeError(f"workspace: expected QkNormWorkspace, got {type(workspace).__name__}")
+        if _index(workspace.buf) != c.index:
+            raise ValueError(f"workspace: on {workspace.buf.device}, the call's heads are on cuda:{c.index}")
+        mine = (lay.n_logical_tokens, q.shape[1], 0 if k is None else k.shape[1], c.D)
+        if workspace.sizes != mine:
+            raise ValueError(f"workspace: for (tokens, query heads, key heads, head_dim) {workspace.sizes}, the call has {mine}")
+        ws = workspace.buf.data_ptr()
+    rc = _rb._load().qk_norm_rotary_bwd(qs, ks, c.D, eps, c.code, c.param, c.layout(), c.rotary(rotary, position), ws,
+                                        c.stream)
+    if rc:
+        _rb._check(rc, "qk_norm_rotary_bwd")
+    return dq, dk
+
+
+class QkNormWorkspace:
+    """Device workspace of one reduction of the weight gradients of the norms of queries and keys (k_heads = 0:
+    queries alone), allocated by PyTorch.  begin, any number of qk_norm_rotary_bwd calls that hold every logical
+    token exactly once in all, finalize."""
+
+    def __init__(self, n_logical_tokens: int, q_heads: int, k_heads: int, head_dim: int, device="cuda"):
+        self.sizes = (int(n_logical_tokens), int(q_heads), int(k_heads), int(head_dim))
+        self.bytes = int(_rb._load().qk_norm_workspace_bytes(*self.sizes))
+        if self.bytes == 0:
+            raise _rb.RmsNormError(-2, "qk_norm_workspace_bytes")
+        self.buf = torch.empty(self.bytes, dtype=torch.uint8, device=device)
+        if self.buf.data_ptr() % 256:
+            raise RuntimeError("workspace allocation is not 256-byte aligned")
+
+    def _stream(self, stream) -> int:
+        index = _index(self.buf)
+        if index != _current():
+            raise ValueError(f"workspace: on {self.buf.device}, the current device is cuda:{_current()}")
+        if stream is None:
+            return _raw_stream(index)
+        if stream.device_index != index:
+            raise ValueError(f"stream: on {stream.device}, the workspace is on {self.buf.device}")
+        return stream.cuda_stream
+
+    def _gradient(self, t, name: str, stream):
+        D = self.sizes[3]
+        if t is None:
+            if stream is None:
+                return torch.empty(D, dtype=torch.float32, device=self.buf.device)
+            with torch.cuda.stream(stream):
+                return torch.empty(D, dtype=torch.float32, device=self.buf.device)
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name}: expected a float32 tensor")
+        if not _is_cuda(t) or _index(t) != _index(self.buf) or not t.is_contiguous() or t.numel() < D:
+            raise ValueError(f"{name}: expected a contiguous tensor of at least {D} elements on {self.buf.device}")
+        return t
+
+    def begin(self, stream=None):
+        rc = _rb._load().qk_norm_begin(self.buf.data_ptr(), self.bytes, *self.sizes, self._stream(stream))
+        if rc:
+            _rb._check(rc, "qk_norm_begin")
+
+    def finalize(self, dq_weight=None, dk_weight=None, stream=None, grad_scale: float = 1.0):
+        """(dq_weight, dk_weight) of the reduction, each root multiplied once by grad_scale; without keys
+        dk_weight is None."""
+        at = self._stream(stream)
+        dq_weight = self._gradient(dq_weight, "dq_weight", stream)
+        if self.sizes[2]:
+            dk_weight = self._gradient(dk_weight, "dk_weight", stream)
+        elif dk_weight is not None:
+            raise ValueError("dk_weight: the workspace has no keys")
+        rc = _rb._load().qk_norm_finalize(self.buf.data_ptr(), *self.sizes, grad_scale, dq_weight.data_ptr(),
+                                          None if dk_weight is None else dk_weight.data_ptr(), at)
+        if rc:
+            _rb._check(rc, "qk_norm_finalize")
+        return dq_weight, dk_weight
+
+    def status(self, stream=None) -> int:
+        out = ctypes.c_int32(0)
+        _rb._check(_rb._load().qk_norm_status(self.buf.data_ptr(), self._stream(stream), ctypes.byref(out)),
+                   "qk_norm_status")
+        return int(out.value)

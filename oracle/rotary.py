@@ -1,0 +1,162 @@
+"""FP64 oracle of the rotary operators (TEST INFRASTRUCTURE ONLY).
+
+Plain numpy in float64 from the closed forms; shares no code with the CUDA
+library.  Besides the values it returns, element by element, how far an FP32
+evaluation of the same formulas may be from them, and replays the order of the
+weight gradients in float32.
+
+Arrays are [tokens, heads, D].  U is the relative rounding error of one FP32
+operation.  A cosine or sine of the kernels is off by at most 4 U: the angle by
+2 pi (2^-32 + 2^-34) = 0.03 U (top 32 bits of the fraction of a turn; turns per
+position rounded to 2^-65, positions below 2^31), the Taylor polynomials by 0.03 U,
+their roundings by less than 2 U (sine) and 3 U (cosine); the product with scale
+adds one more rounding.
+"""
+from __future__ import annotations
+
+from fractions import Fraction
+
+import numpy as np
+
+U = 2.0 ** -24
+ANGLE = 5               # U of a cosine or sine, times scale
+RSTD = 12               # U of 1 / rms: a sum of squares of depth 15, halved by the root, and four roundings
+
+# 1 / (2 pi) to 400 bits, from Machin's formula in integers
+def _inverse_turn(bits: int = 400) -> Fraction:
+    one = 1 << (bits + 16)
+
+    def arctan_inverse(n):
+        total, power, k = 0, one // n, 0
+        while power:
+            total += (-1) ** k * (power // (2 * k + 1))
+            power //= n * n
+            k += 1
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    return Fraction(one, 2 * pi)
+
+
+INVERSE_TURN = _inverse_turn()
+
+
+def turns(frequency: float) -> Fraction:
+    """Turns per position of a frequency in radians per position."""
+    return Fraction(float(frequency)) * INVERSE_TURN
+
+
+def cos_sin_far(position: int, frequency: float):
+    """Cosine and sine at any position: the fraction of a turn exactly, then float64."""
+    t = turns(frequency) * int(position)
+    t -= round(t)
+    a = 2 * np.pi * float(t)
+    return np.cos(a), np.sin(a)
+
+
+def pairs(rotary_dim: int, first: int, interleaved: bool):
+    i = np.arange(rotary_dim // 2)
+    return (first + 2 * i, first + 2 * i + 1) if interleaved else (first + i, first + rotary_dim // 2 + i)
+
+
+def rotate(x, position, freq, rotary_dim, first, interleaved, scale=1.0, back=False):
+    """(y, err) of [T, H, D] heads at positions [T] (|position| up to 2^20 or so)."""
+    x = np.asarray(x, dtype=np.float64)
+    a, b = pairs(rotary_dim, first, interleaved)
+    angle = np.asarray(position, dtype=np.float64)[:, None] * np.asarray(freq)[None, :]
+    c, s = (scale * np.cos(angle))[:, None], (scale * np.sin(angle))[:, None]
+    if back:
+        s = -s
+    y, err = x.copy(), np.zeros_like(x)
+    xa, xb = x[..., a], x[..., b]
+    y[..., a], y[..., b] = xa * c - xb * s, xb * c + xa * s
+    e = (ANGLE + 2) * U * abs(scale) * (np.abs(xa) + np.abs(xb))
+    err[..., a], err[..., b] = e, e
+    return y, err
+
+
+def _spread(v, rotary_dim, first, interleaved, scale):
+    """Per element: the sizes that meet in a rotated element (its own column's outside)."""
+    a, b = pairs(rotary_dim, first, interleaved)
+    out = np.abs(v).copy()
+    both = abs(scale) * (np.abs(v[..., a]) + np.abs(v[..., b]))
+    out[..., a], out[..., b] = both, both
+    return out
+
+
+def forward(x, w, position, freq, rotary_dim, first, interleaved, scale, eps):
+    """(y, err) of norm and rotation: z = x rstd w is off by (RSTD + 2) U of itself."""
+    x = np.asarray(x, dtype=np.float64)
+    rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    z = x * rstd * w
+    y, err = rotate(z, position, freq, rotary_dim, first, interleaved, scale)
+    return y, err + (RSTD + 2) * U * _spread(z, rotary_dim, first, interleaved, scale)
+
+
+def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, eps, groups=None):
+    """(dx, dweight, err_dx, err_dw), dx unrounded.
+
+    g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
+    (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
+    8 tokens, the chunks, the groups of a warp, 16 warps and 8 CTAs."""
+    x = np.asarray(x, dtype=np.float64)
+    D = x.shape[-1]
+    rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    xhat = x * rstd
+    g, eg = rotate(dy, position, freq, rotary_dim, first, interleaved, scale, back=True)
+    a = g * w
+    ea = np.abs(w) * eg + U * np.abs(a)
+    m = (a * xhat).mean(-1, keepdims=True)
+    em = rstd * ((np.abs(x) * ea).sum(-1, keepdims=True) + 15 * U * np.abs(a * x).sum(-1, keepdims=True)) / D \
+        + (RSTD + 2) * U * np.abs(m)
+    t = a - xhat * m
+    dx = rstd * t
+    et = ea + np.abs(xhat) * em + (RSTD + 1) * U * np.abs(xhat * m) + U * np.abs(t)
+    err = rstd * et + (RSTD + 1) * U * np.abs(dx)
+    term = g * xhat
+    n = x.shape[0]
+    chain = 8 + 8 + (x.shape[1] + 7) // 8 + (n + 1023) // 1024 + 24
+    err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
+    return dx, term.sum((0, 1)), err, err_dw
+
+
+def rounded(err, ref, dtype: str):
+    """Bound after one rounding to the type: half a step of the value (bf16 2^-8, fp16 2^-11 of it),
+    or half the smallest subnormal, on top of the FP32 error."""
+    half, tiny = {"bfloat16": (2.0 ** -8, 2.0 ** -134), "float16": (2.0 ** -11, 2.0 ** -25), "float32": (0.0, 0.0)}[dtype]
+    return err + half * (np.abs(ref) + err) + tiny
+
+
+def grad_replay(leaf: np.ndarray) -> np.ndarray:
+    """float32 replay of a weight gradient's order for exact leaves g xhat [tokens, heads, D]."""
+    leaf = leaf.astype(np.float32)
+    n, heads, D = leaf.shape
+    chunks = (heads + 7) // 8
+    per = (heads + chunks - 1) // chunks
+    groups = (n + 7) // 8
+    value = []
+    for g in range(groups):
+        v = None
+        for c in range(chunks):
+            u = None
+            for t in range(8 * g, min(8 * g + 8, n)):
+                s = np.zeros(D, np.float32)
+                for h in range(c * per, min(c * per + per, heads)):
+                    s = s + leaf[t, h]
+                u = s if u is None else u + s
+            v = u if v is None else v + u
+        value.append(v)
+    share = (groups + 7) // 8
+    total = None
+    for r in range(8):
+        warps = []
+        for w in range(16):
+            acc = np.zeros(D, np.float32)
+            for g in range(r * share + w, min((r + 1) * share, groups), 16):
+                acc = acc + value[g]
+            warps.append(acc)
+        s = warps[0]
+        for w in range(1, 16):
+            s = s + warps[w]
+        total = s if total is None else total + s
+    return total
