@@ -23,9 +23,9 @@
  * The guarantee.  Every output is bitwise identical for the same logical token
  * multiset whatever its physical layout (and whatever the strides).  Row sums
  * use a fixed tree that depends only on D and the rotary parameters.  A weight
- * gradient is summed in canonical order: the heads of a token in chunks of at
- * most 8 (ceil(heads / 8) chunks of equal size, the last one shorter), from the
- * first to the last head of the chunk; 8 logical tokens of a group from the
+ * gradient is summed in canonical order: a token's heads, queries then keys, in
+ * ceil(heads / 8) chunks of equal size (the last one shorter), each from its
+ * first to its last head of the kind; 8 logical tokens of a group from the
  * first to the last; then chunks and groups by a fixed tree over their number.
  * Groups that a call does not hold whole and in consecutive slots leave their
  * tokens' sums in the workspace, and qk_norm_finalize adds them in the same
@@ -50,7 +50,7 @@ extern "C" {
 #endif
 
 /*
- * The rotation of a call.  position: DEVICE int32, one per token slot (not read
+ * The rotation of a call.  position: DEVICE int32, one per token slot (any value
  * in padding).  turns: DEVICE array (16-byte aligned) of rotary_dim / 2 words, the
  * turns per position of pair i in units of 2^-64 turn (rotary_turns).  scale multiplies
  * cos and sin (1 unless a long-context scaling asks for another factor).
@@ -68,7 +68,7 @@ typedef struct rmsnorm_rotary {
  * The heads of one tensor (queries or keys) in a call.  Head h of token slot t
  * starts at element t * token_stride + h * head_stride of its tensor, so slices
  * of a joined projection and head-major tensors need no copy.  Data pointers are
- * 16-byte aligned and strides multiples of 8 and not negative; strides of inputs
+ * 16-byte aligned (FP32: 32) and strides multiples of 8 and not negative; strides of inputs
  * may be 0 (one head or token read by all), outputs may not overlap themselves.
  * A stride that is never taken (one slot, one head) is not looked at.  out may
  * be `in` or `dy` with that tensor's strides (other overlaps are not allowed).

@@ -14,6 +14,7 @@ namespace {
 constexpr int64_t kMaxHeadDim = 512, kMaxHeads = 65535;
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) != 0; }
 bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // A tensor's strides.  A stride that is never taken (one slot, one head) is set to 0.
@@ -36,11 +37,15 @@ int output_check(const Strides &s, int64_t n, int32_t heads, int64_t D) {
 
 bool same(const Strides &a, const Strides &b) { return a.token == b.token && a.head == b.head; }
 
-int side_check(const rmsnorm_heads_t *h, int64_t n, int64_t D, bool norm, bool bwd) {
+// Data pointers start on whole vectors of 8 elements.
+bool off_data(const void *p, int32_t dtype) { return dtype == LAYERNORM_FP32 ? off32(p) : off16(p); }
+
+int side_check(const rmsnorm_heads_t *h, int64_t n, int64_t D, int32_t dtype, bool norm, bool bwd) {
     if (h->heads < 1 || h->heads > kMaxHeads || h->reserved0 != 0) return RMSNORM_ERR_LAYOUT;
     if (n == 0) return RMSNORM_OK;
     if (!h->in || !h->out || (bwd && !h->dy)) return RMSNORM_ERR_NULL;
-    if (off16(h->in) || off16(h->out) || (bwd && off16(h->dy)) || (norm && off16(h->weight))) return RMSNORM_ERR_ALIGN;
+    if (off_data(h->in, dtype) || off_data(h->out, dtype) || (bwd && off_data(h->dy, dtype)) || (norm && off16(h->weight)))
+        return RMSNORM_ERR_ALIGN;
     const Strides in = taken(h->in_token, h->in_head, n, h->heads), out = taken(h->out_token, h->out_head, n, h->heads),
                   dy = taken(h->dy_token, h->dy_head, n, h->heads);
     int rc;
@@ -51,7 +56,7 @@ int side_check(const rmsnorm_heads_t *h, int64_t n, int64_t D, bool norm, bool b
     return RMSNORM_OK;
 }
 
-HeadsParams side_params(const rmsnorm_heads_t *h, int64_t n, int chunks) {
+HeadsParams side_params(const rmsnorm_heads_t *h, int64_t n) {
     HeadsParams s = {};
     const Strides in = taken(h->in_token, h->in_head, n, h->heads), out = taken(h->out_token, h->out_head, n, h->heads),
                   dy = taken(h->dy_token, h->dy_head, n, h->heads);
@@ -65,8 +70,6 @@ HeadsParams side_params(const rmsnorm_heads_t *h, int64_t n, int chunks) {
     s.dy_h = dy.head;
     s.out_t = out.token;
     s.out_h = out.head;
-    s.heads = h->heads;
-    s.per = (h->heads + chunks - 1) / chunks;
     return s;
 }
 
@@ -99,7 +102,7 @@ int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float ep
     const int64_t n = L->n_tokens, lim = int64_t(1) << 31;
     const bool norm = mode > 0, bwd = mode > 1;
     int rc;
-    if ((rc = side_check(q, n, D, norm, bwd)) || (k && (rc = side_check(k, n, D, norm, bwd)))) return rc;
+    if ((rc = side_check(q, n, D, dtype, norm, bwd)) || (k && (rc = side_check(k, n, D, dtype, norm, bwd)))) return rc;
     if (n >= lim || n * (q->heads + (k ? k->heads : 0)) >= lim) return RMSNORM_ERR_LAYOUT;
     if (workspace && (rc = ws_check(workspace, L->n_logical_tokens, q->heads, k ? k->heads : 0, D))) return rc;
     if (n == 0) return RMSNORM_OK;
@@ -112,12 +115,10 @@ int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float ep
     if ((rc = device_info(&d))) return rc;
 
     RotaryParams p = {};
-    p.chunks_q = qk_chunks(q->heads);
-    p.chunks = p.chunks_q + (k ? qk_chunks(k->heads) : 0);
-    p.side[0] = side_params(q, n, p.chunks_q);
-    if (k) p.side[1] = side_params(k, n, p.chunks - p.chunks_q);
-    p.most = p.side[0].per > p.side[1].per ? p.side[0].per : p.side[1].per;
-    p.by_chunks = Divisor(uint32_t(p.chunks));
+    p.side[0] = side_params(q, n);
+    if (k) p.side[1] = side_params(k, n);
+    p.hq = q->heads;
+    p.heads = q->heads + (k ? k->heads : 0);
     p.tok_id = L->tok_id;
     p.position = r->position;
     p.turns = r->turns;
@@ -163,14 +164,40 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ float4 plus(const float4 &a, const float4 &b) {
+    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
+// A group's sum of four columns over the partial sums `slots` from its tokens' own.
+__device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool check) {
+    const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < slots; ++c) {
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool some = false;
+        for (int i = 0; i < n; ++i) {
+            const int64_t t = g * kQkGroup + i;
+            if (ws.flag[t] != 2) {
+                if (check && c == 0) qk_report(ws, kStMissing);
+                continue;
+            }
+            const float4 x = *reinterpret_cast<const float4 *>(ws.spill + ((slot0 + c) * ws.n + t) * ws.D + col);
+            u = some ? plus(u, x) : x;
+            some = true;
+        }
+        v = c ? plus(v, u) : u;
+    }
+    return v;
+}
 
 // Both weight gradients in one launch: a cluster takes 32 columns of one of them, its
-// CTAs consecutive shares of the groups, a CTA's warps every 16th group of the share.
-// Chunks of a group from the first to the last, groups of a warp likewise, then the
-// warps, then the CTAs: an order that depends on the sizes alone.
+// 8 CTAs x 16 warps x 4 eighth-warps consecutive shares of the groups.  The partial sums
+// of a group from the first chunk to the last, the groups of a share likewise, then the
+// four shares of a warp in pairs, the warps, the CTAs: an order that depends on the sizes
+// alone.
 __global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps * 32)
     qk_finalize_kernel(const __grid_constant__ QkWs ws, float scale, float *dq, float *dk, int slices) {
-    __shared__ float part[kFinalWarps][32];
+    __shared__ float4 part[kFinalWarps][8];
     __shared__ float whole[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (!qk_header_ok(ws)) {                             // the same for the whole cluster
@@ -178,43 +205,47 @@ __global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps
         return;
     }
     const bool keys = int(blockIdx.x) >= slices;
-    const int col = (int(blockIdx.x) - (keys ? slices : 0)) * 32 + lane;
-    const int chunk0 = keys ? ws.chunks_q : 0, chunks = keys ? ws.chunks_k : ws.chunks_q;
-    const int64_t per = (ws.groups + kFinalCtas - 1) / kFinalCtas, g0 = blockIdx.y * per;
+    const int col0 = (int(blockIdx.x) - (keys ? slices : 0)) * 32, col = col0 + (lane & 7) * 4;
+    const int slot0 = keys ? ws.cut.q_slots : 0, slots = keys ? ws.cut.slots - ws.cut.q_slots : ws.cut.q_slots;
+    constexpr int kShares = kFinalCtas * kFinalWarps * 4;
+    const int64_t per = (ws.groups + kShares - 1) / kShares;
+    const int64_t g0 = ((int64_t(blockIdx.y) * kFinalWarps + warp) * 4 + (lane >> 3)) * per;
     const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
-    const bool mine = col < ws.D, check = blockIdx.x == 0;
-    float acc = 0.f;
-    for (int64_t g = g0 + warp; g < g1; g += kFinalWarps) {
-        const int64_t t = g * kQkGroup + lane;
-        const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup;
-        const int32_t f = lane < n ? ws.flag[t] : 0;
-        const uint32_t in_partial = __ballot_sync(kFull, f == 1), stored = __ballot_sync(kFull, f == 2);
-        if (check && lane == 0 && (in_partial | stored) != (1u << n) - 1u) qk_report(ws, kStMissing);
-        if (!mine) continue;
-        float v = 0.f;
-        for (int c = 0; c < chunks; ++c) {
-            float u = 0.f;
-            if (in_partial) {
-                u = ws.partial[(int64_t(chunk0 + c) * ws.groups + g) * ws.D + col];
-            } else {
-                bool first = true;
-                for (int i = 0; i < n; ++i) {
-                    if (!((stored >> i) & 1)) continue;
-                    const float x = ws.spill[(int64_t(chunk0 + c) * ws.n + g * kQkGroup + i) * ws.D + col];
-                    u = first ? x : __fadd_rn(u, x);
-                    first = false;
-                }
+    const bool check = blockIdx.x == 0 && (lane & 7) == 0;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < ws.D) {
+        const float *src = ws.partial + int64_t(slot0) * ws.groups * ws.D + col;
+        constexpr int kAhead = 4;                        // groups of a batch of loads
+        for (int64_t g = g0; g < g1; g += kAhead) {
+            int32_t there[kAhead];
+            float4 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) there[j] = g + j < g1 ? ws.whole[g + j] : 0;
+            // (a partial that is not there is read all the same: its memory is)
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) v[j] = g + j < g1 ? *reinterpret_cast<const float4 *>(src + (g + j) * ws.D) : acc;
+            for (int c = 1; c < slots; ++c) {
+                const float *s = src + c * ws.groups * ws.D;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (g + j < g1) v[j] = plus(v[j], *reinterpret_cast<const float4 *>(s + (g + j) * ws.D));
             }
-            v = c ? __fadd_rn(v, u) : u;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (g + j < g1) acc = plus(acc, there[j] ? v[j] : qk_loose_group(ws, g + j, slot0, slots, col, check));
         }
-        acc = __fadd_rn(acc, v);
     }
-    part[warp][lane] = acc;
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1)
+        acc = plus(acc, make_float4(__shfl_xor_sync(kFull, acc.x, o), __shfl_xor_sync(kFull, acc.y, o),
+                                    __shfl_xor_sync(kFull, acc.z, o), __shfl_xor_sync(kFull, acc.w, o)));
+    if (lane < 8) part[warp][lane] = acc;
     __syncthreads();
     if (warp == 0) {
-        float v = part[0][lane];
+        const float *f = reinterpret_cast<const float *>(part);
+        float v = f[lane];
 #pragma unroll
-        for (int i = 1; i < kFinalWarps; ++i) v = __fadd_rn(v, part[i][lane]);
+        for (int i = 1; i < kFinalWarps; ++i) v = __fadd_rn(v, f[i * 32 + lane]);
         whole[lane] = v;
     }
     cluster_barrier();
@@ -224,7 +255,7 @@ __global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps
 #pragma unroll
         for (int i = 1; i < kFinalCtas; ++i) v = __fadd_rn(v, ld_cluster_f32(map_to_rank(at, uint32_t(i))));
         float *dst = keys ? dk : dq;
-        if (dst && mine) dst[col] = scale != 1.f ? __fmul_rn(v, scale) : v;
+        if (dst && col0 + lane < ws.D) dst[col0 + lane] = scale != 1.f ? __fmul_rn(v, scale) : v;
     }
     cluster_barrier();                                   // the sums stay until they are read
 }

@@ -2,11 +2,12 @@
 // head, and their backward pass (sm_103a): what the kernels share, and the row
 // kernels.
 //
-// A head is held by a team of lanes, 16 columns a lane: always both columns of
-// its 8 pairs, so the rotation needs no exchange between lanes.  In the half
-// layout a lane has 8 columns of the first half and the 8 that go with them, else 16 in a
-// row.  A team stays with one token and walks over a chunk of its heads, so the
-// lane's 8 sines and cosines are formed once per chunk.
+// A head is held by a team of lanes, two vectors of 8 columns a lane.  Where the
+// halves of the rotation are made of whole vectors a lane has the two that turn into
+// each other, so the rotation needs no exchange between lanes; neighbouring pairs lie
+// inside a vector anyway; halves of other sizes fetch their partners from shared
+// memory.  A team stays with one token and walks over a chunk of its heads, queries
+// and keys alike, so the lane's cosines and sines are formed once per chunk.
 #pragma once
 #include <type_traits>
 
@@ -16,30 +17,48 @@
 
 namespace rbi {
 
-constexpr int kChunkHeads = 8;                           // most heads of a chunk of the weight gradients' order
-constexpr int kQkGroup = 8;                              // logical tokens of a group of that order
+constexpr int kChunkHeads = 8;                           // most heads of a chunk
+constexpr int kQkGroup = 8;                              // logical tokens of a group of the weight gradients' order
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
 
-inline int qk_chunks(int heads) { return (heads + kChunkHeads - 1) / kChunkHeads; }
+// The heads of a token, queries then keys, are cut into chunks of equal size (the last
+// one shorter).  A chunk that holds both kinds has a partial sum of each: slots of the
+// queries' chunks come first, then those of the chunks that hold keys.
+struct QkChunks {
+    int32_t chunks, per;             // chunks of a token, heads of a chunk
+    int32_t q_slots, k_first, slots; // chunks with queries; first chunk with keys; all partial sums
+    QkChunks() = default;
+    QkChunks(int32_t hq, int32_t hk) {
+        const int32_t all = hq + hk;
+        chunks = (all + kChunkHeads - 1) / kChunkHeads;
+        per = (all + chunks - 1) / chunks;
+        q_slots = (hq + per - 1) / per;
+        k_first = hq / per;
+        slots = q_slots + (hk ? chunks - k_first : 0);
+    }
+};
 
 struct QkWs {
     WsHeader *hdr;                   // n_rows tokens; hidden = the sizes (qk_sizes)
     int32_t *flag;                   // [N] 0 nothing, 1 in its group's partial, 2 its own sums stored
-    float *partial;                  // [chunks of q, then k][groups][D]
-    float *spill;                    // [chunks][N][D]: a token's sums
+    int32_t *whole;                  // [groups] 1: the group's partial is there
+    float *partial;                  // [slots][groups][D]
+    float *spill;                    // [slots][N][D]: a token's sums
     int64_t n, groups, sizes;
-    int32_t chunks_q, chunks_k, D;
+    QkChunks cut;
+    int32_t D;
 };
 
 inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(hq) << 16 | int64_t(hk) << 32; }
 
 struct QkWsLayout {
-    int64_t off_partial, off_spill, total;
+    int64_t off_whole, off_partial, off_spill, total;
     QkWsLayout(int64_t N, int32_t hq, int32_t hk, int64_t D) {
-        const int64_t chunks = qk_chunks(hq) + qk_chunks(hk), groups = (N + kQkGroup - 1) / kQkGroup;
-        off_partial = align256(256 + N * 4);
-        off_spill = align256(off_partial + chunks * groups * D * 4);
-        total = align256(off_spill + chunks * N * D * 4);
+        const int64_t slots = QkChunks(hq, hk).slots, groups = (N + kQkGroup - 1) / kQkGroup;
+        off_whole = align256(256 + N * 4);
+        off_partial = align256(off_whole + groups * 4);
+        off_spill = align256(off_partial + slots * groups * D * 4);
+        total = align256(off_spill + slots * N * D * 4);
     }
 };
 
@@ -49,13 +68,13 @@ inline QkWs qk_ws(void *base, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     QkWs w;
     w.hdr = reinterpret_cast<WsHeader *>(b);
     w.flag = reinterpret_cast<int32_t *>(b + 256);
+    w.whole = reinterpret_cast<int32_t *>(b + L.off_whole);
     w.partial = reinterpret_cast<float *>(b + L.off_partial);
     w.spill = reinterpret_cast<float *>(b + L.off_spill);
     w.n = N;
     w.groups = (N + kQkGroup - 1) / kQkGroup;
     w.sizes = qk_sizes(D, hq, hk);
-    w.chunks_q = qk_chunks(hq);
-    w.chunks_k = qk_chunks(hk);
+    w.cut = QkChunks(hq, hk);
     w.D = int32_t(D);
     return w;
 }
@@ -72,7 +91,6 @@ struct HeadsParams {                 // one tensor's heads; strides in elements
     const void *in, *dy, *w;
     void *out;
     int64_t in_t, in_h, dy_t, dy_h, out_t, out_h;
-    int32_t heads, per;              // heads; heads of a chunk
 };
 
 struct RotaryParams {
@@ -81,66 +99,56 @@ struct RotaryParams {
     const uint64_t *turns;
     int64_t n_tokens;
     int32_t D, rot, first;
-    int32_t chunks_q, chunks;        // chunks of the queries, of both
-    int32_t team;                    // lanes of a head
-    int32_t most;                    // most heads of a chunk
+    int32_t hq, heads;               // query heads, heads of both
+    int32_t chunks, per;             // chunks of a token, heads of a chunk
+    int32_t lanes, team;             // lanes of a head that hold columns; lanes of a team
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
+    uint32_t units;                  // teams' (warps') pieces of work
     float scale, sign;               // sign: of the sine (-1 turns back)
     float eps, inv_d;
-    uint32_t units;                  // teams' (warps') pieces of work
     Divisor by_chunks{1}, by_team{1};
     QkWs ws;
 };
 
 // ----------------------------------------------------------------- a lane's columns
 
-// WIDE: two vectors of 8 columns, at[0] and at[1].  Else (rotary sizes that are not
-// made of whole vectors) eight pieces of two columns: at[0..3] go with the first
-// vector's pairs of registers, at[4..7] with the second's.  -1: nothing there.
-template <bool INTER, bool WIDE>
+// Which columns turn into each other.  kHalf: halves made of whole vectors; kNear:
+// neighbouring columns; kSplit: halves that begin or end inside a vector.
+enum { kHalf = 0, kNear = 1, kSplit = 2 };
+
+template <int PAIRS>
 struct LaneColumns {
-    int32_t at[WIDE ? 2 : 8];
-    int32_t turned;                  // the lane's first `turned` pairs rotate, 8 lane .. of the head
+    int32_t at[2];                   // first columns of the lane's vectors, -1: none
+    uint32_t turned;                 // bit i: register pair i (0..3 first vector, 4..7 second) turns
 };
 
-__device__ __forceinline__ int outside(int e, int first, int rot) { return e < first ? e : e + rot; }
-
-template <bool INTER, bool WIDE>
-__device__ __forceinline__ LaneColumns<INTER, WIDE> lane_columns(int lane, int D, int rot, int first, bool in_place) {
-    LaneColumns<INTER, WIDE> c;
-    const int half = rot >> 1, rest = D - rot;
-    const int t = half - 8 * lane;
-    c.turned = t < 0 ? 0 : t > 8 ? 8 : t;
-    if constexpr (WIDE) {
+template <int PAIRS>
+__device__ __forceinline__ LaneColumns<PAIRS> lane_columns(int lane, const RotaryParams &p) {
+    LaneColumns<PAIRS> c;
+    const int rest = p.D - p.rot;
+    if constexpr (PAIRS == kHalf) {
+        // first the lanes of the rotation, then those of the other columns
+        const int e = 16 * lane - p.rot;
+        c.turned = e < 0 ? 0xffu : 0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            int e;                                       // column among those outside the rotation
-            if constexpr (INTER) {
-                const int v = 2 * lane + i;
-                c.at[i] = first + 8 * v;
-                e = 8 * v - rot;
-            } else {
-                c.at[i] = first + 8 * lane + i * half;
-                e = 16 * lane - rot + 8 * i;
-                if (c.turned) e = -1;
-            }
-            if (e >= 0) c.at[i] = e < rest && !in_place ? outside(e, first, rot) : -1;
+            const int o = e + 8 * i;                     // column among those outside
+            c.at[i] = e < 0 ? p.first + 8 * lane + i * (p.rot >> 1) : o < rest && !p.in_place ? (o < p.first ? o : o + p.rot) : -1;
         }
     } else {
+        c.turned = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int e;
-            if constexpr (INTER) {
-                const int p = 8 * lane + i;
-                c.at[i] = first + 2 * p;
-                e = 2 * p - rot;
-            } else {
-                const int p = 8 * lane + 2 * (i & 3);    // first pair of the unit
-                c.at[i] = first + p + (i >> 2) * half;
-                e = 2 * p - rot + 2 * (i >> 2);
-                if (p < half) e = -1;
+        for (int i = 0; i < 2; ++i) {
+            c.at[i] = 8 * (lane + i * p.lanes);
+            if (lane >= p.lanes || c.at[i] >= p.D) c.at[i] = -1;
+            uint32_t t = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = c.at[i] + 2 * j - p.first;
+                if (c.at[i] >= 0 && k >= 0 && k < p.rot) t |= 1u << j;
             }
-            if (e >= 0) c.at[i] = e < rest && !in_place ? outside(e, first, rot) : -1;
+            if (p.in_place && !t) c.at[i] = -1;
+            c.turned |= t << (4 * i);
         }
     }
     return c;
@@ -149,190 +157,219 @@ __device__ __forceinline__ LaneColumns<INTER, WIDE> lane_columns(int lane, int D
 // The lane's 16 elements as they are in memory.
 template <class E>
 struct Raw {
-    static constexpr int kW = 4 * int(sizeof(E));        // 32-bit words; pair i of registers is kW / 8 of them
-    uint32_t w[kW];
+    static constexpr int kQ = int(sizeof(E)) / 2;        // 16-byte words of a vector
+    uint4 q[2 * kQ];
 };
 
-__device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
-template <class E, bool INTER, bool WIDE>
-__device__ __forceinline__ void load_lane(Raw<E> &r, const void *base, int64_t off, const LaneColumns<INTER, WIDE> &c, bool on) {
-    const E *p = static_cast<const E *>(base) + off;
-    constexpr int Q = int(sizeof(E)) / 2;                // 16-byte words of a vector
-    if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < Q; ++k) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (on && c.at[i] >= 0) v = ld_stream_v4(reinterpret_cast<const uint4 *>(p + c.at[i]) + k);
-                uint32_t *w = r.w + (i * Q + k) * 4;
-                w[0] = v.x;
-                w[1] = v.y;
-                w[2] = v.z;
-                w[3] = v.w;
-            }
+// 8 elements at once: FP32 vectors are 32-byte aligned.
+template <class E>
+__device__ __forceinline__ void load_vector(uint4 *q, const void *p) {
+    if constexpr (sizeof(E) == 4) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y), "=r"(q[1].z), "=r"(q[1].w)
+                     : "l"(p));
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int k = 0; k < Q; ++k)
-                r.w[i * Q + k] = on && c.at[i] >= 0 ? reinterpret_cast<const uint32_t *>(p + c.at[i])[k] : 0u;
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w) : "l"(p));
     }
 }
-
-template <class E, bool INTER, bool WIDE>
-__device__ __forceinline__ void store_lane(const Raw<E> &r, void *base, int64_t off, const LaneColumns<INTER, WIDE> &c) {
-    E *p = static_cast<E *>(base) + off;
-    constexpr int Q = int(sizeof(E)) / 2;
-    if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (c.at[i] >= 0) {
-#pragma unroll
-                for (int k = 0; k < Q; ++k) {
-                    const uint32_t *w = r.w + (i * Q + k) * 4;
-                    st_global_v4(reinterpret_cast<uint4 *>(p + c.at[i]) + k, make_uint4(w[0], w[1], w[2], w[3]));
-                }
-            }
+template <class E>
+__device__ __forceinline__ void store_vector(void *p, const uint4 *q) {
+    if constexpr (sizeof(E) == 4) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(q[0].x), "r"(q[0].y), "r"(q[0].z), "r"(q[0].w),
+                     "r"(q[1].x), "r"(q[1].y), "r"(q[1].z), "r"(q[1].w)
+                     : "memory");
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c.at[i] >= 0) {
-#pragma unroll
-                for (int k = 0; k < Q; ++k) reinterpret_cast<uint32_t *>(p + c.at[i])[k] = r.w[i * Q + k];
-            }
+        st_global_v4(p, q[0]);
     }
 }
 
 template <class E>
 __device__ __forceinline__ f2_t up2(const Raw<E> &r, int i) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
     if constexpr (sizeof(E) == 4) {
-        return f2_make(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+        return f2_make(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else if constexpr (std::is_same_v<E, __half>) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         return f2_make(p.x, p.y);
     } else {
-        return f2_from_bf16x2(r.w[i]);
+        return f2_from_bf16x2(w[i]);
     }
 }
 template <class E>
 __device__ __forceinline__ void down2(Raw<E> &r, int i, f2_t v) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(r.q);
     if constexpr (sizeof(E) == 4) {
-        r.w[2 * i] = __float_as_uint(f2_lo(v));
-        r.w[2 * i + 1] = __float_as_uint(f2_hi(v));
+        w[2 * i] = __float_as_uint(f2_lo(v));
+        w[2 * i + 1] = __float_as_uint(f2_hi(v));
     } else if constexpr (std::is_same_v<E, __half>) {
         const __half2 h = __floats2half2_rn(f2_lo(v), f2_hi(v));
-        r.w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
     } else {
-        r.w[i] = f2_to_bf16x2(v);
+        w[i] = f2_to_bf16x2(v);
     }
 }
 
-// A lane's columns of a parameter vector (NULL: ones).
-template <class E, bool INTER, bool WIDE>
-__device__ __forceinline__ void lane_weights(const void *w, int f32, const LaneColumns<INTER, WIDE> &c, f2_t (&f)[8]) {
+// Both weights in shared memory, as FP32: quad j of vector v of a side at
+// [(2 side + j) V + v], so that neighbouring lanes read neighbouring 16 bytes.
+template <class E>
+__device__ __forceinline__ void stage_weights(float4 *sw, const RotaryParams &p) {
+    const int V = p.D >> 3;
+    for (int i = threadIdx.x; i < 2 * V; i += blockDim.x) {
+        const int side = i >= V, v = i - side * V;
+        f2_t f[4];
+        oct_param<E>(p.side[side].w, p.params_f32, v, 1.f, f);
+        sw[2 * side * V + v] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
+        sw[(2 * side + 1) * V + v] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
+    }
+}
+template <int PAIRS>
+__device__ __forceinline__ void lane_weights(const float4 *sw, int side, const LaneColumns<PAIRS> &c, int V, f2_t (&f)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = WIDE ? c.at[i >> 2] : c.at[i];
-        f[i] = f2_make(1.f, 1.f);
-        if (w && at >= 0) {
-            const int col = WIDE ? at + 2 * (i & 3) : at;
-            if (f32 || sizeof(E) == 4) {
-                const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(w) + col);
-                f[i] = f2_make(v.x, v.y);
-            } else {
-                Raw<E> r;
-                r.w[0] = *reinterpret_cast<const uint32_t *>(static_cast<const E *>(w) + col);
-                f[i] = up2<E>(r, 0);
-            }
+    for (int i = 0; i < 2; ++i) {
+        const int v = c.at[i] < 0 ? 0 : c.at[i] >> 3;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 q = sw[(2 * side + j) * V + v];
+            f[4 * i + 2 * j] = f2_make(q.x, q.y);
+            f[4 * i + 2 * j + 1] = f2_make(q.z, q.w);
         }
     }
 }
 
 // ----------------------------------------------------------------- angles
 
-// Cosine and sine of position * turns / 2^64 turns.  The product modulo 2^64 is
-// exact; its top 32 bits, off by less than 2^-32 turn, are split into a quadrant
-// and a rest of at most 1/8 turn either way, y = rest in radians.  sin y and cos y
-// are their Taylor polynomials of degree 9 and 10: what is left out is below
-// (pi/4)^11 / 11! = 1.8e-9 and (pi/4)^12 / 12! = 1.2e-10.  y is formed with what
-// the float of the rest loses, and enters as y + d: sin + d cos, cos - d sin.
-__device__ __forceinline__ void cos_sin(int32_t position, uint64_t turns, float &c, float &s) {
-    const int32_t top = int32_t(uint64_t(int64_t(position)) * turns >> 32);
-    const uint32_t quadrant = (uint32_t(top) + 0x20000000u) >> 30;
-    const int32_t rest = int32_t(uint32_t(top) - (quadrant << 30));
-    const float f = __int2float_rn(rest);
-    const float lost = __int2float_rn(rest - __float2int_rn(f));
-    // 2 pi / 2^32 in two floats: 0x1.921fb6p-30 and pi's next bits
-    const float kHi = 0x1.921fb6p-30f, kLo = -0x1.777a5cp-55f;
-    const float y = __fmul_rn(f, kHi);
-    const float d = __fmaf_rn(lost, kHi, __fmaf_rn(f, kLo, __fmaf_rn(f, kHi, -y)));
-    const float z = __fmul_rn(y, y);
-    float p = __fmaf_rn(z, 1.f / 362880.f, -1.f / 5040.f);
-    p = __fmaf_rn(z, p, 1.f / 120.f);
-    p = __fmaf_rn(z, p, -1.f / 6.f);
-    const float sy = __fmaf_rn(__fmul_rn(z, y), p, y);
-    float q = __fmaf_rn(z, -1.f / 3628800.f, 1.f / 40320.f);
-    q = __fmaf_rn(z, q, -1.f / 720.f);
-    q = __fmaf_rn(z, q, 1.f / 24.f);
-    q = __fmaf_rn(z, q, -0.5f);
-    const float cy = __fmaf_rn(z, q, 1.f);
-    const float sn = __fmaf_rn(d, cy, sy), cs = __fmaf_rn(-d, sy, cy);
-    c = quadrant & 1 ? sn : cs;
-    s = quadrant & 1 ? cs : sn;
-    if ((quadrant + 1) & 2) c = -c;
-    if (quadrant & 2) s = -s;
+// Cosines and sines of position * turns / 2^64 turns, for two pairs.  The product
+// modulo 2^64 is exact; its top 32 bits, off by less than 2^-32 turn, are split into
+// a quadrant and a rest of at most 1/8 turn either way, y = rest in radians.  sin y
+// and cos y are their Taylor polynomials of degree 9 and 10: what is left out is
+// below (pi/4)^11 / 11! = 1.8e-9 and (pi/4)^12 / 12! = 1.2e-10.  FINE (FP32 heads): y
+// is formed with what the float of the rest loses, and enters as y + d: sin + d cos,
+// cos - d sin; without that the angle is off by up to 2^-23 / 2 more.
+template <bool FINE>
+__device__ __forceinline__ void cos_sin(int32_t position, uint64_t t0, uint64_t t1, f2_t &c, f2_t &s) {
+    const uint32_t a = uint32_t(uint64_t(int64_t(position)) * t0 >> 32), b = uint32_t(uint64_t(int64_t(position)) * t1 >> 32);
+    const uint32_t qa = (a + 0x20000000u) >> 30, qb = (b + 0x20000000u) >> 30;
+    const int32_t ra = int32_t(a - (qa << 30)), rb = int32_t(b - (qb << 30));
+    const float fa = __int2float_rn(ra), fb = __int2float_rn(rb);
+    // 2 pi / 2^32 in two floats
+    const f2_t hi = f2_both(0x1.921fb6p-30f), lo = f2_both(-0x1.777a5cp-55f), f = f2_make(fa, fb);
+    const f2_t y = f2_mul(f, hi), z = f2_mul(y, y);
+    f2_t p = f2_fma(z, f2_both(1.f / 362880.f), f2_both(-1.f / 5040.f));
+    p = f2_fma(z, p, f2_both(1.f / 120.f));
+    p = f2_fma(z, p, f2_both(-1.f / 6.f));
+    f2_t sn = f2_fma(f2_mul(z, y), p, y);
+    f2_t q = f2_fma(z, f2_both(-1.f / 3628800.f), f2_both(1.f / 40320.f));
+    q = f2_fma(z, q, f2_both(-1.f / 720.f));
+    q = f2_fma(z, q, f2_both(1.f / 24.f));
+    q = f2_fma(z, q, f2_both(-0.5f));
+    f2_t cs = f2_fma(z, q, f2_both(1.f));
+    if constexpr (FINE) {
+        const f2_t lost = f2_make(__int2float_rn(ra - __float2int_rn(fa)), __int2float_rn(rb - __float2int_rn(fb)));
+        const f2_t minus = f2_both(-1.f);
+        const f2_t d = f2_fma(lost, hi, f2_fma(f, lo, f2_fma(f, hi, f2_mul(y, minus))));
+        const f2_t sn1 = f2_fma(d, cs, sn);
+        cs = f2_fma(f2_mul(d, minus), sn, cs);
+        sn = sn1;
+    }
+    // quadrant 1: (-sin, cos), 2: (-cos, -sin), 3: (sin, -cos): the signs' bits
+    const uint32_t ca = __float_as_uint(qa & 1 ? f2_lo(sn) : f2_lo(cs)) ^ (((qa + 1) & 2) << 30);
+    const uint32_t cb = __float_as_uint(qb & 1 ? f2_hi(sn) : f2_hi(cs)) ^ (((qb + 1) & 2) << 30);
+    const uint32_t sa = __float_as_uint(qa & 1 ? f2_lo(cs) : f2_lo(sn)) ^ ((qa & 2) << 30);
+    const uint32_t sb = __float_as_uint(qb & 1 ? f2_hi(cs) : f2_hi(sn)) ^ ((qb & 2) << 30);
+    c = f2_make(__uint_as_float(ca), __uint_as_float(cb));
+    s = f2_make(__uint_as_float(sa), __uint_as_float(sb));
 }
 
-// The lane's 8 pairs of cosine and sine, times scale, in registers of two.
-__device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, int turned, f2_t (&c)[4],
-                                            f2_t (&s)[4]) {
-    const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(p.turns) + lane * 4;
+// The lane's cosines and sines, times scale.  kHalf: of its 8 pairs, in columns'
+// order; kNear: likewise, 4 pairs a vector; kSplit: of the pair that each of its 16
+// columns belongs to, the sine negative in first halves.
+template <int PAIRS>
+struct Angles {
+    static constexpr int kN = PAIRS == kSplit ? 8 : 4;
+    f2_t c[kN], s[kN];
+};
+template <class E, int PAIRS>
+__device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, const LaneColumns<PAIRS> &col,
+                                            Angles<PAIRS> &a) {
+    const int half = p.rot >> 1;
+    const f2_t cs = f2_both(p.scale), ss = f2_both(__fmul_rn(p.scale, p.sign));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float c0 = 1.f, c1 = 1.f, s0 = 0.f, s1 = 0.f;
-        if (2 * i < turned) {                            // the number of pairs is even
-            const ulonglong2 v = t[i];
-            cos_sin(position, v.x, c0, s0);
-            cos_sin(position, v.y, c1, s1);
+    for (int i = 0; i < Angles<PAIRS>::kN; ++i) {
+        a.c[i] = f2_make(1.f, 1.f);
+        a.s[i] = f2_make(0.f, 0.f);
+        // the first of two pairs that follow each other
+        int k;
+        bool first = true, two = true, any;
+        if constexpr (PAIRS == kHalf) {
+            k = 8 * lane + 2 * i;
+            any = col.turned != 0;
+        } else if constexpr (PAIRS == kNear) {
+            k = (col.at[i >> 1] - p.first) / 2 + 2 * (i & 1);         // both even
+            first = (col.turned >> (2 * i)) & 1;
+            two = (col.turned >> (2 * i + 1)) & 1;
+            any = first || two;
+        } else {
+            k = col.at[i >> 2] + 2 * (i & 3) - p.first;
+            any = (col.turned >> i) & 1;
         }
-        c[i] = f2_mul(f2_make(c0, c1), f2_both(p.scale));
-        s[i] = f2_mul(f2_make(s0, s1), f2_both(__fmul_rn(p.scale, p.sign)));
+        if (any) {
+            const bool second_half = PAIRS == kSplit && k >= half;
+            if (second_half) k -= half;
+            const uint64_t t0 = first ? p.turns[k] : 0, t1 = two ? p.turns[k + 1] : 0;
+            f2_t c, s;
+            cos_sin<sizeof(E) == 4>(position, t0, t1, c, s);
+            a.c[i] = f2_mul(c, cs);
+            a.s[i] = f2_mul(s, PAIRS == kSplit && !second_half ? f2_mul(ss, f2_both(-1.f)) : ss);
+        }
     }
 }
 
-// Rotates the lane's pairs: f[0..3] first vector, f[4..7] second.
-template <bool INTER>
-__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const f2_t (&c)[4], const f2_t (&s)[4], int turned) {
-    if constexpr (!INTER) {
+// Turns the lane's columns.  kSplit: through the team's row of D floats in shared
+// memory, all lanes of the warp at the same time.
+template <int PAIRS>
+__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, const LaneColumns<PAIRS> &col, const RotaryParams &p,
+                                          float *row) {
+    if constexpr (PAIRS == kHalf) {
+        if (col.turned) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (2 * i < turned) {
-                const f2_t a = f[i], b = f[4 + i], n = f2_make(-f2_lo(s[i]), -f2_hi(s[i]));
-                f[i] = f2_fma(a, c[i], f2_mul(b, n));
-                f[4 + i] = f2_fma(b, c[i], f2_mul(a, s[i]));
+            for (int i = 0; i < 4; ++i) {
+                const f2_t x = f[i], y = f[4 + i], n = f2_mul(a.s[i], f2_both(-1.f));
+                f[i] = f2_fma(x, a.c[i], f2_mul(y, n));
+                f[4 + i] = f2_fma(y, a.c[i], f2_mul(x, a.s[i]));
             }
         }
-    } else {
+    } else if constexpr (PAIRS == kNear) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i < turned) {
-                const float a = f2_lo(f[i]), b = f2_hi(f[i]);
-                const float ci = i & 1 ? f2_hi(c[i >> 1]) : f2_lo(c[i >> 1]), si = i & 1 ? f2_hi(s[i >> 1]) : f2_lo(s[i >> 1]);
-                f[i] = f2_make(__fmaf_rn(a, ci, -__fmul_rn(b, si)), __fmaf_rn(b, ci, __fmul_rn(a, si)));
-            }
+            const float x = f2_lo(f[i]), y = f2_hi(f[i]);
+            const float c = i & 1 ? f2_hi(a.c[i >> 1]) : f2_lo(a.c[i >> 1]), s = i & 1 ? f2_hi(a.s[i >> 1]) : f2_lo(a.s[i >> 1]);
+            if ((col.turned >> i) & 1) f[i] = f2_make(__fmaf_rn(x, c, -__fmul_rn(y, s)), __fmaf_rn(y, c, __fmul_rn(x, s)));
         }
+    } else {
+        const int half = p.rot >> 1;
+        __syncwarp();                                    // the row before has been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (col.at[i] >= 0) {
+                *reinterpret_cast<ulonglong2 *>(row + col.at[i]) = make_ulonglong2(f[4 * i], f[4 * i + 1]);
+                *reinterpret_cast<ulonglong2 *>(row + col.at[i] + 4) = make_ulonglong2(f[4 * i + 2], f[4 * i + 3]);
+            }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((col.turned >> i) & 1) {
+                const int c = col.at[i >> 2] + 2 * (i & 3);
+                const f2_t y = *reinterpret_cast<const f2_t *>(row + (c - p.first < half ? c + half : c - half));
+                f[i] = f2_fma(f[i], a.c[i], f2_mul(y, a.s[i]));
+            }
     }
 }
 
-// Pair i of registers holds rotated columns.
-template <bool INTER>
-__device__ __forceinline__ bool is_turned(int i, int turned) { return INTER ? i < turned : 2 * (i & 3) < turned; }
+// Register pair i holds rotated columns.
+template <int PAIRS>
+__device__ __forceinline__ bool is_turned(int i, const LaneColumns<PAIRS> &col) {
+    return PAIRS == kHalf ? col.turned != 0 : (col.turned >> i) & 1;
+}
 
 // Sum over the lanes of a team of a power of two.
 __device__ __forceinline__ float team_add(float v, int team) {
@@ -342,7 +379,8 @@ __device__ __forceinline__ float team_add(float v, int team) {
     return v;
 }
 
-// Row sums of products f g: pairs 0, 1, .. by FMA, then the two columns of a pair.
+// A lane's part of a row's sum of products f g: register pairs by FMA, then the two
+// columns of a pair.
 __device__ __forceinline__ float lane_dot(const f2_t (&f)[8], const f2_t (&g)[8]) {
     f2_t v = f2_mul(f[0], g[0]);
 #pragma unroll
@@ -356,52 +394,77 @@ __device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) { retu
 
 constexpr int kRotaryThreads = 256;
 
-template <class E, bool INTER, bool WIDE, bool NORM>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+// U: heads whose loads are issued at once.
+template <class E, int PAIRS, bool NORM, int U>
+__global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    extern __shared__ float4 shared[];                   // the weights (NORM), the teams' rows (kSplit)
+    constexpr bool kTogether = NORM || PAIRS == kSplit;  // the lanes of a warp exchange values
     const uint32_t mine = p.by_team.quotient(threadIdx.x), teams = p.by_team.quotient(kRotaryThreads);
     const int lane = int(threadIdx.x - mine * uint32_t(p.team));
     const uint32_t unit = blockIdx.x * teams + mine, token = p.by_chunks.quotient(unit);
-    int chunk = int(unit - token * uint32_t(p.chunks));
-    bool on = mine < teams && unit < p.units;
-    if (on) on = p.tok_id[token] >= 0;
-    if constexpr (!NORM) {
-        if (!on) return;
+    const int head0 = int(unit - token * uint32_t(p.chunks)) * p.per;
+    const bool in = mine < teams && unit < p.units;
+    const int32_t id = in ? p.tok_id[token] : -1, position = in ? p.position[token] : 0;
+    if constexpr (NORM) stage_weights<E>(shared, p);
+    int n = p.heads - head0 < p.per ? p.heads - head0 : p.per;
+    if (id < 0) n = 0;
+    if constexpr (!kTogether) {
+        if (n == 0) return;
     }
-    const LaneColumns<INTER, WIDE> col = lane_columns<INTER, WIDE>(lane, p.D, p.rot, p.first, p.in_place);
-    const HeadsParams &h = p.side[chunk >= p.chunks_q];
-    if (chunk >= p.chunks_q) chunk -= p.chunks_q;
-    const int head0 = chunk * h.per;
-    int n = h.heads - head0;
-    if (n > h.per) n = h.per;
-    if (!on) n = 0;
-    f2_t c[4], s[4], w[8];
-    lane_angles(p, on ? p.position[token] : 0, lane, col.turned, c, s);
-    if constexpr (NORM) lane_weights<E, INTER, WIDE>(h.w, p.params_f32, col, w);
-    int64_t in = int64_t(token) * h.in_t + head0 * h.in_h, out = int64_t(token) * h.out_t + head0 * h.out_h;
-    constexpr int U = sizeof(E) == 4 ? 2 : 4;
-    for (int i = 0; i < (NORM ? p.most : n); i += U) {
+    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    const E *const q_in = static_cast<const E *>(p.side[0].in) + int64_t(token) * p.side[0].in_t;
+    const E *const k_in = static_cast<const E *>(p.side[1].in) + int64_t(token) * p.side[1].in_t;
+    E *const q_out = static_cast<E *>(p.side[0].out) + int64_t(token) * p.side[0].out_t;
+    E *const k_out = static_cast<E *>(p.side[1].out) + int64_t(token) * p.side[1].out_t;
+    float *row = nullptr;
+    if constexpr (PAIRS == kSplit) row = reinterpret_cast<float *>(shared + (NORM ? p.D / 2 : 0)) + mine * p.D;
+    Angles<PAIRS> a;
+    for (int i = 0; i < (kTogether ? p.per : n); i += U) {
         Raw<E> r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) load_lane<E, INTER, WIDE>(r[u], h.in, in + u * h.in_h, col, i + u < n);
+        for (int u = 0; u < U; ++u) {
+            const int h = head0 + i + u;
+            const E *src = h < p.hq ? q_in + h * p.side[0].in_h : k_in + (h - p.hq) * p.side[1].in_h;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint4 *q = r[u].q + j * Raw<E>::kQ;
+#pragma unroll
+                for (int l = 0; l < Raw<E>::kQ; ++l) q[l] = make_uint4(0, 0, 0, 0);
+                if (i + u < n && col.at[j] >= 0) load_vector<E>(q, src + col.at[j]);
+            }
+        }
+        if (i == 0) {
+            if constexpr (NORM) {
+                __syncthreads();
+                if (__all_sync(kFull, n == 0)) return;
+            }
+            lane_angles<E, PAIRS>(p, position, lane, col, a);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (i + u >= (kTogether ? p.per : n)) break;
+            const int h = head0 + i + u;
             f2_t f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
             if constexpr (NORM) {
-                const float rstd = qk_rstd(team_add(lane_dot(f, f), p.team), p);
+                f2_t w[8];
+                lane_weights<PAIRS>(shared, h >= p.hq, col, p.D >> 3, w);
+                const f2_t rstd = f2_both(qk_rstd(team_add(lane_dot(f, f), p.team), p));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], f2_both(rstd)), w[j]);
+                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
             }
-            turn_lane<INTER>(f, c, s, col.turned);
-            Raw<E> y = r[u];
+            turn_lane<PAIRS>(f, a, col, p, row);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (NORM || is_turned<INTER>(j, col.turned)) down2<E>(y, j, f[j]);
-            if (i + u < n) store_lane<E, INTER, WIDE>(y, h.out, out + u * h.out_h, col);
+                if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r[u], j, f[j]);
+            if (i + u < n) {
+                E *dst = h < p.hq ? q_out + h * p.side[0].out_h : k_out + (h - p.hq) * p.side[1].out_h;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r[u].q + j * Raw<E>::kQ);
+            }
         }
-        in += U * h.in_h;
-        out += U * h.out_h;
     }
 }
 
@@ -413,141 +476,220 @@ constexpr int kQkWarps = 4;
 // one chunk of heads: the run, 8 consecutive slots that hold a whole group in logical
 // order and start among them (at most one does), and the active slots that
 // belong to no run.  Slots of a run that starts in the window before are that
-// window's.
+// window's.  Lanes 0 .. 22 hold the ids and positions of slots 8 w - 7 on.
 struct Window {
-    int64_t run;                     // first slot of the run, -1: none
+    int32_t id, position;
+    int run;                         // lane of the run's first slot, -1: none
     uint32_t loose;                  // bit j: slot 8 w + j on its own
 };
 __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bool grads) {
     const int lane = threadIdx.x & 31;
-    const int64_t first = w * 8 - 7, slot = first + lane;            // lanes 7 .. 14 are the window, 22 the last slot of its run
-    const int32_t id = lane < 23 && slot >= 0 && slot < p.n_tokens ? p.tok_id[slot] : -1;
+    const int64_t slot = w * 8 - 7 + lane;               // lanes 7 .. 14 are the window, 21 the last slot of its run
+    const bool in = lane < 23 && slot >= 0 && slot < p.n_tokens;
     Window r;
+    r.id = in ? p.tok_id[slot] : -1;
+    r.position = in ? p.position[slot] : 0;
     r.run = -1;
     if (!grads) {
-        r.loose = (__ballot_sync(kFull, id >= 0) >> 7) & 0xffu;
+        r.loose = (__ballot_sync(kFull, r.id >= 0) >> 7) & 0xffu;
         return r;
     }
-    const int32_t before = __shfl_up_sync(kFull, id, 1);
-    const uint32_t begins = __ballot_sync(kFull, id >= 0 && (id & 7) == 0 && int64_t(id) + 8 <= p.ws.n);
-    const uint32_t follows = __ballot_sync(kFull, lane > 0 && id > 0 && (id & 7) != 0 && id == before + 1);
+    const int32_t before = __shfl_up_sync(kFull, r.id, 1);
+    const uint32_t begins = __ballot_sync(kFull, r.id >= 0 && (r.id & 7) == 0 && int64_t(r.id) + 8 <= p.ws.n);
+    const uint32_t follows = __ballot_sync(kFull, lane > 0 && r.id > 0 && (r.id & 7) != 0 && r.id == before + 1);
     // run from lane s: begins at s and follows at s + 1 .. s + 7
-    const int s = lane - (id & 7);
-    const bool whole = id >= 0 && s >= 0 && s + 7 < 23 && ((begins >> s) & 1) && ((follows >> (s + 1)) & 0x7f) == 0x7f;
-    const uint32_t starts = __ballot_sync(kFull, whole && (id & 7) == 0) & 0x7f80u;
-    r.loose = (__ballot_sync(kFull, id >= 0 && !whole) >> 7) & 0xffu;
-    if (starts) r.run = first + (__ffs(starts) - 1);
+    const int s = lane - (r.id & 7);
+    const bool whole = r.id >= 0 && s >= 0 && s + 7 < 23 && ((begins >> s) & 1) && ((follows >> (s + 1)) & 0x7f) == 0x7f;
+    const uint32_t starts = __ballot_sync(kFull, whole && (r.id & 7) == 0) & 0x7f80u;
+    r.loose = (__ballot_sync(kFull, r.id >= 0 && !whole) >> 7) & 0xffu;
+    if (starts) r.run = __ffs(starts) - 1;
     return r;
 }
 
-template <class E, bool INTER, bool WIDE, bool GRADS>
-__global__ void __launch_bounds__(kQkWarps * 32) qk_bwd_kernel(const __grid_constant__ RotaryParams p) {
+// Heads on their way into shared memory: a ring of kDepth rows a team, every lane
+// copying its own columns of x and dy to places that only it reads.
+template <class E>
+struct Ring {
+    static constexpr int kPieces = 4 * Raw<E>::kQ;       // 16-byte pieces of a lane's row: x, dy
+    static constexpr int kDepth = sizeof(E) == 4 ? 3 : 4;
+    static constexpr int kBytes = kPieces * kDepth * 512;   // of a warp
+};
+
+inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool straddles) {
+    // both weights, then per warp: ring, the run's tokens' sums (of both kinds where a chunk has both), kSplit's rows
+    return 16 * D + kQkWarps * (ring_bytes + (grads ? kQkGroup * D * 4 * (straddles ? 2 : 1) : 0) + (split ? 2048 : 0));
+}
+
+template <class E, int PAIRS, bool GRADS>
+__global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
     extern __shared__ float4 shared[];
     const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
-    if (unit >= p.units) return;
-    const uint32_t win = p.by_chunks.quotient(unit);
-    const int chunk_all = int(unit - win * uint32_t(p.chunks));
-    const HeadsParams &h = p.side[chunk_all >= p.chunks_q];
-    const int chunk = chunk_all >= p.chunks_q ? chunk_all - p.chunks_q : chunk_all;
+    const bool in = unit < p.units;
+    const uint32_t win = p.by_chunks.quotient(in ? unit : 0);
+    const int chunk = int((in ? unit : 0) - win * uint32_t(p.chunks));
     const bool grads = GRADS && qk_header_ok(p.ws);
     if (GRADS && !grads && unit == 0 && lane32 == 0) qk_report(p.ws, kStHeader);
-    const Window wd = window_of(p, win, grads);
+    Window wd = window_of(p, win, grads);
+    if (!in) {
+        wd.run = -1;
+        wd.loose = 0;
+    }
+    stage_weights<E>(shared, p);
 
     const int lane = lane32 & (p.team - 1), team = lane32 / p.team, teams = 32 / p.team;
-    const LaneColumns<INTER, WIDE> col = lane_columns<INTER, WIDE>(lane, p.D, p.rot, p.first, false);
-    const int head0 = chunk * h.per;
-    int heads = h.heads - head0;
-    if (heads > h.per) heads = h.per;
-    f2_t w[8];
-    lane_weights<E, INTER, WIDE>(h.w, p.params_f32, col, w);
-    float *sums = reinterpret_cast<float *>(shared) + size_t(warp) * kQkGroup * p.D;   // [8][D] of the run's tokens
+    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    const int head0 = chunk * p.per, heads = p.heads - head0 < p.per ? p.heads - head0 : p.per;
+    const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
+    const int run_steps = in_run ? (kQkGroup + teams - 1) / teams : 0, steps = run_steps + (loose + teams - 1) / teams;
 
-    const int loose = __popc(wd.loose), in_run = wd.run >= 0 ? 8 : 0;
-    // the run's tokens first, then the loose ones
-    for (int t0 = 0; t0 < in_run + loose; t0 = t0 < in_run && t0 + teams >= in_run ? in_run : t0 + teams) {
-        const int t = t0 + team, end = t0 < in_run ? in_run : in_run + loose;
-        const bool on = t < end;
-        int64_t slot = 0;
-        if (t < in_run) {
-            slot = wd.run + t;
-        } else if (on) {                                 // the (t - in_run)th loose slot
-            uint32_t m = wd.loose;
-            for (int i = t - in_run; i > 0; --i) m &= m - 1;
-            slot = int64_t(win) * 8 + (__ffs(m) - 1);
+    using R = Ring<E>;
+    const int sums_bytes = GRADS ? kQkGroup * p.D * 4 * (straddles ? 2 : 1) : 0;
+    uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
+    const uint32_t ring = smem_addr(mine) + lane32 * 16;
+    float *const sums = reinterpret_cast<float *>(mine + R::kBytes);                    // [kinds][8][D] of the run's tokens
+    float *const row = reinterpret_cast<float *>(mine + R::kBytes + sums_bytes) + team * p.D;
+
+    // Lane (of the window's ids) of this team's slot in a step, -1: none.
+    auto place = [&](int step) {
+        if (step < run_steps) {
+            const int t = step * teams + team;
+            return t < kQkGroup ? wd.run + t : -1;
         }
-        f2_t c[4], s[4], acc[8];
-        lane_angles(p, on ? p.position[slot] : 0, lane, col.turned, c, s);
+        const int t = (step - run_steps) * teams + team;
+        if (t >= loose) return -1;
+        uint32_t m = wd.loose;
+        for (int i = t; i > 0; --i) m &= m - 1;
+        return 6 + __ffs(m);
+    };
+    // The copies of the next row: one commit a row, empty rows too.
+    int f_step = 0, f_head = 0, f_stage = 0, f_place = place(0);
+    auto fetch = [&]() {
+        if (f_step < steps) {
+            const bool on = f_place >= 0;
+            const int64_t slot = on ? int64_t(win) * 8 - 7 + f_place : 0;
+            const int h = head0 + f_head, side = h >= p.hq, k = side ? h - p.hq : h;
+            const HeadsParams &s = p.side[side];
+            const E *x = static_cast<const E *>(s.in) + slot * s.in_t + k * s.in_h;
+            const E *g = static_cast<const E *>(s.dy) + slot * s.dy_t + k * s.dy_h;
+            uint32_t dst = ring + f_stage * (R::kPieces * 512);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool some = on && col.at[j] >= 0;
+                const int at = some ? col.at[j] : 0;
+#pragma unroll
+                for (int l = 0; l < Raw<E>::kQ; ++l) {
+                    cp_async_zfill(dst + (j * Raw<E>::kQ + l) * 512, reinterpret_cast<const uint4 *>(x + at) + l, some ? 16 : 0);
+                    cp_async_zfill(dst + ((2 + j) * Raw<E>::kQ + l) * 512, reinterpret_cast<const uint4 *>(g + at) + l, some ? 16 : 0);
+                }
+            }
+            f_stage = f_stage + 1 == R::kDepth ? 0 : f_stage + 1;
+            if (++f_head == heads) {
+                f_head = 0;
+                if (++f_step < steps) f_place = place(f_step);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch();
+    __syncthreads();                                     // the weights
+    if (steps == 0) return;
+
+    Angles<PAIRS> a;
+    f2_t acc[8];
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int at = place(step);
+        const bool on = at >= 0;
+        const int64_t slot = on ? int64_t(win) * 8 - 7 + at : 0;
+        const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, col, a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
-        int64_t in = slot * h.in_t + head0 * h.in_h, dyo = slot * h.dy_t + head0 * h.dy_h, out = slot * h.out_t + head0 * h.out_h;
-        Raw<E> rx, rg;
-        load_lane<E, INTER, WIDE>(rx, h.in, in, col, on);
-        load_lane<E, INTER, WIDE>(rg, h.dy, dyo, col, on);
+        if (GRADS && grads && on && chunk == 0 && lane == 0) {
+            const bool run = step < run_steps;
+            const bool known = int64_t(id) < p.ws.n;
+            const int bad = known ? (atomicExch(p.ws.flag + id, run ? 1 : 2) ? kStDouble : 0) : kStPlan;
+            if (bad) qk_report(p.ws, bad);
+        }
         for (int i = 0; i < heads; ++i) {
-            f2_t x[8], g[8], a[8];
+            fetch();
+            cp_async_wait<R::kDepth - 1>();
+            Raw<E> rx, rg;
+            const uint32_t src = ring + stage * (R::kPieces * 512);
+#pragma unroll
+            for (int l = 0; l < 2 * Raw<E>::kQ; ++l) {
+                ld_shared_vec(src + l * 512, rx.q[l]);
+                ld_shared_vec(src + (2 * Raw<E>::kQ + l) * 512, rg.q[l]);
+            }
+            stage = stage + 1 == R::kDepth ? 0 : stage + 1;
+            const int h = head0 + i, side = h >= p.hq;
+            f2_t x[8], g[8], b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] = up2<E>(rx, j);
                 g[j] = up2<E>(rg, j);
             }
-            in += h.in_h;
-            dyo += h.dy_h;
-            if (i + 1 < heads) {
-                load_lane<E, INTER, WIDE>(rx, h.in, in, col, on);
-                load_lane<E, INTER, WIDE>(rg, h.dy, dyo, col, on);
-            }
-            turn_lane<INTER>(g, c, s, col.turned);
+            turn_lane<PAIRS>(g, a, col, p, row);
+            lane_weights<PAIRS>(shared, side, col, p.D >> 3, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = f2_mul(g[j], w[j]);
-            const float ss = team_add(lane_dot(x, x), p.team), sa = team_add(lane_dot(a, x), p.team);
-            const float rstd = qk_rstd(ss, p), m = row_mean_gxhat(sa, rstd, float(p.D), p.inv_d);
-            Raw<E> y;
+            for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
+            const float ss = team_add(lane_dot(x, x), p.team), sb = team_add(lane_dot(b, x), p.team);
+            const float rstd = qk_rstd(ss, p), m = row_mean_gxhat(sb, rstd, float(p.D), p.inv_d);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] = f2_mul(x[j], f2_both(rstd));
                 if constexpr (GRADS) acc[j] = f2_fma(g[j], x[j], acc[j]);
-                down2<E>(y, j, f2_mul(f2_fma(x[j], f2_both(-m), a[j]), f2_both(rstd)));
+                down2<E>(rx, j, f2_mul(f2_fma(x[j], f2_both(-m), b[j]), f2_both(rstd)));
             }
-            if (on) store_lane<E, INTER, WIDE>(y, h.out, out, col);
-            out += h.out_h;
-        }
-        if (GRADS && grads && on) {
-            const int32_t id = p.tok_id[slot];
-            float *dst = sums + (t & 7) * p.D;
-            bool keep = true;
-            if (t >= in_run) {
-                keep = int64_t(id) < p.ws.n;
-                dst = p.ws.spill + (int64_t(chunk_all) * p.ws.n + id) * p.D;
-                if (chunk_all == 0 && lane == 0) {
-                    const int bad = keep ? (atomicExch(p.ws.flag + id, 2) ? kStDouble : 0) : kStPlan;
-                    if (bad) qk_report(p.ws, bad);
-                }
-            } else if (chunk_all == 0 && lane == 0 && atomicExch(p.ws.flag + id, 1)) {
-                qk_report(p.ws, kStDouble);
-            }
-            if (keep) {
+            if (on) {
+                const HeadsParams &s = p.side[side];
+                E *dst = static_cast<E *>(s.out) + slot * s.out_t + (side ? h - p.hq : h) * s.out_h;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int at = WIDE ? col.at[j >> 2] : col.at[j];
-                    if (at >= 0)
-                        *reinterpret_cast<float2 *>(dst + (WIDE ? at + 2 * (j & 3) : at)) = make_float2(f2_lo(acc[j]), f2_hi(acc[j]));
+                for (int j = 0; j < 2; ++j)
+                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Raw<E>::kQ);
+            }
+            // the last head of its kind in the chunk: the token's sums are complete
+            if (GRADS && (i + 1 == heads || h + 1 == p.hq)) {
+                if (grads && on) {
+                    float *dst = sums + (side && straddles ? kQkGroup * p.D : 0) + (at - wd.run) * p.D;
+                    bool keep = true;
+                    if (step >= run_steps) {
+                        keep = int64_t(id) < p.ws.n;
+                        const int64_t slot_of = side ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
+                        dst = p.ws.spill + (slot_of * p.ws.n + id) * p.D;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (keep && col.at[j] >= 0) {
+                            *reinterpret_cast<ulonglong2 *>(dst + col.at[j]) = make_ulonglong2(acc[4 * j], acc[4 * j + 1]);
+                            *reinterpret_cast<ulonglong2 *>(dst + col.at[j] + 4) = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);
+                        }
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
             }
         }
     }
     if (GRADS && grads && in_run) {
         __syncwarp();
-        const int64_t g = p.tok_id[wd.run] >> 3;
-        float *dst = p.ws.partial + (int64_t(chunk_all) * p.ws.groups + g) * p.D;
-        for (int k = lane32 * 4; k < p.D; k += 128) {
-            float4 v = *reinterpret_cast<const float4 *>(sums + k);
+        const int64_t g = __shfl_sync(kFull, wd.id, wd.run) >> 3;
+        if (chunk == 0 && lane32 == 0) p.ws.whole[g] = 1;
+        for (int side = head0 < p.hq ? 0 : 1; side < 2; ++side) {
+            if (side && head0 + heads <= p.hq) break;
+            const float *src = sums + (side && straddles ? kQkGroup * p.D : 0);
+            const int64_t slot_of = side ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
+            float *dst = p.ws.partial + (slot_of * p.ws.groups + g) * p.D;
+            for (int k = lane32 * 4; k < p.D; k += 128) {
+                float4 v = *reinterpret_cast<const float4 *>(src + k);
 #pragma unroll
-            for (int t = 1; t < kQkGroup; ++t) {
-                const float4 u = *reinterpret_cast<const float4 *>(sums + t * p.D + k);
-                v = make_float4(__fadd_rn(v.x, u.x), __fadd_rn(v.y, u.y), __fadd_rn(v.z, u.z), __fadd_rn(v.w, u.w));
+                for (int t = 1; t < kQkGroup; ++t) {
+                    const float4 u = *reinterpret_cast<const float4 *>(src + t * p.D + k);
+                    v = make_float4(__fadd_rn(v.x, u.x), __fadd_rn(v.y, u.y), __fadd_rn(v.z, u.z), __fadd_rn(v.w, u.w));
+                }
+                *reinterpret_cast<float4 *>(dst + k) = v;
             }
-            *reinterpret_cast<float4 *>(dst + k) = v;
         }
     }
 }

@@ -10,44 +10,57 @@ inline int lanes_pow2(int lanes) {
     return p;
 }
 
-template <class E, bool INTER, bool WIDE>
-static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
-    const int lanes = (p.D + 15) / 16;
-    if (mode <= 1) {
-        p.team = mode == 0 ? (p.in_place ? (p.rot + 15) / 16 : lanes) : lanes_pow2(lanes);
-        p.by_team = Divisor(uint32_t(p.team));
-        const uint32_t teams = uint32_t(kRotaryThreads / p.team);
-        p.units = uint32_t(p.n_tokens * p.chunks);
-        const unsigned grid = (p.units + teams - 1) / teams;
-        if (mode == 0) rotary_kernel<E, INTER, WIDE, false><<<grid, kRotaryThreads, 0, stream>>>(p);
-        else rotary_kernel<E, INTER, WIDE, true><<<grid, kRotaryThreads, 0, stream>>>(p);
-    } else {
-        p.team = lanes_pow2(lanes);
-        p.units = uint32_t((p.n_tokens + kQkGroup - 1) / kQkGroup * p.chunks);
-        const unsigned grid = (p.units + kQkWarps - 1) / kQkWarps;
-        if (mode == 2) {
-            qk_bwd_kernel<E, INTER, WIDE, false><<<grid, kQkWarps * 32, 0, stream>>>(p);
-        } else {
-            auto kern = qk_bwd_kernel<E, INTER, WIDE, true>;
-            static KernelInfo info;
-            DeviceInfo *d = nullptr;
-            int regs = 0;
-            if (int rc = device_info(&d)) return rc;
-            if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
-            kern<<<grid, kQkWarps * 32, size_t(kQkWarps) * kQkGroup * p.D * 4, stream>>>(p);
-        }
-    }
+template <class E, int PAIRS, bool NORM>
+static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
+    constexpr int U = sizeof(E) == 4 ? 2 : 4;
+    p.team = NORM || PAIRS == kSplit ? lanes_pow2(p.lanes) : PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
+    p.by_team = Divisor(uint32_t(p.team));
+    const uint32_t teams = uint32_t(kRotaryThreads / p.team);
+    p.units = uint32_t(p.n_tokens * p.chunks);
+    const int smem = (NORM ? 16 * p.D : 0) + (PAIRS == kSplit ? int(teams) * p.D * 4 : 0);
+    rotary_kernel<E, PAIRS, NORM, U><<<(p.units + teams - 1) / teams, kRotaryThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
 }
 
+template <class E, int PAIRS, bool GRADS>
+static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
+    auto kern = qk_bwd_kernel<E, PAIRS, GRADS>;
+    static KernelInfo info;
+    DeviceInfo *d = nullptr;
+    int regs = 0;
+    if (int rc = device_info(&d)) return rc;
+    if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
+    p.team = lanes_pow2(p.lanes);
+    p.units = uint32_t((p.n_tokens + kQkGroup - 1) / kQkGroup * p.chunks);
+    const bool straddles = p.hq % p.per != 0 && p.heads > p.hq;
+    kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
+           qk_bwd_smem(Ring<E>::kBytes, p.D, PAIRS == kSplit, GRADS, straddles), stream>>>(p, straddles);
+    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
+    count_launch();
+    return RMSNORM_OK;
+}
+
+template <class E, int PAIRS>
+static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
+    switch (mode) {
+        case 0: return rotary_launch_fwd<E, PAIRS, false>(p, stream);
+        case 1: return rotary_launch_fwd<E, PAIRS, true>(p, stream);
+        case 2: return rotary_launch_bwd<E, PAIRS, false>(p, stream);
+        default: return rotary_launch_bwd<E, PAIRS, true>(p, stream);
+    }
+}
+
 template <class E>
 int rotary_run(RotaryParams p, int mode, bool interleaved, cudaStream_t stream) {
-    // Vectors of 8 columns where the rotation is made of whole ones, else pieces of two.
-    const bool wide = p.first % 8 == 0 && p.rot % (interleaved ? 8 : 16) == 0;
-    if (interleaved) return wide ? rotary_launch<E, true, true>(p, mode, stream) : rotary_launch<E, true, false>(p, mode, stream);
-    return wide ? rotary_launch<E, false, true>(p, mode, stream) : rotary_launch<E, false, false>(p, mode, stream);
+    p.lanes = (p.D + 15) / 16;
+    const QkChunks cut(p.hq, p.heads - p.hq);
+    p.chunks = cut.chunks;
+    p.per = cut.per;
+    p.by_chunks = Divisor(uint32_t(p.chunks));
+    if (interleaved) return rotary_launch<E, kNear>(p, mode, stream);
+    return p.first % 8 == 0 && p.rot % 16 == 0 ? rotary_launch<E, kHalf>(p, mode, stream) : rotary_launch<E, kSplit>(p, mode, stream);
 }
 
 }  // namespace rbi

@@ -93,12 +93,13 @@ def forward(x, w, position, freq, rotary_dim, first, interleaved, scale, eps):
     return y, err + (RSTD + 2) * U * _spread(z, rotary_dim, first, interleaved, scale)
 
 
-def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, eps, groups=None):
+def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, eps):
     """(dx, dweight, err_dx, err_dw), dx unrounded.
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    8 tokens, the chunks, the groups of a warp, 16 warps and 8 CTAs."""
+    8 tokens, the chunks (at most one more than full ones), the groups of one of 512 shares, 2 steps
+    between the shares of a warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
     rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
@@ -115,7 +116,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 8 + (x.shape[1] + 7) // 8 + (n + 1023) // 1024 + 24
+    chain = 8 + 8 + (x.shape[1] + 7) // 8 + 1 + (n + 4095) // 4096 + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -127,36 +128,45 @@ def rounded(err, ref, dtype: str):
     return err + half * (np.abs(ref) + err) + tiny
 
 
-def grad_replay(leaf: np.ndarray) -> np.ndarray:
-    """float32 replay of a weight gradient's order for exact leaves g xhat [tokens, heads, D]."""
-    leaf = leaf.astype(np.float32)
-    n, heads, D = leaf.shape
+def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
+    """float32 replay of both weight gradients' order for exact leaves g xhat [tokens, heads, D]."""
+    n, hq, D = q_leaf.shape
+    heads = hq + k_leaf.shape[1]
+    leaf = np.concatenate([q_leaf, k_leaf], 1).astype(np.float32)
     chunks = (heads + 7) // 8
     per = (heads + chunks - 1) // chunks
     groups = (n + 7) // 8
-    value = []
-    for g in range(groups):
-        v = None
-        for c in range(chunks):
-            u = None
-            for t in range(8 * g, min(8 * g + 8, n)):
-                s = np.zeros(D, np.float32)
-                for h in range(c * per, min(c * per + per, heads)):
-                    s = s + leaf[t, h]
-                u = s if u is None else u + s
-            v = u if v is None else v + u
-        value.append(v)
-    share = (groups + 7) // 8
-    total = None
-    for r in range(8):
-        warps = []
-        for w in range(16):
+    shares = 8 * 16 * 4
+    share = (groups + shares - 1) // shares
+    out = []
+    for lo, hi in ((0, hq), (hq, heads)):
+        value = []
+        for g in range(groups):
+            v = None
+            for c in range(chunks):
+                mine = range(max(lo, c * per), min(hi, c * per + per))
+                if not len(mine):
+                    continue
+                u = None
+                for t in range(8 * g, min(8 * g + 8, n)):
+                    s = np.zeros(D, np.float32)
+                    for h in mine:
+                        s = s + leaf[t, h]
+                    u = s if u is None else u + s
+                v = u if v is None else v + u
+            value.append(v)
+        part = []
+        for r in range(shares):
             acc = np.zeros(D, np.float32)
-            for g in range(r * share + w, min((r + 1) * share, groups), 16):
+            for g in range(r * share, min((r + 1) * share, groups)):
                 acc = acc + value[g]
-            warps.append(acc)
-        s = warps[0]
-        for w in range(1, 16):
-            s = s + warps[w]
-        total = s if total is None else total + s
-    return total
+            part.append(acc)
+        warps = [(part[i] + part[i + 1]) + (part[i + 2] + part[i + 3]) for i in range(0, shares, 4)]
+        total = None
+        for r in range(8):
+            s = warps[16 * r]
+            for w in range(1, 16):
+                s = s + warps[16 * r + w]
+            total = s if total is None else total + s
+        out.append(total)
+    return out
