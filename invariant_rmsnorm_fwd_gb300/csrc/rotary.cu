@@ -84,7 +84,14 @@ int ws_check(const void *ws, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     return ws_sizes_check(N, hq, hk, D);
 }
 
-// mode as in rotary_run; back: turn the other way.
+template <class E>
+int run(const RotaryParams &p, int mode, bool interleaved, cudaStream_t s) {
+    if (interleaved) return rotary_run_pairs<E, kNear>(p, mode, s);
+    // halves of whole vectors, or not
+    return p.first % 8 == 0 && p.rot % 16 == 0 ? rotary_run_pairs<E, kHalf>(p, mode, s) : rotary_run_pairs<E, kSplit>(p, mode, s);
+}
+
+// mode as in rotary_run_pairs; back: turn the other way.
 int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float eps, int32_t dtype, int32_t param_dtype,
          const rmsnorm_layout_t *L, const rmsnorm_rotary_t *r, void *workspace, int mode, bool back, rmsnorm_stream_t stream) {
     if (dtype < LAYERNORM_BF16 || dtype > LAYERNORM_FP32 || (param_dtype != dtype && param_dtype != LAYERNORM_FP32))
@@ -131,13 +138,13 @@ int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float ep
     p.scale = r->scale;
     p.sign = back ? -1.f : 1.f;
     p.eps = eps;
-    p.inv_d = (D & (D - 1)) == 0 ? float(1.0 / double(D)) : 0.f;
+    p.inv_d = float(1.0 / double(D));
     if (workspace) p.ws = qk_ws(workspace, L->n_logical_tokens, q->heads, k ? k->heads : 0, D);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case LAYERNORM_BF16: return rotary_run<__nv_bfloat16>(p, mode, r->interleaved, s);
-        case LAYERNORM_FP16: return rotary_run<__half>(p, mode, r->interleaved, s);
-        default: return rotary_run<float>(p, mode, r->interleaved, s);
+        case LAYERNORM_BF16: return run<__nv_bfloat16>(p, mode, r->interleaved, s);
+        case LAYERNORM_FP16: return run<__half>(p, mode, r->interleaved, s);
+        default: return run<float>(p, mode, r->interleaved, s);
     }
 }
 
@@ -281,7 +288,7 @@ extern "C" int qk_norm_rotary_fwd(const rmsnorm_heads_t *q, const rmsnorm_heads_
 extern "C" int qk_norm_rotary_bwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t head_dim, float eps,
                                   int32_t dtype, int32_t param_dtype, const rmsnorm_layout_t *layout,
                                   const rmsnorm_rotary_t *rotary, void *workspace, rmsnorm_stream_t stream) {
-    return call(q, k, head_dim, eps, dtype, param_dtype, layout, rotary, workspace, workspace ? 3 : 2, true, stream);
+    return call(q, k, head_dim, eps, dtype, param_dtype, layout, rotary, workspace, 2, true, stream);
 }
 
 extern "C" size_t qk_norm_workspace_bytes(int64_t n_logical_tokens, int32_t q_heads, int32_t k_heads, int64_t head_dim) {

@@ -161,15 +161,20 @@ struct Raw {
     uint4 q[2 * kQ];
 };
 
-// 8 elements at once: FP32 vectors are 32-byte aligned.
+// 8 elements at once if `on`, else whatever the registers hold (nothing that depends on
+// it is stored).  FP32 vectors are 32-byte aligned.
 template <class E>
-__device__ __forceinline__ void load_vector(uint4 *q, const void *p) {
+__device__ __forceinline__ void load_vector(uint4 *q, const void *p, bool on) {
     if constexpr (sizeof(E) == 4) {
-        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
+                     "@p ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
                      : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y), "=r"(q[1].z), "=r"(q[1].w)
-                     : "l"(p));
+                     : "l"(p), "r"(uint32_t(on)));
     } else {
-        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w) : "l"(p));
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                     "@p ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
+                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w)
+                     : "l"(p), "r"(uint32_t(on)));
     }
 }
 template <class E>
@@ -183,16 +188,20 @@ __device__ __forceinline__ void store_vector(void *p, const uint4 *q) {
     }
 }
 
-template <class E>
+// Register pair i as FP32.  AGAIN: not merged with an earlier unpacking, so that only
+// the packed values stay in registers in between.
+template <class E, bool AGAIN = false>
 __device__ __forceinline__ f2_t up2(const Raw<E> &r, int i) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
     if constexpr (sizeof(E) == 4) {
         return f2_make(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else if constexpr (std::is_same_v<E, __half>) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        uint32_t v = w[i];
+        if constexpr (AGAIN) asm volatile("" : "+r"(v));
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&v));
         return f2_make(p.x, p.y);
     } else {
-        return f2_from_bf16x2(w[i]);
+        return AGAIN ? f2_from_bf16x2_v(w[i]) : f2_from_bf16x2(w[i]);
     }
 }
 template <class E>
@@ -371,36 +380,72 @@ __device__ __forceinline__ bool is_turned(int i, const LaneColumns<PAIRS> &col) 
     return PAIRS == kHalf ? col.turned != 0 : (col.turned >> i) & 1;
 }
 
-// Sum over the lanes of a team of a power of two.
+// Sum over the lanes of a team, neighbours half a team apart first.  TEAM 0: of
+// `team` lanes, known when the kernel runs.
+template <int TEAM>
 __device__ __forceinline__ float team_add(float v, int team) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        if (o < team) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
+    for (int o = TEAM ? TEAM / 2 : 16; o >= 1; o >>= 1)
+        if (TEAM || o < team) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
 
-// A lane's part of a row's sum of products f g: register pairs by FMA, then the two
-// columns of a pair.
-__device__ __forceinline__ float lane_dot(const f2_t (&f)[8], const f2_t (&g)[8]) {
-    f2_t v = f2_mul(f[0], g[0]);
+// A lane's part of a row's sum of products f g: register pairs of each vector by FMA,
+// their two columns, the two vectors (those that the lane has).
+template <int PAIRS>
+__device__ __forceinline__ float lane_dot(const f2_t (&f)[8], const f2_t (&g)[8], const LaneColumns<PAIRS> &col) {
+    f2_t a = f2_mul(f[0], g[0]), b = f2_mul(f[4], g[4]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v = f2_fma(f[i], g[i], v);
-    return __fadd_rn(f2_lo(v), f2_hi(v));
+    for (int i = 1; i < 4; ++i) {
+        a = f2_fma(f[i], g[i], a);
+        b = f2_fma(f[4 + i], g[4 + i], b);
+    }
+    const float x = __fadd_rn(f2_lo(a), f2_hi(a)), y = __fadd_rn(f2_lo(b), f2_hi(b));
+    return __fadd_rn(col.at[0] >= 0 ? x : 0.f, col.at[1] >= 0 ? y : 0.f);
 }
 
-__device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) { return row_rstd(ss, float(p.D), p.inv_d, p.eps); }
+// 1 / sqrt(ss / D + eps): the function's value and one step of Newton's iteration
+// (where that is a number: 0 and infinity keep the function's infinity and 0).
+__device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) {
+    const float v = __fmaf_rn(ss, p.inv_d, p.eps), r = rsqrtf(v);
+    const float e = __fmaf_rn(-__fmul_rn(v, r), r, 1.f);
+    return e == e ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
+}
+
+// qk_rstd of the rows whose lanes' sums are s[0 .. 3], for the whole team.  From four
+// lanes on every lane hands rows on while it adds up, so that a row's root is taken
+// in a quarter of the team only; the additions are team_add's.
+template <int TEAM>
+__device__ __forceinline__ void team_rstd(float (&s)[4], const RotaryParams &p) {
+    if constexpr (TEAM >= 4) {
+        const bool h = threadIdx.x & (TEAM / 2), l = threadIdx.x & (TEAM / 4);
+        const float a = __fadd_rn(h ? s[2] : s[0], __shfl_xor_sync(kFull, h ? s[0] : s[2], TEAM / 2));
+        const float b = __fadd_rn(h ? s[3] : s[1], __shfl_xor_sync(kFull, h ? s[1] : s[3], TEAM / 2));
+        float v = __fadd_rn(l ? b : a, __shfl_xor_sync(kFull, l ? a : b, TEAM / 4));
+#pragma unroll
+        for (int o = TEAM / 8; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
+        const float r = qk_rstd(v, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = __shfl_sync(kFull, r, (i >> 1) * (TEAM / 2) + (i & 1) * (TEAM / 4), TEAM);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = qk_rstd(team_add<TEAM>(s[i], p.team), p);
+    }
+}
 
 // ----------------------------------------------------------------- forward, and rotation alone
 
 constexpr int kRotaryThreads = 256;
 
-// U: heads whose loads are issued at once.
-template <class E, int PAIRS, bool NORM, int U>
+// The heads of a chunk go through in fours, whose loads are issued together.
+template <class E, int PAIRS, bool NORM, int TEAM>
 __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
     extern __shared__ float4 shared[];                   // the weights (NORM), the teams' rows (kSplit)
     constexpr bool kTogether = NORM || PAIRS == kSplit;  // the lanes of a warp exchange values
-    const uint32_t mine = p.by_team.quotient(threadIdx.x), teams = p.by_team.quotient(kRotaryThreads);
-    const int lane = int(threadIdx.x - mine * uint32_t(p.team));
+    constexpr int U = 4, Q = Raw<E>::kQ;
+    const uint32_t mine = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : p.by_team.quotient(threadIdx.x);
+    const uint32_t teams = TEAM ? kRotaryThreads / (TEAM ? TEAM : 1) : p.by_team.quotient(kRotaryThreads);
+    const int lane = int(threadIdx.x - mine * uint32_t(TEAM ? TEAM : p.team));
     const uint32_t unit = blockIdx.x * teams + mine, token = p.by_chunks.quotient(unit);
     const int head0 = int(unit - token * uint32_t(p.chunks)) * p.per;
     const bool in = mine < teams && unit < p.units;
@@ -412,10 +457,13 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
         if (n == 0) return;
     }
     const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    const E *const q_in = static_cast<const E *>(p.side[0].in) + int64_t(token) * p.side[0].in_t;
-    const E *const k_in = static_cast<const E *>(p.side[1].in) + int64_t(token) * p.side[1].in_t;
-    E *const q_out = static_cast<E *>(p.side[0].out) + int64_t(token) * p.side[0].out_t;
-    E *const k_out = static_cast<E *>(p.side[1].out) + int64_t(token) * p.side[1].out_t;
+    // the row of head h, and of the next one
+    auto row_of = [&](const void *q, int64_t q_t, int64_t q_h, const void *k, int64_t k_t, int64_t k_h, int h) {
+        return h < p.hq ? static_cast<const E *>(q) + (token * q_t + h * q_h) : static_cast<const E *>(k) + (token * k_t + (h - p.hq) * k_h);
+    };
+    const HeadsParams &qs = p.side[0], &ks = p.side[1];
+    const E *src = row_of(qs.in, qs.in_t, qs.in_h, ks.in, ks.in_t, ks.in_h, head0);
+    E *dst = const_cast<E *>(row_of(qs.out, qs.out_t, qs.out_h, ks.out, ks.out_t, ks.out_h, head0));
     float *row = nullptr;
     if constexpr (PAIRS == kSplit) row = reinterpret_cast<float *>(shared + (NORM ? p.D / 2 : 0)) + mine * p.D;
     Angles<PAIRS> a;
@@ -424,14 +472,9 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = head0 + i + u;
-            const E *src = h < p.hq ? q_in + h * p.side[0].in_h : k_in + (h - p.hq) * p.side[1].in_h;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint4 *q = r[u].q + j * Raw<E>::kQ;
-#pragma unroll
-                for (int l = 0; l < Raw<E>::kQ; ++l) q[l] = make_uint4(0, 0, 0, 0);
-                if (i + u < n && col.at[j] >= 0) load_vector<E>(q, src + col.at[j]);
-            }
+            for (int j = 0; j < 2; ++j) load_vector<E>(r[u].q + j * Q, src + col.at[j], i + u < n && col.at[j] >= 0);
+            src = h + 1 == p.hq ? static_cast<const E *>(ks.in) + token * ks.in_t : src + (h < p.hq ? qs.in_h : ks.in_h);
         }
         if (i == 0) {
             if constexpr (NORM) {
@@ -440,30 +483,40 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
             }
             lane_angles<E, PAIRS>(p, position, lane, col, a);
         }
+        float s[U];
+        if constexpr (NORM) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                f2_t f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
+                s[u] = lane_dot<PAIRS>(f, f, col);
+            }
+            team_rstd<TEAM>(s, p);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i + u >= (kTogether ? p.per : n)) break;
             const int h = head0 + i + u;
             f2_t f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
+            for (int j = 0; j < 8; ++j) f[j] = up2<E, NORM>(r[u], j);
             if constexpr (NORM) {
                 f2_t w[8];
                 lane_weights<PAIRS>(shared, h >= p.hq, col, p.D >> 3, w);
-                const f2_t rstd = f2_both(qk_rstd(team_add(lane_dot(f, f), p.team), p));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], f2_both(s[u])), w[j]);
             }
             turn_lane<PAIRS>(f, a, col, p, row);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r[u], j, f[j]);
             if (i + u < n) {
-                E *dst = h < p.hq ? q_out + h * p.side[0].out_h : k_out + (h - p.hq) * p.side[1].out_h;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r[u].q + j * Raw<E>::kQ);
+                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r[u].q + j * Q);
             }
+            dst = h + 1 == p.hq ? static_cast<E *>(ks.out) + token * ks.out_t : dst + (h < p.hq ? qs.out_h : ks.out_h);
         }
     }
 }
@@ -520,7 +573,8 @@ inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool strad
     return 16 * D + kQkWarps * (ring_bytes + (grads ? kQkGroup * D * 4 * (straddles ? 2 : 1) : 0) + (split ? 2048 : 0));
 }
 
-template <class E, int PAIRS, bool GRADS>
+// With ws.hdr == NULL there are no gradients: every active slot is one on its own.
+template <class E, int PAIRS, int TEAM>
 __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
     extern __shared__ float4 shared[];
     const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -528,8 +582,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     const bool in = unit < p.units;
     const uint32_t win = p.by_chunks.quotient(in ? unit : 0);
     const int chunk = int((in ? unit : 0) - win * uint32_t(p.chunks));
-    const bool grads = GRADS && qk_header_ok(p.ws);
-    if (GRADS && !grads && unit == 0 && lane32 == 0) qk_report(p.ws, kStHeader);
+    const bool grads = p.ws.hdr && qk_header_ok(p.ws);
+    if (p.ws.hdr && !grads && unit == 0 && lane32 == 0) qk_report(p.ws, kStHeader);
     Window wd = window_of(p, win, grads);
     if (!in) {
         wd.run = -1;
@@ -537,14 +591,15 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     }
     stage_weights<E>(shared, p);
 
-    const int lane = lane32 & (p.team - 1), team = lane32 / p.team, teams = 32 / p.team;
+    const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
     const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    const int head0 = chunk * p.per, heads = p.heads - head0 < p.per ? p.heads - head0 : p.per;
+    const int head0 = chunk * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
     const int run_steps = in_run ? (kQkGroup + teams - 1) / teams : 0, steps = run_steps + (loose + teams - 1) / teams;
 
     using R = Ring<E>;
-    const int sums_bytes = GRADS ? kQkGroup * p.D * 4 * (straddles ? 2 : 1) : 0;
+    constexpr int Q = Raw<E>::kQ;
+    const int sums_bytes = p.ws.hdr ? kQkGroup * p.D * 4 * (straddles ? 2 : 1) : 0;
     uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
     const uint32_t ring = smem_addr(mine) + lane32 * 16;
     float *const sums = reinterpret_cast<float *>(mine + R::kBytes);                    // [kinds][8][D] of the run's tokens
@@ -562,31 +617,41 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
         for (int i = t; i > 0; --i) m &= m - 1;
         return 6 + __ffs(m);
     };
-    // The copies of the next row: one commit a row, empty rows too.
-    int f_step = 0, f_head = 0, f_stage = 0, f_place = place(0);
+    // The copies of the next row: one commit a row.  A row's address follows from the
+    // one before but for the first of each kind of a token.
+    int f_step = 0, f_head = head0;
+    uint32_t f_dst = ring;
+    const E *f_x = nullptr, *f_g = nullptr;
+    bool f_on = false;
     auto fetch = [&]() {
         if (f_step < steps) {
-            const bool on = f_place >= 0;
-            const int64_t slot = on ? int64_t(win) * 8 - 7 + f_place : 0;
-            const int h = head0 + f_head, side = h >= p.hq, k = side ? h - p.hq : h;
-            const HeadsParams &s = p.side[side];
-            const E *x = static_cast<const E *>(s.in) + slot * s.in_t + k * s.in_h;
-            const E *g = static_cast<const E *>(s.dy) + slot * s.dy_t + k * s.dy_h;
-            uint32_t dst = ring + f_stage * (R::kPieces * 512);
+            const bool keys = f_head >= p.hq;
+            const HeadsParams &s = p.side[keys];
+            if (f_head == head0 || f_head == p.hq) {
+                const int at = place(f_step);
+                f_on = at >= 0;
+                const int64_t slot = f_on ? int64_t(win) * 8 - 7 + at : 0;
+                const int h = keys ? f_head - p.hq : f_head;
+                f_x = static_cast<const E *>(s.in) + (slot * s.in_t + h * s.in_h);
+                f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool some = on && col.at[j] >= 0;
-                const int at = some ? col.at[j] : 0;
+                const bool some = f_on && col.at[j] >= 0;
+                const int at = col.at[j] >= 0 ? col.at[j] : 0;
 #pragma unroll
-                for (int l = 0; l < Raw<E>::kQ; ++l) {
-                    cp_async_zfill(dst + (j * Raw<E>::kQ + l) * 512, reinterpret_cast<const uint4 *>(x + at) + l, some ? 16 : 0);
-                    cp_async_zfill(dst + ((2 + j) * Raw<E>::kQ + l) * 512, reinterpret_cast<const uint4 *>(g + at) + l, some ? 16 : 0);
+                for (int l = 0; l < Q; ++l) {
+                    cp_async_zfill(f_dst + (j * Q + l) * 512, reinterpret_cast<const uint4 *>(f_x + at) + l, some ? 16 : 0);
+                    cp_async_zfill(f_dst + ((2 + j) * Q + l) * 512, reinterpret_cast<const uint4 *>(f_g + at) + l, some ? 16 : 0);
                 }
             }
-            f_stage = f_stage + 1 == R::kDepth ? 0 : f_stage + 1;
-            if (++f_head == heads) {
-                f_head = 0;
-                if (++f_step < steps) f_place = place(f_step);
+            f_x += s.in_h;
+            f_g += s.dy_h;
+            f_dst += R::kPieces * 512;
+            if (f_dst == ring + R::kBytes) f_dst = ring;
+            if (++f_head == end) {
+                f_head = head0;
+                ++f_step;
             }
         }
         cp_async_commit();
@@ -597,90 +662,84 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     if (steps == 0) return;
 
     Angles<PAIRS> a;
-    f2_t acc[8];
-    int stage = 0;
+    uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
-        const bool on = at >= 0;
+        const bool on = at >= 0, run = step < run_steps;
         const int64_t slot = on ? int64_t(win) * 8 - 7 + at : 0;
         const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
         lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, col, a);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
-        if (GRADS && grads && on && chunk == 0 && lane == 0) {
-            const bool run = step < run_steps;
-            const bool known = int64_t(id) < p.ws.n;
+        const bool known = int64_t(id) < p.ws.n;
+        if (grads && on && chunk == 0 && lane == 0) {
             const int bad = known ? (atomicExch(p.ws.flag + id, run ? 1 : 2) ? kStDouble : 0) : kStPlan;
             if (bad) qk_report(p.ws, bad);
         }
-        for (int i = 0; i < heads; ++i) {
-            fetch();
-            cp_async_wait<R::kDepth - 1>();
-            Raw<E> rx, rg;
-            const uint32_t src = ring + stage * (R::kPieces * 512);
+        // the token's heads of one kind after the other
+        for (int h = head0; h < end;) {
+            const bool keys = h >= p.hq;
+            const int stop = keys || end < p.hq ? end : p.hq;
+            const HeadsParams &s = p.side[keys];
+            E *dst = static_cast<E *>(s.out) + (slot * s.out_t + (keys ? h - p.hq : h) * s.out_h);
+            f2_t acc[8];
 #pragma unroll
-            for (int l = 0; l < 2 * Raw<E>::kQ; ++l) {
-                ld_shared_vec(src + l * 512, rx.q[l]);
-                ld_shared_vec(src + (2 * Raw<E>::kQ + l) * 512, rg.q[l]);
-            }
-            stage = stage + 1 == R::kDepth ? 0 : stage + 1;
-            const int h = head0 + i, side = h >= p.hq;
-            f2_t x[8], g[8], b[8];
+            for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
+            for (; h < stop; ++h) {
+                fetch();
+                cp_async_wait<R::kDepth - 1>();
+                Raw<E> rx, rg;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = up2<E>(rx, j);
-                g[j] = up2<E>(rg, j);
-            }
-            turn_lane<PAIRS>(g, a, col, p, row);
-            lane_weights<PAIRS>(shared, side, col, p.D >> 3, b);
+                for (int l = 0; l < 2 * Q; ++l) {
+                    ld_shared_vec(from + l * 512, rx.q[l]);
+                    ld_shared_vec(from + (2 * Q + l) * 512, rg.q[l]);
+                }
+                from += R::kPieces * 512;
+                if (from == ring + R::kBytes) from = ring;
+                f2_t x[8], g[8], b[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
-            const float ss = team_add(lane_dot(x, x), p.team), sb = team_add(lane_dot(b, x), p.team);
-            const float rstd = qk_rstd(ss, p), m = row_mean_gxhat(sb, rstd, float(p.D), p.inv_d);
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = up2<E>(rx, j);
+                    g[j] = up2<E>(rg, j);
+                }
+                turn_lane<PAIRS>(g, a, col, p, row);
+                lane_weights<PAIRS>(shared, keys, col, p.D >> 3, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = f2_mul(x[j], f2_both(rstd));
-                if constexpr (GRADS) acc[j] = f2_fma(g[j], x[j], acc[j]);
-                down2<E>(rx, j, f2_mul(f2_fma(x[j], f2_both(-m), b[j]), f2_both(rstd)));
-            }
-            if (on) {
-                const HeadsParams &s = p.side[side];
-                E *dst = static_cast<E *>(s.out) + slot * s.out_t + (side ? h - p.hq : h) * s.out_h;
+                for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
+                const float ss = team_add<TEAM>(lane_dot<PAIRS>(x, x, col), size), sb = team_add<TEAM>(lane_dot<PAIRS>(b, x, col), size);
+                const float rstd = qk_rstd(ss, p), m = __fmul_rn(__fmul_rn(sb, rstd), p.inv_d);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Raw<E>::kQ);
-            }
-            // the last head of its kind in the chunk: the token's sums are complete
-            if (GRADS && (i + 1 == heads || h + 1 == p.hq)) {
-                if (grads && on) {
-                    float *dst = sums + (side && straddles ? kQkGroup * p.D : 0) + (at - wd.run) * p.D;
-                    bool keep = true;
-                    if (step >= run_steps) {
-                        keep = int64_t(id) < p.ws.n;
-                        const int64_t slot_of = side ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
-                        dst = p.ws.spill + (slot_of * p.ws.n + id) * p.D;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = f2_mul(x[j], f2_both(rstd));
+                    acc[j] = f2_fma(g[j], x[j], acc[j]);
+                    down2<E>(rx, j, f2_mul(f2_fma(x[j], f2_both(-m), b[j]), f2_both(rstd)));
+                }
+                if (on) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (keep && col.at[j] >= 0) {
-                            *reinterpret_cast<ulonglong2 *>(dst + col.at[j]) = make_ulonglong2(acc[4 * j], acc[4 * j + 1]);
-                            *reinterpret_cast<ulonglong2 *>(dst + col.at[j] + 4) = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);
-                        }
+                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Q);
                 }
+                dst += s.out_h;
+            }
+            if (grads && on && (run || known)) {
+                const int64_t part = keys ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
+                float *to = run ? sums + ((keys && straddles ? kQkGroup : 0) + at - wd.run) * p.D : p.ws.spill + (part * p.ws.n + id) * p.D;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
+                for (int j = 0; j < 2; ++j)
+                    if (col.at[j] >= 0) {
+                        *reinterpret_cast<ulonglong2 *>(to + col.at[j]) = make_ulonglong2(acc[4 * j], acc[4 * j + 1]);
+                        *reinterpret_cast<ulonglong2 *>(to + col.at[j] + 4) = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);
+                    }
             }
         }
     }
-    if (GRADS && grads && in_run) {
+    if (grads && in_run) {
         __syncwarp();
         const int64_t g = __shfl_sync(kFull, wd.id, wd.run) >> 3;
         if (chunk == 0 && lane32 == 0) p.ws.whole[g] = 1;
-        for (int side = head0 < p.hq ? 0 : 1; side < 2; ++side) {
-            if (side && head0 + heads <= p.hq) break;
-            const float *src = sums + (side && straddles ? kQkGroup * p.D : 0);
-            const int64_t slot_of = side ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
-            float *dst = p.ws.partial + (slot_of * p.ws.groups + g) * p.D;
+        for (int keys = head0 < p.hq ? 0 : 1; keys < 2; ++keys) {
+            if (keys && end <= p.hq) break;
+            const float *src = sums + (keys && straddles ? kQkGroup * p.D : 0);
+            const int64_t part = keys ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
+            float *dst = p.ws.partial + (part * p.ws.groups + g) * p.D;
             for (int k = lane32 * 4; k < p.D; k += 128) {
                 float4 v = *reinterpret_cast<const float4 *>(src + k);
 #pragma unroll
@@ -695,8 +754,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
 }
 
 // Launches the rows of one call for element type E (rotary_*.cu instantiate it).
-// mode: 0 rotation alone, 1 norm and rotation, 2 their backward pass, 3 with weight gradients.
-template <class E>
-int rotary_run(RotaryParams p, int mode, bool interleaved, cudaStream_t stream);
+// mode: 0 rotation alone, 1 norm and rotation, 2 their backward pass.
+template <class E, int PAIRS>
+int rotary_run_pairs(RotaryParams p, int mode, cudaStream_t stream);
 
 }  // namespace rbi

@@ -20,7 +20,9 @@ import numpy as np
 
 U = 2.0 ** -24
 ANGLE = 5               # U of a cosine or sine, times scale
-RSTD = 12               # U of 1 / rms: a sum of squares of depth 15, halved by the root, and four roundings
+# U of 1 / rms: a sum of squares of depth 16 (4 products and 5 additions of a lane, 5 of a team, 1/D and the
+# rounding with eps), halved by the root, and 2.5 of the root (one Newton step: its products and its sum)
+RSTD = 12
 
 # 1 / (2 pi) to 400 bits, from Machin's formula in integers
 def _inverse_turn(bits: int = 400) -> Fraction:
@@ -109,7 +111,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     ea = np.abs(w) * eg + U * np.abs(a)
     m = (a * xhat).mean(-1, keepdims=True)
     em = rstd * ((np.abs(x) * ea).sum(-1, keepdims=True) + 15 * U * np.abs(a * x).sum(-1, keepdims=True)) / D \
-        + (RSTD + 2) * U * np.abs(m)
+        + (RSTD + 3) * U * np.abs(m)                     # its three products and 1/D on top of the root's
     t = a - xhat * m
     dx = rstd * t
     et = ea + np.abs(xhat) * em + (RSTD + 1) * U * np.abs(xhat * m) + U * np.abs(t)
