@@ -175,22 +175,25 @@ __device__ __forceinline__ float4 plus(const float4 &a, const float4 &b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
 
-// A group's sum of four columns over the partial sums `slots` from its tokens' own.
+// A group's sum of four columns over the partial sums `slots` from its tokens' own, in
+// the order in which a warp of the backward pass adds up a whole group.
 __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool check) {
-    const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup;
+    const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup, share = qk_share(32 / qk_team(ws.D));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < slots; ++c) {
         float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool some = false;
-        for (int i = 0; i < n; ++i) {
-            const int64_t t = g * kQkGroup + i;
-            if (ws.flag[t] != 2) {
-                if (check && c == 0) qk_report(ws, kStMissing);
-                continue;
+        for (int first = 0; first < n; first += share) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = first; i < first + share && i < n; ++i) {
+                const int64_t t = g * kQkGroup + i;
+                if (ws.flag[t] != 2) {
+                    if (check && c == 0) qk_report(ws, kStMissing);
+                    continue;
+                }
+                const float4 x = *reinterpret_cast<const float4 *>(ws.spill + ((slot0 + c) * ws.n + t) * ws.D + col);
+                s = i > first ? plus(s, x) : x;
             }
-            const float4 x = *reinterpret_cast<const float4 *>(ws.spill + ((slot0 + c) * ws.n + t) * ws.D + col);
-            u = some ? plus(u, x) : x;
-            some = true;
+            u = first ? plus(u, s) : s;
         }
         v = c ? plus(v, u) : u;
     }

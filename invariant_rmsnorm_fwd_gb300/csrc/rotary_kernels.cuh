@@ -38,6 +38,16 @@ struct QkChunks {
     }
 };
 
+// Lanes of a team: the power of two that holds D / 16 lanes.
+__host__ __device__ inline int qk_team(int D) {
+    int p = 1;
+    while (16 * p < D) p <<= 1;
+    return p;
+}
+// The 8 tokens of a group are summed in shares of as many consecutive tokens as each of
+// a warp's teams takes, from the first to the last, then the shares likewise.
+__host__ __device__ inline int qk_share(int teams) { return teams < kQkGroup ? kQkGroup / teams : 1; }
+
 struct QkWs {
     WsHeader *hdr;                   // n_rows tokens; hidden = the sizes (qk_sizes)
     int32_t *flag;                   // [N] 0 nothing, 1 in its group's partial, 2 its own sums stored
@@ -559,8 +569,10 @@ __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bo
     return r;
 }
 
-// Heads on their way into shared memory: a ring of kDepth rows a team, every lane
-// copying its own columns of x and dy to places that only it reads.
+// Heads on their way into shared memory: a ring of kDepth rows a team.  Every lane copies
+// its own columns of x and dy; in FP32, where they are 32 bytes a vector, two lanes copy
+// first the one's, then the other's, so that no copy takes half a sector (backward of
+// 17,620 tokens, 32+8 heads of 128: XXX us).
 template <class E>
 struct Ring {
     static constexpr int kPieces = 4 * Raw<E>::kQ;       // 16-byte pieces of a lane's row: x, dy
@@ -569,8 +581,9 @@ struct Ring {
 };
 
 inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool straddles) {
-    // both weights, then per warp: ring, the run's tokens' sums (of both kinds where a chunk has both), kSplit's rows
-    return 16 * D + kQkWarps * (ring_bytes + (grads ? kQkGroup * D * 4 * (straddles ? 2 : 1) : 0) + (split ? 2048 : 0));
+    // both weights, then per warp: ring, the teams' sums (of both kinds where a chunk has both), kSplit's rows; teams x D
+    // floats are at most 2048 bytes
+    return 16 * D + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0) + (split ? 2048 : 0));
 }
 
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
@@ -592,25 +605,24 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     stage_weights<E>(shared, p);
 
     const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
+    const int share = qk_share(teams);
     const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
     const int head0 = chunk * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
-    const int run_steps = in_run ? (kQkGroup + teams - 1) / teams : 0, steps = run_steps + (loose + teams - 1) / teams;
+    const int run_steps = in_run ? share : 0, steps = run_steps + (loose + teams - 1) / teams;
 
     using R = Ring<E>;
     constexpr int Q = Raw<E>::kQ;
-    const int sums_bytes = p.ws.hdr ? kQkGroup * p.D * 4 * (straddles ? 2 : 1) : 0;
+    const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
     uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
     const uint32_t ring = smem_addr(mine) + lane32 * 16;
-    float *const sums = reinterpret_cast<float *>(mine + R::kBytes);                    // [kinds][8][D] of the run's tokens
+    // [kinds][teams][D]: each team's sums over its tokens of the run; a lane has its own columns
+    float *const sums = reinterpret_cast<float *>(mine + R::kBytes);
     float *const row = reinterpret_cast<float *>(mine + R::kBytes + sums_bytes) + team * p.D;
 
     // Lane (of the window's ids) of this team's slot in a step, -1: none.
     auto place = [&](int step) {
-        if (step < run_steps) {
-            const int t = step * teams + team;
-            return t < kQkGroup ? wd.run + t : -1;
-        }
+        if (step < run_steps) return team * share < kQkGroup ? wd.run + team * share + step : -1;
         const int t = (step - run_steps) * teams + team;
         if (t >= loose) return -1;
         uint32_t m = wd.loose;
@@ -621,6 +633,17 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     // one before but for the first of each kind of a token.
     int f_step = 0, f_head = head0;
     uint32_t f_dst = ring;
+    // copy l: columns of the vector's owner, which half of it, the owner's place
+    int f_at[Q][2], f_half[Q], f_lane[Q];
+    const bool pairs = Q == 2 && size > 1;
+    const int odd = lane32 & 1;
+#pragma unroll
+    for (int l = 0; l < Q; ++l) {
+        f_half[l] = pairs ? odd : l;
+        f_lane[l] = pairs ? (l - odd) * 16 : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f_at[l][j] = pairs ? __shfl_sync(kFull, col.at[j], (lane32 & ~1) + l) : col.at[j];
+    }
     const E *f_x = nullptr, *f_g = nullptr;
     bool f_on = false;
     auto fetch = [&]() {
@@ -636,15 +659,15 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const bool some = f_on && col.at[j] >= 0;
-                const int at = col.at[j] >= 0 ? col.at[j] : 0;
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int l = 0; l < Q; ++l) {
-                    cp_async_zfill(f_dst + (j * Q + l) * 512, reinterpret_cast<const uint4 *>(f_x + at) + l, some ? 16 : 0);
-                    cp_async_zfill(f_dst + ((2 + j) * Q + l) * 512, reinterpret_cast<const uint4 *>(f_g + at) + l, some ? 16 : 0);
+                    const bool some = f_on && f_at[l][j] >= 0;
+                    const int at = (some ? f_at[l][j] : 0) + 4 * f_half[l];
+                    const uint32_t dst = f_dst + f_lane[l] + (j * Q + f_half[l]) * 512;
+                    cp_async_zfill(dst, f_x + at, some ? 16 : 0);
+                    cp_async_zfill(dst + 2 * Q * 512, f_g + at, some ? 16 : 0);
                 }
-            }
             f_x += s.in_h;
             f_g += s.dy_h;
             f_dst += R::kPieces * 512;
@@ -684,8 +707,9 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
             for (; h < stop; ++h) {
+                cp_async_wait<R::kDepth - 2>();
+                __syncwarp();                            // everyone's copies of this row; and the row before has been read
                 fetch();
-                cp_async_wait<R::kDepth - 1>();
                 Raw<E> rx, rg;
 #pragma unroll
                 for (int l = 0; l < 2 * Q; ++l) {
@@ -721,12 +745,18 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
             }
             if (grads && on && (run || known)) {
                 const int64_t part = keys ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
-                float *to = run ? sums + ((keys && straddles ? kQkGroup : 0) + at - wd.run) * p.D : p.ws.spill + (part * p.ws.n + id) * p.D;
+                float *to = run ? sums + ((keys && straddles ? teams : 0) + team) * p.D : p.ws.spill + (part * p.ws.n + id) * p.D;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (col.at[j] >= 0) {
-                        *reinterpret_cast<ulonglong2 *>(to + col.at[j]) = make_ulonglong2(acc[4 * j], acc[4 * j + 1]);
-                        *reinterpret_cast<ulonglong2 *>(to + col.at[j] + 4) = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);
+                        ulonglong2 *q = reinterpret_cast<ulonglong2 *>(to + col.at[j]);
+                        ulonglong2 u = make_ulonglong2(acc[4 * j], acc[4 * j + 1]), v = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);
+                        if (run && step > 0) {
+                            u = make_ulonglong2(f2_add(q[0].x, u.x), f2_add(q[0].y, u.y));
+                            v = make_ulonglong2(f2_add(q[1].x, v.x), f2_add(q[1].y, v.y));
+                        }
+                        q[0] = u;
+                        q[1] = v;
                     }
             }
         }
@@ -737,13 +767,12 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
         if (chunk == 0 && lane32 == 0) p.ws.whole[g] = 1;
         for (int keys = head0 < p.hq ? 0 : 1; keys < 2; ++keys) {
             if (keys && end <= p.hq) break;
-            const float *src = sums + (keys && straddles ? kQkGroup * p.D : 0);
+            const float *src = sums + (keys && straddles ? teams * p.D : 0);
             const int64_t part = keys ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
             float *dst = p.ws.partial + (part * p.ws.groups + g) * p.D;
             for (int k = lane32 * 4; k < p.D; k += 128) {
                 float4 v = *reinterpret_cast<const float4 *>(src + k);
-#pragma unroll
-                for (int t = 1; t < kQkGroup; ++t) {
+                for (int t = 1; t * share < kQkGroup; ++t) {
                     const float4 u = *reinterpret_cast<const float4 *>(src + t * p.D + k);
                     v = make_float4(__fadd_rn(v.x, u.x), __fadd_rn(v.y, u.y), __fadd_rn(v.z, u.z), __fadd_rn(v.w, u.w));
                 }

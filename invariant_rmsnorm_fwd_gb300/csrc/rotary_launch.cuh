@@ -4,12 +4,6 @@
 
 namespace rbi {
 
-inline int lanes_pow2(int lanes) {
-    int p = 1;
-    while (p < lanes) p <<= 1;
-    return p;
-}
-
 template <class E, int PAIRS, bool NORM, int TEAM>
 static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     p.by_team = Divisor(uint32_t(p.team));
@@ -47,7 +41,7 @@ static int rotary_launch_norm(RotaryParams &p, int mode, cudaStream_t stream) {
 template <class E, int PAIRS>
 static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
     // The rotation alone needs no team of a power of two but where it exchanges columns.
-    p.team = mode || PAIRS == kSplit ? lanes_pow2(p.lanes) : PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
+    p.team = mode || PAIRS == kSplit ? qk_team(p.D) : PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
     if (mode == 0) return rotary_launch_fwd<E, PAIRS, false, 0>(p, stream);
     if constexpr (PAIRS != kSplit) {
         if (p.team == 4) return rotary_launch_norm<E, PAIRS, 4>(p, mode, stream);

@@ -138,6 +138,8 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
     chunks = (heads + 7) // 8
     per = (heads + chunks - 1) // chunks
     groups = (n + 7) // 8
+    team = 1 << max(0, int(np.ceil(np.log2(D / 16))))
+    tokens = max(1, 8 // (32 // team))                                # of a group, added up by one team
     shares = 8 * 16 * 4
     share = (groups + shares - 1) // shares
     out = []
@@ -150,11 +152,14 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
                 if not len(mine):
                     continue
                 u = None
-                for t in range(8 * g, min(8 * g + 8, n)):
-                    s = np.zeros(D, np.float32)
-                    for h in mine:
-                        s = s + leaf[t, h]
-                    u = s if u is None else u + s
+                for first in range(8 * g, min(8 * g + 8, n), tokens):
+                    part = None
+                    for t in range(first, min(first + tokens, n, 8 * g + 8)):
+                        s = np.zeros(D, np.float32)
+                        for h in mine:
+                            s = s + leaf[t, h]
+                        part = s if part is None else part + s
+                    u = part if u is None else u + part
                 v = u if v is None else v + u
             value.append(v)
         part = []
