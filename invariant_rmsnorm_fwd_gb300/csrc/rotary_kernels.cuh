@@ -198,20 +198,16 @@ __device__ __forceinline__ void store_vector(void *p, const uint4 *q) {
     }
 }
 
-// Register pair i as FP32.  AGAIN: not merged with an earlier unpacking, so that only
-// the packed values stay in registers in between.
-template <class E, bool AGAIN = false>
+template <class E>
 __device__ __forceinline__ f2_t up2(const Raw<E> &r, int i) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
     if constexpr (sizeof(E) == 4) {
         return f2_make(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else if constexpr (std::is_same_v<E, __half>) {
-        uint32_t v = w[i];
-        if constexpr (AGAIN) asm volatile("" : "+r"(v));
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         return f2_make(p.x, p.y);
     } else {
-        return AGAIN ? f2_from_bf16x2_v(w[i]) : f2_from_bf16x2(w[i]);
+        return f2_from_bf16x2(w[i]);
     }
 }
 template <class E>
@@ -400,18 +396,17 @@ __device__ __forceinline__ float team_add(float v, int team) {
     return v;
 }
 
-// A lane's part of a row's sum of products f g: register pairs of each vector by FMA,
-// their two columns, the two vectors (those that the lane has).
-template <int PAIRS>
-__device__ __forceinline__ float lane_dot(const f2_t (&f)[8], const f2_t (&g)[8], const LaneColumns<PAIRS> &col) {
+// A lane's part of a row's sum of products f g (columns that are not there are zeros):
+// register pairs of each vector by FMA, the two vectors, the two columns.
+__device__ __forceinline__ float lane_dot(const f2_t (&f)[8], const f2_t (&g)[8]) {
     f2_t a = f2_mul(f[0], g[0]), b = f2_mul(f[4], g[4]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
         a = f2_fma(f[i], g[i], a);
         b = f2_fma(f[4 + i], g[4 + i], b);
     }
-    const float x = __fadd_rn(f2_lo(a), f2_hi(a)), y = __fadd_rn(f2_lo(b), f2_hi(b));
-    return __fadd_rn(col.at[0] >= 0 ? x : 0.f, col.at[1] >= 0 ? y : 0.f);
+    a = f2_add(a, b);
+    return __fadd_rn(f2_lo(a), f2_hi(a));
 }
 
 // 1 / sqrt(ss / D + eps): the function's value and one step of Newton's iteration
@@ -422,52 +417,29 @@ __device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) {
     return e == e ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
 }
 
-// qk_rstd of the rows whose lanes' sums are s[0 .. 3], for the whole team.  From four
-// lanes on every lane hands rows on while it adds up, so that a row's root is taken
-// in a quarter of the team only; the additions are team_add's.
-template <int TEAM>
-__device__ __forceinline__ void team_rstd(float (&s)[4], const RotaryParams &p) {
-    if constexpr (TEAM >= 4) {
-        const bool h = threadIdx.x & (TEAM / 2), l = threadIdx.x & (TEAM / 4);
-        const float a = __fadd_rn(h ? s[2] : s[0], __shfl_xor_sync(kFull, h ? s[0] : s[2], TEAM / 2));
-        const float b = __fadd_rn(h ? s[3] : s[1], __shfl_xor_sync(kFull, h ? s[1] : s[3], TEAM / 2));
-        float v = __fadd_rn(l ? b : a, __shfl_xor_sync(kFull, l ? a : b, TEAM / 4));
-#pragma unroll
-        for (int o = TEAM / 8; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
-        const float r = qk_rstd(v, p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = __shfl_sync(kFull, r, (i >> 1) * (TEAM / 2) + (i & 1) * (TEAM / 4), TEAM);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = qk_rstd(team_add<TEAM>(s[i], p.team), p);
-    }
-}
-
 // ----------------------------------------------------------------- forward, and rotation alone
 
 constexpr int kRotaryThreads = 256;
 
-// The heads of a chunk go through in fours, whose loads are issued together.
-template <class E, int PAIRS, bool NORM, int TEAM>
+// Rotation alone.  The heads of a chunk go through in fours, whose loads are issued together.
+template <class E, int PAIRS>
 __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    extern __shared__ float4 shared[];                   // the weights (NORM), the teams' rows (kSplit)
-    constexpr bool kTogether = NORM || PAIRS == kSplit;  // the lanes of a warp exchange values
+    extern __shared__ float4 shared[];                   // kSplit: the teams' rows
+    constexpr bool kTogether = PAIRS == kSplit;          // the lanes of a team exchange values
     constexpr int U = 4, Q = Raw<E>::kQ;
-    const uint32_t mine = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : p.by_team.quotient(threadIdx.x);
-    const uint32_t teams = TEAM ? kRotaryThreads / (TEAM ? TEAM : 1) : p.by_team.quotient(kRotaryThreads);
-    const int lane = int(threadIdx.x - mine * uint32_t(TEAM ? TEAM : p.team));
+    const uint32_t mine = p.by_team.quotient(threadIdx.x), teams = p.by_team.quotient(kRotaryThreads);
+    const int lane = int(threadIdx.x - mine * uint32_t(p.team));
     const uint32_t unit = blockIdx.x * teams + mine, token = p.by_chunks.quotient(unit);
     const int head0 = int(unit - token * uint32_t(p.chunks)) * p.per;
     const bool in = mine < teams && unit < p.units;
     const int32_t id = in ? p.tok_id[token] : -1, position = in ? p.position[token] : 0;
-    if constexpr (NORM) stage_weights<E>(shared, p);
     int n = p.heads - head0 < p.per ? p.heads - head0 : p.per;
     if (id < 0) n = 0;
     if constexpr (!kTogether) {
         if (n == 0) return;
     }
     const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    // the row of head h, and of the next one
+    // the row of head h
     auto row_of = [&](const void *q, int64_t q_t, int64_t q_h, const void *k, int64_t k_t, int64_t k_h, int h) {
         return h < p.hq ? static_cast<const E *>(q) + (token * q_t + h * q_h) : static_cast<const E *>(k) + (token * k_t + (h - p.hq) * k_h);
     };
@@ -475,7 +447,7 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
     const E *src = row_of(qs.in, qs.in_t, qs.in_h, ks.in, ks.in_t, ks.in_h, head0);
     E *dst = const_cast<E *>(row_of(qs.out, qs.out_t, qs.out_h, ks.out, ks.out_t, ks.out_h, head0));
     float *row = nullptr;
-    if constexpr (PAIRS == kSplit) row = reinterpret_cast<float *>(shared + (NORM ? p.D / 2 : 0)) + mine * p.D;
+    if constexpr (PAIRS == kSplit) row = reinterpret_cast<float *>(shared) + mine * p.D;
     Angles<PAIRS> a;
     for (int i = 0; i < (kTogether ? p.per : n); i += U) {
         Raw<E> r[U];
@@ -486,41 +458,18 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
             for (int j = 0; j < 2; ++j) load_vector<E>(r[u].q + j * Q, src + col.at[j], i + u < n && col.at[j] >= 0);
             src = h + 1 == p.hq ? static_cast<const E *>(ks.in) + token * ks.in_t : src + (h < p.hq ? qs.in_h : ks.in_h);
         }
-        if (i == 0) {
-            if constexpr (NORM) {
-                __syncthreads();
-                if (__all_sync(kFull, n == 0)) return;
-            }
-            lane_angles<E, PAIRS>(p, position, lane, col, a);
-        }
-        float s[U];
-        if constexpr (NORM) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                f2_t f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
-                s[u] = lane_dot<PAIRS>(f, f, col);
-            }
-            team_rstd<TEAM>(s, p);
-        }
+        if (i == 0) lane_angles<E, PAIRS>(p, position, lane, col, a);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i + u >= (kTogether ? p.per : n)) break;
             const int h = head0 + i + u;
             f2_t f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = up2<E, NORM>(r[u], j);
-            if constexpr (NORM) {
-                f2_t w[8];
-                lane_weights<PAIRS>(shared, h >= p.hq, col, p.D >> 3, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], f2_both(s[u])), w[j]);
-            }
+            for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
             turn_lane<PAIRS>(f, a, col, p, row);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r[u], j, f[j]);
+                if (is_turned<PAIRS>(j, col)) down2<E>(r[u], j, f[j]);
             if (i + u < n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -531,9 +480,154 @@ __global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_
     }
 }
 
-// ----------------------------------------------------------------- backward of the norm and the rotation
+// ----------------------------------------------------------------- rows through shared memory
 
 constexpr int kQkWarps = 4;
+
+// Heads on their way into shared memory: a ring of kDepth rows a team.  Every lane copies
+// its own columns of its TENSORS tensors; in FP32, where they are 32 bytes a vector, two
+// lanes copy first the one's, then the other's, so that no copy takes half a sector.
+template <class E, int TENSORS>
+struct Ring {
+    static constexpr int kPieces = 2 * TENSORS * Raw<E>::kQ;         // 16-byte pieces of a lane's row
+    static constexpr int kDepth = TENSORS == 1 ? 6 : sizeof(E) == 4 ? 3 : 4;
+    static constexpr int kBytes = kPieces * kDepth * 512;            // of a warp
+};
+template <class E, int PAIRS>
+struct Copies {
+    static constexpr int kQ = Raw<E>::kQ;
+    int at[kQ][2], half[kQ], lane[kQ];                   // copy l: columns of the vector's owner, which half of it, the owner's place
+    __device__ __forceinline__ Copies(const LaneColumns<PAIRS> &col, int size) {
+        const bool pairs = kQ == 2 && size > 1;
+        const int lane32 = threadIdx.x & 31, odd = lane32 & 1;
+#pragma unroll
+        for (int l = 0; l < kQ; ++l) {
+            half[l] = pairs ? odd : l;
+            lane[l] = pairs ? (l - odd) * 16 : 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) at[l][j] = pairs ? __shfl_sync(kFull, col.at[j], (lane32 & ~1) + l) : col.at[j];
+        }
+    }
+    __device__ __forceinline__ void issue(uint32_t dst, const E *row, bool on) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int l = 0; l < kQ; ++l) {
+                const bool some = on && at[l][j] >= 0;
+                cp_async_zfill(dst + lane[l] + (j * kQ + half[l]) * 512, row + (some ? at[l][j] : 0) + 4 * half[l], some ? 16 : 0);
+            }
+    }
+};
+template <class E>
+__device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
+#pragma unroll
+    for (int l = 0; l < 2 * Raw<E>::kQ; ++l) ld_shared_vec(src + l * 512, r.q[l]);
+}
+
+// Norm and rotation.  A warp takes `slots` consecutive slots of a call (at most 32) and one
+// chunk of heads; its teams take the active ones in turns.
+template <class E, int PAIRS, int TEAM>
+__global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_constant__ RotaryParams p, int slots) {
+    extern __shared__ float4 shared[];
+    using R = Ring<E, 1>;
+    const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t unit = blockIdx.x * kQkWarps + warp;
+    const bool in = unit < p.units;
+    const uint32_t win = p.by_chunks.quotient(in ? unit : 0);
+    const int64_t first = int64_t(win) * slots;
+    const bool mine = in && lane32 < slots && first + lane32 < p.n_tokens;
+    const int32_t id = mine ? p.tok_id[first + lane32] : -1, position = mine ? p.position[first + lane32] : 0;
+    stage_weights<E>(shared, p);
+    const int head0 = int((in ? unit : 0) - win * uint32_t(p.chunks)) * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
+    const uint32_t active = __ballot_sync(kFull, id >= 0);
+    const int count = __popc(active);
+    const bool dense = active == (count == 32 ? kFull : (1u << count) - 1u);
+    const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
+    const int steps = (count + teams - 1) / teams;
+    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    const Copies<E, PAIRS> copies(col, size);
+    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + (PAIRS == kSplit ? 2048 : 0));
+    const uint32_t ring = smem_addr(place_of) + lane32 * 16;
+    float *const row = reinterpret_cast<float *>(place_of + R::kBytes) + team * p.D;
+
+    // Lane (of the slots' ids) of this team's slot in a step, -1: none.
+    auto place = [&](int step) {
+        const int t = step * teams + team;
+        if (t >= count) return -1;
+        if (dense) return t;
+        uint32_t m = active;
+        for (int i = t; i > 0; --i) m &= m - 1;
+        return __ffs(m) - 1;
+    };
+    int f_step = 0, f_head = head0;
+    uint32_t f_dst = ring;
+    const E *f_x = nullptr;
+    bool f_on = false;
+    auto fetch = [&]() {
+        if (f_step < steps) {
+            const bool keys = f_head >= p.hq;
+            const HeadsParams &s = p.side[keys];
+            if (f_head == head0 || f_head == p.hq) {
+                const int at = place(f_step);
+                f_on = at >= 0;
+                f_x = static_cast<const E *>(s.in) + ((f_on ? first + at : 0) * s.in_t + (keys ? f_head - p.hq : f_head) * s.in_h);
+            }
+            copies.issue(f_dst, f_x, f_on);
+            f_x += s.in_h;
+            f_dst += R::kPieces * 512;
+            if (f_dst == ring + R::kBytes) f_dst = ring;
+            if (++f_head == end) {
+                f_head = head0;
+                ++f_step;
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch();
+    __syncthreads();                                     // the weights
+
+    Angles<PAIRS> a;
+    uint32_t from = ring;
+    for (int step = 0; step < steps; ++step) {
+        const int at = place(step);
+        const bool on = at >= 0;
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), lane, col, a);
+        for (int h = head0; h < end;) {                  // the token's heads of one kind after the other
+            const bool keys = h >= p.hq;
+            const int stop = keys || end < p.hq ? end : p.hq;
+            const HeadsParams &s = p.side[keys];
+            E *dst = static_cast<E *>(s.out) + ((on ? first + at : 0) * s.out_t + (keys ? h - p.hq : h) * s.out_h);
+            for (; h < stop; ++h) {
+                cp_async_wait<R::kDepth - 2>();
+                __syncwarp();                            // everyone's copies of this row; and the row before has been read
+                fetch();
+                Raw<E> r;
+                take_row<E>(r, from);
+                from += R::kPieces * 512;
+                if (from == ring + R::kBytes) from = ring;
+                f2_t f[8], w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = up2<E>(r, j);
+                const f2_t rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size), p));
+                lane_weights<PAIRS>(shared, keys, col, p.D >> 3, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                turn_lane<PAIRS>(f, a, col, p, row);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) down2<E>(r, j, f[j]);
+                if (on) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r.q + j * Raw<E>::kQ);
+                }
+                dst += s.out_h;
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- backward of the norm and the rotation
 
 // What a warp of the backward pass does with the 8 slots [8 w, 8 w + 8) of a call and
 // one chunk of heads: the run, 8 consecutive slots that hold a whole group in logical
@@ -569,17 +663,6 @@ __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bo
     return r;
 }
 
-// Heads on their way into shared memory: a ring of kDepth rows a team.  Every lane copies
-// its own columns of x and dy; in FP32, where they are 32 bytes a vector, two lanes copy
-// first the one's, then the other's, so that no copy takes half a sector (backward of
-// 17,620 tokens, 32+8 heads of 128: XXX us).
-template <class E>
-struct Ring {
-    static constexpr int kPieces = 4 * Raw<E>::kQ;       // 16-byte pieces of a lane's row: x, dy
-    static constexpr int kDepth = sizeof(E) == 4 ? 3 : 4;
-    static constexpr int kBytes = kPieces * kDepth * 512;   // of a warp
-};
-
 inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool straddles) {
     // both weights, then per warp: ring, the teams' sums (of both kinds where a chunk has both), kSplit's rows; teams x D
     // floats are at most 2048 bytes
@@ -611,7 +694,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
     const int run_steps = in_run ? share : 0, steps = run_steps + (loose + teams - 1) / teams;
 
-    using R = Ring<E>;
+    using R = Ring<E, 2>;
     constexpr int Q = Raw<E>::kQ;
     const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
     uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
@@ -633,17 +716,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     // one before but for the first of each kind of a token.
     int f_step = 0, f_head = head0;
     uint32_t f_dst = ring;
-    // copy l: columns of the vector's owner, which half of it, the owner's place
-    int f_at[Q][2], f_half[Q], f_lane[Q];
-    const bool pairs = Q == 2 && size > 1;
-    const int odd = lane32 & 1;
-#pragma unroll
-    for (int l = 0; l < Q; ++l) {
-        f_half[l] = pairs ? odd : l;
-        f_lane[l] = pairs ? (l - odd) * 16 : 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) f_at[l][j] = pairs ? __shfl_sync(kFull, col.at[j], (lane32 & ~1) + l) : col.at[j];
-    }
+    const Copies<E, PAIRS> copies(col, size);
     const E *f_x = nullptr, *f_g = nullptr;
     bool f_on = false;
     auto fetch = [&]() {
@@ -658,16 +731,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 f_x = static_cast<const E *>(s.in) + (slot * s.in_t + h * s.in_h);
                 f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int l = 0; l < Q; ++l) {
-                    const bool some = f_on && f_at[l][j] >= 0;
-                    const int at = (some ? f_at[l][j] : 0) + 4 * f_half[l];
-                    const uint32_t dst = f_dst + f_lane[l] + (j * Q + f_half[l]) * 512;
-                    cp_async_zfill(dst, f_x + at, some ? 16 : 0);
-                    cp_async_zfill(dst + 2 * Q * 512, f_g + at, some ? 16 : 0);
-                }
+            copies.issue(f_dst, f_x, f_on);
+            copies.issue(f_dst + 2 * Q * 512, f_g, f_on);
             f_x += s.in_h;
             f_g += s.dy_h;
             f_dst += R::kPieces * 512;
@@ -711,11 +776,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 __syncwarp();                            // everyone's copies of this row; and the row before has been read
                 fetch();
                 Raw<E> rx, rg;
-#pragma unroll
-                for (int l = 0; l < 2 * Q; ++l) {
-                    ld_shared_vec(from + l * 512, rx.q[l]);
-                    ld_shared_vec(from + (2 * Q + l) * 512, rg.q[l]);
-                }
+                take_row<E>(rx, from);
+                take_row<E>(rg, from + 2 * Q * 512);
                 from += R::kPieces * 512;
                 if (from == ring + R::kBytes) from = ring;
                 f2_t x[8], g[8], b[8];
@@ -728,7 +790,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 lane_weights<PAIRS>(shared, keys, col, p.D >> 3, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
-                const float ss = team_add<TEAM>(lane_dot<PAIRS>(x, x, col), size), sb = team_add<TEAM>(lane_dot<PAIRS>(b, x, col), size);
+                const float ss = team_add<TEAM>(lane_dot(x, x), size), sb = team_add<TEAM>(lane_dot(b, x), size);
                 const float rstd = qk_rstd(ss, p), m = __fmul_rn(__fmul_rn(sb, rstd), p.inv_d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
