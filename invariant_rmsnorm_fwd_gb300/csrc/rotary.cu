@@ -176,24 +176,41 @@ __device__ __forceinline__ float4 plus(const float4 &a, const float4 &b) {
 }
 
 // A group's sum of four columns over the partial sums `slots` from its tokens' own, in
-// the order in which a warp of the backward pass adds up a whole group.
+// the order in which a warp of the backward pass adds up a whole group.  All loads of a
+// slot are issued at once.
 __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool check) {
     const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup, share = qk_share(32 / qk_team(ws.D));
+    const int64_t t0 = g * kQkGroup;
+    uint32_t there = 0;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < slots; ++c) {
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int first = 0; first < n; first += share) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i = first; i < first + share && i < n; ++i) {
-                const int64_t t = g * kQkGroup + i;
-                if (ws.flag[t] != 2) {
-                    if (check && c == 0) qk_report(ws, kStMissing);
-                    continue;
+        const float *src = ws.spill + ((slot0 + c) * ws.n + t0) * ws.D + col;
+        float4 x[kQkGroup];
+#pragma unroll
+        for (int i = 0; i < kQkGroup; ++i) x[i] = i < n ? *reinterpret_cast<const float4 *>(src + i * ws.D) : v;
+        if (c == 0) {
+            int32_t f[kQkGroup];
+#pragma unroll
+            for (int i = 0; i < kQkGroup; ++i) f[i] = i < n ? ws.flag[t0 + i] : 0;
+#pragma unroll
+            for (int i = 0; i < kQkGroup; ++i) there |= (f[i] == 2) << i;
+            if (check && there != (1u << n) - 1u) qk_report(ws, kStMissing);
+        }
+        float4 u = v, s = v;
+        bool any = false;                                // of the share
+#pragma unroll
+        for (int i = 0; i < kQkGroup; ++i) {
+            if (i < n) {
+                if ((there >> i) & 1) {
+                    s = any ? plus(s, x[i]) : x[i];
+                    any = true;
                 }
-                const float4 x = *reinterpret_cast<const float4 *>(ws.spill + ((slot0 + c) * ws.n + t) * ws.D + col);
-                s = i > first ? plus(s, x) : x;
+                if ((i + 1) % share == 0 || i + 1 == n) {
+                    if (!any) s = make_float4(0.f, 0.f, 0.f, 0.f);
+                    u = i < share ? s : plus(u, s);
+                    any = false;
+                }
             }
-            u = first ? plus(u, s) : s;
         }
         v = c ? plus(v, u) : u;
     }

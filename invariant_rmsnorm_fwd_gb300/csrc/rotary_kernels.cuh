@@ -38,7 +38,7 @@ struct QkChunks {
     }
 };
 
-// Lanes of a team: the power of two that holds D / 16 lanes.
+// Lanes of a team in the backward pass: the power of two that holds D / 16 lanes.
 __host__ __device__ inline int qk_team(int D) {
     int p = 1;
     while (16 * p < D) p <<= 1;
@@ -111,12 +111,12 @@ struct RotaryParams {
     int32_t D, rot, first;
     int32_t hq, heads;               // query heads, heads of both
     int32_t chunks, per;             // chunks of a token, heads of a chunk
-    int32_t lanes, team;             // lanes of a head that hold columns; lanes of a team
+    int32_t lanes, team, teams;      // lanes of a head that hold columns; lanes of a team; a warp's teams
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
     uint32_t units;                  // teams' (warps') pieces of work
     float scale, sign;               // sign: of the sine (-1 turns back)
     float eps, inv_d;
-    Divisor by_chunks{1}, by_team{1};
+    Divisor by_chunks{1}, by_team{1}, by_teams{1};
     QkWs ws;
 };
 
@@ -171,21 +171,13 @@ struct Raw {
     uint4 q[2 * kQ];
 };
 
-// 8 elements at once if `on`, else whatever the registers hold (nothing that depends on
-// it is stored).  FP32 vectors are 32-byte aligned.
-template <class E>
-__device__ __forceinline__ void load_vector(uint4 *q, const void *p, bool on) {
-    if constexpr (sizeof(E) == 4) {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
-                     "@p ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
-                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y), "=r"(q[1].z), "=r"(q[1].w)
-                     : "l"(p), "r"(uint32_t(on)));
-    } else {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-                     "@p ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
-                     : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w)
-                     : "l"(p), "r"(uint32_t(on)));
-    }
+// 8 FP32 elements (32-byte aligned) at once if `on`, else zeros.
+__device__ __forceinline__ void load_f32x8(uint4 *q, const float *p, bool on) {
+    q[0] = q[1] = make_uint4(0, 0, 0, 0);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
+                 "@p ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
+                 : "+r"(q[0].x), "+r"(q[0].y), "+r"(q[0].z), "+r"(q[0].w), "+r"(q[1].x), "+r"(q[1].y), "+r"(q[1].z), "+r"(q[1].w)
+                 : "l"(p), "r"(uint32_t(on)));
 }
 template <class E>
 __device__ __forceinline__ void store_vector(void *p, const uint4 *q) {
@@ -386,14 +378,27 @@ __device__ __forceinline__ bool is_turned(int i, const LaneColumns<PAIRS> &col) 
     return PAIRS == kHalf ? col.turned != 0 : (col.turned >> i) & 1;
 }
 
-// Sum over the lanes of a team, neighbours half a team apart first.  TEAM 0: of
-// `team` lanes, known when the kernel runs.
+// Sum over the lanes of a team, those furthest apart first.  TEAM 0: of `team` lanes,
+// known when the kernel runs.  Teams of a power of two exchange both ways; others fold
+// into their first lane, which hands the sum out.
 template <int TEAM>
-__device__ __forceinline__ float team_add(float v, int team) {
+__device__ __forceinline__ float team_add(float v, int team, int lane) {
+    if constexpr (TEAM > 0 && (TEAM & (TEAM - 1)) == 0) {
 #pragma unroll
-    for (int o = TEAM ? TEAM / 2 : 16; o >= 1; o >>= 1)
-        if (TEAM || o < team) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
-    return v;
+        for (int o = TEAM / 2; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
+        return v;
+    } else {
+        int n = TEAM ? TEAM : team;
+#pragma unroll
+        for (int o = TEAM ? 4 : 16; o >= 1; o >>= 1) {
+            if (o < n) {                                 // lanes 0 .. n - 1 hold sums; the first o (or n - o) add
+                const float u = __shfl_down_sync(kFull, v, o);
+                if (lane + o < n) v = __fadd_rn(v, u);
+                n = o;
+            }
+        }
+        return __shfl_sync(kFull, v, (threadIdx.x & 31) - lane);
+    }
 }
 
 // A lane's part of a row's sum of products f g (columns that are not there are zeros):
@@ -417,117 +422,50 @@ __device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) {
     return e == e ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
 }
 
-// ----------------------------------------------------------------- forward, and rotation alone
-
-constexpr int kRotaryThreads = 256;
-
-// Rotation alone.  The heads of a chunk go through in fours, whose loads are issued together.
-template <class E, int PAIRS>
-__global__ void __launch_bounds__(kRotaryThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    extern __shared__ float4 shared[];                   // kSplit: the teams' rows
-    constexpr bool kTogether = PAIRS == kSplit;          // the lanes of a team exchange values
-    constexpr int U = 4, Q = Raw<E>::kQ;
-    const uint32_t mine = p.by_team.quotient(threadIdx.x), teams = p.by_team.quotient(kRotaryThreads);
-    const int lane = int(threadIdx.x - mine * uint32_t(p.team));
-    const uint32_t unit = blockIdx.x * teams + mine, token = p.by_chunks.quotient(unit);
-    const int head0 = int(unit - token * uint32_t(p.chunks)) * p.per;
-    const bool in = mine < teams && unit < p.units;
-    const int32_t id = in ? p.tok_id[token] : -1, position = in ? p.position[token] : 0;
-    int n = p.heads - head0 < p.per ? p.heads - head0 : p.per;
-    if (id < 0) n = 0;
-    if constexpr (!kTogether) {
-        if (n == 0) return;
-    }
-    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    // the row of head h
-    auto row_of = [&](const void *q, int64_t q_t, int64_t q_h, const void *k, int64_t k_t, int64_t k_h, int h) {
-        return h < p.hq ? static_cast<const E *>(q) + (token * q_t + h * q_h) : static_cast<const E *>(k) + (token * k_t + (h - p.hq) * k_h);
-    };
-    const HeadsParams &qs = p.side[0], &ks = p.side[1];
-    const E *src = row_of(qs.in, qs.in_t, qs.in_h, ks.in, ks.in_t, ks.in_h, head0);
-    E *dst = const_cast<E *>(row_of(qs.out, qs.out_t, qs.out_h, ks.out, ks.out_t, ks.out_h, head0));
-    float *row = nullptr;
-    if constexpr (PAIRS == kSplit) row = reinterpret_cast<float *>(shared) + mine * p.D;
-    Angles<PAIRS> a;
-    for (int i = 0; i < (kTogether ? p.per : n); i += U) {
-        Raw<E> r[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = head0 + i + u;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) load_vector<E>(r[u].q + j * Q, src + col.at[j], i + u < n && col.at[j] >= 0);
-            src = h + 1 == p.hq ? static_cast<const E *>(ks.in) + token * ks.in_t : src + (h < p.hq ? qs.in_h : ks.in_h);
-        }
-        if (i == 0) lane_angles<E, PAIRS>(p, position, lane, col, a);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i + u >= (kTogether ? p.per : n)) break;
-            const int h = head0 + i + u;
-            f2_t f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = up2<E>(r[u], j);
-            turn_lane<PAIRS>(f, a, col, p, row);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (is_turned<PAIRS>(j, col)) down2<E>(r[u], j, f[j]);
-            if (i + u < n) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r[u].q + j * Q);
-            }
-            dst = h + 1 == p.hq ? static_cast<E *>(ks.out) + token * ks.out_t : dst + (h < p.hq ? qs.out_h : ks.out_h);
-        }
-    }
-}
-
-// ----------------------------------------------------------------- rows through shared memory
+// ----------------------------------------------------------------- rows on their way
 
 constexpr int kQkWarps = 4;
 
-// Heads on their way into shared memory: a ring of kDepth rows a team.  Every lane copies
-// its own columns of its TENSORS tensors; in FP32, where they are 32 bytes a vector, two
-// lanes copy first the one's, then the other's, so that no copy takes half a sector.
+// 16-bit heads come through shared memory: a ring of kDepth rows a team, every lane
+// copying its own columns of TENSORS tensors to places that only it reads.  FP32 rows
+// are twice as long and stay in registers, one row ahead, by loads of 32 bytes a lane
+// (17,620 tokens, 32+8 heads of 128: forward 113 us against 175 through a ring of 16-byte
+// copies, which shared memory cannot keep up with).
 template <class E, int TENSORS>
 struct Ring {
-    static constexpr int kPieces = 2 * TENSORS * Raw<E>::kQ;         // 16-byte pieces of a lane's row
-    static constexpr int kDepth = TENSORS == 1 ? 6 : sizeof(E) == 4 ? 3 : 4;
-    static constexpr int kBytes = kPieces * kDepth * 512;            // of a warp
+    static constexpr bool kOn = sizeof(E) == 2;
+    static constexpr int kPieces = 2 * TENSORS;          // 16-byte pieces of a lane's row
+    static constexpr int kDepth = TENSORS == 1 ? 6 : 4;
+    static constexpr int kBytes = kOn ? kPieces * kDepth * 512 : 0;   // of a warp
 };
 template <class E, int PAIRS>
-struct Copies {
-    static constexpr int kQ = Raw<E>::kQ;
-    int at[kQ][2], half[kQ], lane[kQ];                   // copy l: columns of the vector's owner, which half of it, the owner's place
-    __device__ __forceinline__ Copies(const LaneColumns<PAIRS> &col, int size) {
-        const bool pairs = kQ == 2 && size > 1;
-        const int lane32 = threadIdx.x & 31, odd = lane32 & 1;
+__device__ __forceinline__ void copy_row(uint32_t dst, const E *row, const LaneColumns<PAIRS> &col, bool on) {
 #pragma unroll
-        for (int l = 0; l < kQ; ++l) {
-            half[l] = pairs ? odd : l;
-            lane[l] = pairs ? (l - odd) * 16 : 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) at[l][j] = pairs ? __shfl_sync(kFull, col.at[j], (lane32 & ~1) + l) : col.at[j];
-        }
+    for (int j = 0; j < 2; ++j) {
+        const bool some = on && col.at[j] >= 0;
+        cp_async_zfill(dst + j * 512, row + (some ? col.at[j] : 0), some ? 16 : 0);
     }
-    __device__ __forceinline__ void issue(uint32_t dst, const E *row, bool on) const {
+}
+template <class E, int PAIRS>
+__device__ __forceinline__ void load_row(Raw<E> &r, const E *row, const LaneColumns<PAIRS> &col, bool on) {
+    if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int l = 0; l < kQ; ++l) {
-                const bool some = on && at[l][j] >= 0;
-                cp_async_zfill(dst + lane[l] + (j * kQ + half[l]) * 512, row + (some ? at[l][j] : 0) + 4 * half[l], some ? 16 : 0);
-            }
+        for (int j = 0; j < 2; ++j) load_f32x8(r.q + 2 * j, reinterpret_cast<const float *>(row) + col.at[j], on && col.at[j] >= 0);
     }
-};
+}
 template <class E>
 __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 #pragma unroll
     for (int l = 0; l < 2 * Raw<E>::kQ; ++l) ld_shared_vec(src + l * 512, r.q[l]);
 }
 
-// Norm and rotation.  A warp takes `slots` consecutive slots of a call (at most 32) and one
-// chunk of heads; its teams take the active ones in turns.
-template <class E, int PAIRS, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_constant__ RotaryParams p, int slots) {
+// ----------------------------------------------------------------- forward, and rotation alone
+
+// NORM: behind the norm; else the rotation alone.  A warp takes `slots` consecutive slots
+// of a call (at most 32) and one chunk of heads; its teams take the active ones in turns.
+template <class E, int PAIRS, bool NORM, int TEAM>
+__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) == 4 ? 4 : 6)
+    rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
     extern __shared__ float4 shared[];
     using R = Ring<E, 1>;
     const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -537,23 +475,24 @@ __global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_c
     const int64_t first = int64_t(win) * slots;
     const bool mine = in && lane32 < slots && first + lane32 < p.n_tokens;
     const int32_t id = mine ? p.tok_id[first + lane32] : -1, position = mine ? p.position[first + lane32] : 0;
-    stage_weights<E>(shared, p);
+    if constexpr (NORM) stage_weights<E>(shared, p);
     const int head0 = int((in ? unit : 0) - win * uint32_t(p.chunks)) * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const uint32_t active = __ballot_sync(kFull, id >= 0);
     const int count = __popc(active);
     const bool dense = active == (count == 32 ? kFull : (1u << count) - 1u);
-    const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
-    const int steps = (count + teams - 1) / teams;
-    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    const Copies<E, PAIRS> copies(col, size);
-    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + (PAIRS == kSplit ? 2048 : 0));
+    const int size = TEAM ? TEAM : p.team, teams = TEAM ? 32 / (TEAM ? TEAM : 1) : p.teams;
+    const int team = TEAM ? lane32 / (TEAM ? TEAM : 1) : int(p.by_team.quotient(lane32)), lane = lane32 - team * size;
+    const int steps = int(p.by_teams.quotient(count + teams - 1));
+    LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    if (team >= teams) col = {{-1, -1}, 0};              // lanes that are left over
+    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + (NORM ? 16 * p.D : 0) + warp * (R::kBytes + (PAIRS == kSplit ? 2048 : 0));
     const uint32_t ring = smem_addr(place_of) + lane32 * 16;
     float *const row = reinterpret_cast<float *>(place_of + R::kBytes) + team * p.D;
 
     // Lane (of the slots' ids) of this team's slot in a step, -1: none.
     auto place = [&](int step) {
         const int t = step * teams + team;
-        if (t >= count) return -1;
+        if (t >= count || team >= teams) return -1;
         if (dense) return t;
         uint32_t m = active;
         for (int i = t; i > 0; --i) m &= m - 1;
@@ -563,6 +502,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_c
     uint32_t f_dst = ring;
     const E *f_x = nullptr;
     bool f_on = false;
+    Raw<E> next;
     auto fetch = [&]() {
         if (f_step < steps) {
             const bool keys = f_head >= p.hq;
@@ -572,20 +512,24 @@ __global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_c
                 f_on = at >= 0;
                 f_x = static_cast<const E *>(s.in) + ((f_on ? first + at : 0) * s.in_t + (keys ? f_head - p.hq : f_head) * s.in_h);
             }
-            copies.issue(f_dst, f_x, f_on);
+            if constexpr (R::kOn) {
+                copy_row<E>(f_dst, f_x, col, f_on);
+                f_dst += R::kPieces * 512;
+                if (f_dst == ring + R::kBytes) f_dst = ring;
+            } else {
+                load_row<E>(next, f_x, col, f_on);
+            }
             f_x += s.in_h;
-            f_dst += R::kPieces * 512;
-            if (f_dst == ring + R::kBytes) f_dst = ring;
             if (++f_head == end) {
                 f_head = head0;
                 ++f_step;
             }
         }
-        cp_async_commit();
+        if constexpr (R::kOn) cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) fetch();
-    __syncthreads();                                     // the weights
+    for (int i = 0; i < (R::kOn ? R::kDepth - 1 : 1); ++i) fetch();
+    if constexpr (NORM) __syncthreads();                 // the weights
 
     Angles<PAIRS> a;
     uint32_t from = ring;
@@ -599,23 +543,31 @@ __global__ void __launch_bounds__(kQkWarps * 32, 6) qk_fwd_kernel(const __grid_c
             const HeadsParams &s = p.side[keys];
             E *dst = static_cast<E *>(s.out) + ((on ? first + at : 0) * s.out_t + (keys ? h - p.hq : h) * s.out_h);
             for (; h < stop; ++h) {
-                cp_async_wait<R::kDepth - 2>();
-                __syncwarp();                            // everyone's copies of this row; and the row before has been read
-                fetch();
                 Raw<E> r;
-                take_row<E>(r, from);
-                from += R::kPieces * 512;
-                if (from == ring + R::kBytes) from = ring;
-                f2_t f[8], w[8];
+                if constexpr (R::kOn) {
+                    cp_async_wait<R::kDepth - 2>();
+                    fetch();
+                    take_row<E>(r, from);
+                    from += R::kPieces * 512;
+                    if (from == ring + R::kBytes) from = ring;
+                } else {
+                    r = next;
+                    fetch();
+                }
+                f2_t f[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = up2<E>(r, j);
-                const f2_t rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size), p));
-                lane_weights<PAIRS>(shared, keys, col, p.D >> 3, w);
+                if constexpr (NORM) {
+                    f2_t w[8];
+                    const f2_t rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size, lane), p));
+                    lane_weights<PAIRS>(shared, keys, col, p.D >> 3, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                    for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                }
                 turn_lane<PAIRS>(f, a, col, p, row);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) down2<E>(r, j, f[j]);
+                for (int j = 0; j < 8; ++j)
+                    if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r, j, f[j]);
                 if (on) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -671,7 +623,7 @@ inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool strad
 
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
 template <class E, int PAIRS, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
+__global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
     extern __shared__ float4 shared[];
     const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
@@ -695,7 +647,6 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     const int run_steps = in_run ? share : 0, steps = run_steps + (loose + teams - 1) / teams;
 
     using R = Ring<E, 2>;
-    constexpr int Q = Raw<E>::kQ;
     const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
     uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
     const uint32_t ring = smem_addr(mine) + lane32 * 16;
@@ -716,9 +667,9 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
     // one before but for the first of each kind of a token.
     int f_step = 0, f_head = head0;
     uint32_t f_dst = ring;
-    const Copies<E, PAIRS> copies(col, size);
     const E *f_x = nullptr, *f_g = nullptr;
     bool f_on = false;
+    Raw<E> next_x, next_g;
     auto fetch = [&]() {
         if (f_step < steps) {
             const bool keys = f_head >= p.hq;
@@ -731,21 +682,26 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 f_x = static_cast<const E *>(s.in) + (slot * s.in_t + h * s.in_h);
                 f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
             }
-            copies.issue(f_dst, f_x, f_on);
-            copies.issue(f_dst + 2 * Q * 512, f_g, f_on);
+            if constexpr (R::kOn) {
+                copy_row<E>(f_dst, f_x, col, f_on);
+                copy_row<E>(f_dst + 1024, f_g, col, f_on);
+                f_dst += R::kPieces * 512;
+                if (f_dst == ring + R::kBytes) f_dst = ring;
+            } else {
+                load_row<E>(next_x, f_x, col, f_on);
+                load_row<E>(next_g, f_g, col, f_on);
+            }
             f_x += s.in_h;
             f_g += s.dy_h;
-            f_dst += R::kPieces * 512;
-            if (f_dst == ring + R::kBytes) f_dst = ring;
             if (++f_head == end) {
                 f_head = head0;
                 ++f_step;
             }
         }
-        cp_async_commit();
+        if constexpr (R::kOn) cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) fetch();
+    for (int i = 0; i < (R::kOn ? R::kDepth - 1 : 1); ++i) fetch();
     __syncthreads();                                     // the weights
     if (steps == 0) return;
 
@@ -772,14 +728,19 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
             for (; h < stop; ++h) {
-                cp_async_wait<R::kDepth - 2>();
-                __syncwarp();                            // everyone's copies of this row; and the row before has been read
-                fetch();
                 Raw<E> rx, rg;
-                take_row<E>(rx, from);
-                take_row<E>(rg, from + 2 * Q * 512);
-                from += R::kPieces * 512;
-                if (from == ring + R::kBytes) from = ring;
+                if constexpr (R::kOn) {
+                    cp_async_wait<R::kDepth - 2>();
+                    fetch();
+                    take_row<E>(rx, from);
+                    take_row<E>(rg, from + 1024);
+                    from += R::kPieces * 512;
+                    if (from == ring + R::kBytes) from = ring;
+                } else {
+                    rx = next_x;
+                    rg = next_g;
+                    fetch();
+                }
                 f2_t x[8], g[8], b[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -790,7 +751,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 lane_weights<PAIRS>(shared, keys, col, p.D >> 3, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
-                const float ss = team_add<TEAM>(lane_dot(x, x), size), sb = team_add<TEAM>(lane_dot(b, x), size);
+                const float ss = team_add<TEAM>(lane_dot(x, x), size, lane), sb = team_add<TEAM>(lane_dot(b, x), size, lane);
                 const float rstd = qk_rstd(ss, p), m = __fmul_rn(__fmul_rn(sb, rstd), p.inv_d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -801,7 +762,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 4) qk_bwd_kernel(const __grid_c
                 if (on) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Q);
+                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Raw<E>::kQ);
                 }
                 dst += s.out_h;
             }

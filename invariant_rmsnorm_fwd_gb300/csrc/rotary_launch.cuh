@@ -4,34 +4,24 @@
 
 namespace rbi {
 
-template <class E, int PAIRS>
-static int rotary_launch_alone(RotaryParams &p, cudaStream_t stream) {
-    // No team of a power of two but where it exchanges columns.
-    p.team = PAIRS == kSplit ? qk_team(p.D) : PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
-    p.by_team = Divisor(uint32_t(p.team));
-    const uint32_t teams = uint32_t(kRotaryThreads / p.team);
-    p.units = uint32_t(p.n_tokens * p.chunks);
-    rotary_kernel<E, PAIRS><<<(p.units + teams - 1) / teams, kRotaryThreads, PAIRS == kSplit ? int(teams) * p.D * 4 : 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
-    count_launch();
-    return RMSNORM_OK;
-}
-
-template <class E, int PAIRS, int TEAM>
+template <class E, int PAIRS, bool NORM, int TEAM>
 static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
-    auto kern = qk_fwd_kernel<E, PAIRS, TEAM>;
+    auto kern = rotary_kernel<E, PAIRS, NORM, TEAM>;
     static KernelInfo info;
     DeviceInfo *d = nullptr;
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
+    p.by_team = Divisor(uint32_t(p.team));
+    p.teams = 32 / p.team;
+    p.by_teams = Divisor(uint32_t(p.teams));
     // Steps of a warp: up to 4 while that leaves every SM 32 warps' work.
-    const int teams = 32 / p.team;
-    int slots = teams;
-    while (slots < 32 && slots < 4 * teams && p.n_tokens * p.chunks >= int64_t(2) * slots * 32 * d->sms) slots *= 2;
+    int steps = 1;
+    while (steps < 4 && 2 * steps * p.teams <= 32 && p.n_tokens * p.chunks >= int64_t(2) * steps * p.teams * 32 * d->sms) steps *= 2;
+    const int slots = steps * p.teams;
     p.units = uint32_t((p.n_tokens + slots - 1) / slots * p.chunks);
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
-           16 * p.D + kQkWarps * (Ring<E, 1>::kBytes + (PAIRS == kSplit ? 2048 : 0)), stream>>>(p, slots);
+           (NORM ? 16 * p.D : 0) + kQkWarps * (Ring<E, 1>::kBytes + (PAIRS == kSplit ? 2048 : 0)), stream>>>(p, slots);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
@@ -54,21 +44,32 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     return RMSNORM_OK;
 }
 
-template <class E, int PAIRS, int TEAM>
-static int rotary_launch_norm(RotaryParams &p, int mode, cudaStream_t stream) {
-    return mode == 1 ? rotary_launch_fwd<E, PAIRS, TEAM>(p, stream) : rotary_launch_bwd<E, PAIRS, TEAM>(p, stream);
-}
-
 template <class E, int PAIRS>
 static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
-    if (mode == 0) return rotary_launch_alone<E, PAIRS>(p, stream);
-    p.team = qk_team(p.D);
-    if constexpr (PAIRS != kSplit) {
-        if (p.team == 4) return rotary_launch_norm<E, PAIRS, 4>(p, mode, stream);
-        if (p.team == 8) return rotary_launch_norm<E, PAIRS, 8>(p, mode, stream);
-        if (p.team == 16) return rotary_launch_norm<E, PAIRS, 16>(p, mode, stream);
+    if (mode == 0) {
+        p.team = PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
+        return rotary_launch_fwd<E, PAIRS, false, 0>(p, stream);
     }
-    return rotary_launch_norm<E, PAIRS, 0>(p, mode, stream);
+    p.team = qk_team(p.D);
+    if (mode == 1) {
+        // Forward, teams of just the lanes that a head needs where a warp then holds more of them (5 lanes
+        // for 80 columns, 6 for 96).
+        if (32 / p.lanes > 32 / p.team) p.team = p.lanes;
+        if constexpr (PAIRS != kSplit) {
+            if (p.team == 4) return rotary_launch_fwd<E, PAIRS, true, 4>(p, stream);
+            if (p.team == 5) return rotary_launch_fwd<E, PAIRS, true, 5>(p, stream);
+            if (p.team == 6) return rotary_launch_fwd<E, PAIRS, true, 6>(p, stream);
+            if (p.team == 8) return rotary_launch_fwd<E, PAIRS, true, 8>(p, stream);
+            if (p.team == 16) return rotary_launch_fwd<E, PAIRS, true, 16>(p, stream);
+        }
+        return rotary_launch_fwd<E, PAIRS, true, 0>(p, stream);
+    }
+    if constexpr (PAIRS != kSplit) {
+        if (p.team == 4) return rotary_launch_bwd<E, PAIRS, 4>(p, stream);
+        if (p.team == 8) return rotary_launch_bwd<E, PAIRS, 8>(p, stream);
+        if (p.team == 16) return rotary_launch_bwd<E, PAIRS, 16>(p, stream);
+    }
+    return rotary_launch_bwd<E, PAIRS, 0>(p, stream);
 }
 
 // One translation unit per element type and kind of pairs (rotary_*.cu).
