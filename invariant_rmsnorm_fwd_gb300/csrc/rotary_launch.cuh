@@ -15,9 +15,12 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     p.by_team = Divisor(uint32_t(p.team));
     p.teams = 32 / p.team;
     p.by_teams = Divisor(uint32_t(p.teams));
-    // Steps of a warp: up to 4 while that leaves every SM 32 warps' work.
+    // Steps of a warp: until its teams have 16 rows each (8 without the norm, whose rows are
+    // quicker), so that its start is paid for, while every SM has 64 warps to choose from.
     int steps = 1;
-    while (steps < 4 && 2 * steps * p.teams <= 32 && p.n_tokens * p.chunks >= int64_t(2) * steps * p.teams * 32 * d->sms) steps *= 2;
+    while (steps * p.per < (NORM ? 16 : 8) && 2 * steps * p.teams <= 32 &&
+           p.n_tokens * p.chunks >= int64_t(2) * steps * p.teams * 64 * d->sms)
+        steps *= 2;
     const int slots = steps * p.teams;
     p.units = uint32_t((p.n_tokens + slots - 1) / slots * p.chunks);
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
