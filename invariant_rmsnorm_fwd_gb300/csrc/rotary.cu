@@ -136,7 +136,7 @@ int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float ep
     p.params_f32 = param_dtype == LAYERNORM_FP32 ? 1 : 0;
     p.in_place = mode == 0 && q->out == q->in && (!k || k->out == k->in) ? 1 : 0;
     p.scale = r->scale;
-    p.sign = back ? -1.f : 1.f;
+    p.scale_sin = back ? -r->scale : r->scale;
     p.eps = eps;
     p.inv_d = float(1.0 / double(D));
     if (workspace) p.ws = qk_ws(workspace, L->n_logical_tokens, q->heads, k ? k->heads : 0, D);

@@ -114,7 +114,7 @@ struct RotaryParams {
     int32_t lanes, team, teams;      // lanes of a head that hold columns; lanes of a team; a warp's teams
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
     uint32_t units;                  // teams' (warps') pieces of work
-    float scale, sign;               // sign: of the sine (-1 turns back)
+    float scale, scale_sin;          // factors of cosine and sine (negative: turns back)
     float eps, inv_d;
     Divisor by_chunks{1}, by_team{1}, by_teams{1};
     QkWs ws;
@@ -216,117 +216,113 @@ __device__ __forceinline__ void down2(Raw<E> &r, int i, f2_t v) {
     }
 }
 
-// Both weights in shared memory, as FP32: quad j of vector v of a side at
-// [(2 side + j) V + v], so that neighbouring lanes read neighbouring 16 bytes.
-template <class E>
-__device__ __forceinline__ void stage_weights(float4 *sw, const RotaryParams &p) {
-    const int V = p.D >> 3;
-    for (int i = threadIdx.x; i < 2 * V; i += blockDim.x) {
-        const int side = i >= V, v = i - side * V;
-        f2_t f[4];
-        oct_param<E>(p.side[side].w, p.params_f32, v, 1.f, f);
-        sw[2 * side * V + v] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
-        sw[(2 * side + 1) * V + v] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
-    }
+// Both weights in shared memory, as FP32 and in the lanes' order: four columns of a team's
+// lane at [side][quad][lane], 32 lanes apart, so that a lane's reads need one address.
+constexpr int kWeightBytes = 2 * 4 * 32 * 16;
+template <class E, int PAIRS>
+__device__ __forceinline__ void stage_weights(float4 *sw, const RotaryParams &p, int size) {
+    const int i = threadIdx.x, side = i >= 2 * size, lane = (i - side * 2 * size) >> 1, j = i & 1;
+    if (i >= 4 * size) return;                           // (a CTA has at least 128 threads)
+    const int at = lane_columns<PAIRS>(lane, p).at[j];
+    if (at < 0) return;
+    f2_t f[4];
+    oct_param<E>(p.side[side].w, p.params_f32, at >> 3, 1.f, f);
+    float4 *to = sw + (side * 4 + 2 * j) * 32 + lane;
+    to[0] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
+    to[32] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
 }
-template <int PAIRS>
-__device__ __forceinline__ void lane_weights(const float4 *sw, int side, const LaneColumns<PAIRS> &c, int V, f2_t (&f)[8]) {
+// `from`: shared-memory address of the lane's first quad of the side.
+__device__ __forceinline__ void lane_weights(uint32_t from, f2_t (&f)[8]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int v = c.at[i] < 0 ? 0 : c.at[i] >> 3;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 q = sw[(2 * side + j) * V + v];
-            f[4 * i + 2 * j] = f2_make(q.x, q.y);
-            f[4 * i + 2 * j + 1] = f2_make(q.z, q.w);
-        }
-    }
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * i]), "=l"(f[2 * i + 1]) : "r"(from + i * 512));
 }
 
 // ----------------------------------------------------------------- angles
 
-// Cosines and sines of position * turns / 2^64 turns, for two pairs.  The product
-// modulo 2^64 is exact; its top 32 bits, off by less than 2^-32 turn, are split into
-// a quadrant and a rest of at most 1/8 turn either way, y = rest in radians.  sin y
-// and cos y are their Taylor polynomials of degree 9 and 10: what is left out is
-// below (pi/4)^11 / 11! = 1.8e-9 and (pi/4)^12 / 12! = 1.2e-10.  FINE (FP32 heads): y
-// is formed with what the float of the rest loses, and enters as y + d: sin + d cos,
-// cos - d sin; without that the angle is off by up to 2^-23 / 2 more.
+// Cosine and sine of position * turns / 2^64 turns.  The product modulo 2^64 is exact;
+// its top 32 bits, off by less than 2^-32 turn, are a quadrant and a rest of at most
+// 1/8 turn either way, y = rest in radians.  sin y and cos y are their Taylor polynomials
+// of degree 9 and 10: what is left out is below (pi/4)^11 / 11! = 1.8e-9 and
+// (pi/4)^12 / 12! = 1.2e-10.  FINE (FP32 heads): y is formed with what the float of the
+// rest loses, and enters as y + d: sin + d cos, cos - d sin; without that the angle is
+// off by up to 1.7 times 2^-24 more.  (One pair at a time: constants are operands then, in
+// registers of two they would be moves.  2 heads of 128, 270,100 tokens: 70 -> XX us.)
 template <bool FINE>
-__device__ __forceinline__ void cos_sin(int32_t position, uint64_t t0, uint64_t t1, f2_t &c, f2_t &s) {
-    const uint32_t a = uint32_t(uint64_t(int64_t(position)) * t0 >> 32), b = uint32_t(uint64_t(int64_t(position)) * t1 >> 32);
-    const uint32_t qa = (a + 0x20000000u) >> 30, qb = (b + 0x20000000u) >> 30;
-    const int32_t ra = int32_t(a - (qa << 30)), rb = int32_t(b - (qb << 30));
-    const float fa = __int2float_rn(ra), fb = __int2float_rn(rb);
-    // 2 pi / 2^32 in two floats
-    const f2_t hi = f2_both(0x1.921fb6p-30f), lo = f2_both(-0x1.777a5cp-55f), f = f2_make(fa, fb);
-    const f2_t y = f2_mul(f, hi), z = f2_mul(y, y);
-    f2_t p = f2_fma(z, f2_both(1.f / 362880.f), f2_both(-1.f / 5040.f));
-    p = f2_fma(z, p, f2_both(1.f / 120.f));
-    p = f2_fma(z, p, f2_both(-1.f / 6.f));
-    f2_t sn = f2_fma(f2_mul(z, y), p, y);
-    f2_t q = f2_fma(z, f2_both(-1.f / 3628800.f), f2_both(1.f / 40320.f));
-    q = f2_fma(z, q, f2_both(-1.f / 720.f));
-    q = f2_fma(z, q, f2_both(1.f / 24.f));
-    q = f2_fma(z, q, f2_both(-0.5f));
-    f2_t cs = f2_fma(z, q, f2_both(1.f));
+__device__ __forceinline__ void cos_sin(int32_t position, uint64_t turns, float &c, float &s) {
+    const uint32_t top = uint32_t(uint64_t(int64_t(position)) * turns >> 32);
+    const int32_t rest = int32_t(top << 2);              // 4 times the rest: the quadrant has gone
+    const float f = __int2float_rn(rest);
+    const float kHi = 0x1.921fb6p-32f, kLo = -0x1.777a5cp-57f;       // 2 pi / 2^34 in two floats
+    const float y = __fmul_rn(f, kHi), z = __fmul_rn(y, y);
+    float p = __fmaf_rn(z, 1.f / 362880.f, -1.f / 5040.f);
+    p = __fmaf_rn(z, p, 1.f / 120.f);
+    p = __fmaf_rn(z, p, -1.f / 6.f);
+    float sn = __fmaf_rn(__fmul_rn(z, y), p, y);
+    float q = __fmaf_rn(z, -1.f / 3628800.f, 1.f / 40320.f);
+    q = __fmaf_rn(z, q, -1.f / 720.f);
+    q = __fmaf_rn(z, q, 1.f / 24.f);
+    q = __fmaf_rn(z, q, -0.5f);
+    float cs = __fmaf_rn(z, q, 1.f);
     if constexpr (FINE) {
-        const f2_t lost = f2_make(__int2float_rn(ra - __float2int_rn(fa)), __int2float_rn(rb - __float2int_rn(fb)));
-        const f2_t minus = f2_both(-1.f);
-        const f2_t d = f2_fma(lost, hi, f2_fma(f, lo, f2_fma(f, hi, f2_mul(y, minus))));
-        const f2_t sn1 = f2_fma(d, cs, sn);
-        cs = f2_fma(f2_mul(d, minus), sn, cs);
+        // (the float of the rest may be 2^31, beyond an int32)
+        const float lost = __ll2float_rn(int64_t(rest) - __float2ll_rn(f));
+        const float d = __fmaf_rn(lost, kHi, __fmaf_rn(f, kLo, __fmaf_rn(f, kHi, -y)));
+        const float sn1 = __fmaf_rn(d, cs, sn);
+        cs = __fmaf_rn(-d, sn, cs);
         sn = sn1;
     }
-    // quadrant 1: (-sin, cos), 2: (-cos, -sin), 3: (sin, -cos): the signs' bits
-    const uint32_t ca = __float_as_uint(qa & 1 ? f2_lo(sn) : f2_lo(cs)) ^ (((qa + 1) & 2) << 30);
-    const uint32_t cb = __float_as_uint(qb & 1 ? f2_hi(sn) : f2_hi(cs)) ^ (((qb + 1) & 2) << 30);
-    const uint32_t sa = __float_as_uint(qa & 1 ? f2_lo(cs) : f2_lo(sn)) ^ ((qa & 2) << 30);
-    const uint32_t sb = __float_as_uint(qb & 1 ? f2_hi(cs) : f2_hi(sn)) ^ ((qb & 2) << 30);
-    c = f2_make(__uint_as_float(ca), __uint_as_float(cb));
-    s = f2_make(__uint_as_float(sa), __uint_as_float(sb));
+    // quadrants 1 to 3: (cos, sin) = (-sin, cos), (-cos, -sin), (sin, -cos)
+    const uint32_t turned = top + 0x20000000u;           // quadrant in the top two bits
+    const bool swap = turned & 0x40000000u;
+    c = __uint_as_float(__float_as_uint(swap ? sn : cs) ^ ((turned + 0x40000000u) & 0x80000000u));
+    s = __uint_as_float(__float_as_uint(swap ? cs : sn) ^ (turned & 0x80000000u));
 }
 
-// The lane's cosines and sines, times scale.  kHalf: of its 8 pairs, in columns'
-// order; kNear: likewise, 4 pairs a vector; kSplit: of the pair that each of its 16
-// columns belongs to, the sine negative in first halves.
+// The lane's cosines and sines, times scale: kHalf of its 8 pairs in columns' order,
+// kNear likewise, 4 pairs a vector.  kSplit: of all pairs of the team's token, in shared
+// memory: cosines, then sines.  There few lanes may have all the rotated columns (20 of
+// 80), and each of theirs a pair of its own, so the team forms them together.
 template <int PAIRS>
 struct Angles {
-    static constexpr int kN = PAIRS == kSplit ? 8 : 4;
-    f2_t c[kN], s[kN];
+    f2_t c[4], s[4];
+};
+template <>
+struct Angles<kSplit> {
+    float *c, *s;
 };
 template <class E, int PAIRS>
-__device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, const LaneColumns<PAIRS> &col,
+__device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, int size, const LaneColumns<PAIRS> &col,
                                             Angles<PAIRS> &a) {
-    const int half = p.rot >> 1;
-    const f2_t cs = f2_both(p.scale), ss = f2_both(__fmul_rn(p.scale, p.sign));
-#pragma unroll
-    for (int i = 0; i < Angles<PAIRS>::kN; ++i) {
-        a.c[i] = f2_make(1.f, 1.f);
-        a.s[i] = f2_make(0.f, 0.f);
-        // the first of two pairs that follow each other
-        int k;
-        bool first = true, two = true, any;
-        if constexpr (PAIRS == kHalf) {
-            k = 8 * lane + 2 * i;
-            any = col.turned != 0;
-        } else if constexpr (PAIRS == kNear) {
-            k = (col.at[i >> 1] - p.first) / 2 + 2 * (i & 1);         // both even
-            first = (col.turned >> (2 * i)) & 1;
-            two = (col.turned >> (2 * i + 1)) & 1;
-            any = first || two;
-        } else {
-            k = col.at[i >> 2] + 2 * (i & 3) - p.first;
-            any = (col.turned >> i) & 1;
+    if constexpr (PAIRS == kSplit) {
+        __syncwarp();                                    // the token before is done
+        for (int k = lane; 2 * k < p.rot; k += size) {
+            float c, s;
+            cos_sin<sizeof(E) == 4>(position, p.turns[k], c, s);
+            a.c[k] = __fmul_rn(c, p.scale);
+            a.s[k] = __fmul_rn(s, p.scale_sin);
         }
-        if (any) {
-            const bool second_half = PAIRS == kSplit && k >= half;
-            if (second_half) k -= half;
-            const uint64_t t0 = first ? p.turns[k] : 0, t1 = two ? p.turns[k + 1] : 0;
-            f2_t c, s;
-            cos_sin<sizeof(E) == 4>(position, t0, t1, c, s);
-            a.c[i] = f2_mul(c, cs);
-            a.s[i] = f2_mul(s, PAIRS == kSplit && !second_half ? f2_mul(ss, f2_both(-1.f)) : ss);
+        __syncwarp();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
+            if constexpr (PAIRS == kHalf) {
+                if (col.turned) {
+                    const ulonglong2 t = reinterpret_cast<const ulonglong2 *>(p.turns)[4 * lane + i];
+                    cos_sin<sizeof(E) == 4>(position, t.x, c[0], s[0]);
+                    cos_sin<sizeof(E) == 4>(position, t.y, c[1], s[1]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 2 * i + j;             // the register pair
+                    if ((col.turned >> r) & 1)
+                        cos_sin<sizeof(E) == 4>(position, p.turns[(col.at[r >> 2] + 2 * (r & 3) - p.first) >> 1], c[j], s[j]);
+                }
+            }
+            a.c[i] = f2_make(__fmul_rn(c[0], p.scale), __fmul_rn(c[1], p.scale));
+            a.s[i] = f2_make(__fmul_rn(s[0], p.scale_sin), __fmul_rn(s[1], p.scale_sin));
         }
     }
 }
@@ -365,11 +361,22 @@ __device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, 
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if ((col.turned >> i) & 1) {
-                const int c = col.at[i >> 2] + 2 * (i & 3);
-                const f2_t y = *reinterpret_cast<const f2_t *>(row + (c - p.first < half ? c + half : c - half));
-                f[i] = f2_fma(f[i], a.c[i], f2_mul(y, a.s[i]));
+                const int at = col.at[i >> 2] + 2 * (i & 3), k = at - p.first;
+                const bool second = k >= half;
+                const f2_t y = *reinterpret_cast<const f2_t *>(row + (second ? at - half : at + half));
+                const f2_t c = *reinterpret_cast<const f2_t *>(a.c + (second ? k - half : k));
+                const f2_t s = *reinterpret_cast<const f2_t *>(a.s + (second ? k - half : k));
+                f[i] = f2_fma(f[i], c, f2_mul(y, second ? s : f2_mul(s, f2_both(-1.f))));
             }
     }
+}
+
+// kSplit's shared memory of a warp: the teams' rows of D floats, then their cosines and
+// sines (rot / 2 each); teams x D floats are at most 2048 bytes.
+constexpr int kSplitBytes = 4096;
+__device__ __forceinline__ void split_angles(Angles<kSplit> &a, float *row, int team, int teams, const RotaryParams &p) {
+    a.c = row + (teams - team) * p.D + team * p.rot;
+    a.s = a.c + (p.rot >> 1);
 }
 
 // Register pair i holds rotated columns.
@@ -464,7 +471,7 @@ __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 // NORM: behind the norm; else the rotation alone.  A warp takes `slots` consecutive slots
 // of a call (at most 32) and one chunk of heads; its teams take the active ones in turns.
 template <class E, int PAIRS, bool NORM, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) == 4 ? 4 : 6)
+__global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 || NORM ? 5 : 6)
     rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
     extern __shared__ float4 shared[];
     using R = Ring<E, 1>;
@@ -475,17 +482,17 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
     const int64_t first = int64_t(win) * slots;
     const bool mine = in && lane32 < slots && first + lane32 < p.n_tokens;
     const int32_t id = mine ? p.tok_id[first + lane32] : -1, position = mine ? p.position[first + lane32] : 0;
-    if constexpr (NORM) stage_weights<E>(shared, p);
     const int head0 = int((in ? unit : 0) - win * uint32_t(p.chunks)) * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const uint32_t active = __ballot_sync(kFull, id >= 0);
     const int count = __popc(active);
     const bool dense = active == (count == 32 ? kFull : (1u << count) - 1u);
     const int size = TEAM ? TEAM : p.team, teams = TEAM ? 32 / (TEAM ? TEAM : 1) : p.teams;
+    if constexpr (NORM) stage_weights<E, PAIRS>(shared, p, size);
     const int team = TEAM ? lane32 / (TEAM ? TEAM : 1) : int(p.by_team.quotient(lane32)), lane = lane32 - team * size;
     const int steps = int(p.by_teams.quotient(count + teams - 1));
     LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
     if (team >= teams) col = {{-1, -1}, 0};              // lanes that are left over
-    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + (NORM ? 16 * p.D : 0) + warp * (R::kBytes + (PAIRS == kSplit ? 2048 : 0));
+    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + (NORM ? kWeightBytes : 0) + warp * (R::kBytes + (PAIRS == kSplit ? kSplitBytes : 0));
     const uint32_t ring = smem_addr(place_of) + lane32 * 16;
     float *const row = reinterpret_cast<float *>(place_of + R::kBytes) + team * p.D;
 
@@ -532,16 +539,18 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
     if constexpr (NORM) __syncthreads();                 // the weights
 
     Angles<PAIRS> a;
+    if constexpr (PAIRS == kSplit) split_angles(a, row, team, teams, p);
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0;
-        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), lane, col, a);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), team < teams ? lane : p.rot, size, col, a);   // (left-over lanes form none)
         for (int h = head0; h < end;) {                  // the token's heads of one kind after the other
             const bool keys = h >= p.hq;
             const int stop = keys || end < p.hq ? end : p.hq;
             const HeadsParams &s = p.side[keys];
             E *dst = static_cast<E *>(s.out) + ((on ? first + at : 0) * s.out_t + (keys ? h - p.hq : h) * s.out_h);
+            const uint32_t weights = smem_addr(shared) + keys * (kWeightBytes / 2) + lane * 16;
             for (; h < stop; ++h) {
                 Raw<E> r;
                 if constexpr (R::kOn) {
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
                 if constexpr (NORM) {
                     f2_t w[8];
                     const f2_t rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size, lane), p));
-                    lane_weights<PAIRS>(shared, keys, col, p.D >> 3, w);
+                    lane_weights(weights, w);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
                 }
@@ -615,10 +624,10 @@ __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bo
     return r;
 }
 
-inline int qk_bwd_smem(int ring_bytes, int D, bool split, bool grads, bool straddles) {
+inline int qk_bwd_smem(int ring_bytes, bool split, bool grads, bool straddles) {
     // both weights, then per warp: ring, the teams' sums (of both kinds where a chunk has both), kSplit's rows; teams x D
     // floats are at most 2048 bytes
-    return 16 * D + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0) + (split ? 2048 : 0));
+    return kWeightBytes + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0) + (split ? kSplitBytes : 0));
 }
 
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
@@ -637,10 +646,10 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
         wd.run = -1;
         wd.loose = 0;
     }
-    stage_weights<E>(shared, p);
 
     const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
     const int share = qk_share(teams);
+    stage_weights<E, PAIRS>(shared, p, size);
     const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
     const int head0 = chunk * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
@@ -648,7 +657,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
 
     using R = Ring<E, 2>;
     const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
-    uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + 16 * p.D + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? 2048 : 0));
+    uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + kWeightBytes + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? kSplitBytes : 0));
     const uint32_t ring = smem_addr(mine) + lane32 * 16;
     // [kinds][teams][D]: each team's sums over its tokens of the run; a lane has its own columns
     float *const sums = reinterpret_cast<float *>(mine + R::kBytes);
@@ -706,13 +715,14 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
     if (steps == 0) return;
 
     Angles<PAIRS> a;
+    if constexpr (PAIRS == kSplit) split_angles(a, row, team, teams, p);
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0, run = step < run_steps;
         const int64_t slot = on ? int64_t(win) * 8 - 7 + at : 0;
         const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
-        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, col, a);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, size, col, a);
         const bool known = int64_t(id) < p.ws.n;
         if (grads && on && chunk == 0 && lane == 0) {
             const int bad = known ? (atomicExch(p.ws.flag + id, run ? 1 : 2) ? kStDouble : 0) : kStPlan;
@@ -724,6 +734,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
             const int stop = keys || end < p.hq ? end : p.hq;
             const HeadsParams &s = p.side[keys];
             E *dst = static_cast<E *>(s.out) + (slot * s.out_t + (keys ? h - p.hq : h) * s.out_h);
+            const uint32_t weights = smem_addr(shared) + keys * (kWeightBytes / 2) + lane * 16;
             f2_t acc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
@@ -748,7 +759,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
                     g[j] = up2<E>(rg, j);
                 }
                 turn_lane<PAIRS>(g, a, col, p, row);
-                lane_weights<PAIRS>(shared, keys, col, p.D >> 3, b);
+                lane_weights(weights, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
                 const float ss = team_add<TEAM>(lane_dot(x, x), size, lane), sb = team_add<TEAM>(lane_dot(b, x), size, lane);

@@ -24,7 +24,7 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     const int slots = steps * p.teams;
     p.units = uint32_t((p.n_tokens + slots - 1) / slots * p.chunks);
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
-           (NORM ? 16 * p.D : 0) + kQkWarps * (Ring<E, 1>::kBytes + (PAIRS == kSplit ? 2048 : 0)), stream>>>(p, slots);
+           (NORM ? kWeightBytes : 0) + kQkWarps * (Ring<E, 1>::kBytes + (PAIRS == kSplit ? kSplitBytes : 0)), stream>>>(p, slots);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
@@ -41,7 +41,7 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     p.units = uint32_t((p.n_tokens + kQkGroup - 1) / kQkGroup * p.chunks);
     const bool straddles = p.hq % p.per != 0 && p.heads > p.hq;
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
-           qk_bwd_smem(Ring<E, 2>::kBytes, p.D, PAIRS == kSplit, p.ws.hdr != nullptr, straddles), stream>>>(p, straddles);
+           qk_bwd_smem(Ring<E, 2>::kBytes, PAIRS == kSplit, p.ws.hdr != nullptr, straddles), stream>>>(p, straddles);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
