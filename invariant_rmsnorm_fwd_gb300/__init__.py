@@ -89,7 +89,6 @@ def _load():
     lib = ctypes.CDLL(path)
     P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     LP, DP = ctypes.POINTER(_Layout), ctypes.POINTER(_Dropout)
-    RP, HP = ctypes.POINTER(_Rotary), ctypes.POINTER(_Heads)
     sig = {
         "rmsnorm_fwd": ([P, P, I64, F, LP, P, P, P], ctypes.c_int),
         "rmsnorm_bwd_dx": ([P, P, P, I64, F, LP, P, P, P], ctypes.c_int),
@@ -125,10 +124,10 @@ def _load():
         "dropout_fwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
         "dropout_bwd": ([P, I64, I32, LP, DP, P, P], ctypes.c_int),
         "rotary_turns": ([P, I32, P], ctypes.c_int),
-        "rotary_fwd": ([HP, HP, I64, I32, LP, RP, P], ctypes.c_int),
-        "rotary_bwd": ([HP, HP, I64, I32, LP, RP, P], ctypes.c_int),
-        "qk_norm_rotary_fwd": ([HP, HP, I64, F, I32, I32, LP, RP, P], ctypes.c_int),
-        "qk_norm_rotary_bwd": ([HP, HP, I64, F, I32, I32, LP, RP, P, P], ctypes.c_int),
+        "rotary_fwd": ([P, P, I64, I32, P, P, P], ctypes.c_int),
+        "rotary_bwd": ([P, P, I64, I32, P, P, P], ctypes.c_int),
+        "qk_norm_rotary_fwd": ([P, P, I64, F, I32, I32, P, P, P], ctypes.c_int),
+        "qk_norm_rotary_bwd": ([P, P, I64, F, I32, I32, P, P, P, P], ctypes.c_int),
         "qk_norm_workspace_bytes": ([I64, I32, I32, I64], ctypes.c_size_t),
         "qk_norm_begin": ([P, ctypes.c_size_t, I64, I32, I32, I64, P], ctypes.c_int),
         "qk_norm_finalize": ([P, I64, I32, I32, I64, F, P, P, P], ctypes.c_int),

@@ -12,29 +12,29 @@ have that type or float32.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 import torch
 
 import invariant_rmsnorm_fwd_gb300 as _rb
 
-_Heads = _rb._Heads
+# The C structures as bytes: packing them is quicker than building ctypes ones.
+_heads_struct = struct.Struct("QqqQqqQqqQii").pack                   # rmsnorm_heads_t
+_rotary_struct = struct.Struct("QQiiif").pack                        # rmsnorm_rotary_t
+_layout_struct = struct.Struct("qiiqQqQq").pack                      # rmsnorm_layout_t
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _index(t) -> int:
-    """Device index of a CUDA tensor, -1 for a host tensor."""
-    return t.get_device()
+_index = torch.Tensor.get_device                                     # of a CUDA tensor; -1 for a host tensor
 
 
 def _is_cuda(t) -> bool:
     return t.is_cuda
 
 
-def _current() -> int:
-    return torch.cuda.current_device()
-
-
+# The current device, without looking whether CUDA runs (a CUDA tensor is at hand).
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # The raw handle of the current stream, without building a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -88,20 +88,20 @@ class Rotary:
         """The library's descriptor for a call of n slots on device `index`."""
         if not isinstance(position, torch.Tensor) or position.dtype != torch.int32:
             raise TypeError("position: expected an int32 tensor")
-        if not _is_cuda(position) or _index(position) != index:
+        if _index(position) != index:
             raise ValueError(f"position: must be a CUDA tensor on the call's device (got {position.device})")
         if position.dim() != 1 or position.numel() < n or not position.is_contiguous():
             raise ValueError(f"position: expected a contiguous tensor of at least {n} positions, one per token slot")
-        if not _is_cuda(self.turns) or _index(self.turns) != index:
-            raise ValueError(f"rotary: on {self.turns.device}, the call's heads are on cuda:{index}")
-        return ctypes.byref(_rb._Rotary(position.data_ptr(), self.turns.data_ptr(), self.rotary_dim, self.first,
-                                        self.interleaved, self.scale))
+        turns = self.turns
+        if _index(turns) != index:
+            raise ValueError(f"rotary: on {turns.device}, the call's heads are on cuda:{index}")
+        return _rotary_struct(position.data_ptr(), turns.data_ptr(), self.rotary_dim, self.first, self.interleaved, self.scale)
 
 
 class _Call:
     """The checks of one call's tensors.  The first one (the queries') fixes the element
     type, the device and the head width; the others are compared with it."""
-    __slots__ = ("lay", "n", "D", "index", "dtype", "code", "param", "stream")
+    __slots__ = ("lay", "n", "D", "index", "dtype", "code", "stream")
 
     def __init__(self, q, name: str, lay, stream):
         if not isinstance(lay, _rb.CallLayout):
@@ -113,72 +113,86 @@ class _Call:
         if lay.rows_per_token != 1:
             raise ValueError(f"layout: one row per token slot expected (heads are a dimension of the tensors), got "
                              f"rows_per_token {lay.rows_per_token}")
-        self.lay, self.n, self.dtype, self.index = lay, lay.n_tokens, q.dtype, _index(q)
-        self.code = self.param = _DTYPE.get(q.dtype)
-        if self.code is None:
-            raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {q.dtype}")
-        if q.dim() != 3:
-            raise ValueError(f"{name}: expected [n_tokens, heads, head_dim], got shape {tuple(q.shape)}")
-        self.D = q.shape[2]
-        if self.index != _current():
+        dtype, shape, index = q.dtype, q.shape, _index(q)
+        code = _DTYPE.get(dtype)
+        if code is None:
+            raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
+        if len(shape) != 3:
+            raise ValueError(f"{name}: expected [n_tokens, heads, head_dim], got shape {tuple(shape)}")
+        if index != _current():
             raise ValueError(f"{name}: on {q.device}, the current device is cuda:{_current()}")
         if stream is None:
-            self.stream = _raw_stream(self.index)
+            self.stream = _raw_stream(index)
         else:
-            if stream.device_index != self.index:
+            if stream.device_index != index:
                 raise ValueError(f"stream: on {stream.device}, the call's heads are on {q.device}")
             self.stream = stream.cuda_stream
+        self.lay, self.n, self.D, self.index, self.dtype, self.code = lay, lay.n_tokens, shape[2], index, dtype, code
 
-    def heads(self, t, name: str, heads=None):
+    def heads(self, t, name: str, heads: int):
         """(address, token stride, head stride) of a tensor of heads."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
         if t.dtype != self.dtype:
             raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
-        if not _is_cuda(t) or _index(t) != self.index:
+        if _index(t) != self.index:
             raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {t.device})")
         shape, st = t.shape, t.stride()
-        if len(shape) != 3 or shape[2] != self.D or st[2] != 1 or (heads is not None and shape[1] != heads):
-            raise ValueError(f"{name}: expected [n_tokens, {'heads' if heads is None else heads}, {self.D}] with unit "
-                             f"column stride, got shape {tuple(shape)} strides {tuple(st)}")
+        if len(shape) != 3 or shape[2] != self.D or st[2] != 1 or shape[1] != heads:
+            raise ValueError(f"{name}: expected [n_tokens, {heads}, {self.D}] with unit column stride, got shape "
+                             f"{tuple(shape)} strides {tuple(st)}")
         if shape[0] < self.n:
             raise ValueError(f"{name}: {shape[0]} token slots, the call's layout has {self.n}")
         return t.data_ptr(), st[0], st[1]
 
     def weight(self, w, name: str):
-        if w is None:
-            return None
         if not isinstance(w, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(w).__name__}")
         if w.dtype != self.dtype and w.dtype != torch.float32:
             raise TypeError(f"{name}: expected {self.dtype} or torch.float32, got {w.dtype}")
-        if not _is_cuda(w) or _index(w) != self.index:
+        if _index(w) != self.index:
             raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {w.device})")
         if w.dim() != 1 or w.numel() != self.D or not w.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous [{self.D}] tensor, got shape {tuple(w.shape)}")
-        self.param = _DTYPE[w.dtype]
         return w.data_ptr()
 
-    def side(self, x, x_name, out, out_name, dy=None, dy_name="", w=None):
-        """The library's descriptor of one tensor's heads."""
-        at, ts, hs = self.heads(x, x_name)
+    def weights(self, q_weight, k_weight):
+        """Addresses of both weights (0: ones) and the code of their type, one for both."""
+        qw = 0 if q_weight is None else self.weight(q_weight, "q_weight")
+        kw = 0 if k_weight is None else self.weight(k_weight, "k_weight")
+        w = k_weight if q_weight is None else q_weight
+        if w is None:
+            return qw, kw, self.code
+        if k_weight is not None and k_weight.dtype != w.dtype:
+            raise TypeError("q_weight and k_weight: expected one type")
+        return qw, kw, _DTYPE[w.dtype]
+
+    def side(self, x, x_name, out, out_name, dy=None, dy_name="", w=0):
+        """The library's descriptor of one tensor's heads (None without it)."""
+        if x is None:
+            return None
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{x_name}: expected a torch.Tensor, got {type(x).__name__}")
+        if len(x.shape) != 3:
+            raise ValueError(f"{x_name}: expected [n_tokens, heads, {self.D}], got shape {tuple(x.shape)}")
         heads = x.shape[1]
+        at, ts, hs = self.heads(x, x_name, heads)
         o_at, o_ts, o_hs = self.heads(out, out_name, heads)
-        d_at, d_ts, d_hs = self.heads(dy, dy_name, heads) if dy_name else (None, 0, 0)
-        return ctypes.byref(_Heads(at, ts, hs, d_at, d_ts, d_hs, o_at, o_ts, o_hs, w, heads, 0))
+        d_at, d_ts, d_hs = self.heads(dy, dy_name, heads) if dy_name else (0, 0, 0)
+        return _heads_struct(at, ts, hs, d_at, d_ts, d_hs, o_at, o_ts, o_hs, w, heads, 0)
 
     def layout(self):
-        n, tok = self.n, None
+        n, tok = self.n, 0
         if n:
             t = self.lay.tok_id
             if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
                 raise TypeError("layout.tok_id: expected an int32 tensor")
-            if not _is_cuda(t) or _index(t) != self.index:
+            if _index(t) != self.index:
                 raise ValueError(f"layout.tok_id: must be a CUDA tensor on the call's device (got {t.device})")
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"layout.tok_id: expected {n} contiguous ids")
             tok = t.data_ptr()
-        return ctypes.byref(_rb._Layout(n, 1, 0, 0, tok, self.lay.n_logical_tokens, None, 0))
+        return _layout_struct(n, 1, 0, 0, tok, self.lay.n_logical_tokens, 0, 0)
 
     def rotary(self, rotary, position):
         if not isinstance(rotary, Rotary):
@@ -195,24 +209,23 @@ def _new(like, stream):
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
-def _tensor(t, name: str):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+def _outputs(c, q, k, q_out, k_out, names, stream):
+    """Outputs that the caller did not bring."""
+    if k is None:
+        if k_out is not None:
+            raise ValueError(f"{names[1]}: only with the keys")
+    elif not isinstance(k, torch.Tensor):
+        raise TypeError(f"{names[0]}: expected a torch.Tensor, got {type(k).__name__}")
+    elif k_out is None:
+        k_out = _new(k, stream)
+    return _new(q, stream) if q_out is None else q_out, k_out
 
 
 def _rotate(fn: str, q, k, lay, position, rotary, q_out, k_out, names, stream):
     c = _Call(q, names[0], lay, stream)
-    if k is None and k_out is not None:
-        raise ValueError(f"{names[3]}: only with {names[1]}")
-    if k is not None:
-        _tensor(k, names[1])
-    if q_out is None:
-        q_out = _new(q, stream)
-    if k_out is None and k is not None:
-        k_out = _new(k, stream)
-    qs = c.side(q, names[0], q_out, names[2])
-    ks = None if k is None else c.side(k, names[1], k_out, names[3])
-    rc = getattr(_rb._load(), fn)(qs, ks, c.D, c.code, c.layout(), c.rotary(rotary, position), c.stream)
+    q_out, k_out = _outputs(c, q, k, q_out, k_out, (names[1], names[3]), stream)
+    rc = getattr(_rb._load(), fn)(c.side(q, names[0], q_out, names[2]), c.side(k, names[1], k_out, names[3]), c.D, c.code,
+                                  c.layout(), c.rotary(rotary, position), c.stream)
     if rc:
         _rb._check(rc, fn)
     return q_out, k_out
@@ -229,31 +242,17 @@ def rotary_bwd(dq_out, dk_out, lay, position, rotary: Rotary, dq=None, dk=None, 
     return _rotate("rotary_bwd", dq_out, dk_out, lay, position, rotary, dq, dk, ("dq_out", "dk_out", "dq", "dk"), stream)
 
 
-def _pair_weights(c, q_weight, k_weight):
-    """Addresses of both weights, which have one type where both are given."""
-    qw, kw = c.weight(q_weight, "q_weight"), c.weight(k_weight, "k_weight")
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight: expected one type")
-    return qw, kw
-
-
 def qk_norm_rotary_fwd(q, k, q_weight, k_weight, lay, position, rotary: Rotary, eps: float, q_out=None, k_out=None,
                        stream=None):
     """RMS norm of every head of q and k (None: q alone) with its weight (None: ones), and the rotation, in one pass
     with one rounding.  Returns (q_out, k_out)."""
     c = _Call(q, "q", lay, stream)
-    if k is None and (k_out is not None or k_weight is not None):
-        raise ValueError("k_out and k_weight: only with k")
-    if k is not None:
-        _tensor(k, "k")
-    if q_out is None:
-        q_out = _new(q, stream)
-    if k_out is None and k is not None:
-        k_out = _new(k, stream)
-    qw, kw = _pair_weights(c, q_weight, k_weight)
-    qs = c.side(q, "q", q_out, "q_out", w=qw)
-    ks = None if k is None else c.side(k, "k", k_out, "k_out", w=kw)
-    rc = _rb._load().qk_norm_rotary_fwd(qs, ks, c.D, eps, c.code, c.param, c.layout(), c.rotary(rotary, position), c.stream)
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight: only with the keys")
+    q_out, k_out = _outputs(c, q, k, q_out, k_out, ("k", "k_out"), stream)
+    qw, kw, param = c.weights(q_weight, k_weight)
+    rc = _rb._load().qk_norm_rotary_fwd(c.side(q, "q", q_out, "q_out", w=qw), c.side(k, "k", k_out, "k_out", w=kw), c.D, eps,
+                                        c.code, param, c.layout(), c.rotary(rotary, position), c.stream)
     if rc:
         _rb._check(rc, "qk_norm_rotary_fwd")
     return q_out, k_out
@@ -264,17 +263,12 @@ def qk_norm_rotary_bwd(q, k, q_weight, k_weight, dq_out, dk_out, lay, position, 
     """Backward of qk_norm_rotary_fwd (q and k are its inputs).  With a workspace the same pass adds the call's tokens
     to both weight gradients.  Returns (dq, dk); dq may be q or dq_out, dk likewise."""
     c = _Call(q, "q", lay, stream)
-    if k is None and (dk is not None or dk_out is not None or k_weight is not None):
-        raise ValueError("dk, dk_out and k_weight: only with k")
-    if k is not None:
-        _tensor(k, "k")
-    if dq is None:
-        dq = _new(q, stream)
-    if dk is None and k is not None:
-        dk = _new(k, stream)
-    qw, kw = _pair_weights(c, q_weight, k_weight)
+    if k is None and (dk_out is not None or k_weight is not None):
+        raise ValueError("dk_out and k_weight: only with the keys")
+    dq, dk = _outputs(c, q, k, dq, dk, ("k", "dk"), stream)
+    qw, kw, param = c.weights(q_weight, k_weight)
     qs = c.side(q, "q", dq, "dq", dq_out, "dq_out", qw)
-    ks = None if k is None else c.side(k, "k", dk, "dk", dk_out, "dk_out", kw)
+    ks = c.side(k, "k", dk, "dk", dk_out, "dk_out", kw)
     ws = None
     if workspace is not None:
         if not isinstance(workspace, QkNormWorkspace):
@@ -285,8 +279,7 @@ def qk_norm_rotary_bwd(q, k, q_weight, k_weight, dq_out, dk_out, lay, position, 
         if workspace.sizes != mine:
             raise ValueError(f"workspace: for (tokens, query heads, key heads, head_dim) {workspace.sizes}, the call has {mine}")
         ws = workspace.buf.data_ptr()
-    rc = _rb._load().qk_norm_rotary_bwd(qs, ks, c.D, eps, c.code, c.param, c.layout(), c.rotary(rotary, position), ws,
-                                        c.stream)
+    rc = _rb._load().qk_norm_rotary_bwd(qs, ks, c.D, eps, c.code, param, c.layout(), c.rotary(rotary, position), ws, c.stream)
     if rc:
         _rb._check(rc, "qk_norm_rotary_bwd")
     return dq, dk
@@ -325,7 +318,7 @@ class QkNormWorkspace:
                 return torch.empty(D, dtype=torch.float32, device=self.buf.device)
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
             raise TypeError(f"{name}: expected a float32 tensor")
-        if not _is_cuda(t) or _index(t) != _index(self.buf) or not t.is_contiguous() or t.numel() < D:
+        if _index(t) != _index(self.buf) or not t.is_contiguous() or t.numel() < D:
             raise ValueError(f"{name}: expected a contiguous tensor of at least {D} elements on {self.buf.device}")
         return t
 
