@@ -24,8 +24,8 @@
  * multiset whatever its physical layout (and whatever the strides).  Row sums
  * use a fixed tree that depends only on D and the rotary parameters.  A weight
  * gradient is summed in canonical order: a token's heads, queries then keys, in
- * ceil(heads / 8) chunks of equal size (the last one shorter), each from its
- * first to its last head of the kind; the 8 logical tokens of a group in a fixed
+ * chunks of equal size (at most 8 heads, by the number of heads and of logical
+ * tokens; the last one shorter), each from its first to its last head of the kind; the 8 logical tokens of a group in a fixed
  * order that depends on D; then chunks and groups by a fixed tree over their number.
  * Groups that a call does not hold whole and in consecutive slots leave their
  * tokens' sums in the workspace, and qk_norm_finalize adds them in the same

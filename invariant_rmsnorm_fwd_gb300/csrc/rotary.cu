@@ -183,6 +183,7 @@ __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slo
     const int64_t t0 = g * kQkGroup;
     uint32_t there = 0;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int c = 0; c < slots; ++c) {
         const float *src = ws.spill + ((slot0 + c) * ws.n + t0) * ws.D + col;
         float4 x[kQkGroup];

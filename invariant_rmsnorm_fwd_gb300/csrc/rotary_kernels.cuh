@@ -19,18 +19,26 @@ namespace rbi {
 
 constexpr int kChunkHeads = 8;                           // most heads of a chunk
 constexpr int kQkGroup = 8;                              // logical tokens of a group of the weight gradients' order
+constexpr int kBusyWarps = 2432;                         // warps that fill the GPU: 16 on each of 152 SMs
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
 
-// The heads of a token, queries then keys, are cut into chunks of equal size (the last
-// one shorter).  A chunk that holds both kinds has a partial sum of each: slots of the
-// queries' chunks come first, then those of the chunks that hold keys.
+// The backward pass cuts a token's heads, queries then keys, into chunks of equal size
+// (the last one shorter), by the number of heads and of logical tokens alone: of 8 heads,
+// so that a token's angles serve many rows, or half as many and half again, down to 2,
+// while all of them still run at once (2,000 tokens of 40 heads of 128: 16.7 us in chunks
+// of 8, 17.9 in chunks of 4, which are a few warps more than fit; 46 tokens of 6 heads
+// of 16: 8.6 us in chunks of 6, 5.1 of 2).  A chunk that holds both kinds has a partial sum of
+// each: slots of the queries' chunks come first, then those of the chunks that hold keys.
 struct QkChunks {
     int32_t chunks, per;             // chunks of a token, heads of a chunk
     int32_t q_slots, k_first, slots; // chunks with queries; first chunk with keys; all partial sums
     QkChunks() = default;
-    QkChunks(int32_t hq, int32_t hk) {
+    QkChunks(int32_t hq, int32_t hk, int64_t tokens) {
         const int32_t all = hq + hk;
-        chunks = (all + kChunkHeads - 1) / kChunkHeads;
+        const int64_t groups = (tokens + kQkGroup - 1) / kQkGroup;
+        int n = kChunkHeads;
+        while (n > 2 && groups * ((all + n / 2 - 1) / (n / 2)) <= kBusyWarps) n >>= 1;
+        chunks = (all + n - 1) / n;
         per = (all + chunks - 1) / chunks;
         q_slots = (hq + per - 1) / per;
         k_first = hq / per;
@@ -64,7 +72,7 @@ inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(
 struct QkWsLayout {
     int64_t off_whole, off_partial, off_spill, total;
     QkWsLayout(int64_t N, int32_t hq, int32_t hk, int64_t D) {
-        const int64_t slots = QkChunks(hq, hk).slots, groups = (N + kQkGroup - 1) / kQkGroup;
+        const int64_t slots = QkChunks(hq, hk, N).slots, groups = (N + kQkGroup - 1) / kQkGroup;
         off_whole = align256(256 + N * 4);
         off_partial = align256(off_whole + groups * 4);
         off_spill = align256(off_partial + slots * groups * D * 4);
@@ -84,7 +92,7 @@ inline QkWs qk_ws(void *base, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     w.n = N;
     w.groups = (N + kQkGroup - 1) / kQkGroup;
     w.sizes = qk_sizes(D, hq, hk);
-    w.cut = QkChunks(hq, hk);
+    w.cut = QkChunks(hq, hk, N);
     w.D = int32_t(D);
     return w;
 }
@@ -224,9 +232,8 @@ __device__ __forceinline__ void stage_weights(float4 *sw, const RotaryParams &p,
     const int i = threadIdx.x, side = i >= 2 * size, lane = (i - side * 2 * size) >> 1, j = i & 1;
     if (i >= 4 * size) return;                           // (a CTA has at least 128 threads)
     const int at = lane_columns<PAIRS>(lane, p).at[j];
-    if (at < 0) return;
-    f2_t f[4];
-    oct_param<E>(p.side[side].w, p.params_f32, at >> 3, 1.f, f);
+    f2_t f[4] = {0, 0, 0, 0};                            // (columns that are not there: zeros, they enter sums)
+    if (at >= 0) oct_param<E>(p.side[side].w, p.params_f32, at >> 3, 1.f, f);
     float4 *to = sw + (side * 4 + 2 * j) * 32 + lane;
     to[0] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
     to[32] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
@@ -280,16 +287,22 @@ __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turns, float 
 }
 
 // The lane's cosines and sines, times scale: kHalf of its 8 pairs in columns' order,
-// kNear likewise, 4 pairs a vector.  kSplit: of all pairs of the team's token, in shared
-// memory: cosines, then sines.  There few lanes may have all the rotated columns (20 of
-// 80), and each of theirs a pair of its own, so the team forms them together.
+// kNear likewise, 4 pairs a vector.
 template <int PAIRS>
 struct Angles {
     f2_t c[4], s[4];
 };
+// kSplit: few lanes may have all the rotated columns (20 of 80), and each column of theirs a
+// pair of its own, so the team forms all its token's cosines and sines in shared memory.
+// From there every column takes the factors of itself and of its partner, the sine
+// negative in first halves; with the norm in front the weights are multiplied into them.
+// The partner's value comes from where its lane's copy of the row has arrived (16 bits),
+// or from a row of the team's own (FP32).
 template <>
 struct Angles<kSplit> {
     float *c, *s;
+    f2_t own[8], other[8];
+    int32_t from[8];                 // where the partners of register pair i are: bytes from the row's start
 };
 template <class E, int PAIRS>
 __device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, int size, const LaneColumns<PAIRS> &col,
@@ -327,11 +340,9 @@ __device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t posit
     }
 }
 
-// Turns the lane's columns.  kSplit: through the team's row of D floats in shared
-// memory, all lanes of the warp at the same time.
+// Turns the lane's columns.
 template <int PAIRS>
-__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, const LaneColumns<PAIRS> &col, const RotaryParams &p,
-                                          float *row) {
+__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, const LaneColumns<PAIRS> &col) {
     if constexpr (PAIRS == kHalf) {
         if (col.turned) {
 #pragma unroll
@@ -341,42 +352,98 @@ __device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, 
                 f[4 + i] = f2_fma(y, a.c[i], f2_mul(x, a.s[i]));
             }
         }
-    } else if constexpr (PAIRS == kNear) {
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float x = f2_lo(f[i]), y = f2_hi(f[i]);
             const float c = i & 1 ? f2_hi(a.c[i >> 1]) : f2_lo(a.c[i >> 1]), s = i & 1 ? f2_hi(a.s[i >> 1]) : f2_lo(a.s[i >> 1]);
             if ((col.turned >> i) & 1) f[i] = f2_make(__fmaf_rn(x, c, -__fmul_rn(y, s)), __fmaf_rn(y, c, __fmul_rn(x, s)));
         }
-    } else {
-        const int half = p.rot >> 1;
+    }
+}
+
+// kSplit's shared memory of a warp: the teams' rows of D floats (FP32), then their cosines
+// and sines (rot / 2 each); teams x D floats are at most 2048 bytes.
+constexpr int kSplitBytes = 4096;
+// The partner column of a rotated one.
+__device__ __forceinline__ int partner(int at, const RotaryParams &p) {
+    return at - p.first < p.rot >> 1 ? at + (p.rot >> 1) : at - (p.rot >> 1);
+}
+// The vector that holds a column: which of its lane's two, and that lane of the team.
+__device__ __forceinline__ void owner(int at, const RotaryParams &p, int &second, int &lane) {
+    lane = at >> 3;
+    second = lane >= p.lanes;
+    if (second) lane -= p.lanes;
+}
+template <class E>
+__device__ __forceinline__ void split_start(Angles<kSplit> &a, float *row, int team, int teams, int size, const LaneColumns<kSplit> &col,
+                                            const RotaryParams &p) {
+    a.c = row + (teams - team) * p.D + team * p.rot;
+    a.s = a.c + (p.rot >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = partner(col.at[i >> 2] + 2 * (i & 3), p);
+        int second, lane;
+        owner(at, p, second, lane);
+        a.from[i] = sizeof(E) == 4 ? at * 4 : second * 512 + (team * size + lane) * 16 + (at & 7) * 2;
+    }
+}
+// `weights`: shared-memory address of the side's weights, 0 without the norm.
+__device__ __forceinline__ void split_factors(Angles<kSplit> &a, const LaneColumns<kSplit> &col, const RotaryParams &p, uint32_t weights,
+                                              int lane) {
+    if (weights) lane_weights(weights + lane * 16, a.own);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a.other[i] = 0;
+        if ((col.turned >> i) & 1) {
+            const int at = col.at[i >> 2] + 2 * (i & 3), half = p.rot >> 1, k = at - p.first;
+            const f2_t c = *reinterpret_cast<const f2_t *>(a.c + (k < half ? k : k - half));
+            f2_t s = *reinterpret_cast<const f2_t *>(a.s + (k < half ? k : k - half));
+            if (k < half) s = f2_mul(s, f2_both(-1.f));
+            if (weights) {
+                const int to = partner(at, p);
+                int second, of;
+                owner(to, p, second, of);
+                f2_t w;
+                asm volatile("ld.shared.b64 %0, [%1];"
+                             : "=l"(w)
+                             : "r"(weights + (second * 2 + ((to & 7) >> 2)) * 512 + of * 16 + (to & 3) * 4));
+                a.own[i] = f2_mul(a.own[i], c);
+                s = f2_mul(s, w);
+            } else {
+                a.own[i] = c;
+            }
+            a.other[i] = s;
+        }
+    }
+}
+// Turns the lane's columns (and multiplies all of them with the weights, NORM).  `row`:
+// shared-memory address of the row that `from` counts from.
+template <class E, bool NORM>
+__device__ __forceinline__ void split_turn(f2_t (&f)[8], const Angles<kSplit> &a, const LaneColumns<kSplit> &col, uint32_t row) {
+    if constexpr (sizeof(E) == 4) {
         __syncwarp();                                    // the row before has been read
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (col.at[i] >= 0) {
-                *reinterpret_cast<ulonglong2 *>(row + col.at[i]) = make_ulonglong2(f[4 * i], f[4 * i + 1]);
-                *reinterpret_cast<ulonglong2 *>(row + col.at[i] + 4) = make_ulonglong2(f[4 * i + 2], f[4 * i + 3]);
+                const uint32_t to = row + col.at[i] * 4;
+                asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to), "l"(f[4 * i]), "l"(f[4 * i + 1]) : "memory");
+                asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + 16), "l"(f[4 * i + 2]), "l"(f[4 * i + 3]) : "memory");
             }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if ((col.turned >> i) & 1) {
-                const int at = col.at[i >> 2] + 2 * (i & 3), k = at - p.first;
-                const bool second = k >= half;
-                const f2_t y = *reinterpret_cast<const f2_t *>(row + (second ? at - half : at + half));
-                const f2_t c = *reinterpret_cast<const f2_t *>(a.c + (second ? k - half : k));
-                const f2_t s = *reinterpret_cast<const f2_t *>(a.s + (second ? k - half : k));
-                f[i] = f2_fma(f[i], c, f2_mul(y, second ? s : f2_mul(s, f2_both(-1.f))));
-            }
     }
-}
-
-// kSplit's shared memory of a warp: the teams' rows of D floats, then their cosines and
-// sines (rot / 2 each); teams x D floats are at most 2048 bytes.
-constexpr int kSplitBytes = 4096;
-__device__ __forceinline__ void split_angles(Angles<kSplit> &a, float *row, int team, int teams, const RotaryParams &p) {
-    a.c = row + (teams - team) * p.D + team * p.rot;
-    a.s = a.c + (p.rot >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if ((col.turned >> i) & 1) {
+            Raw<E> y;
+            uint32_t *w = reinterpret_cast<uint32_t *>(y.q);
+            if constexpr (sizeof(E) == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(row + a.from[i]) : "memory");
+            else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(row + a.from[i]) : "memory");
+            f[i] = f2_fma(f[i], a.own[i], f2_mul(up2<E>(y, 0), a.other[i]));
+        } else if (NORM) {
+            f[i] = f2_mul(f[i], a.own[i]);
+        }
+    }
 }
 
 // Register pair i holds rotated columns.
@@ -448,10 +515,7 @@ struct Ring {
 template <class E, int PAIRS>
 __device__ __forceinline__ void copy_row(uint32_t dst, const E *row, const LaneColumns<PAIRS> &col, bool on) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const bool some = on && col.at[j] >= 0;
-        cp_async_zfill(dst + j * 512, row + (some ? col.at[j] : 0), some ? 16 : 0);
-    }
+    for (int j = 0; j < 2; ++j) cp_async_zfill(dst + j * 512, row + (col.at[j] >= 0 ? col.at[j] : 0), on && col.at[j] >= 0 ? 16 : 0);
 }
 template <class E, int PAIRS>
 __device__ __forceinline__ void load_row(Raw<E> &r, const E *row, const LaneColumns<PAIRS> &col, bool on) {
@@ -471,11 +535,11 @@ __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 // NORM: behind the norm; else the rotation alone.  A warp takes `slots` consecutive slots
 // of a call (at most 32) and one chunk of heads; its teams take the active ones in turns.
 template <class E, int PAIRS, bool NORM, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 || NORM ? 5 : 6)
+__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E) == 4 || NORM ? 5 : 6)
     rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
     extern __shared__ float4 shared[];
     using R = Ring<E, 1>;
-    const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane32 = threadIdx.x & 31, warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);   // (uniform, for the compiler)
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
     const bool in = unit < p.units;
     const uint32_t win = p.by_chunks.quotient(in ? unit : 0);
@@ -539,24 +603,29 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 || NORM ? 5 : 6)
     if constexpr (NORM) __syncthreads();                 // the weights
 
     Angles<PAIRS> a;
-    if constexpr (PAIRS == kSplit) split_angles(a, row, team, teams, p);
+    if constexpr (PAIRS == kSplit) split_start<E>(a, row, team, teams, size, col, p);
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0;
         lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), team < teams ? lane : p.rot, size, col, a);   // (left-over lanes form none)
+        if constexpr (PAIRS == kSplit && !NORM) split_factors(a, col, p, 0, lane);
         for (int h = head0; h < end;) {                  // the token's heads of one kind after the other
             const bool keys = h >= p.hq;
             const int stop = keys || end < p.hq ? end : p.hq;
             const HeadsParams &s = p.side[keys];
             E *dst = static_cast<E *>(s.out) + ((on ? first + at : 0) * s.out_t + (keys ? h - p.hq : h) * s.out_h);
             const uint32_t weights = smem_addr(shared) + keys * (kWeightBytes / 2) + lane * 16;
+            if constexpr (PAIRS == kSplit && NORM) split_factors(a, col, p, weights - lane * 16, lane);
             for (; h < stop; ++h) {
                 Raw<E> r;
+                uint32_t at_row = smem_addr(row);        // kSplit: the team's row, or (16 bits) the warp's rows as they came
                 if constexpr (R::kOn) {
                     cp_async_wait<R::kDepth - 2>();
+                    if constexpr (PAIRS == kSplit) __syncwarp();     // everyone's; and the row before has been read
                     fetch();
                     take_row<E>(r, from);
+                    at_row = from - lane32 * 16;
                     from += R::kPieces * 512;
                     if (from == ring + R::kBytes) from = ring;
                 } else {
@@ -566,14 +635,22 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 || NORM ? 5 : 6)
                 f2_t f[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = up2<E>(r, j);
-                if constexpr (NORM) {
-                    f2_t w[8];
-                    const f2_t rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size, lane), p));
-                    lane_weights(weights, w);
+                f2_t rstd = 0;
+                if constexpr (NORM) rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size, lane), p));
+                if constexpr (PAIRS == kSplit) {
+                    split_turn<E, NORM>(f, a, col, at_row);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                    for (int j = 0; j < 8; ++j)
+                        if (NORM) f[j] = f2_mul(f[j], rstd);
+                } else {
+                    if constexpr (NORM) {
+                        f2_t w[8];
+                        lane_weights(weights, w);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
+                    }
+                    turn_lane<PAIRS>(f, a, col);
                 }
-                turn_lane<PAIRS>(f, a, col, p, row);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r, j, f[j]);
@@ -632,9 +709,9 @@ inline int qk_bwd_smem(int ring_bytes, bool split, bool grads, bool straddles) {
 
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
 template <class E, int PAIRS, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
+__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
     extern __shared__ float4 shared[];
-    const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane32 = threadIdx.x & 31, warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);   // (uniform, for the compiler)
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
     const bool in = unit < p.units;
     const uint32_t win = p.by_chunks.quotient(in ? unit : 0);
@@ -715,7 +792,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
     if (steps == 0) return;
 
     Angles<PAIRS> a;
-    if constexpr (PAIRS == kSplit) split_angles(a, row, team, teams, p);
+    if constexpr (PAIRS == kSplit) split_start<E>(a, row, team, teams, size, col, p);
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
@@ -723,6 +800,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
         const int64_t slot = on ? int64_t(win) * 8 - 7 + at : 0;
         const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
         lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, size, col, a);
+        if constexpr (PAIRS == kSplit) split_factors(a, col, p, 0, lane);
         const bool known = int64_t(id) < p.ws.n;
         if (grads && on && chunk == 0 && lane == 0) {
             const int bad = known ? (atomicExch(p.ws.flag + id, run ? 1 : 2) ? kStDouble : 0) : kStPlan;
@@ -740,11 +818,14 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
             for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
             for (; h < stop; ++h) {
                 Raw<E> rx, rg;
+                uint32_t at_row = smem_addr(row);
                 if constexpr (R::kOn) {
                     cp_async_wait<R::kDepth - 2>();
+                    if constexpr (PAIRS == kSplit) __syncwarp();
                     fetch();
                     take_row<E>(rx, from);
                     take_row<E>(rg, from + 1024);
+                    at_row = from + 1024 - lane32 * 16;
                     from += R::kPieces * 512;
                     if (from == ring + R::kBytes) from = ring;
                 } else {
@@ -758,7 +839,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
                     x[j] = up2<E>(rx, j);
                     g[j] = up2<E>(rg, j);
                 }
-                turn_lane<PAIRS>(g, a, col, p, row);
+                if constexpr (PAIRS == kSplit) split_turn<E, false>(g, a, col, at_row);
+                else turn_lane<PAIRS>(g, a, col);
                 lane_weights(weights, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);

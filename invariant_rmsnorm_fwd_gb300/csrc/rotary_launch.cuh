@@ -15,6 +15,16 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     p.by_team = Divisor(uint32_t(p.team));
     p.teams = 32 / p.team;
     p.by_teams = Divisor(uint32_t(p.teams));
+    // Heads of a warp: 8, so that a token's angles serve many rows, or half as many and half
+    // again while there are fewer warps than fit (one token of 40 heads of 128: rotation
+    // 4.0 -> 2.6 us, norm and rotation 5.7 -> 3.5; with twice that many warps as the aim
+    // 2,000 tokens take 9.2 -> 10.2 us, with four times 12.9).
+    const int64_t windows = (p.n_tokens + p.teams - 1) / p.teams;
+    int most = kChunkHeads;
+    while (most > 1 && windows * ((p.heads + most - 1) / most) < kBusyWarps) most >>= 1;
+    p.chunks = (p.heads + most - 1) / most;
+    p.per = (p.heads + p.chunks - 1) / p.chunks;
+    p.by_chunks = Divisor(uint32_t(p.chunks));
     // Steps of a warp: until its teams have 16 rows each (8 without the norm, whose rows are
     // quicker), so that its start is paid for, while every SM has 64 warps to choose from.
     int steps = 1;
@@ -38,6 +48,10 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
+    const QkChunks cut = p.ws.hdr ? p.ws.cut : QkChunks(p.hq, p.heads - p.hq, p.n_tokens);
+    p.chunks = cut.chunks;
+    p.per = cut.per;
+    p.by_chunks = Divisor(uint32_t(p.chunks));
     p.units = uint32_t((p.n_tokens + kQkGroup - 1) / kQkGroup * p.chunks);
     const bool straddles = p.hq % p.per != 0 && p.heads > p.hq;
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
@@ -58,7 +72,7 @@ static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
         // Forward, teams of just the lanes that a head needs where a warp then holds more of them (5 lanes
         // for 80 columns, 6 for 96).
         if (32 / p.lanes > 32 / p.team) p.team = p.lanes;
-        if constexpr (PAIRS != kSplit) {
+        {
             if (p.team == 4) return rotary_launch_fwd<E, PAIRS, true, 4>(p, stream);
             if (p.team == 5) return rotary_launch_fwd<E, PAIRS, true, 5>(p, stream);
             if (p.team == 6) return rotary_launch_fwd<E, PAIRS, true, 6>(p, stream);
@@ -67,7 +81,7 @@ static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
         }
         return rotary_launch_fwd<E, PAIRS, true, 0>(p, stream);
     }
-    if constexpr (PAIRS != kSplit) {
+    {
         if (p.team == 4) return rotary_launch_bwd<E, PAIRS, 4>(p, stream);
         if (p.team == 8) return rotary_launch_bwd<E, PAIRS, 8>(p, stream);
         if (p.team == 16) return rotary_launch_bwd<E, PAIRS, 16>(p, stream);
@@ -79,10 +93,6 @@ static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
 template <class E, int PAIRS>
 int rotary_run_pairs(RotaryParams p, int mode, cudaStream_t stream) {
     p.lanes = (p.D + 15) / 16;
-    const QkChunks cut(p.hq, p.heads - p.hq);
-    p.chunks = cut.chunks;
-    p.per = cut.per;
-    p.by_chunks = Divisor(uint32_t(p.chunks));
     return rotary_launch<E, PAIRS>(p, mode, stream);
 }
 

@@ -100,7 +100,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    8 tokens, the chunks (at most one more than full ones), the groups of one of 512 shares, 2 steps
+    8 tokens, the chunks (at most as many as heads), the groups of one of 512 shares, 2 steps
     between the shares of a warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
@@ -118,7 +118,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 8 + (x.shape[1] + 7) // 8 + 1 + (n + 4095) // 4096 + 2 + 24
+    chain = 8 + 8 + x.shape[1] + 1 + (n + 4095) // 4096 + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -135,9 +135,12 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
     n, hq, D = q_leaf.shape
     heads = hq + k_leaf.shape[1]
     leaf = np.concatenate([q_leaf, k_leaf], 1).astype(np.float32)
-    chunks = (heads + 7) // 8
-    per = (heads + chunks - 1) // chunks
     groups = (n + 7) // 8
+    most = 8
+    while most > 2 and groups * -(-heads // (most // 2)) <= 2432:
+        most //= 2
+    chunks = -(-heads // most)
+    per = (heads + chunks - 1) // chunks
     team = 1 << max(0, int(np.ceil(np.log2(D / 16))))
     tokens = max(1, 8 // (32 // team))                                # of a group, added up by one team
     shares = 8 * 16 * 4

@@ -77,24 +77,31 @@ def test_norm_closed_forms():
 
 
 def test_replay_of_small_cases():
-    """9 + 2 heads: chunks of 6 and 5, the second with 3 query heads and both key heads; one full group and a token."""
-    q, k = RNG.standard_normal((9, 9, 16)).astype(np.float32), RNG.standard_normal((9, 2, 16)).astype(np.float32)
+    """9 tokens make few groups, so chunks are of two heads, the second one of both kinds: a full group's tokens chunk by
+    chunk, then the chunks; then the ninth token's."""
+    q, k = RNG.standard_normal((9, 3, 16)).astype(np.float32), RNG.standard_normal((9, 2, 16)).astype(np.float32)
     gq, gk = O.grad_replay(q, k)
 
     def left(v):
-        s = np.zeros_like(v[0])
-        for r in v:
-            s = s + r
-        return s
-
-    def group(v):                                                     # width 16: one lane a team, a token a team
         s = v[0]
         for r in v[1:]:
             s = s + r
         return s
 
-    first = group([left(q[t, :6]) for t in range(8)]) + group([left(q[t, 6:]) for t in range(8)])
-    last = left(q[8, :6]) + left(q[8, 6:])
-    assert np.array_equal(gq, first + last)                           # shares of one group each
-    assert np.array_equal(gk, group([left(k[t]) for t in range(8)]) + left(k[8]))
-    assert np.allclose(gq, q.sum((0, 1)), atol=1e-4)
+    for got, parts in ((gq, (q[:, :2], q[:, 2:])), (gk, (k[:, :1], k[:, 1:]))):
+        tokens = [[left(p[t]) for t in range(9)] for p in parts]               # heads of a chunk
+        first = left([left(p[:8]) for p in tokens])                   # width 16: one lane a team, a token a team
+        assert np.array_equal(got, first + left([p[8] for p in tokens]))
+        assert np.allclose(got, np.concatenate(parts, 1).sum((0, 1)), atol=1e-4)
+
+
+def test_replay_keeps_many_heads_in_chunks():
+    """2,440 tokens of 60 + 3 heads: chunks of 8, the last one with 4 query heads and all key heads.  Leaves are zero but
+    in one token, whose sums show the chunks."""
+    q, k = np.zeros((2440, 60, 8), np.float32), np.zeros((2440, 3, 8), np.float32)
+    big = np.float32(2.0 ** 24)
+    q[77, 0], q[77, 1], q[77, 8], q[77, 15] = big, -big, 1.0, big     # (big - big + 3) + (1 + big): 1 is lost in the second chunk
+    q[77, 7] = 3.0
+    k[77, 0], k[77, 2] = 1.0, 2.0
+    gq, gk = O.grad_replay(q, k)
+    assert np.array_equal(gq, np.full(8, np.float32(3.0) + (np.float32(1.0) + big))) and np.array_equal(gk, np.full(8, 3.0, np.float32))
