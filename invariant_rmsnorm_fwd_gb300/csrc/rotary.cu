@@ -165,6 +165,7 @@ __global__ void qk_begin_kernel(QkWs ws) {
 }
 
 constexpr int kFinalCtas = 8, kFinalWarps = 16;
+constexpr int64_t kFinalAlone = 256;                     // groups that one CTA adds up without a cluster
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
@@ -218,13 +219,15 @@ __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slo
     return v;
 }
 
-// Both weight gradients in one launch: a cluster takes 32 columns of one of them, its
-// 8 CTAs x 16 warps x 4 eighth-warps consecutive shares of the groups.  The partial sums
+// Both weight gradients in one launch: a cluster of CTAS takes 32 columns of one of them,
+// its CTAs x 16 warps x 4 quarter-warps consecutive shares of the groups.  The partial sums
 // of a group from the first chunk to the last, the groups of a share likewise, then the
 // four shares of a warp in pairs, the warps, the CTAs: an order that depends on the sizes
-// alone.
-__global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps * 32)
-    qk_finalize_kernel(const __grid_constant__ QkWs ws, float scale, float *dq, float *dk, int slices) {
+// alone.  What bounds it: latency (a launch, the header, a share's 1 to 3 rounds of loads,
+// the cluster's exchange).  33,384 tokens, 5 partial sums of 128 columns a group, 12.8 MB: 6.7 us; up
+// to 256 groups one CTA does without the exchange (46 tokens: XX us, YY in a cluster).
+template <int CTAS>
+__device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *dq, float *dk, int slices) {
     __shared__ float4 part[kFinalWarps][8];
     __shared__ float whole[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -235,7 +238,7 @@ __global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps
     const bool keys = int(blockIdx.x) >= slices;
     const int col0 = (int(blockIdx.x) - (keys ? slices : 0)) * 32, col = col0 + (lane & 7) * 4;
     const int slot0 = keys ? ws.cut.q_slots : 0, slots = keys ? ws.cut.slots - ws.cut.q_slots : ws.cut.q_slots;
-    constexpr int kShares = kFinalCtas * kFinalWarps * 4;
+    constexpr int kShares = CTAS * kFinalWarps * 4;
     const int64_t per = (ws.groups + kShares - 1) / kShares;
     const int64_t g0 = ((int64_t(blockIdx.y) * kFinalWarps + warp) * 4 + (lane >> 3)) * per;
     const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
@@ -276,16 +279,26 @@ __global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps
         for (int i = 1; i < kFinalWarps; ++i) v = __fadd_rn(v, f[i * 32 + lane]);
         whole[lane] = v;
     }
-    cluster_barrier();
+    if constexpr (CTAS > 1) cluster_barrier();
     if (blockIdx.y == 0 && warp == 0) {
-        const uint32_t at = smem_addr(&whole[lane]);
         float v = whole[lane];
+        if constexpr (CTAS > 1) {
+            const uint32_t at = smem_addr(&whole[lane]);
 #pragma unroll
-        for (int i = 1; i < kFinalCtas; ++i) v = __fadd_rn(v, ld_cluster_f32(map_to_rank(at, uint32_t(i))));
+            for (int i = 1; i < CTAS; ++i) v = __fadd_rn(v, ld_cluster_f32(map_to_rank(at, uint32_t(i))));
+        }
         float *dst = keys ? dk : dq;
         if (dst && col0 + lane < ws.D) dst[col0 + lane] = scale != 1.f ? __fmul_rn(v, scale) : v;
     }
-    cluster_barrier();                                   // the sums stay until they are read
+    if constexpr (CTAS > 1) cluster_barrier();           // the sums stay until they are read
+}
+__global__ void __cluster_dims__(1, kFinalCtas, 1) __launch_bounds__(kFinalWarps * 32)
+    qk_finalize_kernel(const __grid_constant__ QkWs ws, float scale, float *dq, float *dk, int slices) {
+    qk_finalize<kFinalCtas>(ws, scale, dq, dk, slices);
+}
+__global__ void __launch_bounds__(kFinalWarps * 32)
+    qk_finalize_small_kernel(const __grid_constant__ QkWs ws, float scale, float *dq, float *dk, int slices) {
+    qk_finalize<1>(ws, scale, dq, dk, slices);
 }
 
 }  // namespace
@@ -346,9 +359,13 @@ extern "C" int qk_norm_finalize(void *workspace, int64_t n_logical_tokens, int32
     DeviceInfo *d = nullptr;
     if ((rc = device_info(&d))) return rc;
     const int slices = int(head_dim + 31) / 32;
-    qk_finalize_kernel<<<dim3(unsigned(slices * (k_heads ? 2 : 1)), kFinalCtas), kFinalWarps * 32, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(
-        qk_ws(workspace, n_logical_tokens, q_heads, k_heads, head_dim), grad_scale, dq_weight, dk_weight, slices);
+    const unsigned gx = unsigned(slices * (k_heads ? 2 : 1));
+    const QkWs ws = qk_ws(workspace, n_logical_tokens, q_heads, k_heads, head_dim);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (ws.groups > kFinalAlone)
+        qk_finalize_kernel<<<dim3(gx, kFinalCtas), kFinalWarps * 32, 0, s>>>(ws, grad_scale, dq_weight, dk_weight, slices);
+    else
+        qk_finalize_small_kernel<<<gx, kFinalWarps * 32, 0, s>>>(ws, grad_scale, dq_weight, dk_weight, slices);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;

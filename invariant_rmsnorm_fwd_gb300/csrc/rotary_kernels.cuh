@@ -509,7 +509,7 @@ template <class E, int TENSORS>
 struct Ring {
     static constexpr bool kOn = sizeof(E) == 2;
     static constexpr int kPieces = 2 * TENSORS;          // 16-byte pieces of a lane's row
-    static constexpr int kDepth = TENSORS == 1 ? 6 : 4;
+    static constexpr int kDepth = TENSORS == 1 ? 5 : 4;
     static constexpr int kBytes = kOn ? kPieces * kDepth * 512 : 0;   // of a warp
 };
 template <class E, int PAIRS>

@@ -90,7 +90,8 @@ class Rotary:
             raise TypeError("position: expected an int32 tensor")
         if _index(position) != index:
             raise ValueError(f"position: must be a CUDA tensor on the call's device (got {position.device})")
-        if position.dim() != 1 or position.numel() < n or not position.is_contiguous():
+        shape = position.shape
+        if len(shape) != 1 or shape[0] < n or not position.is_contiguous():
             raise ValueError(f"position: expected a contiguous tensor of at least {n} positions, one per token slot")
         turns = self.turns
         if _index(turns) != index:
@@ -129,21 +130,18 @@ class _Call:
             self.stream = stream.cuda_stream
         self.lay, self.n, self.D, self.index, self.dtype, self.code = lay, lay.n_tokens, shape[2], index, dtype, code
 
-    def heads(self, t, name: str, heads: int):
-        """(address, token stride, head stride) of a tensor of heads."""
+    def refuse(self, t, name: str, heads):
+        """Says what is wrong with a tensor of heads."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
         if t.dtype != self.dtype:
             raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
         if _index(t) != self.index:
             raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {t.device})")
-        shape, st = t.shape, t.stride()
-        if len(shape) != 3 or shape[2] != self.D or st[2] != 1 or shape[1] != heads:
-            raise ValueError(f"{name}: expected [n_tokens, {heads}, {self.D}] with unit column stride, got shape "
-                             f"{tuple(shape)} strides {tuple(st)}")
-        if shape[0] < self.n:
-            raise ValueError(f"{name}: {shape[0]} token slots, the call's layout has {self.n}")
-        return t.data_ptr(), st[0], st[1]
+        if len(t.shape) == 3 and t.shape[0] < self.n:
+            raise ValueError(f"{name}: {t.shape[0]} token slots, the call's layout has {self.n}")
+        raise ValueError(f"{name}: expected [n_tokens, {heads}, {self.D}] with unit column stride, got shape {tuple(t.shape)} "
+                         f"strides {tuple(t.stride())}")
 
     def weight(self, w, name: str):
         if not isinstance(w, torch.Tensor):
@@ -152,7 +150,7 @@ class _Call:
             raise TypeError(f"{name}: expected {self.dtype} or torch.float32, got {w.dtype}")
         if _index(w) != self.index:
             raise ValueError(f"{name}: must be a CUDA tensor on the call's device (got {w.device})")
-        if w.dim() != 1 or w.numel() != self.D or not w.is_contiguous():
+        if w.shape != (self.D,) or not w.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous [{self.D}] tensor, got shape {tuple(w.shape)}")
         return w.data_ptr()
 
@@ -171,15 +169,29 @@ class _Call:
         """The library's descriptor of one tensor's heads (None without it)."""
         if x is None:
             return None
+        dtype, index, n, D = self.dtype, self.index, self.n, self.D
         if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{x_name}: expected a torch.Tensor, got {type(x).__name__}")
-        if len(x.shape) != 3:
-            raise ValueError(f"{x_name}: expected [n_tokens, heads, {self.D}], got shape {tuple(x.shape)}")
-        heads = x.shape[1]
-        at, ts, hs = self.heads(x, x_name, heads)
-        o_at, o_ts, o_hs = self.heads(out, out_name, heads)
-        d_at, d_ts, d_hs = self.heads(dy, dy_name, heads) if dy_name else (0, 0, 0)
-        return _heads_struct(at, ts, hs, d_at, d_ts, d_hs, o_at, o_ts, o_hs, w, heads, 0)
+            self.refuse(x, x_name, "heads")
+        shape, st = x.shape, x.stride()
+        if len(shape) != 3 or x.dtype is not dtype or _index(x) != index or shape[2] != D or st[2] != 1 or shape[0] < n:
+            self.refuse(x, x_name, "heads")
+        heads = shape[1]
+        if not isinstance(out, torch.Tensor):
+            self.refuse(out, out_name, heads)
+        o_shape, o_st = out.shape, out.stride()
+        if (o_shape != shape and (len(o_shape) != 3 or o_shape[1] != heads or o_shape[2] != D or o_shape[0] < n)) \
+                or out.dtype is not dtype or _index(out) != index or o_st[2] != 1:
+            self.refuse(out, out_name, heads)
+        if not dy_name:
+            return _heads_struct(x.data_ptr(), st[0], st[1], 0, 0, 0, out.data_ptr(), o_st[0], o_st[1], w, heads, 0)
+        if not isinstance(dy, torch.Tensor):
+            self.refuse(dy, dy_name, heads)
+        d_shape, d_st = dy.shape, dy.stride()
+        if (d_shape != shape and (len(d_shape) != 3 or d_shape[1] != heads or d_shape[2] != D or d_shape[0] < n)) \
+                or dy.dtype is not dtype or _index(dy) != index or d_st[2] != 1:
+            self.refuse(dy, dy_name, heads)
+        return _heads_struct(x.data_ptr(), st[0], st[1], dy.data_ptr(), d_st[0], d_st[1], out.data_ptr(), o_st[0], o_st[1], w,
+                             heads, 0)
 
     def layout(self):
         n, tok = self.n, 0

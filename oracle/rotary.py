@@ -100,8 +100,8 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    8 tokens, the chunks (at most as many as heads), the groups of one of 512 shares, 2 steps
-    between the shares of a warp, 16 warps and 8 CTAs."""
+    8 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 up
+    to 256 groups), 2 steps between the shares of a warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
     rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
@@ -118,7 +118,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 8 + x.shape[1] + 1 + (n + 4095) // 4096 + 2 + 24
+    chain = 8 + 8 + x.shape[1] + 1 + max((n + 4095) // 4096, 4) + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -143,7 +143,8 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
     per = (heads + chunks - 1) // chunks
     team = 1 << max(0, int(np.ceil(np.log2(D / 16))))
     tokens = max(1, 8 // (32 // team))                                # of a group, added up by one team
-    shares = 8 * 16 * 4
+    ctas = 8 if groups > 256 else 1
+    shares = ctas * 16 * 4
     share = (groups + shares - 1) // shares
     out = []
     for lo, hi in ((0, hq), (hq, heads)):
@@ -173,7 +174,7 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
             part.append(acc)
         warps = [(part[i] + part[i + 1]) + (part[i + 2] + part[i + 3]) for i in range(0, shares, 4)]
         total = None
-        for r in range(8):
+        for r in range(ctas):
             s = warps[16 * r]
             for w in range(1, 16):
                 s = s + warps[16 * r + w]
