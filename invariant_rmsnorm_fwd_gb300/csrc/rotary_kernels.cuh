@@ -8,6 +8,15 @@
 // inside a vector anyway; halves of other sizes fetch their partners from shared
 // memory.  A team stays with one token and walks over a chunk of its heads, queries
 // and keys alike, so the lane's cosines and sines are formed once per chunk.
+//
+// What bounds it (bf16, 32+8 heads of 128, 33,384 tokens; DRAM floor at the copy rate of
+// 6.78 TB/s in brackets): memory.  Rotation 100.3 us (100.9), norm and rotation 104 (100.9),
+// backward 157 and, with both weight gradients from begin to finalize, 168 (151.4).  FP32,
+// 17,620 tokens: 117, 117 (106.5), 192 (159.8).  Fewer rows for a token's angles and a
+// warp's start, or idle lanes, make it issue: 1+1 heads of 128, 270,100 tokens, 51 and 64
+// (41.1), backward 151 (61.5); heads of 80, backward, 162 (94.6), 5 of 8 lanes.  Split halves
+// pay for their exchange: heads of 96 with 68 columns turning, rotation 33 (22.3); of 128 with
+// 104, backward 48 (20.1).
 #pragma once
 #include <type_traits>
 
@@ -121,7 +130,7 @@ struct RotaryParams {
     int32_t chunks, per;             // chunks of a token, heads of a chunk
     int32_t lanes, team, teams;      // lanes of a head that hold columns; lanes of a team; a warp's teams
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
-    uint32_t units;                  // teams' (warps') pieces of work
+    uint32_t units;                  // warps' pieces of work
     float scale, scale_sin;          // factors of cosine and sine (negative: turns back)
     float eps, inv_d;
     Divisor by_chunks{1}, by_team{1}, by_teams{1};
@@ -253,8 +262,9 @@ __device__ __forceinline__ void lane_weights(uint32_t from, f2_t (&f)[8]) {
 // of degree 9 and 10: what is left out is below (pi/4)^11 / 11! = 1.8e-9 and
 // (pi/4)^12 / 12! = 1.2e-10.  FINE (FP32 heads): y is formed with what the float of the
 // rest loses, and enters as y + d: sin + d cos, cos - d sin; without that the angle is
-// off by up to 1.7 times 2^-24 more.  (One pair at a time: constants are operands then, in
-// registers of two they would be moves.  2 heads of 128, 270,100 tokens: 70 -> XX us.)
+// off by up to 1.7 times 2^-24 more.  (One pair at a time: constants are operands of its
+// instructions, in registers of two they are moves.  1+1 heads of 128, 270,100 tokens, with
+// the norm: 70 -> 67 us.)
 template <bool FINE>
 __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turns, float &c, float &s) {
     const uint32_t top = uint32_t(uint64_t(int64_t(position)) * turns >> 32);
@@ -503,8 +513,10 @@ constexpr int kQkWarps = 4;
 // 16-bit heads come through shared memory: a ring of kDepth rows a team, every lane
 // copying its own columns of TENSORS tensors to places that only it reads.  FP32 rows
 // are twice as long and stay in registers, one row ahead, by loads of 32 bytes a lane
-// (17,620 tokens, 32+8 heads of 128: forward 113 us against 175 through a ring of 16-byte
-// copies, which shared memory cannot keep up with).
+// (17,620 tokens, 32+8 heads of 128: forward 117 us against 175 through a ring, backward 192
+// against 269; two rows ahead: equal).  Depths measured (bf16): forward 4, 5, 6, 8 rows, heads
+// of 80, 33,384 tokens: 75, 75, 77.5, 80 us, heads of 64: 58, 56.5, 56.7, 58; backward 3, 4, 5
+// rows, heads of 128: 173, 168, 168, 16+1 heads of 256: 101, 100, 111.
 template <class E, int TENSORS>
 struct Ring {
     static constexpr bool kOn = sizeof(E) == 2;
@@ -533,7 +545,10 @@ __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 // ----------------------------------------------------------------- forward, and rotation alone
 
 // NORM: behind the norm; else the rotation alone.  A warp takes `slots` consecutive slots
-// of a call (at most 32) and one chunk of heads; its teams take the active ones in turns.
+// of a call (at most 32) and one chunk of heads; its teams take the active ones in turns,
+// so padding costs a warp nothing but its ids.  CTAs an SM: with 6, the norm's 80 registers
+// are as fast on large calls and 0.3 us slower on small ones; FP32 at 4 of 128 registers takes
+// 125 us where 5 take 117; split halves spill at 5.
 template <class E, int PAIRS, bool NORM, int TEAM>
 __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E) == 4 || NORM ? 5 : 6)
     rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
@@ -707,6 +722,13 @@ inline int qk_bwd_smem(int ring_bytes, bool split, bool grads, bool straddles) {
     return kWeightBytes + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0) + (split ? kSplitBytes : 0));
 }
 
+// The backward pass, for a window and a chunk of heads a warp.  Both row sums of a row (of
+// x^2 and of g w x) come from one pass over it; the weight gradients add up in registers
+// over a token's heads of one kind, in shared memory over a team's tokens of the run, and
+// leave as one partial sum a run.  It holds x, g, g w, a token's angles and the sums: 128
+// registers for 16 warps an SM (12 warps at 168 registers: 183 us where 16 take 169; split
+// halves, which would spill, and FP32 have 12).  Left on the table: about 330 instructions a
+// warp for 4 rows of 128, of which some 20 % are addresses and copies.
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
 template <class E, int PAIRS, int TEAM>
 __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
