@@ -180,37 +180,39 @@ __device__ __forceinline__ float4 plus(const float4 &a, const float4 &b) {
 // the order in which a warp of the backward pass adds up a whole group.  All loads of a
 // slot are issued at once.
 __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool check) {
-    const int n = ws.n - g * kQkGroup < kQkGroup ? int(ws.n - g * kQkGroup) : kQkGroup, share = qk_share(32 / qk_team(ws.D));
-    const int64_t t0 = g * kQkGroup;
+    const int64_t t0 = g * ws.group;
+    const int n = ws.n - t0 < ws.group ? int(ws.n - t0) : ws.group;
     uint32_t there = 0;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int c = 0; c < slots; ++c) {
         const float *src = ws.spill + ((slot0 + c) * ws.n + t0) * ws.D + col;
-        float4 x[kQkGroup];
+        float4 x[kMostGroup];
 #pragma unroll
-        for (int i = 0; i < kQkGroup; ++i) x[i] = i < n ? *reinterpret_cast<const float4 *>(src + i * ws.D) : v;
+        for (int i = 0; i < kMostGroup; ++i) x[i] = i < n ? *reinterpret_cast<const float4 *>(src + i * ws.D) : v;
         if (c == 0) {
-            int32_t f[kQkGroup];
+            int32_t f[kMostGroup];
 #pragma unroll
-            for (int i = 0; i < kQkGroup; ++i) f[i] = i < n ? ws.flag[t0 + i] : 0;
+            for (int i = 0; i < kMostGroup; ++i) f[i] = i < n ? ws.flag[t0 + i] : 0;
 #pragma unroll
-            for (int i = 0; i < kQkGroup; ++i) there |= (f[i] == 2) << i;
+            for (int i = 0; i < kMostGroup; ++i) there |= (f[i] == 2) << i;
             if (check && there != (1u << n) - 1u) qk_report(ws, kStMissing);
         }
         float4 u = v, s = v;
         bool any = false;                                // of the share
+        int left = ws.share;
 #pragma unroll
-        for (int i = 0; i < kQkGroup; ++i) {
+        for (int i = 0; i < kMostGroup; ++i) {
             if (i < n) {
                 if ((there >> i) & 1) {
                     s = any ? plus(s, x[i]) : x[i];
                     any = true;
                 }
-                if ((i + 1) % share == 0 || i + 1 == n) {
+                if (--left == 0 || i + 1 == n) {
                     if (!any) s = make_float4(0.f, 0.f, 0.f, 0.f);
-                    u = i < share ? s : plus(u, s);
+                    u = i < ws.share ? s : plus(u, s);
                     any = false;
+                    left = ws.share;
                 }
             }
         }

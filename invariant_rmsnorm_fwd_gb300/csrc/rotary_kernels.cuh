@@ -14,7 +14,7 @@
 // backward 157 and, with both weight gradients from begin to finalize, 168 (151.4).  FP32,
 // 17,620 tokens: 117, 117 (106.5), 192 (159.8).  Fewer rows for a token's angles and a
 // warp's start, or idle lanes, make it issue: 1+1 heads of 128, 270,100 tokens, 51 and 64
-// (41.1), backward 151 (61.5); heads of 80, backward, 162 (94.6), 5 of 8 lanes.  Split halves
+// (41.1), backward 152 (61.5); heads of 80, backward, 138 (94.6).  Split halves
 // pay for their exchange: heads of 96 with 68 columns turning, rotation 33 (22.3); of 128 with
 // 104, backward 48 (20.1).
 #pragma once
@@ -27,12 +27,32 @@
 namespace rbi {
 
 constexpr int kChunkHeads = 8;                           // most heads of a chunk
-constexpr int kQkGroup = 8;                              // logical tokens of a group of the weight gradients' order
+constexpr int kMostGroup = 10;                           // most logical tokens of a group of the weight gradients' order
 constexpr int kBusyWarps = 2432;                         // warps that fill the GPU: 16 on each of 152 SMs
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
 
+// How a warp takes heads of D columns: in teams of as many lanes as hold them, or of the
+// power of two above where that makes no fewer teams.  The logical tokens of a group, the unit
+// that a warp of the backward pass adds up, are as many as it has teams, or a small
+// multiple of that: each team takes a share of consecutive tokens, from the first to the last, then
+// the shares are added likewise.  Teams of 1 and 2 lanes (16 columns, 32) have groups of 8.
+__host__ __device__ constexpr int group_of(int teams) { return teams > kMostGroup ? 8 : teams >= 5 ? teams : 8 / teams * teams; }
+__host__ __device__ constexpr int share_of(int teams) { return teams >= group_of(teams) ? 1 : group_of(teams) / teams; }
+struct QkTeams {
+    int size, teams, group, share;
+    explicit QkTeams(int D) {
+        const int lanes = (D + 15) / 16;
+        size = 1;
+        while (size < lanes) size <<= 1;
+        if (32 / lanes > 32 / size) size = lanes;
+        teams = 32 / size;
+        group = group_of(teams);
+        share = share_of(teams);
+    }
+};
+
 // The backward pass cuts a token's heads, queries then keys, into chunks of equal size
-// (the last one shorter), by the number of heads and of logical tokens alone: of 8 heads,
+// (the last one shorter), by the number of heads and of groups alone: of 8 heads,
 // so that a token's angles serve many rows, or half as many and half again, down to 2,
 // while all of them still run at once (2,000 tokens of 40 heads of 128: 16.7 us in chunks
 // of 8, 17.9 in chunks of 4, which are a few warps more than fit; 46 tokens of 6 heads
@@ -42,9 +62,8 @@ struct QkChunks {
     int32_t chunks, per;             // chunks of a token, heads of a chunk
     int32_t q_slots, k_first, slots; // chunks with queries; first chunk with keys; all partial sums
     QkChunks() = default;
-    QkChunks(int32_t hq, int32_t hk, int64_t tokens) {
+    QkChunks(int32_t hq, int32_t hk, int64_t groups) {
         const int32_t all = hq + hk;
-        const int64_t groups = (tokens + kQkGroup - 1) / kQkGroup;
         int n = kChunkHeads;
         while (n > 2 && groups * ((all + n / 2 - 1) / (n / 2)) <= kBusyWarps) n >>= 1;
         chunks = (all + n - 1) / n;
@@ -55,16 +74,6 @@ struct QkChunks {
     }
 };
 
-// Lanes of a team in the backward pass: the power of two that holds D / 16 lanes.
-__host__ __device__ inline int qk_team(int D) {
-    int p = 1;
-    while (16 * p < D) p <<= 1;
-    return p;
-}
-// The 8 tokens of a group are summed in shares of as many consecutive tokens as each of
-// a warp's teams takes, from the first to the last, then the shares likewise.
-__host__ __device__ inline int qk_share(int teams) { return teams < kQkGroup ? kQkGroup / teams : 1; }
-
 struct QkWs {
     WsHeader *hdr;                   // n_rows tokens; hidden = the sizes (qk_sizes)
     int32_t *flag;                   // [N] 0 nothing, 1 in its group's partial, 2 its own sums stored
@@ -73,7 +82,7 @@ struct QkWs {
     float *spill;                    // [slots][N][D]: a token's sums
     int64_t n, groups, sizes;
     QkChunks cut;
-    int32_t D;
+    int32_t D, group, share;
 };
 
 inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(hq) << 16 | int64_t(hk) << 32; }
@@ -81,7 +90,8 @@ inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(
 struct QkWsLayout {
     int64_t off_whole, off_partial, off_spill, total;
     QkWsLayout(int64_t N, int32_t hq, int32_t hk, int64_t D) {
-        const int64_t slots = QkChunks(hq, hk, N).slots, groups = (N + kQkGroup - 1) / kQkGroup;
+        const int group = QkTeams(int(D)).group;
+        const int64_t groups = (N + group - 1) / group, slots = QkChunks(hq, hk, groups).slots;
         off_whole = align256(256 + N * 4);
         off_partial = align256(off_whole + groups * 4);
         off_spill = align256(off_partial + slots * groups * D * 4);
@@ -99,9 +109,12 @@ inline QkWs qk_ws(void *base, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     w.partial = reinterpret_cast<float *>(b + L.off_partial);
     w.spill = reinterpret_cast<float *>(b + L.off_spill);
     w.n = N;
-    w.groups = (N + kQkGroup - 1) / kQkGroup;
+    const QkTeams t{int(D)};
+    w.group = t.group;
+    w.share = t.share;
+    w.groups = (N + t.group - 1) / t.group;
     w.sizes = qk_sizes(D, hq, hk);
-    w.cut = QkChunks(hq, hk, N);
+    w.cut = QkChunks(hq, hk, w.groups);
     w.D = int32_t(D);
     return w;
 }
@@ -129,11 +142,12 @@ struct RotaryParams {
     int32_t hq, heads;               // query heads, heads of both
     int32_t chunks, per;             // chunks of a token, heads of a chunk
     int32_t lanes, team, teams;      // lanes of a head that hold columns; lanes of a team; a warp's teams
+    int32_t group, share;            // backward: tokens of a group, of a team's share of it
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
     uint32_t units;                  // warps' pieces of work
     float scale, scale_sin;          // factors of cosine and sine (negative: turns back)
     float eps, inv_d;
-    Divisor by_chunks{1}, by_team{1}, by_teams{1};
+    Divisor by_chunks{1}, by_team{1}, by_teams{1}, by_group{1};
     QkWs ws;
 };
 
@@ -682,36 +696,40 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E)
 
 // ----------------------------------------------------------------- backward of the norm and the rotation
 
-// What a warp of the backward pass does with the 8 slots [8 w, 8 w + 8) of a call and
-// one chunk of heads: the run, 8 consecutive slots that hold a whole group in logical
-// order and start among them (at most one does), and the active slots that
+// What a warp of the backward pass does with the G slots [G w, G w + G) of a call (G the
+// tokens of a group) and one chunk of heads: the run, G consecutive slots that hold a whole group in
+// logical order and start among them (at most one does), and the active slots that
 // belong to no run.  Slots of a run that starts in the window before are that
-// window's.  Lanes 0 .. 22 hold the ids and positions of slots 8 w - 7 on.
+// window's.  Lanes 0 .. 3 G - 3 hold the ids and positions of slots G w - (G - 1) on.
 struct Window {
     int32_t id, position;
     int run;                         // lane of the run's first slot, -1: none
-    uint32_t loose;                  // bit j: slot 8 w + j on its own
+    uint32_t loose;                  // bit j: slot G w + j on its own
 };
+// GROUP: G, or 0 where the kernel learns it when it runs.
+template <int GROUP>
 __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bool grads) {
-    const int lane = threadIdx.x & 31;
-    const int64_t slot = w * 8 - 7 + lane;               // lanes 7 .. 14 are the window, 21 the last slot of its run
-    const bool in = lane < 23 && slot >= 0 && slot < p.n_tokens;
+    const int lane = threadIdx.x & 31, G = GROUP ? GROUP : p.group;
+    const uint32_t mine = (1u << G) - 1u, behind = mine >> 1;        // the window's slots; the G - 1 that follow a group's first
+    const int64_t slot = w * G - (G - 1) + lane;         // lanes G - 1 .. 2 G - 2 are the window
+    const bool in = lane < 3 * G - 2 && slot >= 0 && slot < p.n_tokens;
     Window r;
     r.id = in ? p.tok_id[slot] : -1;
     r.position = in ? p.position[slot] : 0;
     r.run = -1;
     if (!grads) {
-        r.loose = (__ballot_sync(kFull, r.id >= 0) >> 7) & 0xffu;
+        r.loose = (__ballot_sync(kFull, r.id >= 0) >> (G - 1)) & mine;
         return r;
     }
     const int32_t before = __shfl_up_sync(kFull, r.id, 1);
-    const uint32_t begins = __ballot_sync(kFull, r.id >= 0 && (r.id & 7) == 0 && int64_t(r.id) + 8 <= p.ws.n);
-    const uint32_t follows = __ballot_sync(kFull, lane > 0 && r.id > 0 && (r.id & 7) != 0 && r.id == before + 1);
-    // run from lane s: begins at s and follows at s + 1 .. s + 7
-    const int s = lane - (r.id & 7);
-    const bool whole = r.id >= 0 && s >= 0 && s + 7 < 23 && ((begins >> s) & 1) && ((follows >> (s + 1)) & 0x7f) == 0x7f;
-    const uint32_t starts = __ballot_sync(kFull, whole && (r.id & 7) == 0) & 0x7f80u;
-    r.loose = (__ballot_sync(kFull, r.id >= 0 && !whole) >> 7) & 0xffu;
+    const int nth = r.id < 0 ? 0 : r.id - int(GROUP ? uint32_t(r.id) / uint32_t(G) : p.by_group.quotient(uint32_t(r.id))) * G;   // of its group
+    const uint32_t begins = __ballot_sync(kFull, r.id >= 0 && nth == 0 && int64_t(r.id) + G <= p.ws.n);
+    const uint32_t follows = __ballot_sync(kFull, lane > 0 && r.id > 0 && nth != 0 && r.id == before + 1);
+    // run from lane s: begins at s and follows at s + 1 .. s + G - 1
+    const int s = lane - nth;
+    const bool whole = r.id >= 0 && s >= 0 && s + G <= 3 * G - 2 && ((begins >> s) & 1) && ((follows >> (s + 1)) & behind) == behind;
+    const uint32_t starts = __ballot_sync(kFull, whole && nth == 0) & (mine << (G - 1));
+    r.loose = (__ballot_sync(kFull, r.id >= 0 && !whole) >> (G - 1)) & mine;
     if (starts) r.run = __ffs(starts) - 1;
     return r;
 }
@@ -740,36 +758,40 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
     const int chunk = int((in ? unit : 0) - win * uint32_t(p.chunks));
     const bool grads = p.ws.hdr && qk_header_ok(p.ws);
     if (p.ws.hdr && !grads && unit == 0 && lane32 == 0) qk_report(p.ws, kStHeader);
-    Window wd = window_of(p, win, grads);
+    constexpr int kTeams = TEAM ? 32 / (TEAM ? TEAM : 1) : 1;
+    const int size = TEAM ? TEAM : p.team, teams = TEAM ? kTeams : p.teams;
+    const int G = TEAM ? group_of(kTeams) : p.group, share = TEAM ? share_of(kTeams) : p.share;
+    Window wd = window_of<TEAM ? group_of(kTeams) : 0>(p, win, grads);
     if (!in) {
         wd.run = -1;
         wd.loose = 0;
     }
 
-    const int size = TEAM ? TEAM : p.team, lane = lane32 & (size - 1), team = lane32 / size, teams = 32 / size;
-    const int share = qk_share(teams);
+    const int team = TEAM ? lane32 / (TEAM ? TEAM : 1) : int(p.by_team.quotient(lane32)), lane = lane32 - team * size;
     stage_weights<E, PAIRS>(shared, p, size);
-    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
+    if (team >= teams) col = {{-1, -1}, 0};              // lanes that are left over
     const int head0 = chunk * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
-    const int in_run = wd.run >= 0 ? kQkGroup : 0, loose = __popc(wd.loose);
-    const int run_steps = in_run ? share : 0, steps = run_steps + (loose + teams - 1) / teams;
+    const int loose = __popc(wd.loose), run_steps = wd.run >= 0 ? share : 0;
+    const int steps = run_steps + (TEAM ? (loose + kTeams - 1) / kTeams : int(p.by_teams.quotient(loose + teams - 1)));
 
     using R = Ring<E, 2>;
     const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
     uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + kWeightBytes + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? kSplitBytes : 0));
     const uint32_t ring = smem_addr(mine) + lane32 * 16;
-    // [kinds][teams][D]: each team's sums over its tokens of the run; a lane has its own columns
+    // [kinds][teams][D]: each team's sums over its share of the run; a lane has its own columns
     float *const sums = reinterpret_cast<float *>(mine + R::kBytes);
     float *const row = reinterpret_cast<float *>(mine + R::kBytes + sums_bytes) + team * p.D;
 
     // Lane (of the window's ids) of this team's slot in a step, -1: none.
     auto place = [&](int step) {
-        if (step < run_steps) return team * share < kQkGroup ? wd.run + team * share + step : -1;
+        if (team >= teams) return -1;
+        if (step < run_steps) return team * share < G ? wd.run + team * share + step : -1;
         const int t = (step - run_steps) * teams + team;
         if (t >= loose) return -1;
         uint32_t m = wd.loose;
         for (int i = t; i > 0; --i) m &= m - 1;
-        return 6 + __ffs(m);
+        return G - 2 + __ffs(m);
     };
     // The copies of the next row: one commit a row.  A row's address follows from the
     // one before but for the first of each kind of a token.
@@ -785,7 +807,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
             if (f_head == head0 || f_head == p.hq) {
                 const int at = place(f_step);
                 f_on = at >= 0;
-                const int64_t slot = f_on ? int64_t(win) * 8 - 7 + at : 0;
+                const int64_t slot = f_on ? int64_t(win) * G - (G - 1) + at : 0;
                 const int h = keys ? f_head - p.hq : f_head;
                 f_x = static_cast<const E *>(s.in) + (slot * s.in_t + h * s.in_h);
                 f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
@@ -819,9 +841,9 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0, run = step < run_steps;
-        const int64_t slot = on ? int64_t(win) * 8 - 7 + at : 0;
+        const int64_t slot = on ? int64_t(win) * G - (G - 1) + at : 0;
         const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
-        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, size, col, a);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), team < teams ? lane : p.rot, size, col, a);
         if constexpr (PAIRS == kSplit) split_factors(a, col, p, 0, lane);
         const bool known = int64_t(id) < p.ws.n;
         if (grads && on && chunk == 0 && lane == 0) {
@@ -899,9 +921,10 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
             }
         }
     }
-    if (grads && in_run) {
+    if (grads && run_steps) {
         __syncwarp();
-        const int64_t g = __shfl_sync(kFull, wd.id, wd.run) >> 3;
+        const uint32_t begins = uint32_t(__shfl_sync(kFull, wd.id, wd.run));
+        const int64_t g = TEAM ? begins / uint32_t(G) : p.by_group.quotient(begins);
         if (chunk == 0 && lane32 == 0) p.ws.whole[g] = 1;
         for (int keys = head0 < p.hq ? 0 : 1; keys < 2; ++keys) {
             if (keys && end <= p.hq) break;
@@ -910,7 +933,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
             float *dst = p.ws.partial + (part * p.ws.groups + g) * p.D;
             for (int k = lane32 * 4; k < p.D; k += 128) {
                 float4 v = *reinterpret_cast<const float4 *>(src + k);
-                for (int t = 1; t * share < kQkGroup; ++t) {
+                for (int t = 1; t * share < G; ++t) {
                     const float4 u = *reinterpret_cast<const float4 *>(src + t * p.D + k);
                     v = make_float4(__fadd_rn(v.x, u.x), __fadd_rn(v.y, u.y), __fadd_rn(v.z, u.z), __fadd_rn(v.w, u.w));
                 }

@@ -4,6 +4,12 @@
 
 namespace rbi {
 
+inline void set_teams(RotaryParams &p) {
+    p.by_team = Divisor(uint32_t(p.team));
+    p.teams = 32 / p.team;
+    p.by_teams = Divisor(uint32_t(p.teams));
+}
+
 template <class E, int PAIRS, bool NORM, int TEAM>
 static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     auto kern = rotary_kernel<E, PAIRS, NORM, TEAM>;
@@ -12,9 +18,7 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
-    p.by_team = Divisor(uint32_t(p.team));
-    p.teams = 32 / p.team;
-    p.by_teams = Divisor(uint32_t(p.teams));
+    set_teams(p);
     // Heads of a warp: 8, so that a token's angles serve many rows, or half as many and half
     // again while there are fewer warps than fit (one token of 40 heads of 128: rotation
     // 4.0 -> 2.6 us, norm and rotation 5.7 -> 3.5; with twice that many warps as the aim
@@ -50,11 +54,17 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
-    const QkChunks cut = p.ws.hdr ? p.ws.cut : QkChunks(p.hq, p.heads - p.hq, p.n_tokens);
+    set_teams(p);
+    const QkTeams t(p.D);
+    p.group = t.group;
+    p.share = t.share;
+    p.by_group = Divisor(uint32_t(t.group));
+    const int64_t windows = (p.n_tokens + t.group - 1) / t.group;
+    const QkChunks cut = p.ws.hdr ? p.ws.cut : QkChunks(p.hq, p.heads - p.hq, windows);
     p.chunks = cut.chunks;
     p.per = cut.per;
     p.by_chunks = Divisor(uint32_t(p.chunks));
-    p.units = uint32_t((p.n_tokens + kQkGroup - 1) / kQkGroup * p.chunks);
+    p.units = uint32_t(windows * p.chunks);
     const bool straddles = p.hq % p.per != 0 && p.heads > p.hq;
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
            qk_bwd_smem(Ring<E, 2>::kBytes, PAIRS == kSplit, p.ws.hdr != nullptr, straddles), stream>>>(p, straddles);
@@ -70,26 +80,19 @@ static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
         p.team = PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
         return rotary_launch_fwd<E, PAIRS, false, 0>(p, stream);
     }
-    p.team = qk_team(p.D);
-    if (mode == 1) {
-        // Forward, teams of just the lanes that a head needs where a warp then holds more of them (5 lanes
-        // for 80 columns, 6 for 96, 10 for 160): bf16, 32+8 heads of 80, 33,384 tokens, 95 -> 75 us; of 160,
-        // 17,620 tokens, 101 -> 75; of 96 54 -> 48; of 48 31.6 -> 32.2; FP32 heads of 72 33 -> 27.
-        if (32 / p.lanes > 32 / p.team) p.team = p.lanes;
-        switch (p.team) {
-            case 4: return rotary_launch_fwd<E, PAIRS, true, 4>(p, stream);
-            case 5: return rotary_launch_fwd<E, PAIRS, true, 5>(p, stream);
-            case 6: return rotary_launch_fwd<E, PAIRS, true, 6>(p, stream);
-            case 8: return rotary_launch_fwd<E, PAIRS, true, 8>(p, stream);
-            case 16: return rotary_launch_fwd<E, PAIRS, true, 16>(p, stream);
-            default: return rotary_launch_fwd<E, PAIRS, true, 0>(p, stream);
-        }
-    }
+    // Teams of just the lanes that a head needs where a warp then holds more of them (5 lanes for 80 columns, 6
+    // for 96, 10 for 160).  Forward, bf16, 32+8 heads of 80, 33,384 tokens: 95 -> 75 us; of 160, 17,620 tokens,
+    // 101 -> 75; of 96 54 -> 48; of 48 31.6 -> 32.2; FP32 heads of 72 33 -> 27.  Backward, heads of 80: 166 -> 138;
+    // of 160 170 -> 147; of 96, 17,620 tokens, 97 -> 87; of 48 62 -> 60.
+    p.team = QkTeams(p.D).size;
+    const bool fwd = mode == 1;
     switch (p.team) {
-        case 4: return rotary_launch_bwd<E, PAIRS, 4>(p, stream);
-        case 8: return rotary_launch_bwd<E, PAIRS, 8>(p, stream);
-        case 16: return rotary_launch_bwd<E, PAIRS, 16>(p, stream);
-        default: return rotary_launch_bwd<E, PAIRS, 0>(p, stream);
+        case 4: return fwd ? rotary_launch_fwd<E, PAIRS, true, 4>(p, stream) : rotary_launch_bwd<E, PAIRS, 4>(p, stream);
+        case 5: return fwd ? rotary_launch_fwd<E, PAIRS, true, 5>(p, stream) : rotary_launch_bwd<E, PAIRS, 5>(p, stream);
+        case 6: return fwd ? rotary_launch_fwd<E, PAIRS, true, 6>(p, stream) : rotary_launch_bwd<E, PAIRS, 6>(p, stream);
+        case 8: return fwd ? rotary_launch_fwd<E, PAIRS, true, 8>(p, stream) : rotary_launch_bwd<E, PAIRS, 8>(p, stream);
+        case 16: return fwd ? rotary_launch_fwd<E, PAIRS, true, 16>(p, stream) : rotary_launch_bwd<E, PAIRS, 16>(p, stream);
+        default: return fwd ? rotary_launch_fwd<E, PAIRS, true, 0>(p, stream) : rotary_launch_bwd<E, PAIRS, 0>(p, stream);
     }
 }
 

@@ -100,7 +100,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    8 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 up
+    10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 up
     to 256 groups), 2 steps between the shares of a warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
@@ -118,7 +118,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 8 + x.shape[1] + 1 + max((n + 4095) // 4096, 4) + 2 + 24
+    chain = 8 + 10 + x.shape[1] + 1 + max(n // (512 * 5) + 1, 4) + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -135,14 +135,18 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
     n, hq, D = q_leaf.shape
     heads = hq + k_leaf.shape[1]
     leaf = np.concatenate([q_leaf, k_leaf], 1).astype(np.float32)
-    groups = (n + 7) // 8
+    lanes = (D + 15) // 16                                            # of a head; teams are of these or the next power of two
+    size = 1 << (lanes - 1).bit_length()
+    size = lanes if 32 // lanes > 32 // size else size
+    teams = 32 // size
+    group = 8 if teams > 10 else teams if teams >= 5 else 8 // teams * teams
+    tokens = max(1, group // teams)                                   # of a group, added up by one team
+    groups = -(-n // group)
     most = 8
     while most > 2 and groups * -(-heads // (most // 2)) <= 2432:
         most //= 2
     chunks = -(-heads // most)
     per = (heads + chunks - 1) // chunks
-    team = 1 << max(0, int(np.ceil(np.log2(D / 16))))
-    tokens = max(1, 8 // (32 // team))                                # of a group, added up by one team
     ctas = 8 if groups > 256 else 1
     shares = ctas * 16 * 4
     share = (groups + shares - 1) // shares
@@ -156,9 +160,9 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
                 if not len(mine):
                     continue
                 u = None
-                for first in range(8 * g, min(8 * g + 8, n), tokens):
+                for first in range(group * g, min(group * g + group, n), tokens):
                     part = None
-                    for t in range(first, min(first + tokens, n, 8 * g + 8)):
+                    for t in range(first, min(first + tokens, n)):
                         s = np.zeros(D, np.float32)
                         for h in mine:
                             s = s + leaf[t, h]

@@ -68,7 +68,8 @@ def test_rows_of_large_calls_are_those_of_small_ones(n, hq, hk, D, rot, first, i
 
 
 @pytest.mark.parametrize("hq,hk,D,rot,inter,dtype", [(32, 8, 128, 128, False, BF), (3, 1, 64, 64, True, BF), (10, 1, 256, 128, False, FP16),
-                                                     (1, 1, 80, 20, False, F32), (6, 2, 24, 24, True, BF)],
+                                                     (1, 1, 80, 20, False, F32), (6, 2, 24, 24, True, BF), (32, 8, 80, 80, False, BF),
+                                                     (4, 1, 160, 160, True, FP16), (8, 2, 48, 40, False, BF), (5, 1, 96, 96, True, F32)],
                          ids=lambda v: str(v).replace("torch.", ""))
 def test_gradients_of_many_tokens_in_every_layout(hq, hk, D, rot, inter, dtype):
     lengths = np.asarray([4099, 17, 3500, 1, 8, 5003, 260])
