@@ -221,8 +221,8 @@ def _new(like, stream):
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
-def _outputs(c, q, k, q_out, k_out, names, stream):
-    """Outputs that the caller did not bring."""
+def _outputs(q, k, q_out, k_out, names, stream):
+    """Outputs that the caller did not bring (called where one is missing, or is there without its input)."""
     if k is None:
         if k_out is not None:
             raise ValueError(f"{names[1]}: only with the keys")
@@ -233,25 +233,29 @@ def _outputs(c, q, k, q_out, k_out, names, stream):
     return _new(q, stream) if q_out is None else q_out, k_out
 
 
-def _rotate(fn: str, q, k, lay, position, rotary, q_out, k_out, names, stream):
-    c = _Call(q, names[0], lay, stream)
-    q_out, k_out = _outputs(c, q, k, q_out, k_out, (names[1], names[3]), stream)
-    rc = getattr(_rb._load(), fn)(c.side(q, names[0], q_out, names[2]), c.side(k, names[1], k_out, names[3]), c.D, c.code,
-                                  c.layout(), c.rotary(rotary, position), c.stream)
-    if rc:
-        _rb._check(rc, fn)
-    return q_out, k_out
-
-
 def rotary_fwd(q, k, lay, position, rotary: Rotary, q_out=None, k_out=None, stream=None):
     """Turns the heads of q and k (None: q alone) by their tokens' positions; position: int32, one per token slot.
     Returns (q_out, k_out); in place (q_out is q) only the rotated columns are touched."""
-    return _rotate("rotary_fwd", q, k, lay, position, rotary, q_out, k_out, ("q", "k", "q_out", "k_out"), stream)
+    c = _Call(q, "q", lay, stream)
+    if q_out is None or (k_out is None) != (k is None):
+        q_out, k_out = _outputs(q, k, q_out, k_out, ("k", "k_out"), stream)
+    rc = _rb._load().rotary_fwd(c.side(q, "q", q_out, "q_out"), c.side(k, "k", k_out, "k_out"), c.D, c.code, c.layout(),
+                                c.rotary(rotary, position), c.stream)
+    if rc:
+        _rb._check(rc, "rotary_fwd")
+    return q_out, k_out
 
 
 def rotary_bwd(dq_out, dk_out, lay, position, rotary: Rotary, dq=None, dk=None, stream=None):
     """Gradients of rotary_fwd's inputs from those of its outputs: the heads turned back (times scale)."""
-    return _rotate("rotary_bwd", dq_out, dk_out, lay, position, rotary, dq, dk, ("dq_out", "dk_out", "dq", "dk"), stream)
+    c = _Call(dq_out, "dq_out", lay, stream)
+    if dq is None or (dk is None) != (dk_out is None):
+        dq, dk = _outputs(dq_out, dk_out, dq, dk, ("dk_out", "dk"), stream)
+    rc = _rb._load().rotary_bwd(c.side(dq_out, "dq_out", dq, "dq"), c.side(dk_out, "dk_out", dk, "dk"), c.D, c.code, c.layout(),
+                                c.rotary(rotary, position), c.stream)
+    if rc:
+        _rb._check(rc, "rotary_bwd")
+    return dq, dk
 
 
 def qk_norm_rotary_fwd(q, k, q_weight, k_weight, lay, position, rotary: Rotary, eps: float, q_out=None, k_out=None,
@@ -261,7 +265,8 @@ def qk_norm_rotary_fwd(q, k, q_weight, k_weight, lay, position, rotary: Rotary, 
     c = _Call(q, "q", lay, stream)
     if k is None and k_weight is not None:
         raise ValueError("k_weight: only with the keys")
-    q_out, k_out = _outputs(c, q, k, q_out, k_out, ("k", "k_out"), stream)
+    if q_out is None or (k_out is None) != (k is None):
+        q_out, k_out = _outputs(q, k, q_out, k_out, ("k", "k_out"), stream)
     qw, kw, param = c.weights(q_weight, k_weight)
     rc = _rb._load().qk_norm_rotary_fwd(c.side(q, "q", q_out, "q_out", w=qw), c.side(k, "k", k_out, "k_out", w=kw), c.D, eps,
                                         c.code, param, c.layout(), c.rotary(rotary, position), c.stream)
@@ -277,7 +282,8 @@ def qk_norm_rotary_bwd(q, k, q_weight, k_weight, dq_out, dk_out, lay, position, 
     c = _Call(q, "q", lay, stream)
     if k is None and (dk_out is not None or k_weight is not None):
         raise ValueError("dk_out and k_weight: only with the keys")
-    dq, dk = _outputs(c, q, k, dq, dk, ("k", "dk"), stream)
+    if dq is None or (dk is None) != (k is None):
+        dq, dk = _outputs(q, k, dq, dk, ("k", "dk"), stream)
     qw, kw, param = c.weights(q_weight, k_weight)
     qs = c.side(q, "q", dq, "dq", dq_out, "dq_out", qw)
     ks = c.side(k, "k", dk, "dk", dk_out, "dk_out", kw)
