@@ -23,7 +23,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-f
 SOURCES = ["rmsnorm_bi.cu", "rows_fwd.cu", "rows_dx.cu", "rows_dxdw.cu", "rows_adddxdw.cu", "gemm_dw.cu",
            "layernorm.cu", "ln_rows_bf16.cu", "ln_rows_fp16.cu", "ln_rows_fp32.cu",
            "ln_narrow_bf16.cu", "ln_narrow_fp16.cu", "ln_narrow_fp32.cu",
-           "rotary.cu", *(f"rotary_{pairs}_{t}.cu" for pairs in ("half", "near", "split") for t in ("bf16", "fp16", "fp32")),
+           "rotary.cu", *(f"rotary_{pairs}_{t}.cu" for pairs in ("half", "near", "quad", "split") for t in ("bf16", "fp16", "fp32")),
            "rotary_turns.cpp", "plan.cpp"]
 
 

@@ -87,8 +87,9 @@ int ws_check(const void *ws, int64_t N, int32_t hq, int32_t hk, int64_t D) {
 template <class E>
 int run(const RotaryParams &p, int mode, bool interleaved, cudaStream_t s) {
     if (interleaved) return rotary_run_pairs<E, kNear>(p, mode, s);
-    // halves of whole vectors, or not
-    return p.first % 8 == 0 && p.rot % 16 == 0 ? rotary_run_pairs<E, kHalf>(p, mode, s) : rotary_run_pairs<E, kSplit>(p, mode, s);
+    // halves of whole vectors, of whole pieces of 4 columns, or of 2
+    if (p.first % 8 == 0 && p.rot % 16 == 0) return rotary_run_pairs<E, kHalf>(p, mode, s);
+    return p.first % 4 == 0 && p.rot % 8 == 0 ? rotary_run_pairs<E, kQuad>(p, mode, s) : rotary_run_pairs<E, kSplit>(p, mode, s);
 }
 
 // mode as in rotary_run_pairs; back: turn the other way.

@@ -2,21 +2,23 @@
 // head, and their backward pass (sm_103a): what the kernels share, and the row
 // kernels.
 //
-// A head is held by a team of lanes, two vectors of 8 columns a lane.  Where the
-// halves of the rotation are made of whole vectors a lane has the two that turn into
-// each other, so the rotation needs no exchange between lanes; neighbouring pairs lie
-// inside a vector anyway; halves of other sizes fetch their partners from shared
-// memory.  A team stays with one token and walks over a chunk of its heads, queries
-// and keys alike, so the lane's cosines and sines are formed once per chunk.
+// A head is held by a team of lanes, 16 columns a lane: two vectors of 8, those that turn
+// into each other where the halves of the rotation are made of whole vectors (neighbouring
+// pairs lie inside a vector anyway), or, halves of other sizes, pieces of four or two
+// columns, as many and their partners.  So the rotation needs no exchange between lanes.
+// A team stays with one token and walks over a chunk of its heads, queries and keys
+// alike, so the lane's cosines and sines are formed once per chunk.
 //
 // What bounds it (bf16, 32+8 heads of 128, 33,384 tokens; DRAM floor at the copy rate of
 // 6.78 TB/s in brackets): memory.  Rotation 100.3 us (100.9), norm and rotation 104 (100.9),
 // backward 157 and, with both weight gradients from begin to finalize, 168 (151.4).  FP32,
 // 17,620 tokens: 117, 117 (106.5), 192 (159.8).  Fewer rows for a token's angles and a
 // warp's start, or idle lanes, make it issue: 1+1 heads of 128, 270,100 tokens, 51 and 64
-// (41.1), backward 152 (61.5); heads of 80, backward, 138 (94.6).  Split halves
-// pay for their exchange: heads of 96 with 68 columns turning, rotation 33 (22.3); of 128 with
-// 104, backward 48 (20.1).
+// (41.1), backward 152 (61.5); heads of 80, backward, 138 (94.6).  Pieces
+// pay for their way through shared memory, about 60 instructions a row of a warp more: 16+16
+// heads of 72 that turn whole, 17,620 tokens, 35 and 43 (24.0), backward 73 (36.0); 32+8 heads of
+// 120, 57 and 63 (49.9), 113 (74.9).  (Vectors that take each partner's value from where its
+// lane's copy arrived, with two factors a column: 45, 49, 92; 80, 83, 141.)
 #pragma once
 #include <type_traits>
 
@@ -144,6 +146,9 @@ struct RotaryParams {
     int32_t lanes, team, teams;      // lanes of a head that hold columns; lanes of a team; a warp's teams
     int32_t group, share;            // backward: tokens of a group, of a team's share of it
     int32_t params_f32, in_place;    // in_place: columns outside the rotation are already where they belong
+    // in pieces: vectors that come and go; bytes between teams' places; pieces of a lane (and their partners) that may
+    // turn; 1: all columns are taken as pieces (with the norm)
+    int32_t vector0, vectors, pitch, turning, all_pieces;
     uint32_t units;                  // warps' pieces of work
     float scale, scale_sin;          // factors of cosine and sine (negative: turns back)
     float eps, inv_d;
@@ -154,20 +159,56 @@ struct RotaryParams {
 // ----------------------------------------------------------------- a lane's columns
 
 // Which columns turn into each other.  kHalf: halves made of whole vectors; kNear:
-// neighbouring columns; kSplit: halves that begin or end inside a vector.
-enum { kHalf = 0, kNear = 1, kSplit = 2 };
+// neighbouring columns; kQuad: halves that begin and end on multiples of 4 columns (whole
+// heads of 72, 88, 120); kSplit: others.
+enum { kHalf = 0, kNear = 1, kQuad = 2, kSplit = 3 };
+__host__ __device__ constexpr bool in_pieces(int pairs) { return pairs >= kQuad; }
+// Register pairs (of columns) of a piece.
+__host__ __device__ constexpr int piece_pairs(int pairs) { return pairs == kQuad ? 2 : 1; }
 
-template <int PAIRS>
-struct LaneColumns {
+struct VectorColumns {
     int32_t at[2];                   // first columns of the lane's vectors, -1: none
     uint32_t turned;                 // bit i: register pair i (0..3 first vector, 4..7 second) turns
 };
+// In pieces: those of the second half of the list are what the first turn into.  Rows come and
+// go as vectors of 8 columns like the others', through a place of the team's in shared memory,
+// where lanes next to each other take pieces next to each other.  Pieces that do not
+// turn are not taken by the rotation alone.
+template <int PAIRS>
+struct PieceColumns {
+    static constexpr int kPairs = piece_pairs(PAIRS), kPieces = 8 / kPairs, kHalf = kPieces / 2;
+    int32_t at[kPieces];             // first columns of the pieces, -1: none
+    int32_t vector[2];               // vectors that the lane brings and stores, -1: none
+    uint32_t turned;                 // as above
+};
+template <int PAIRS>
+using LaneColumns = std::conditional_t<in_pieces(PAIRS), PieceColumns<PAIRS>, VectorColumns>;
 
 template <int PAIRS>
-__device__ __forceinline__ LaneColumns<PAIRS> lane_columns(int lane, const RotaryParams &p) {
+__device__ __forceinline__ LaneColumns<PAIRS> lane_columns(int lane, int size, const RotaryParams &p) {
     LaneColumns<PAIRS> c;
     const int rest = p.D - p.rot;
-    if constexpr (PAIRS == kHalf) {
+    if constexpr (in_pieces(PAIRS)) {
+        using C = PieceColumns<PAIRS>;
+        constexpr int kPiece = 2 * C::kPairs;            // columns
+        const int turning = p.rot / (2 * kPiece), others = p.all_pieces ? rest / (2 * kPiece) : 0;
+        c.turned = 0;
+#pragma unroll
+        for (int j = 0; j < C::kHalf; ++j) {
+            const int k = j * size + lane, o = kPiece * (k - turning), o2 = o + (rest >> 1);
+            if (k < turning) {
+                c.at[j] = p.first + kPiece * k;
+                c.at[C::kHalf + j] = c.at[j] + (p.rot >> 1);
+                c.turned |= (C::kPairs == 2 ? 0x33u : 0x11u) << (j * C::kPairs);
+            } else {
+                const bool there = k < turning + others;
+                c.at[j] = !there ? -1 : o < p.first ? o : o + p.rot;
+                c.at[C::kHalf + j] = !there ? -1 : o2 < p.first ? o2 : o2 + p.rot;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c.vector[j] = lane + j * size < p.vectors ? p.vector0 + lane + j * size : -1;
+    } else if constexpr (PAIRS == kHalf) {
         // first the lanes of the rotation, then those of the other columns
         const int e = 16 * lane - p.rot;
         c.turned = e < 0 ? 0xffu : 0u;
@@ -192,6 +233,15 @@ __device__ __forceinline__ LaneColumns<PAIRS> lane_columns(int lane, const Rotar
             c.turned |= t << (4 * i);
         }
     }
+    return c;
+}
+
+template <int PAIRS>
+__device__ __forceinline__ LaneColumns<PAIRS> no_columns() {
+    LaneColumns<PAIRS> c;
+    for (int32_t &at : c.at) at = -1;
+    if constexpr (in_pieces(PAIRS)) c.vector[0] = c.vector[1] = -1;
+    c.turned = 0;
     return c;
 }
 
@@ -250,13 +300,35 @@ __device__ __forceinline__ void down2(Raw<E> &r, int i, f2_t v) {
 // Both weights in shared memory, as FP32 and in the lanes' order: four columns of a team's
 // lane at [side][quad][lane], 32 lanes apart, so that a lane's reads need one address.
 constexpr int kWeightBytes = 2 * 4 * 32 * 16;
+template <class E>
+__device__ __forceinline__ f2_t two_params(const void *w, int f32, int at) {
+    if (!w) return f2_both(1.f);
+    Raw<E> r;
+    if constexpr (sizeof(E) == 2)
+        if (!f32) {
+            r.q[0].x = *reinterpret_cast<const uint32_t *>(static_cast<const E *>(w) + at);
+            return up2<E>(r, 0);
+        }
+    const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(w) + at);
+    return f2_make(v.x, v.y);
+}
 template <class E, int PAIRS>
 __device__ __forceinline__ void stage_weights(float4 *sw, const RotaryParams &p, int size) {
     const int i = threadIdx.x, side = i >= 2 * size, lane = (i - side * 2 * size) >> 1, j = i & 1;
     if (i >= 4 * size) return;                           // (a CTA has at least 128 threads)
-    const int at = lane_columns<PAIRS>(lane, p).at[j];
+    const LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, size, p);
     f2_t f[4] = {0, 0, 0, 0};                            // (columns that are not there: zeros, they enter sums)
-    if (at >= 0) oct_param<E>(p.side[side].w, p.params_f32, at >> 3, 1.f, f);
+    if constexpr (in_pieces(PAIRS)) {
+        using C = PieceColumns<PAIRS>;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+            const int at = j ? col.at[C::kHalf + l / C::kPairs] : col.at[l / C::kPairs];
+            if (at >= 0) f[l] = two_params<E>(p.side[side].w, p.params_f32, at + 2 * (l % C::kPairs));
+        }
+    } else {
+        const int at = col.at[j];
+        if (at >= 0) oct_param<E>(p.side[side].w, p.params_f32, at >> 3, 1.f, f);
+    }
     float4 *to = sw + (side * 4 + 2 * j) * 32 + lane;
     to[0] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
     to[32] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
@@ -311,63 +383,50 @@ __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turns, float 
 }
 
 // The lane's cosines and sines, times scale: kHalf of its 8 pairs in columns' order,
-// kNear likewise, 4 pairs a vector.
-template <int PAIRS>
+// kNear likewise, 4 pairs a vector; in pieces those of their columns.
 struct Angles {
     f2_t c[4], s[4];
 };
-// kSplit: few lanes may have all the rotated columns (20 of 80), and each column of theirs a
-// pair of its own, so the team forms all its token's cosines and sines in shared memory.
-// From there every column takes the factors of itself and of its partner, the sine
-// negative in first halves; with the norm in front the weights are multiplied into them.
-// The partner's value comes from where its lane's copy of the row has arrived (16 bits),
-// or from a row of the team's own (FP32).
-template <>
-struct Angles<kSplit> {
-    float *c, *s;
-    f2_t own[8], other[8];
-    int32_t from[8];                 // where the partners of register pair i are: bytes from the row's start
-};
 template <class E, int PAIRS>
 __device__ __forceinline__ void lane_angles(const RotaryParams &p, int32_t position, int lane, int size, const LaneColumns<PAIRS> &col,
-                                            Angles<PAIRS> &a) {
-    if constexpr (PAIRS == kSplit) {
-        __syncwarp();                                    // the token before is done
-        for (int k = lane; 2 * k < p.rot; k += size) {
-            float c, s;
-            cos_sin<sizeof(E) == 4>(position, p.turns[k], c, s);
-            a.c[k] = __fmul_rn(c, p.scale);
-            a.s[k] = __fmul_rn(s, p.scale_sin);
-        }
-        __syncwarp();
-    } else {
+                                            Angles &a) {
+    constexpr int kW = piece_pairs(PAIRS);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
-            if constexpr (PAIRS == kHalf) {
-                if (col.turned) {
-                    const ulonglong2 t = reinterpret_cast<const ulonglong2 *>(p.turns)[4 * lane + i];
-                    cos_sin<sizeof(E) == 4>(position, t.x, c[0], s[0]);
-                    cos_sin<sizeof(E) == 4>(position, t.y, c[1], s[1]);
-                }
-            } else {
+    for (int i = 0; i < 4; ++i) {
+        float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
+        if constexpr (PAIRS == kNear) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = 2 * i + j;             // the register pair
-                    if ((col.turned >> r) & 1)
-                        cos_sin<sizeof(E) == 4>(position, p.turns[(col.at[r >> 2] + 2 * (r & 3) - p.first) >> 1], c[j], s[j]);
-                }
+            for (int j = 0; j < 2; ++j) {
+                const int r = 2 * i + j;                 // the register pair
+                if ((col.turned >> r) & 1)
+                    cos_sin<sizeof(E) == 4>(position, p.turns[(col.at[r >> 2] + 2 * (r & 3) - p.first) >> 1], c[j], s[j]);
             }
-            a.c[i] = f2_make(__fmul_rn(c[0], p.scale), __fmul_rn(c[1], p.scale));
-            a.s[i] = f2_make(__fmul_rn(s[0], p.scale_sin), __fmul_rn(s[1], p.scale_sin));
+        } else if (PAIRS == kHalf ? col.turned != 0 : i / kW < p.turning && ((col.turned >> i) & 1)) {
+            const ulonglong2 t = reinterpret_cast<const ulonglong2 *>(p.turns)[PAIRS == kHalf ? 4 * lane + i : (i / kW * size + lane) * kW + i % kW];
+            cos_sin<sizeof(E) == 4>(position, t.x, c[0], s[0]);
+            cos_sin<sizeof(E) == 4>(position, t.y, c[1], s[1]);
         }
+        a.c[i] = f2_make(__fmul_rn(c[0], p.scale), __fmul_rn(c[1], p.scale));
+        a.s[i] = f2_make(__fmul_rn(s[0], p.scale_sin), __fmul_rn(s[1], p.scale_sin));
     }
 }
 
 // Turns the lane's columns.
-template <int PAIRS>
-__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, const LaneColumns<PAIRS> &col) {
-    if constexpr (PAIRS == kHalf) {
+template <int PAIRS, bool ALL>
+__device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles &a, const LaneColumns<PAIRS> &col, const RotaryParams &p) {
+    if constexpr (in_pieces(PAIRS)) {
+        // (pieces that do not turn have partners that do not either: they keep their values, not times 1 plus times 0, which
+        // an infinity would spoil; a lane's pieces that are not there may become anything but are not stored)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i / piece_pairs(PAIRS) >= p.turning) continue;
+            const f2_t x = f[i], y = f[4 + i], n = f2_mul(a.s[i], f2_both(-1.f));
+            const f2_t u = f2_fma(x, a.c[i], f2_mul(y, n)), v = f2_fma(y, a.c[i], f2_mul(x, a.s[i]));
+            const bool turns = !ALL || ((col.turned >> i) & 1);
+            f[i] = turns ? u : x;
+            f[4 + i] = turns ? v : y;
+        }
+    } else if constexpr (PAIRS == kHalf) {
         if (col.turned) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -382,90 +441,6 @@ __device__ __forceinline__ void turn_lane(f2_t (&f)[8], const Angles<PAIRS> &a, 
             const float x = f2_lo(f[i]), y = f2_hi(f[i]);
             const float c = i & 1 ? f2_hi(a.c[i >> 1]) : f2_lo(a.c[i >> 1]), s = i & 1 ? f2_hi(a.s[i >> 1]) : f2_lo(a.s[i >> 1]);
             if ((col.turned >> i) & 1) f[i] = f2_make(__fmaf_rn(x, c, -__fmul_rn(y, s)), __fmaf_rn(y, c, __fmul_rn(x, s)));
-        }
-    }
-}
-
-// kSplit's shared memory of a warp: the teams' rows of D floats (FP32), then their cosines
-// and sines (rot / 2 each); teams x D floats are at most 2048 bytes.
-constexpr int kSplitBytes = 4096;
-// The partner column of a rotated one.
-__device__ __forceinline__ int partner(int at, const RotaryParams &p) {
-    return at - p.first < p.rot >> 1 ? at + (p.rot >> 1) : at - (p.rot >> 1);
-}
-// The vector that holds a column: which of its lane's two, and that lane of the team.
-__device__ __forceinline__ void owner(int at, const RotaryParams &p, int &second, int &lane) {
-    lane = at >> 3;
-    second = lane >= p.lanes;
-    if (second) lane -= p.lanes;
-}
-template <class E>
-__device__ __forceinline__ void split_start(Angles<kSplit> &a, float *row, int team, int teams, int size, const LaneColumns<kSplit> &col,
-                                            const RotaryParams &p) {
-    a.c = row + (teams - team) * p.D + team * p.rot;
-    a.s = a.c + (p.rot >> 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = partner(col.at[i >> 2] + 2 * (i & 3), p);
-        int second, lane;
-        owner(at, p, second, lane);
-        a.from[i] = sizeof(E) == 4 ? at * 4 : second * 512 + (team * size + lane) * 16 + (at & 7) * 2;
-    }
-}
-// `weights`: shared-memory address of the side's weights, 0 without the norm.
-__device__ __forceinline__ void split_factors(Angles<kSplit> &a, const LaneColumns<kSplit> &col, const RotaryParams &p, uint32_t weights,
-                                              int lane) {
-    if (weights) lane_weights(weights + lane * 16, a.own);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a.other[i] = 0;
-        if ((col.turned >> i) & 1) {
-            const int at = col.at[i >> 2] + 2 * (i & 3), half = p.rot >> 1, k = at - p.first;
-            const f2_t c = *reinterpret_cast<const f2_t *>(a.c + (k < half ? k : k - half));
-            f2_t s = *reinterpret_cast<const f2_t *>(a.s + (k < half ? k : k - half));
-            if (k < half) s = f2_mul(s, f2_both(-1.f));
-            if (weights) {
-                const int to = partner(at, p);
-                int second, of;
-                owner(to, p, second, of);
-                f2_t w;
-                asm volatile("ld.shared.b64 %0, [%1];"
-                             : "=l"(w)
-                             : "r"(weights + (second * 2 + ((to & 7) >> 2)) * 512 + of * 16 + (to & 3) * 4));
-                a.own[i] = f2_mul(a.own[i], c);
-                s = f2_mul(s, w);
-            } else {
-                a.own[i] = c;
-            }
-            a.other[i] = s;
-        }
-    }
-}
-// Turns the lane's columns (and multiplies all of them with the weights, NORM).  `row`:
-// shared-memory address of the row that `from` counts from.
-template <class E, bool NORM>
-__device__ __forceinline__ void split_turn(f2_t (&f)[8], const Angles<kSplit> &a, const LaneColumns<kSplit> &col, uint32_t row) {
-    if constexpr (sizeof(E) == 4) {
-        __syncwarp();                                    // the row before has been read
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (col.at[i] >= 0) {
-                const uint32_t to = row + col.at[i] * 4;
-                asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to), "l"(f[4 * i]), "l"(f[4 * i + 1]) : "memory");
-                asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + 16), "l"(f[4 * i + 2]), "l"(f[4 * i + 3]) : "memory");
-            }
-        __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if ((col.turned >> i) & 1) {
-            Raw<E> y;
-            uint32_t *w = reinterpret_cast<uint32_t *>(y.q);
-            if constexpr (sizeof(E) == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(row + a.from[i]) : "memory");
-            else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(row + a.from[i]) : "memory");
-            f[i] = f2_fma(f[i], a.own[i], f2_mul(up2<E>(y, 0), a.other[i]));
-        } else if (NORM) {
-            f[i] = f2_mul(f[i], a.own[i]);
         }
     }
 }
@@ -525,35 +500,127 @@ __device__ __forceinline__ float qk_rstd(float ss, const RotaryParams &p) {
 constexpr int kQkWarps = 4;
 
 // 16-bit heads come through shared memory: a ring of kDepth rows a team, every lane
-// copying its own columns of TENSORS tensors to places that only it reads.  FP32 rows
+// copying its own columns of TENSORS tensors to places that only it reads (in pieces: its
+// vectors, to the team's place).  FP32 rows
 // are twice as long and stay in registers, one row ahead, by loads of 32 bytes a lane
 // (17,620 tokens, 32+8 heads of 128: forward 117 us against 175 through a ring, backward 192
-// against 269; two rows ahead: equal).  Depths measured (bf16): forward 4, 5, 6, 8 rows, heads
+// against 269; two rows ahead: equal; in pieces they go to the team's place from there).
+// Depths measured (bf16): forward 4, 5, 6, 8 rows, heads
 // of 80, 33,384 tokens: 75, 75, 77.5, 80 us, heads of 64: 58, 56.5, 56.7, 58; backward 3, 4, 5
-// rows, heads of 128: 173, 168, 168, 16+1 heads of 256: 101, 100, 111.
-template <class E, int TENSORS>
+// rows, heads of 128: 173, 168, 168, 16+1 heads of 256: 101, 100, 111.  In pieces the backward
+// pass has 3, so that 16 warps fit.
+template <class E, int TENSORS, int PAIRS>
 struct Ring {
     static constexpr bool kOn = sizeof(E) == 2;
-    static constexpr int kPieces = 2 * TENSORS;          // 16-byte pieces of a lane's row
-    static constexpr int kDepth = TENSORS == 1 ? 5 : 4;
-    static constexpr int kBytes = kOn ? kPieces * kDepth * 512 : 0;   // of a warp
+    static constexpr int kRow = in_pieces(PAIRS) ? 800 * int(sizeof(E)) : 1024;   // bytes of a warp's rows of one tensor
+    static constexpr int kDepth = !kOn ? 1 : TENSORS == 1 ? 5 : in_pieces(PAIRS) ? 3 : 4;
+    static constexpr int kBytes = kOn || in_pieces(PAIRS) ? TENSORS * kRow * kDepth : 0;   // of a warp
 };
+// In pieces: the bytes from one team's place to the next, so that the lanes of all teams find
+// a piece in different banks: the words of a team's pieces, rounded up to whole vectors, modulo the 32
+// banks, or, small teams, any odd number of 16 bytes.  At most 800 elements / teams.  Vectors
+// and pieces in words.
+inline int pieces_pitch(int vectors, int vector, int size, int teams, int piece) {
+    const int words = vectors * vector, apart = (size * piece + 3) & ~3;
+    return teams == 1 ? 4 * words : size * piece > 4 ? 4 * (words + ((apart - words) & 31)) : 4 * (words | 4);
+}
 template <class E, int PAIRS>
 __device__ __forceinline__ void copy_row(uint32_t dst, const E *row, const LaneColumns<PAIRS> &col, bool on) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) cp_async_zfill(dst + j * 512, row + (col.at[j] >= 0 ? col.at[j] : 0), on && col.at[j] >= 0 ? 16 : 0);
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (in_pieces(PAIRS)) {
+            if (col.vector[j] >= 0) cp_async_zfill(dst + col.vector[j] * 16, row + col.vector[j] * 8, on ? 16 : 0);
+        } else {
+            cp_async_zfill(dst + j * 512, row + (col.at[j] >= 0 ? col.at[j] : 0), on && col.at[j] >= 0 ? 16 : 0);
+        }
+    }
 }
 template <class E, int PAIRS>
 __device__ __forceinline__ void load_row(Raw<E> &r, const E *row, const LaneColumns<PAIRS> &col, bool on) {
     if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) load_f32x8(r.q + 2 * j, reinterpret_cast<const float *>(row) + col.at[j], on && col.at[j] >= 0);
+        for (int j = 0; j < 2; ++j) {
+            int at = col.at[j];
+            if constexpr (in_pieces(PAIRS)) at = col.vector[j] * 8;
+            load_f32x8(r.q + 2 * j, reinterpret_cast<const float *>(row) + at, on && at >= 0);
+        }
     }
 }
 template <class E>
 __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 #pragma unroll
     for (int l = 0; l < 2 * Raw<E>::kQ; ++l) ld_shared_vec(src + l * 512, r.q[l]);
+}
+// In pieces, `place`: shared-memory address of the team's column 0 (which need not be there).
+// FP32 vectors from registers to their place.
+__device__ __forceinline__ void st_shared_vec(uint32_t to, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+template <class E, int PAIRS>
+__device__ __forceinline__ void bring_row(const Raw<E> &r, uint32_t place, const LaneColumns<PAIRS> &col) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (col.vector[j] >= 0) {
+#pragma unroll
+            for (int l = 0; l < Raw<E>::kQ; ++l) st_shared_vec(place + col.vector[j] * 8 * int(sizeof(E)) + l * 16, r.q[2 * j + l]);
+        }
+}
+// ALL: also those that do not turn.
+template <class E, int PAIRS, bool ALL>
+__device__ __forceinline__ void take_pieces(Raw<E> &r, uint32_t place, const LaneColumns<PAIRS> &col, const RotaryParams &p) {
+    using C = PieceColumns<PAIRS>;
+    constexpr int kWords = C::kPairs * int(sizeof(E)) / 2;           // of a piece
+    uint32_t *w = reinterpret_cast<uint32_t *>(r.q);
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) {
+        uint32_t *v = w + i * kWords;
+#pragma unroll
+        for (int l = 0; l < kWords; ++l) v[l] = 0;
+        if (!ALL && i % C::kHalf >= p.turning) continue;
+        if (col.at[i] >= 0) {
+            const uint32_t from = place + col.at[i] * int(sizeof(E));
+            if constexpr (kWords == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(from) : "memory");
+            else if constexpr (kWords == 2) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(from) : "memory");
+            else asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(from) : "memory");
+        }
+    }
+}
+template <class E, int PAIRS, bool ALL>
+__device__ __forceinline__ void put_pieces(const Raw<E> &r, uint32_t place, const LaneColumns<PAIRS> &col, const RotaryParams &p) {
+    using C = PieceColumns<PAIRS>;
+    constexpr int kWords = C::kPairs * int(sizeof(E)) / 2;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) {
+        const uint32_t *v = w + i * kWords;
+        if (!ALL && i % C::kHalf >= p.turning) continue;
+        if (col.at[i] >= 0) {
+            const uint32_t to = place + col.at[i] * int(sizeof(E));
+            if constexpr (kWords == 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v[0]) : "memory");
+            else if constexpr (kWords == 2) asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(v[0]), "r"(v[1]) : "memory");
+            else st_shared_vec(to, make_uint4(v[0], v[1], v[2], v[3]));
+        }
+    }
+}
+// The lane's columns to memory (in pieces: the team's, by way of its place).
+template <class E, int PAIRS, bool ALL>
+__device__ __forceinline__ void store_row(E *dst, const Raw<E> &r, uint32_t place, const LaneColumns<PAIRS> &col, const RotaryParams &p, bool on) {
+    if constexpr (in_pieces(PAIRS)) {
+        put_pieces<E, PAIRS, ALL>(r, place, col, p);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (on && col.vector[j] >= 0) {
+                uint4 v[Raw<E>::kQ];
+#pragma unroll
+                for (int l = 0; l < Raw<E>::kQ; ++l) ld_shared_vec(place + col.vector[j] * 8 * int(sizeof(E)) + l * 16, v[l]);
+                store_vector<E>(dst + col.vector[j] * 8, v);
+            }
+    } else if (on) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r.q + j * Raw<E>::kQ);
+    }
 }
 
 // ----------------------------------------------------------------- forward, and rotation alone
@@ -562,12 +629,12 @@ __device__ __forceinline__ void take_row(Raw<E> &r, uint32_t src) {
 // of a call (at most 32) and one chunk of heads; its teams take the active ones in turns,
 // so padding costs a warp nothing but its ids.  CTAs an SM: with 6, the norm's 80 registers
 // are as fast on large calls and 0.3 us slower on small ones; FP32 at 4 of 128 registers takes
-// 125 us where 5 take 117; split halves spill at 5.
+// 125 us where 5 take 117; in pieces FP32 needs them (16 bits, heads of 120: 74 -> 70 us with 5).
 template <class E, int PAIRS, bool NORM, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E) == 4 || NORM ? 5 : 6)
+__global__ void __launch_bounds__(kQkWarps * 32, in_pieces(PAIRS) ? (sizeof(E) == 4 ? 4 : 5) : sizeof(E) == 4 || NORM ? 5 : 6)
     rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
     extern __shared__ float4 shared[];
-    using R = Ring<E, 1>;
+    using R = Ring<E, 1, PAIRS>;
     const int lane32 = threadIdx.x & 31, warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);   // (uniform, for the compiler)
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
     const bool in = unit < p.units;
@@ -583,11 +650,9 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E)
     if constexpr (NORM) stage_weights<E, PAIRS>(shared, p, size);
     const int team = TEAM ? lane32 / (TEAM ? TEAM : 1) : int(p.by_team.quotient(lane32)), lane = lane32 - team * size;
     const int steps = int(p.by_teams.quotient(count + teams - 1));
-    LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    if (team >= teams) col = {{-1, -1}, 0};              // lanes that are left over
-    uint8_t *place_of = reinterpret_cast<uint8_t *>(shared) + (NORM ? kWeightBytes : 0) + warp * (R::kBytes + (PAIRS == kSplit ? kSplitBytes : 0));
-    const uint32_t ring = smem_addr(place_of) + lane32 * 16;
-    float *const row = reinterpret_cast<float *>(place_of + R::kBytes) + team * p.D;
+    LaneColumns<PAIRS> col = team < teams ? lane_columns<PAIRS>(lane, size, p) : no_columns<PAIRS>();   // (lanes that are left over)
+    const uint32_t ring = smem_addr(shared) + (NORM ? kWeightBytes : 0) + warp * R::kBytes +
+                          (in_pieces(PAIRS) ? team * p.pitch - p.vector0 * 8 * int(sizeof(E)) : lane32 * 16);
 
     // Lane (of the slots' ids) of this team's slot in a step, -1: none.
     auto place = [&](int step) {
@@ -613,11 +678,11 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E)
                 f_x = static_cast<const E *>(s.in) + ((f_on ? first + at : 0) * s.in_t + (keys ? f_head - p.hq : f_head) * s.in_h);
             }
             if constexpr (R::kOn) {
-                copy_row<E>(f_dst, f_x, col, f_on);
-                f_dst += R::kPieces * 512;
+                copy_row<E, PAIRS>(f_dst, f_x, col, f_on);
+                f_dst += R::kRow;
                 if (f_dst == ring + R::kBytes) f_dst = ring;
             } else {
-                load_row<E>(next, f_x, col, f_on);
+                load_row<E, PAIRS>(next, f_x, col, f_on);
             }
             f_x += s.in_h;
             if (++f_head == end) {
@@ -631,32 +696,36 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E)
     for (int i = 0; i < (R::kOn ? R::kDepth - 1 : 1); ++i) fetch();
     if constexpr (NORM) __syncthreads();                 // the weights
 
-    Angles<PAIRS> a;
-    if constexpr (PAIRS == kSplit) split_start<E>(a, row, team, teams, size, col, p);
+    Angles a;
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0;
-        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), team < teams ? lane : p.rot, size, col, a);   // (left-over lanes form none)
-        if constexpr (PAIRS == kSplit && !NORM) split_factors(a, col, p, 0, lane);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, position, on ? at : 0), lane, size, col, a);
         for (int h = head0; h < end;) {                  // the token's heads of one kind after the other
             const bool keys = h >= p.hq;
             const int stop = keys || end < p.hq ? end : p.hq;
             const HeadsParams &s = p.side[keys];
             E *dst = static_cast<E *>(s.out) + ((on ? first + at : 0) * s.out_t + (keys ? h - p.hq : h) * s.out_h);
             const uint32_t weights = smem_addr(shared) + keys * (kWeightBytes / 2) + lane * 16;
-            if constexpr (PAIRS == kSplit && NORM) split_factors(a, col, p, weights - lane * 16, lane);
             for (; h < stop; ++h) {
                 Raw<E> r;
-                uint32_t at_row = smem_addr(row);        // kSplit: the team's row, or (16 bits) the warp's rows as they came
+                uint32_t place_of = ring;                // in pieces: where the row is
                 if constexpr (R::kOn) {
                     cp_async_wait<R::kDepth - 2>();
-                    if constexpr (PAIRS == kSplit) __syncwarp();     // everyone's; and the row before has been read
+                    if constexpr (in_pieces(PAIRS)) __syncwarp();     // everyone's; and the row before has been read
                     fetch();
-                    take_row<E>(r, from);
-                    at_row = from - lane32 * 16;
-                    from += R::kPieces * 512;
+                    if constexpr (in_pieces(PAIRS)) take_pieces<E, PAIRS, NORM>(r, from, col, p);
+                    else take_row<E>(r, from);
+                    place_of = from;
+                    from += R::kRow;
                     if (from == ring + R::kBytes) from = ring;
+                } else if constexpr (in_pieces(PAIRS)) {
+                    __syncwarp();                        // the row before has left
+                    bring_row<E, PAIRS>(next, ring, col);
+                    __syncwarp();
+                    fetch();
+                    take_pieces<E, PAIRS, NORM>(r, ring, col, p);
                 } else {
                     r = next;
                     fetch();
@@ -666,28 +735,17 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit ? 4 : sizeof(E)
                 for (int j = 0; j < 8; ++j) f[j] = up2<E>(r, j);
                 f2_t rstd = 0;
                 if constexpr (NORM) rstd = f2_both(qk_rstd(team_add<TEAM>(lane_dot(f, f), size, lane), p));
-                if constexpr (PAIRS == kSplit) {
-                    split_turn<E, NORM>(f, a, col, at_row);
+                if constexpr (NORM) {
+                    f2_t w[8];
+                    lane_weights(weights, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (NORM) f[j] = f2_mul(f[j], rstd);
-                } else {
-                    if constexpr (NORM) {
-                        f2_t w[8];
-                        lane_weights(weights, w);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
-                    }
-                    turn_lane<PAIRS>(f, a, col);
+                    for (int j = 0; j < 8; ++j) f[j] = f2_mul(f2_mul(f[j], rstd), w[j]);
                 }
+                turn_lane<PAIRS, NORM>(f, a, col, p);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (NORM || is_turned<PAIRS>(j, col)) down2<E>(r, j, f[j]);
-                if (on) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], r.q + j * Raw<E>::kQ);
-                }
+                    if (NORM || in_pieces(PAIRS) || is_turned<PAIRS>(j, col)) down2<E>(r, j, f[j]);
+                store_row<E, PAIRS, NORM>(dst, r, place_of, col, p, on);
                 dst += s.out_h;
             }
         }
@@ -734,22 +792,22 @@ __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bo
     return r;
 }
 
-inline int qk_bwd_smem(int ring_bytes, bool split, bool grads, bool straddles) {
-    // both weights, then per warp: ring, the teams' sums (of both kinds where a chunk has both), kSplit's rows; teams x D
-    // floats are at most 2048 bytes
-    return kWeightBytes + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0) + (split ? kSplitBytes : 0));
+inline int qk_bwd_smem(int ring_bytes, bool grads, bool straddles) {
+    // both weights, then per warp: ring, the teams' sums (of both kinds where a chunk has both); teams x D floats are at
+    // most 2048 bytes
+    return kWeightBytes + kQkWarps * (ring_bytes + (grads ? (straddles ? 4096 : 2048) : 0));
 }
 
 // The backward pass, for a window and a chunk of heads a warp.  Both row sums of a row (of
 // x^2 and of g w x) come from one pass over it; the weight gradients add up in registers
 // over a token's heads of one kind, in shared memory over a team's tokens of the run, and
 // leave as one partial sum a run.  It holds x, g, g w, a token's angles and the sums: 128
-// registers for 16 warps an SM (12 warps at 168 registers: 183 us where 16 take 169; split
-// halves, which would spill, and FP32 have 12).  Left on the table: about 330 instructions a
+// registers for 16 warps an SM (12 warps at 168 registers: 183 us where 16 take 169; in
+// pieces, heads of 72, 82 and 73; FP32, which would spill, has 12).  Left on the table: about 330 instructions a
 // warp for 4 rows of 128, of which some 20 % are addresses and copies.
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
 template <class E, int PAIRS, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
+__global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
     extern __shared__ float4 shared[];
     const int lane32 = threadIdx.x & 31, warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);   // (uniform, for the compiler)
     const uint32_t unit = blockIdx.x * kQkWarps + warp;
@@ -769,19 +827,17 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
 
     const int team = TEAM ? lane32 / (TEAM ? TEAM : 1) : int(p.by_team.quotient(lane32)), lane = lane32 - team * size;
     stage_weights<E, PAIRS>(shared, p, size);
-    LaneColumns<PAIRS> col = lane_columns<PAIRS>(lane, p);
-    if (team >= teams) col = {{-1, -1}, 0};              // lanes that are left over
+    LaneColumns<PAIRS> col = team < teams ? lane_columns<PAIRS>(lane, size, p) : no_columns<PAIRS>();   // (lanes that are left over)
     const int head0 = chunk * p.per, end = p.heads - head0 < p.per ? p.heads : head0 + p.per;
     const int loose = __popc(wd.loose), run_steps = wd.run >= 0 ? share : 0;
     const int steps = run_steps + (TEAM ? (loose + kTeams - 1) / kTeams : int(p.by_teams.quotient(loose + teams - 1)));
 
-    using R = Ring<E, 2>;
+    using R = Ring<E, 2, PAIRS>;
     const int sums_bytes = p.ws.hdr ? (straddles ? 4096 : 2048) : 0;
-    uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + kWeightBytes + warp * (R::kBytes + sums_bytes + (PAIRS == kSplit ? kSplitBytes : 0));
-    const uint32_t ring = smem_addr(mine) + lane32 * 16;
+    uint8_t *mine = reinterpret_cast<uint8_t *>(shared) + kWeightBytes + warp * (R::kBytes + sums_bytes);
+    const uint32_t ring = smem_addr(mine) + (in_pieces(PAIRS) ? team * p.pitch - p.vector0 * 8 * int(sizeof(E)) : lane32 * 16);
     // [kinds][teams][D]: each team's sums over its share of the run; a lane has its own columns
     float *const sums = reinterpret_cast<float *>(mine + R::kBytes);
-    float *const row = reinterpret_cast<float *>(mine + R::kBytes + sums_bytes) + team * p.D;
 
     // Lane (of the window's ids) of this team's slot in a step, -1: none.
     auto place = [&](int step) {
@@ -813,13 +869,13 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
                 f_g = static_cast<const E *>(s.dy) + (slot * s.dy_t + h * s.dy_h);
             }
             if constexpr (R::kOn) {
-                copy_row<E>(f_dst, f_x, col, f_on);
-                copy_row<E>(f_dst + 1024, f_g, col, f_on);
-                f_dst += R::kPieces * 512;
+                copy_row<E, PAIRS>(f_dst, f_x, col, f_on);
+                copy_row<E, PAIRS>(f_dst + R::kRow, f_g, col, f_on);
+                f_dst += 2 * R::kRow;
                 if (f_dst == ring + R::kBytes) f_dst = ring;
             } else {
-                load_row<E>(next_x, f_x, col, f_on);
-                load_row<E>(next_g, f_g, col, f_on);
+                load_row<E, PAIRS>(next_x, f_x, col, f_on);
+                load_row<E, PAIRS>(next_g, f_g, col, f_on);
             }
             f_x += s.in_h;
             f_g += s.dy_h;
@@ -835,16 +891,14 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
     __syncthreads();                                     // the weights
     if (steps == 0) return;
 
-    Angles<PAIRS> a;
-    if constexpr (PAIRS == kSplit) split_start<E>(a, row, team, teams, size, col, p);
+    Angles a;
     uint32_t from = ring;
     for (int step = 0; step < steps; ++step) {
         const int at = place(step);
         const bool on = at >= 0, run = step < run_steps;
         const int64_t slot = on ? int64_t(win) * G - (G - 1) + at : 0;
         const int32_t id = __shfl_sync(kFull, wd.id, on ? at : 0);
-        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), team < teams ? lane : p.rot, size, col, a);
-        if constexpr (PAIRS == kSplit) split_factors(a, col, p, 0, lane);
+        lane_angles<E, PAIRS>(p, __shfl_sync(kFull, wd.position, on ? at : 0), lane, size, col, a);
         const bool known = int64_t(id) < p.ws.n;
         if (grads && on && chunk == 0 && lane == 0) {
             const int bad = known ? (atomicExch(p.ws.flag + id, run ? 1 : 2) ? kStDouble : 0) : kStPlan;
@@ -862,16 +916,29 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
             for (int j = 0; j < 8; ++j) acc[j] = f2_make(0.f, 0.f);
             for (; h < stop; ++h) {
                 Raw<E> rx, rg;
-                uint32_t at_row = smem_addr(row);
+                uint32_t place_of = ring;                // in pieces: where the row is
                 if constexpr (R::kOn) {
                     cp_async_wait<R::kDepth - 2>();
-                    if constexpr (PAIRS == kSplit) __syncwarp();
+                    if constexpr (in_pieces(PAIRS)) __syncwarp();
                     fetch();
-                    take_row<E>(rx, from);
-                    take_row<E>(rg, from + 1024);
-                    at_row = from + 1024 - lane32 * 16;
-                    from += R::kPieces * 512;
+                    if constexpr (in_pieces(PAIRS)) {
+                        take_pieces<E, PAIRS, true>(rx, from, col, p);
+                        take_pieces<E, PAIRS, true>(rg, from + R::kRow, col, p);
+                    } else {
+                        take_row<E>(rx, from);
+                        take_row<E>(rg, from + R::kRow);
+                    }
+                    place_of = from;
+                    from += 2 * R::kRow;
                     if (from == ring + R::kBytes) from = ring;
+                } else if constexpr (in_pieces(PAIRS)) {
+                    __syncwarp();                        // the row before has left
+                    bring_row<E, PAIRS>(next_x, ring, col);
+                    bring_row<E, PAIRS>(next_g, ring + R::kRow, col);
+                    __syncwarp();
+                    fetch();
+                    take_pieces<E, PAIRS, true>(rx, ring, col, p);
+                    take_pieces<E, PAIRS, true>(rg, ring + R::kRow, col, p);
                 } else {
                     rx = next_x;
                     rg = next_g;
@@ -883,8 +950,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
                     x[j] = up2<E>(rx, j);
                     g[j] = up2<E>(rg, j);
                 }
-                if constexpr (PAIRS == kSplit) split_turn<E, false>(g, a, col, at_row);
-                else turn_lane<PAIRS>(g, a, col);
+                turn_lane<PAIRS, true>(g, a, col, p);
                 lane_weights(weights, b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[j] = f2_mul(g[j], b[j]);
@@ -896,18 +962,20 @@ __global__ void __launch_bounds__(kQkWarps * 32, PAIRS == kSplit || sizeof(E) ==
                     acc[j] = f2_fma(g[j], x[j], acc[j]);
                     down2<E>(rx, j, f2_mul(f2_fma(x[j], f2_both(-m), b[j]), f2_both(rstd)));
                 }
-                if (on) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (col.at[j] >= 0) store_vector<E>(dst + col.at[j], rx.q + j * Raw<E>::kQ);
-                }
+                store_row<E, PAIRS, true>(dst, rx, place_of, col, p, on);
                 dst += s.out_h;
             }
             if (grads && on && (run || known)) {
                 const int64_t part = keys ? p.ws.cut.q_slots + chunk - p.ws.cut.k_first : chunk;
                 float *to = run ? sums + ((keys && straddles ? teams : 0) + team) * p.D : p.ws.spill + (part * p.ws.n + id) * p.D;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < (in_pieces(PAIRS) ? 8 : 0); ++j)
+                    if (col.at[j / piece_pairs(PAIRS)] >= 0) {
+                        f2_t *q = reinterpret_cast<f2_t *>(to + col.at[j / piece_pairs(PAIRS)] + 2 * (j % piece_pairs(PAIRS)));
+                        *q = run && step > 0 ? f2_add(*q, acc[j]) : acc[j];
+                    }
+#pragma unroll
+                for (int j = 0; j < (in_pieces(PAIRS) ? 0 : 2); ++j)
                     if (col.at[j] >= 0) {
                         ulonglong2 *q = reinterpret_cast<ulonglong2 *>(to + col.at[j]);
                         ulonglong2 u = make_ulonglong2(acc[4 * j], acc[4 * j + 1]), v = make_ulonglong2(acc[4 * j + 2], acc[4 * j + 3]);

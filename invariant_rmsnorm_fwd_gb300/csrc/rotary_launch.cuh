@@ -4,10 +4,13 @@
 
 namespace rbi {
 
-inline void set_teams(RotaryParams &p) {
+// element: bytes; pairs: register pairs of a piece.
+inline void set_teams(RotaryParams &p, int element, int pairs) {
     p.by_team = Divisor(uint32_t(p.team));
     p.teams = 32 / p.team;
     p.by_teams = Divisor(uint32_t(p.teams));
+    p.pitch = pieces_pitch(p.vectors, 2 * element, p.team, p.teams, pairs * element / 2);
+    p.turning = (p.rot / (4 * pairs) + p.team - 1) / p.team;
 }
 
 template <class E, int PAIRS, bool NORM, int TEAM>
@@ -18,7 +21,7 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
-    set_teams(p);
+    set_teams(p, int(sizeof(E)), piece_pairs(PAIRS));
     // Heads of a warp: 8, so that a token's angles serve many rows, or half as many and half
     // again while there are fewer warps than fit (one token of 40 heads of 128: rotation
     // 4.0 -> 2.6 us, norm and rotation 5.7 -> 3.5; with twice that many warps as the aim
@@ -40,7 +43,7 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     const int slots = steps * p.teams;
     p.units = uint32_t((p.n_tokens + slots - 1) / slots * p.chunks);
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
-           (NORM ? kWeightBytes : 0) + kQkWarps * (Ring<E, 1>::kBytes + (PAIRS == kSplit ? kSplitBytes : 0)), stream>>>(p, slots);
+           (NORM ? kWeightBytes : 0) + kQkWarps * Ring<E, 1, PAIRS>::kBytes, stream>>>(p, slots);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
@@ -54,7 +57,7 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     int regs = 0;
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
-    set_teams(p);
+    set_teams(p, int(sizeof(E)), piece_pairs(PAIRS));
     const QkTeams t(p.D);
     p.group = t.group;
     p.share = t.share;
@@ -67,7 +70,7 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     p.units = uint32_t(windows * p.chunks);
     const bool straddles = p.hq % p.per != 0 && p.heads > p.hq;
     kern<<<(p.units + kQkWarps - 1) / kQkWarps, kQkWarps * 32,
-           qk_bwd_smem(Ring<E, 2>::kBytes, PAIRS == kSplit, p.ws.hdr != nullptr, straddles), stream>>>(p, straddles);
+           qk_bwd_smem(Ring<E, 2, PAIRS>::kBytes, p.ws.hdr != nullptr, straddles), stream>>>(p, straddles);
     if (cudaGetLastError() != cudaSuccess) return RMSNORM_ERR_CUDA;
     count_launch();
     return RMSNORM_OK;
@@ -77,7 +80,7 @@ template <class E, int PAIRS>
 static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
     if (mode == 0) {
         // (heads of 80 with 24 columns turning, 33,384 tokens: 76 us, in teams of a power of two 92; else equal)
-        p.team = PAIRS == kHalf && p.in_place ? p.rot / 16 : p.lanes;
+        p.team = p.in_place && PAIRS != kNear ? PAIRS == kHalf ? p.rot / 16 : (p.vectors + 1) / 2 : p.lanes;
         return rotary_launch_fwd<E, PAIRS, false, 0>(p, stream);
     }
     // Teams of just the lanes that a head needs where a warp then holds more of them (5 lanes for 80 columns, 6
@@ -100,6 +103,9 @@ static int rotary_launch(RotaryParams &p, int mode, cudaStream_t stream) {
 template <class E, int PAIRS>
 int rotary_run_pairs(RotaryParams p, int mode, cudaStream_t stream) {
     p.lanes = (p.D + 15) / 16;
+    p.vector0 = p.in_place ? p.first / 8 : 0;
+    p.all_pieces = mode > 0;
+    p.vectors = p.in_place ? (p.first + p.rot + 7) / 8 - p.vector0 : p.D / 8;
     return rotary_launch<E, PAIRS>(p, mode, stream);
 }
 

@@ -95,7 +95,13 @@ CASES = [(32, 8, 128, 128, 0, False, BF, None, 1.0), (4, 1, 64, 64, 0, True, FP1
          (17, 9, 40, 24, 2, True, F32, None, 1.0), (2, 1, 512, 512, 0, False, BF, None, 1.0),
          (1, 3, 504, 8, 496, True, FP16, None, 1.0), (3, 1, 512, 20, 490, False, F32, None, 1.0),
          (12, 12, 192, 64, 128, False, BF, None, 1.0), (64, 8, 32, 32, 0, False, FP16, None, 1.0),
-         (6, 2, 112, 56, 0, True, BF, None, 1.0), (33, 1, 160, 160, 0, True, BF, F32, 1.0)]
+         (6, 2, 112, 56, 0, True, BF, None, 1.0), (33, 1, 160, 160, 0, True, BF, F32, 1.0),
+         # halves that begin or end inside a vector of 8 columns, on multiples of 4 columns and of 2
+         (4, 2, 72, 72, 0, False, BF, None, 1.0), (2, 2, 88, 88, 0, False, FP16, F32, 1.0), (9, 1, 120, 120, 0, False, F32, None, 1.0),
+         (8, 4, 96, 24, 4, False, BF, None, 1.1), (2, 1, 64, 8, 52, False, FP16, None, 1.0), (1, 1, 16, 8, 4, False, F32, F32, 1.0),
+         (3, 3, 256, 200, 20, False, BF, F32, 1.0), (2, 1, 184, 72, 6, False, FP16, None, 1.0), (5, 1, 48, 40, 0, False, BF, None, 1.0),
+         (2, 1, 512, 504, 4, False, BF, F32, 1.0), (2, 2, 512, 508, 2, False, F32, None, 1.0), (3, 1, 8, 4, 2, False, BF, None, 1.0),
+         (13, 2, 32, 28, 4, False, FP16, None, 0.8), (3, 1, 144, 8, 60, False, F32, None, 1.0), (1, 0, 176, 172, 4, False, BF, None, 1.0)]
 
 
 @pytest.mark.parametrize("hq,hk,D,rot,first,inter,dtype,param,scale", CASES,
@@ -299,6 +305,26 @@ def test_a_bad_head_stays_alone():
     z = torch.zeros_like(s.q)                                         # rows of zeros: 0 with eps
     y, _ = rb.qk_norm_rotary_fwd(z, None, s.qw, None, s.layout(), s.pos, s.rot, EPS)
     assert not y.float().abs().any()
+
+
+def test_an_infinity_spoils_its_own_columns():
+    """rstd is 0 in a row with an infinity: the other columns are zeros, it and the one it turns with are NaN."""
+    n = 9
+    for dtype in (BF, F32):
+        for D, rot, first, inter in ((64, 32, 16, False), (72, 24, 4, False), (80, 20, 2, False), (96, 40, 6, True)):
+            s = Setup(n, 2, 1, D, rot, first, inter, dtype)
+            for col in (0, D - 1, first, first + rot - 1, first + rot // 2):
+                x = s.q.clone()
+                x[3, 1, col] = float("inf")
+                y, _ = rb.qk_norm_rotary_fwd(x, s.k, s.qw, s.kw, s.layout(), s.pos, s.rot, EPS)
+                bad, j = {col}, col - first
+                if 0 <= j < rot:
+                    bad.add(first + (j ^ 1 if inter else (j + rot // 2) % rot))
+                assert set(torch.isnan(y[3, 1]).nonzero().flatten().tolist()) == bad, (dtype, D, col)
+                assert not y[3, 1, [c for c in range(D) if c not in bad]].any()
+                clean = torch.ones(n, 2, dtype=torch.bool, device="cuda")
+                clean[3, 1] = False
+                assert torch.isfinite(y[clean]).all()
 
 
 def test_status_bits():
