@@ -166,7 +166,8 @@ __global__ void qk_begin_kernel(QkWs ws) {
 }
 
 constexpr int kFinalCtas = 8, kFinalWarps = 16;
-constexpr int64_t kFinalAlone = 256;                     // groups that one CTA adds up without a cluster
+// Whether one CTA for 32 columns does without a cluster.
+bool final_alone(const QkWs &ws) { return ws.groups <= 256 && ws.cut.slots <= 8; }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
@@ -177,29 +178,25 @@ __device__ __forceinline__ float4 plus(const float4 &a, const float4 &b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
 
-// A group's sum of four columns over the partial sums `slots` from its tokens' own, in
-// the order in which a warp of the backward pass adds up a whole group.  All loads of a
-// slot are issued at once.
-__device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool check) {
+// A group's sum of four columns (col on, `have`: there are any) over the partial sums `slots` from
+// its tokens' own, in the order in which a warp of the backward pass adds up a whole
+// group.  The whole warp does it for one group: quarter q takes the partial sums q, q + 4, ..., all loads of
+// one at once, and everyone adds the quarters' sums up in order.
+__device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slot0, int slots, int col, bool have, bool check) {
+    const int lane = threadIdx.x & 31;
     const int64_t t0 = g * ws.group;
     const int n = ws.n - t0 < ws.group ? int(ws.n - t0) : ws.group;
-    uint32_t there = 0;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = 0; c < slots; ++c) {
+    const uint32_t there = __ballot_sync(kFull, lane < n && ws.flag[t0 + (lane < n ? lane : 0)] == 2);
+    if (check && lane == 0 && there != (1u << n) - 1u) qk_report(ws, kStMissing);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v = zero;
+    for (int c0 = 0; c0 < slots; c0 += 4) {
+        const int c = c0 + (lane >> 3);
         const float *src = ws.spill + ((slot0 + c) * ws.n + t0) * ws.D + col;
         float4 x[kMostGroup];
 #pragma unroll
-        for (int i = 0; i < kMostGroup; ++i) x[i] = i < n ? *reinterpret_cast<const float4 *>(src + i * ws.D) : v;
-        if (c == 0) {
-            int32_t f[kMostGroup];
-#pragma unroll
-            for (int i = 0; i < kMostGroup; ++i) f[i] = i < n ? ws.flag[t0 + i] : 0;
-#pragma unroll
-            for (int i = 0; i < kMostGroup; ++i) there |= (f[i] == 2) << i;
-            if (check && there != (1u << n) - 1u) qk_report(ws, kStMissing);
-        }
-        float4 u = v, s = v;
+        for (int i = 0; i < kMostGroup; ++i) x[i] = have && c < slots && i < n ? *reinterpret_cast<const float4 *>(src + i * ws.D) : zero;
+        float4 u = zero, s = zero;
         bool any = false;                                // of the share
         int left = ws.share;
 #pragma unroll
@@ -210,16 +207,68 @@ __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slo
                     any = true;
                 }
                 if (--left == 0 || i + 1 == n) {
-                    if (!any) s = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!any) s = zero;
                     u = i < ws.share ? s : plus(u, s);
                     any = false;
                     left = ws.share;
                 }
             }
         }
-        v = c ? plus(v, u) : u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int from = 8 * k + (lane & 7);
+            const float4 w = make_float4(__shfl_sync(kFull, u.x, from), __shfl_sync(kFull, u.y, from), __shfl_sync(kFull, u.z, from),
+                                         __shfl_sync(kFull, u.w, from));
+            if (c0 + k < slots) v = c0 + k ? plus(v, w) : w;
+        }
     }
     return v;
+}
+
+// Adds the groups [g, g1) of a quarter-warp's share, at most GROUPS of them, to acc; the loads of SLOTS
+// partial sums of each go out together.
+template <int GROUPS, int SLOTS>
+__device__ __forceinline__ float4 qk_add_groups(const QkWs &ws, float4 acc, int64_t g, int64_t g1, int slot0, int slots, int col, bool have,
+                                                bool check) {
+    const int lane = threadIdx.x & 31;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *src = ws.partial + (slot0 * ws.groups + g) * ws.D + col;
+    bool in[GROUPS], loose[GROUPS];
+    float4 v[GROUPS];
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+        in[j] = have && g + j < g1;
+        loose[j] = g + j < g1 && !ws.whole[g + j];
+    }
+    // (a partial that is not there is read all the same: its memory is)
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) v[j] = in[j] ? *reinterpret_cast<const float4 *>(src + j * ws.D) : zero;
+    for (int c = 1; c < slots; c += SLOTS) {
+        float4 x[SLOTS][GROUPS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+            for (int j = 0; j < GROUPS; ++j)
+                x[i][j] = in[j] && c + i < slots ? *reinterpret_cast<const float4 *>(src + ((c + i) * ws.groups + j) * ws.D) : zero;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+            for (int j = 0; j < GROUPS; ++j)
+                if (c + i < slots) v[j] = plus(v[j], x[i][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+        uint32_t left = __ballot_sync(kFull, loose[j]) & 0x01010101u;
+        while (left) {
+            const int from = __ffs(left) - 1;
+            left &= left - 1;
+            const int64_t its = int64_t(__shfl_sync(kFull, (unsigned long long)(g + j), from));
+            const float4 u = qk_loose_group(ws, its, slot0, slots, col, have, check);
+            if (lane >> 3 == from >> 3) v[j] = u;
+        }
+        if (in[j]) acc = plus(acc, v[j]);
+    }
+    return acc;
 }
 
 // Both weight gradients in one launch: a cluster of CTAS takes 32 columns of one of them,
@@ -228,7 +277,8 @@ __device__ __noinline__ float4 qk_loose_group(const QkWs &ws, int64_t g, int slo
 // four shares of a warp in pairs, the warps, the CTAs: an order that depends on the sizes
 // alone.  What bounds it: latency (a launch, the header, a share's 1 to 3 rounds of loads,
 // the cluster's exchange).  33,384 tokens, 5 partial sums of 128 columns a group, 12.8 MB: 6.7 us; up
-// to 256 groups one CTA does without the exchange (46 tokens: 5.1 us, 5.7 in a cluster).
+// to 256 groups of 8 partial sums one CTA does without the exchange (46 tokens: 5.1 us, 5.7 in a
+// cluster).
 template <int CTAS>
 __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *dq, float *dk, int slices) {
     __shared__ float4 part[kFinalWarps][8];
@@ -245,30 +295,13 @@ __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *
     const int64_t per = (ws.groups + kShares - 1) / kShares;
     const int64_t g0 = ((int64_t(blockIdx.y) * kFinalWarps + warp) * 4 + (lane >> 3)) * per;
     const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
-    const bool check = blockIdx.x == 0 && (lane & 7) == 0;
+    const bool check = blockIdx.x == 0, have = col < ws.D;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (col < ws.D) {
-        const float *src = ws.partial + int64_t(slot0) * ws.groups * ws.D + col;
-        constexpr int kAhead = 4;                        // groups of a batch of loads
-        for (int64_t g = g0; g < g1; g += kAhead) {
-            int32_t there[kAhead];
-            float4 v[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) there[j] = g + j < g1 ? ws.whole[g + j] : 0;
-            // (a partial that is not there is read all the same: its memory is)
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) v[j] = g + j < g1 ? *reinterpret_cast<const float4 *>(src + (g + j) * ws.D) : acc;
-            for (int c = 1; c < slots; ++c) {
-                const float *s = src + c * ws.groups * ws.D;
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (g + j < g1) v[j] = plus(v[j], *reinterpret_cast<const float4 *>(s + (g + j) * ws.D));
-            }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (g + j < g1) acc = plus(acc, there[j] ? v[j] : qk_loose_group(ws, g + j, slot0, slots, col, check));
-        }
-    }
+    // (the warp's quarters go together)
+    if (per < 3)
+        for (int64_t i = 0; i < per; ++i) acc = qk_add_groups<1, 8>(ws, acc, g0 + i, g1, slot0, slots, col, have, check);
+    else
+        for (int64_t i = 0; i < per; i += 4) acc = qk_add_groups<4, 2>(ws, acc, g0 + i, g1, slot0, slots, col, have, check);
 #pragma unroll
     for (int o = 8; o <= 16; o <<= 1)
         acc = plus(acc, make_float4(__shfl_xor_sync(kFull, acc.x, o), __shfl_xor_sync(kFull, acc.y, o),
@@ -365,7 +398,7 @@ extern "C" int qk_norm_finalize(void *workspace, int64_t n_logical_tokens, int32
     const unsigned gx = unsigned(slices * (k_heads ? 2 : 1));
     const QkWs ws = qk_ws(workspace, n_logical_tokens, q_heads, k_heads, head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (ws.groups > kFinalAlone)
+    if (!final_alone(ws))
         qk_finalize_kernel<<<dim3(gx, kFinalCtas), kFinalWarps * 32, 0, s>>>(ws, grad_scale, dq_weight, dk_weight, slices);
     else
         qk_finalize_small_kernel<<<gx, kFinalWarps * 32, 0, s>>>(ws, grad_scale, dq_weight, dk_weight, slices);

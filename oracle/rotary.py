@@ -100,8 +100,8 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 up
-    to 256 groups), 2 steps between the shares of a warp, 16 warps and 8 CTAs."""
+    10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 in
+    small calls), 2 steps between the shares of a warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
     rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
@@ -147,7 +147,8 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
         most //= 2
     chunks = -(-heads // most)
     per = (heads + chunks - 1) // chunks
-    ctas = 8 if groups > 256 else 1
+    slots = -(-hq // per) + (chunks - hq // per if heads > hq else 0)
+    ctas = 1 if groups <= 256 and slots <= 8 else 8
     shares = ctas * 16 * 4
     share = (groups + shares - 1) // shares
     out = []
