@@ -272,7 +272,7 @@ __device__ __forceinline__ float4 qk_add_groups(const QkWs &ws, float4 acc, int6
 }
 
 // Both weight gradients in one launch: a cluster of CTAS takes 32 columns of one of them,
-// its CTAs x 16 warps x 4 quarter-warps consecutive shares of the groups.  The partial sums
+// its CTAs x 16 warps x 4 quarter-warps consecutive shares of the groups, first all first quarters.  The partial sums
 // of a group from the first chunk to the last, the groups of a share likewise, then the
 // four shares of a warp in pairs, the warps, the CTAs: an order that depends on the sizes
 // alone.  What bounds it: latency (a launch, the header, a share's 1 to 3 rounds of loads,
@@ -293,7 +293,9 @@ __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *
     const int slot0 = keys ? ws.cut.q_slots : 0, slots = keys ? ws.cut.slots - ws.cut.q_slots : ws.cut.q_slots;
     constexpr int kShares = CTAS * kFinalWarps * 4;
     const int64_t per = (ws.groups + kShares - 1) / kShares;
-    const int64_t g0 = ((int64_t(blockIdx.y) * kFinalWarps + warp) * 4 + (lane >> 3)) * per;
+    // (few groups: one a warp, so that cut ones are not added up one after the other; 1,140 tokens whose 142 groups are
+    // all cut, 33 partial sums each: 26 us with four a warp)
+    const int64_t g0 = ((lane >> 3) * (CTAS * kFinalWarps) + int(blockIdx.y) * kFinalWarps + warp) * per;
     const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
     const bool check = blockIdx.x == 0, have = col < ws.D;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -301,7 +303,7 @@ __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *
     if (per < 3)
         for (int64_t i = 0; i < per; ++i) acc = qk_add_groups<1, 8>(ws, acc, g0 + i, g1, slot0, slots, col, have, check);
     else
-        for (int64_t i = 0; i < per; i += 4) acc = qk_add_groups<4, 2>(ws, acc, g0 + i, g1, slot0, slots, col, have, check);
+        for (int64_t i = 0; i < per; i += 4) acc = qk_add_groups<4, 4>(ws, acc, g0 + i, g1, slot0, slots, col, have, check);
 #pragma unroll
     for (int o = 8; o <= 16; o <<= 1)
         acc = plus(acc, make_float4(__shfl_xor_sync(kFull, acc.x, o), __shfl_xor_sync(kFull, acc.y, o),

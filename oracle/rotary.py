@@ -177,7 +177,8 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
             for g in range(r * share, min((r + 1) * share, groups)):
                 acc = acc + value[g]
             part.append(acc)
-        warps = [(part[i] + part[i + 1]) + (part[i + 2] + part[i + 3]) for i in range(0, shares, 4)]
+        w = 16 * ctas
+        warps = [(part[i] + part[w + i]) + (part[2 * w + i] + part[3 * w + i]) for i in range(w)]
         total = None
         for r in range(ctas):
             s = warps[16 * r]
