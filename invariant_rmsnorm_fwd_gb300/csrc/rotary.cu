@@ -276,9 +276,9 @@ __device__ __forceinline__ float4 qk_add_groups(const QkWs &ws, float4 acc, int6
 // of a group from the first chunk to the last, the groups of a share likewise, then the
 // four shares of a warp in pairs, the warps, the CTAs: an order that depends on the sizes
 // alone.  What bounds it: latency (a launch, the header, a share's 1 to 3 rounds of loads,
-// the cluster's exchange).  33,384 tokens, 5 partial sums of 128 columns a group, 12.8 MB: 6.7 us; up
-// to 256 groups of 8 partial sums one CTA does without the exchange (46 tokens: 5.1 us, 5.7 in a
-// cluster).
+// the cluster's exchange).  33,384 tokens, 5 partial sums of 128 columns a group, 12.8 MB: 7.3 us; up
+// to 256 groups of 8 partial sums one CTA does without the exchange (46 tokens: 3.9 us; before loads went out
+// eight at once 5.1, 5.7 in a cluster).
 template <int CTAS>
 __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *dq, float *dk, int slices) {
     __shared__ float4 part[kFinalWarps][8];

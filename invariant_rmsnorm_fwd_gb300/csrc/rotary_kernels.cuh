@@ -34,22 +34,34 @@ constexpr int kBusyWarps = 2432;                         // warps that fill the 
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
 
 // How a warp takes heads of D columns: in teams of as many lanes as hold them, or of the
-// power of two above where that makes no fewer teams.  The logical tokens of a group, the unit
-// that a warp of the backward pass adds up, are as many as it has teams, or a small
-// multiple of that: each team takes a share of consecutive tokens, from the first to the last, then
-// the shares are added likewise.  Teams of 1 and 2 lanes (16 columns, 32) have groups of 8.
-__host__ __device__ constexpr int group_of(int teams) { return teams > kMostGroup ? 8 : teams >= 5 ? teams : 8 / teams * teams; }
-__host__ __device__ constexpr int share_of(int teams) { return teams >= group_of(teams) ? 1 : group_of(teams) / teams; }
+// power of two above where that makes no fewer teams.
 struct QkTeams {
-    int size, teams, group, share;
+    int size, teams;
     explicit QkTeams(int D) {
         const int lanes = (D + 15) / 16;
         size = 1;
         while (size < lanes) size <<= 1;
         if (32 / lanes > 32 / size) size = lanes;
         teams = 32 / size;
-        group = group_of(teams);
-        share = share_of(teams);
+    }
+};
+
+// The logical tokens of a group, the unit that a warp of the backward pass adds up, by the sizes
+// (tokens, heads, D) alone: as many as a warp has teams, or, fewer than 5 teams, a multiple up to
+// 8: each team takes a share of consecutive tokens, from the first to the last, then
+// the shares are added likewise.  The multiple is halved while the groups' chunks of heads
+// are too few for a round and a half of warps (644 tokens of 60 heads of 192: 42 us in groups of 8, 33 of 4, 25 of
+// 2; 17,620 of 17 of 256: 99, 101, 114).  More than 10 teams (heads up to 32 columns) have groups of 8.
+struct QkGroups {
+    int group, share;
+    int64_t groups;
+    QkGroups(int D, int32_t heads, int64_t tokens) {
+        const int teams = QkTeams(D).teams;
+        group = teams > kMostGroup ? 8 : teams >= 5 ? teams : 8 / teams * teams;
+        while (group / 2 >= teams && group > 2 && (tokens + group - 1) / group * ((heads + kChunkHeads - 1) / kChunkHeads) <= kBusyWarps * 3 / 2)
+            group /= 2;
+        share = teams >= group ? 1 : group / teams;
+        groups = (tokens + group - 1) / group;
     }
 };
 
@@ -92,8 +104,7 @@ inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(
 struct QkWsLayout {
     int64_t off_whole, off_partial, off_spill, total;
     QkWsLayout(int64_t N, int32_t hq, int32_t hk, int64_t D) {
-        const int group = QkTeams(int(D)).group;
-        const int64_t groups = (N + group - 1) / group, slots = QkChunks(hq, hk, groups).slots;
+        const int64_t groups = QkGroups(int(D), hq + hk, N).groups, slots = QkChunks(hq, hk, groups).slots;
         off_whole = align256(256 + N * 4);
         off_partial = align256(off_whole + groups * 4);
         off_spill = align256(off_partial + slots * groups * D * 4);
@@ -111,10 +122,10 @@ inline QkWs qk_ws(void *base, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     w.partial = reinterpret_cast<float *>(b + L.off_partial);
     w.spill = reinterpret_cast<float *>(b + L.off_spill);
     w.n = N;
-    const QkTeams t{int(D)};
+    const QkGroups t(int(D), hq + hk, N);
     w.group = t.group;
     w.share = t.share;
-    w.groups = (N + t.group - 1) / t.group;
+    w.groups = t.groups;
     w.sizes = qk_sizes(D, hq, hk);
     w.cut = QkChunks(hq, hk, w.groups);
     w.D = int32_t(D);
@@ -764,10 +775,8 @@ struct Window {
     int run;                         // lane of the run's first slot, -1: none
     uint32_t loose;                  // bit j: slot G w + j on its own
 };
-// GROUP: G, or 0 where the kernel learns it when it runs.
-template <int GROUP>
 __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bool grads) {
-    const int lane = threadIdx.x & 31, G = GROUP ? GROUP : p.group;
+    const int lane = threadIdx.x & 31, G = p.group;
     const uint32_t mine = (1u << G) - 1u, behind = mine >> 1;        // the window's slots; the G - 1 that follow a group's first
     const int64_t slot = w * G - (G - 1) + lane;         // lanes G - 1 .. 2 G - 2 are the window
     const bool in = lane < 3 * G - 2 && slot >= 0 && slot < p.n_tokens;
@@ -780,7 +789,7 @@ __device__ __forceinline__ Window window_of(const RotaryParams &p, int64_t w, bo
         return r;
     }
     const int32_t before = __shfl_up_sync(kFull, r.id, 1);
-    const int nth = r.id < 0 ? 0 : r.id - int(GROUP ? uint32_t(r.id) / uint32_t(G) : p.by_group.quotient(uint32_t(r.id))) * G;   // of its group
+    const int nth = r.id < 0 ? 0 : r.id - int(p.by_group.quotient(uint32_t(r.id))) * G;   // of its group
     const uint32_t begins = __ballot_sync(kFull, r.id >= 0 && nth == 0 && int64_t(r.id) + G <= p.ws.n);
     const uint32_t follows = __ballot_sync(kFull, lane > 0 && r.id > 0 && nth != 0 && r.id == before + 1);
     // run from lane s: begins at s and follows at s + 1 .. s + G - 1
@@ -818,8 +827,8 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
     if (p.ws.hdr && !grads && unit == 0 && lane32 == 0) qk_report(p.ws, kStHeader);
     constexpr int kTeams = TEAM ? 32 / (TEAM ? TEAM : 1) : 1;
     const int size = TEAM ? TEAM : p.team, teams = TEAM ? kTeams : p.teams;
-    const int G = TEAM ? group_of(kTeams) : p.group, share = TEAM ? share_of(kTeams) : p.share;
-    Window wd = window_of<TEAM ? group_of(kTeams) : 0>(p, win, grads);
+    const int G = p.group, share = p.share;
+    Window wd = window_of(p, win, grads);
     if (!in) {
         wd.run = -1;
         wd.loose = 0;
@@ -992,7 +1001,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_
     if (grads && run_steps) {
         __syncwarp();
         const uint32_t begins = uint32_t(__shfl_sync(kFull, wd.id, wd.run));
-        const int64_t g = TEAM ? begins / uint32_t(G) : p.by_group.quotient(begins);
+        const int64_t g = p.by_group.quotient(begins);
         if (chunk == 0 && lane32 == 0) p.ws.whole[g] = 1;
         for (int keys = head0 < p.hq ? 0 : 1; keys < 2; ++keys) {
             if (keys && end <= p.hq) break;

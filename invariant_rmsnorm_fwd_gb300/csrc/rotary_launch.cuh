@@ -58,7 +58,7 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
     set_teams(p, int(sizeof(E)), piece_pairs(PAIRS));
-    const QkTeams t(p.D);
+    const QkGroups t(p.D, p.heads, p.ws.hdr ? p.ws.n : p.n_tokens);
     p.group = t.group;
     p.share = t.share;
     p.by_group = Divisor(uint32_t(t.group));

@@ -100,8 +100,9 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
     (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
-    10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (64 in
-    small calls), 2 steps between the shares of a warp, 16 warps and 8 CTAs."""
+    10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (of 5 and more tokens,
+    or at most 2 x 3648 smaller ones; 64 shares of up to 256 groups), 2 steps between the shares of a
+    warp, 16 warps and 8 CTAs."""
     x = np.asarray(x, dtype=np.float64)
     D = x.shape[-1]
     rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
@@ -118,7 +119,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 10 + x.shape[1] + 1 + max(n // (512 * 5) + 1, 4) + 2 + 24
+    chain = 8 + 10 + x.shape[1] + 1 + max(n // (512 * 5) + 1, 15) + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -140,6 +141,8 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
     size = lanes if 32 // lanes > 32 // size else size
     teams = 32 // size
     group = 8 if teams > 10 else teams if teams >= 5 else 8 // teams * teams
+    while group // 2 >= teams and group > 2 and -(-n // group) * -(-heads // 8) <= 3648:
+        group //= 2
     tokens = max(1, group // teams)                                   # of a group, added up by one team
     groups = -(-n // group)
     most = 8
