@@ -131,6 +131,7 @@ int call(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64_t D, float ep
     p.position = r->position;
     p.turns = r->turns;
     p.n_tokens = n;
+    p.active = L->n_logical_tokens < 1 ? 1 : L->n_logical_tokens < n ? L->n_logical_tokens : n;
     p.D = int32_t(D);
     p.rot = r->rotary_dim;
     p.first = r->first;

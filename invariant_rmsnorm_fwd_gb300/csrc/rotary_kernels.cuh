@@ -150,7 +150,7 @@ struct RotaryParams {
     HeadsParams side[2];             // queries, keys
     const int32_t *tok_id, *position;
     const uint64_t *turns;
-    int64_t n_tokens;
+    int64_t n_tokens, active;        // slots; tokens that may be among them
     int32_t D, rot, first;
     int32_t hq, heads;               // query heads, heads of both
     int32_t chunks, per;             // chunks of a token, heads of a chunk
@@ -641,8 +641,10 @@ __device__ __forceinline__ void store_row(E *dst, const Raw<E> &r, uint32_t plac
 // so padding costs a warp nothing but its ids.  CTAs an SM: with 6, the norm's 80 registers
 // are as fast on large calls and 0.3 us slower on small ones; FP32 at 4 of 128 registers takes
 // 125 us where 5 take 117; in pieces FP32 needs them (16 bits, heads of 120: 74 -> 70 us with 5).
+template <class E, int PAIRS, bool NORM>
+constexpr int kFwdCtas = in_pieces(PAIRS) ? (sizeof(E) == 4 ? 4 : 5) : sizeof(E) == 4 || NORM ? 5 : 6;
 template <class E, int PAIRS, bool NORM, int TEAM>
-__global__ void __launch_bounds__(kQkWarps * 32, in_pieces(PAIRS) ? (sizeof(E) == 4 ? 4 : 5) : sizeof(E) == 4 || NORM ? 5 : 6)
+__global__ void __launch_bounds__(kQkWarps * 32, kFwdCtas<E, PAIRS, NORM>)
     rotary_kernel(const __grid_constant__ RotaryParams p, int slots) {
     extern __shared__ float4 shared[];
     using R = Ring<E, 1, PAIRS>;

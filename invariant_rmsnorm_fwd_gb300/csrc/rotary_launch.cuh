@@ -13,6 +13,28 @@ inline void set_teams(RotaryParams &p, int element, int pairs) {
     p.turning = (p.rot / (4 * pairs) + p.team - 1) / p.team;
 }
 
+// Heads of a warp of the forward pass: those, up to `most`, with which the warps' rounds take
+// least if a warp's start and a token's angles take as long as `start` rows.  A call of a
+// few tokens gets many warps of few heads (one token of 40 heads of 128: rotation 4.0 -> 2.6 us,
+// norm and rotation 5.7 -> 3.1), but not just more than run at once (3,902 of 2+1 of 192: 7.3 -> 5.6).
+// Halves and neighbours alone, which memory bounds, have at most 8 heads (32+8 of 128, 33,384 tokens:
+// 100.3 us, 102.5 with 20); others up to 24 (16+16 of 72, 17,620 tokens, with the norm: 43 -> 37, 8+8 of 40
+// 19 -> 15, 32+8 of 144 78 -> 72, of 128 104 -> 105).  5 rows for 16 bits, 3 for FP32 (80 columns, 20 turning: 90 us for 96).
+inline int forward_heads(int64_t windows, int32_t heads, int most, int start, int64_t at_once) {
+    int64_t best = INT64_MAX;
+    int per = most;
+    for (const int n : {24, 16, 12, 8, 6, 4, 3, 2, 1}) {
+        if (n > most) continue;
+        const int64_t chunks = (heads + n - 1) / n, rows = (heads + chunks - 1) / chunks;
+        const int64_t time = (windows * chunks + at_once - 1) / at_once * (rows + start);
+        if (time < best) {
+            best = time;
+            per = n;
+        }
+    }
+    return per;
+}
+
 template <class E, int PAIRS, bool NORM, int TEAM>
 static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     auto kern = rotary_kernel<E, PAIRS, NORM, TEAM>;
@@ -22,13 +44,9 @@ static int rotary_launch_fwd(RotaryParams &p, cudaStream_t stream) {
     if (int rc = device_info(&d)) return rc;
     if (int rc = info.get(reinterpret_cast<const void *>(kern), d->max_smem, &regs)) return rc;
     set_teams(p, int(sizeof(E)), piece_pairs(PAIRS));
-    // Heads of a warp: 8, so that a token's angles serve many rows, or half as many and half
-    // again while there are fewer warps than fit (one token of 40 heads of 128: rotation
-    // 4.0 -> 2.6 us, norm and rotation 5.7 -> 3.5; with twice that many warps as the aim
-    // 2,000 tokens take 9.2 -> 10.2 us, with four times 12.9).
-    const int64_t windows = (p.n_tokens + p.teams - 1) / p.teams;
-    int most = kChunkHeads;
-    while (most > 1 && windows * ((p.heads + most - 1) / most) < kBusyWarps) most >>= 1;
+    const int64_t windows = (p.active + p.teams - 1) / p.teams;
+    const int most = forward_heads(windows, p.heads, NORM || in_pieces(PAIRS) ? 24 : kChunkHeads, sizeof(E) == 4 ? 3 : 5,
+                                   int64_t(kFwdCtas<E, PAIRS, NORM>) * kQkWarps * d->sms);
     p.chunks = (p.heads + most - 1) / most;
     p.per = (p.heads + p.chunks - 1) / p.chunks;
     p.by_chunks = Divisor(uint32_t(p.chunks));
