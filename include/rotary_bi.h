@@ -24,12 +24,12 @@
  * multiset whatever its physical layout (and whatever the strides).  Row sums
  * use a fixed tree that depends only on D and the rotary parameters.  A weight
  * gradient is summed in canonical order: a token's heads, queries then keys, in
- * chunks of equal size (at most 8 heads, by the number of heads and of logical
- * tokens; the last one shorter), each from its first to its last head of the
- * kind; the logical tokens of a group (2 to 10, by the sizes) in a fixed order; then
- * chunks and groups by a fixed tree over their number.  Groups that a call does
- * not hold whole and in consecutive slots leave their tokens' sums in the
- * workspace, and qk_norm_finalize adds them in the same order.  No plan is
+ * chunks of equal size (at most 16 heads, by the sizes; the last one shorter),
+ * each from its first to its last head of the kind; the logical tokens of a
+ * group (2 to 10, by the sizes) in a fixed order; then chunks and groups by a
+ * fixed tree over their number.  Groups that a call does not hold whole and in
+ * consecutive slots leave their tokens' sums in the workspace, and
+ * qk_norm_finalize adds them in the same order.  No plan is
  * needed.  Inactive slots are neither read nor written.
  *
  * Element types.  All tensors of a call have one type, weights that type or

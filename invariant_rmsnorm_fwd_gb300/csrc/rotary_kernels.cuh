@@ -28,7 +28,7 @@
 
 namespace rbi {
 
-constexpr int kChunkHeads = 8;                           // most heads of a chunk
+constexpr int kChunkHeads = 8;                           // heads of a usual chunk
 constexpr int kMostGroup = 10;                           // most logical tokens of a group of the weight gradients' order
 constexpr int kBusyWarps = 2432;                         // warps that fill the GPU: 16 on each of 152 SMs
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
@@ -66,20 +66,28 @@ struct QkGroups {
 };
 
 // The backward pass cuts a token's heads, queries then keys, into chunks of equal size
-// (the last one shorter), by the number of heads and of groups alone: of 8 heads,
-// so that a token's angles serve many rows, or half as many and half again, down to 2,
-// while all of them still run at once (2,000 tokens of 40 heads of 128: 16.7 us in chunks
-// of 8, 17.9 in chunks of 4, which are a few warps more than fit; 46 tokens of 6 heads
-// of 16: 8.6 us in chunks of 6, 5.1 of 2).  A chunk that holds both kinds has a partial sum of
-// each: slots of the queries' chunks come first, then those of the chunks that hold keys.
+// (the last one shorter), by the sizes alone: of up to 16 heads, those with which the
+// warps' rounds take least if a token's angles and a warp's start take as long as two rows
+// each (17,620 tokens of 16+16 heads of 72: 72 us in chunks of 8, 63 of 16; 33,384 of 32+8 of 128: 167 of 10, 168
+// of 8, 171 of 14; 46 of 4+2 of 16: 8.6 of 6, 5.1 of 2).  A chunk that holds both
+// kinds has a partial sum of each: slots of the queries' chunks come first, then those of the chunks
+// that hold keys.
 struct QkChunks {
     int32_t chunks, per;             // chunks of a token, heads of a chunk
     int32_t q_slots, k_first, slots; // chunks with queries; first chunk with keys; all partial sums
     QkChunks() = default;
-    QkChunks(int32_t hq, int32_t hk, int64_t groups) {
+    QkChunks(int32_t hq, int32_t hk, int64_t groups, int share) {
         const int32_t all = hq + hk;
-        int n = kChunkHeads;
-        while (n > 2 && groups * ((all + n / 2 - 1) / (n / 2)) <= kBusyWarps) n >>= 1;
+        int64_t best = INT64_MAX;
+        int n = 2;
+        for (const int most : {16, 12, 8, 6, 4, 3, 2}) {
+            const int64_t c = (all + most - 1) / most, rows = (all + c - 1) / c;
+            const int64_t time = (groups * c + kBusyWarps - 1) / kBusyWarps * (share * (rows + 2) + 2);
+            if (time < best) {
+                best = time;
+                n = most;
+            }
+        }
         chunks = (all + n - 1) / n;
         per = (all + chunks - 1) / chunks;
         q_slots = (hq + per - 1) / per;
@@ -104,7 +112,8 @@ inline int64_t qk_sizes(int64_t D, int32_t hq, int32_t hk) { return D | int64_t(
 struct QkWsLayout {
     int64_t off_whole, off_partial, off_spill, total;
     QkWsLayout(int64_t N, int32_t hq, int32_t hk, int64_t D) {
-        const int64_t groups = QkGroups(int(D), hq + hk, N).groups, slots = QkChunks(hq, hk, groups).slots;
+        const QkGroups t(int(D), hq + hk, N);
+        const int64_t groups = t.groups, slots = QkChunks(hq, hk, groups, t.share).slots;
         off_whole = align256(256 + N * 4);
         off_partial = align256(off_whole + groups * 4);
         off_spill = align256(off_partial + slots * groups * D * 4);
@@ -127,7 +136,7 @@ inline QkWs qk_ws(void *base, int64_t N, int32_t hq, int32_t hk, int64_t D) {
     w.share = t.share;
     w.groups = t.groups;
     w.sizes = qk_sizes(D, hq, hk);
-    w.cut = QkChunks(hq, hk, w.groups);
+    w.cut = QkChunks(hq, hk, w.groups, w.share);
     w.D = int32_t(D);
     return w;
 }
@@ -523,17 +532,18 @@ constexpr int kQkWarps = 4;
 template <class E, int TENSORS, int PAIRS>
 struct Ring {
     static constexpr bool kOn = sizeof(E) == 2;
-    static constexpr int kRow = in_pieces(PAIRS) ? 800 * int(sizeof(E)) : 1024;   // bytes of a warp's rows of one tensor
+    static constexpr int kRow = in_pieces(PAIRS) ? 768 * int(sizeof(E)) : 1024;   // bytes of a warp's rows of one tensor
     static constexpr int kDepth = !kOn ? 1 : TENSORS == 1 ? 5 : in_pieces(PAIRS) ? 3 : 4;
     static constexpr int kBytes = kOn || in_pieces(PAIRS) ? TENSORS * kRow * kDepth : 0;   // of a warp
 };
 // In pieces: the bytes from one team's place to the next, so that the lanes of all teams find
 // a piece in different banks: the words of a team's pieces, rounded up to whole vectors, modulo the 32
-// banks, or, small teams, any odd number of 16 bytes.  At most 800 elements / teams.  Vectors
+// banks, or, small teams, any odd number of 16 bytes.  At most 768 elements / teams.  Vectors
 // and pieces in words.
 inline int pieces_pitch(int vectors, int vector, int size, int teams, int piece) {
     const int words = vectors * vector, apart = (size * piece + 3) & ~3;
-    return teams == 1 ? 4 * words : size * piece > 4 ? 4 * (words + ((apart - words) & 31)) : 4 * (words | 4);
+    const int far = words + ((apart - words) & 31), most = 96 * vector / teams;
+    return 4 * (teams == 1 ? words : size * piece > 4 && far <= most ? far : words | 4);
 }
 template <class E, int PAIRS>
 __device__ __forceinline__ void copy_row(uint32_t dst, const E *row, const LaneColumns<PAIRS> &col, bool on) {

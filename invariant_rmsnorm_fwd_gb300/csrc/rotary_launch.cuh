@@ -81,7 +81,7 @@ static int rotary_launch_bwd(RotaryParams &p, cudaStream_t stream) {
     p.share = t.share;
     p.by_group = Divisor(uint32_t(t.group));
     const int64_t windows = (p.n_tokens + t.group - 1) / t.group;
-    const QkChunks cut = p.ws.hdr ? p.ws.cut : QkChunks(p.hq, p.heads - p.hq, windows);
+    const QkChunks cut = p.ws.hdr ? p.ws.cut : QkChunks(p.hq, p.heads - p.hq, windows, t.share);
     p.chunks = cut.chunks;
     p.per = cut.per;
     p.by_chunks = Divisor(uint32_t(p.chunks));

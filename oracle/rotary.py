@@ -99,7 +99,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     """(dx, dweight, err_dx, err_dw), dx unrounded.
 
     g = rot'(dy) as in rotate; a = g w; the row's sum of a x has depth 15; xhat is off by
-    (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 8 heads,
+    (RSTD + 1) U of itself.  The weight gradient adds its terms along chains of 16 heads,
     10 tokens, the chunks (at most as many as heads), the groups of one of 512 shares (of 5 and more tokens,
     or at most 2 x 3648 smaller ones; 64 shares of up to 256 groups), 2 steps between the shares of a
     warp, 16 warps and 8 CTAs."""
@@ -119,7 +119,7 @@ def backward(x, w, dy, position, freq, rotary_dim, first, interleaved, scale, ep
     err = rstd * et + (RSTD + 1) * U * np.abs(dx)
     term = g * xhat
     n = x.shape[0]
-    chain = 8 + 10 + x.shape[1] + 1 + max(n // (512 * 5) + 1, 15) + 2 + 24
+    chain = 16 + 10 + x.shape[1] + 1 + max(n // (512 * 5) + 1, 15) + 2 + 24
     err_dw = (np.abs(xhat) * eg).sum((0, 1)) + (RSTD + 2 + chain) * U * np.abs(term).sum((0, 1))
     return dx, term.sum((0, 1)), err, err_dw
 
@@ -145,10 +145,12 @@ def grad_replay(q_leaf: np.ndarray, k_leaf: np.ndarray):
         group //= 2
     tokens = max(1, group // teams)                                   # of a group, added up by one team
     groups = -(-n // group)
-    most = 8
-    while most > 2 and groups * -(-heads // (most // 2)) <= 2432:
-        most //= 2
-    chunks = -(-heads // most)
+    best = None
+    for most in (16, 12, 8, 6, 4, 3, 2):
+        c = -(-heads // most)
+        time = -(-groups * c // 2432) * (tokens * (-(-heads // c) + 2) + 2)
+        if best is None or time < best:
+            best, chunks = time, c
     per = (heads + chunks - 1) // chunks
     slots = -(-hq // per) + (chunks - hq // per if heads > hq else 0)
     ctas = 1 if groups <= 256 and slots <= 8 else 8

@@ -194,7 +194,7 @@ def test_gradient_order_replayed():
                                 (2500, 60, 3, 8, False), (2500, 57, 6, 24, True), (700, 5, 2, 80, True), (333, 11, 1, 96, True),
                                 (901, 3, 1, 160, True), (450, 2, 2, 48, True), (1500, 37, 2, 72, True), (123, 4, 4, 512, False),
                                 (211, 9, 1, 192, False), (611, 30, 9, 128, True), (257, 2, 1, 144, False), (4001, 2, 1, 264, True),
-                                (15001, 1, 1, 168, True)):
+                                (15001, 1, 1, 168, True), (5200, 10, 1, 64, False), (9000, 11, 6, 40, True)):
         g = np.random.default_rng(n)
         for kind, chunk in (("full", None), ("chunked", 61), ("permuted", None), ("padded_left", None)):
             sign = lambda h: np.where(g.random((n, h, D)) < 0.5, -1.0, 1.0) * 2.0 ** g.integers(-3, 4, (n, h, 1))   # noqa: E731

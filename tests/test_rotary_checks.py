@@ -107,12 +107,12 @@ def test_workspace_refusals_and_size():
     assert size(64, 4, 2, 12) == 0 and size(-1, 4, 2, 64) == 0 and size(1 << 31, 4, 2, 64) == 0
     assert size(64, 0, 2, 64) == 0 and size(64, 4, -1, 64) == 0 and size(64, 65536, 2, 64) == 0 and size(64, 4, 2, 520) == 0
     n, D = 900, 128
-    # few tokens: groups of 4 and a partial sum for 4 heads; many: of 8, 40 heads in 4 chunks of queries, 1 of keys; 10 + 1:
-    # both in the second
+    # few tokens: groups of 4 and a partial sum for 4 heads; many: of 8, 40 heads in 4 chunks, keys in the last one too;
+    # 10 + 1 in one
     assert 0 <= size(n, 32, 8, D) - (256 + 4 * n + 4 * 225 + 10 * (225 + n) * D * 4) < 2048 and size(n, 32, 8, D) % 256 == 0
     n = 40000
     assert 0 <= size(n, 32, 8, D) - (256 + 4 * n + 4 * 5000 + 5 * (5000 + n) * D * 4) < 2048
-    assert 0 <= size(n, 10, 1, D) - (256 + 4 * n + 4 * 5000 + 3 * (5000 + n) * D * 4) < 2048
+    assert 0 <= size(n, 10, 1, D) - (256 + 4 * n + 4 * 5000 + 2 * (5000 + n) * D * 4) < 2048
     big = 1 << 40
     assert lib.qk_norm_begin(P(256), 16, 64, 4, 2, 64, None) == -6 and lib.qk_norm_begin(P(272), big, 64, 4, 2, 64, None) == -3
     assert lib.qk_norm_begin(None, big, 64, 4, 2, 64, None) == -1 and lib.qk_norm_begin(P(256), big, 64, 4, 2, 60, None) == -2
