@@ -10,14 +10,14 @@
 // alike, so the lane's cosines and sines are formed once per chunk.
 //
 // What bounds it (bf16, 32+8 heads of 128, 33,384 tokens; DRAM floor at the copy rate of
-// 6.78 TB/s in brackets): memory.  Rotation 100.3 us (100.9), norm and rotation 104 (100.9),
-// backward 157 and, with both weight gradients from begin to finalize, 168 (151.4).  FP32,
-// 17,620 tokens: 117, 117 (106.5), 192 (159.8).  Fewer rows for a token's angles and a
+// 6.78 TB/s in brackets): memory.  Rotation 100.2 us (100.9), norm and rotation 105 (100.9),
+// backward 156 and, with both weight gradients from begin to finalize, 167 (151.4).  FP32,
+// 17,620 tokens: 117, 114 (106.5), 191 (159.8).  Fewer rows for a token's angles and a
 // warp's start, or idle lanes, make it issue: 1+1 heads of 128, 270,100 tokens, 51 and 64
-// (41.1), backward 152 (61.5); heads of 80, backward, 138 (94.6).  Pieces
+// (41.1), backward 152 (61.5); heads of 80, backward, 126 (94.6).  Pieces
 // pay for their way through shared memory, about 60 instructions a row of a warp more: 16+16
-// heads of 72 that turn whole, 17,620 tokens, 35 and 43 (24.0), backward 73 (36.0); 32+8 heads of
-// 120, 57 and 63 (49.9), 113 (74.9).  (Vectors that take each partner's value from where its
+// heads of 72 that turn whole, 17,620 tokens, 32 and 37 (24.0), backward 64 (36.0); 32+8 heads of
+// 120, 57 and 59 (49.9), 104 (74.9).  (Vectors that take each partner's value from where its
 // lane's copy arrived, with two factors a column: 45, 49, 92; 80, 83, 141.)
 #pragma once
 #include <type_traits>

@@ -235,7 +235,7 @@ def _outputs(q, k, q_out, k_out, names, stream):
 
 def rotary_fwd(q, k, lay, position, rotary: Rotary, q_out=None, k_out=None, stream=None):
     """Turns the heads of q and k (None: q alone) by their tokens' positions; position: int32, one per token slot.
-    Returns (q_out, k_out); in place (q_out is q) only the rotated columns are touched."""
+    Returns (q_out, k_out); in place (q_out is q) columns outside the rotation keep their bits."""
     c = _Call(q, "q", lay, stream)
     if q_out is None or (k_out is None) != (k is None):
         q_out, k_out = _outputs(q, k, q_out, k_out, ("k", "k_out"), stream)
