@@ -490,3 +490,35 @@ def test_a_block_as_it_is_used():
     back, _ = rb.rotary_bwd(r1, None, s.layout(), s.pos, s.rot)
     _, err = O.rotate(_f64(s.k), _f64(s.pos), s.freq, *s.args)
     _within("turned back", _f64(back), _f64(s.k), 4 * err)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_sizes_at_random(seed):
+    """Sizes, widths, parts of the head and layouts at random: bits across layouts, values, rotation in place."""
+    rng = np.random.default_rng(seed)
+    pick = lambda v: v[int(rng.integers(len(v)))]                                           # noqa: E731
+    for _ in range(12):
+        D = pick((8, 16, 24, 40, 56, 64, 72, 80, 88, 96, 120, 128, 136, 160, 192, 200, 256, 264, 384, 512))
+        rot = max(4, pick((D, D // 2, D // 4, int(rng.integers(4, D + 1)))) // 4 * 4)
+        first = (D - rot) // pick((2, 4, 8)) * 2 if rng.random() < 0.5 else 0
+        hq, hk = pick((1, 2, 5, 12, 17, 33)), pick((0, 1, 2, 7))
+        dtype, param = pick((BF, FP16, F32)), pick((None, F32))
+        lengths = rng.integers(1, pick((4, 40, 200)), pick((2, 5, 9)))
+        s = Setup(int(lengths.sum()), hq, hk, D, rot, first, rng.random() < 0.3, dtype, param, pick((1.0, 1.2)))
+        lays = {kind: L.make_layout(kind, lengths, chunk=pick((1, 7, 37)))
+                for kind in ("full", "padded_left", "permuted", "permuted_chunked", "padded_right_chunked")}
+        runs = {kind: harness.run_layout_qk_norm_rotary(lay, s.q, s.k, s.dq, s.dk, s.qw, s.kw, s.pos, s.rot, EPS, 0.5)
+                for kind, lay in lays.items()}
+        sizes = (s.n, hq, hk, D, s.args, dtype)
+        assert harness.assert_batch_invariant(runs, lays).first_failure() is None, sizes
+        assert all(r.status == 0 and r.untouched_padding for r in runs.values()), sizes
+        r = runs["full"]
+        s.check(r.y, r.dx, r.dweight, s.q, s.qw, s.dq, 0.5)
+        if hk:
+            s.check(r.k, r.dk, r.dk_weight, s.k, s.kw, s.dk, 0.5)
+        q, k = rb.rotary_fwd(s.q, s.k, s.layout(), s.pos, s.rot)
+        for x, y in ((s.q, q), (s.k, k)):
+            if x is not None:
+                z = x.clone()
+                rb.rotary_fwd(z, None, s.layout(), s.pos, s.rot, q_out=z)
+                assert _same(z, y), sizes
