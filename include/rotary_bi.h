@@ -125,7 +125,7 @@ int qk_norm_rotary_bwd(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k, int64
  * number of qk_norm_rotary_bwd calls that hold every token exactly once in all,
  * finalize.  finalize multiplies both roots once by grad_scale and may be
  * repeated; dq_weight or dk_weight may be NULL (not both; dk_weight without keys
- * must be).  Status bits: RMSNORM_STATUS_DOUBLE / _MISSING tokens, _HEADER for a
+ * must be), and they may not overlap.  Status bits: RMSNORM_STATUS_DOUBLE / _MISSING tokens, _HEADER for a
  * workspace begun for other sizes (or a call with other head counts; it then
  * contributes nothing), _PLAN for an id that is not below n_logical_tokens (its
  * dx is written, its contribution dropped).

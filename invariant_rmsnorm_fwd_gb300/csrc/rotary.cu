@@ -395,6 +395,11 @@ extern "C" int qk_norm_finalize(void *workspace, int64_t n_logical_tokens, int32
     if (!dq_weight && !dk_weight) return RMSNORM_ERR_NULL;
     if (dk_weight && k_heads == 0) return RMSNORM_ERR_LAYOUT;
     if (off4(dq_weight) || off4(dk_weight)) return RMSNORM_ERR_ALIGN;
+    // both are written at once
+    if (dq_weight && dk_weight) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(dq_weight), b = reinterpret_cast<uintptr_t>(dk_weight);
+        if ((a < b ? b - a : a - b) < uintptr_t(head_dim) * 4) return RMSNORM_ERR_LAYOUT;
+    }
     DeviceInfo *d = nullptr;
     if ((rc = device_info(&d))) return rc;
     const int slices = int(head_dim + 31) / 32;
