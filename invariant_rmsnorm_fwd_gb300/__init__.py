@@ -54,6 +54,8 @@ class _Dropout(ctypes.Structure):
     _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_double)]
 
 
+# The structures of rotary_bi.h.  rotary.py packs the same bytes itself, which is quicker; these are what its packing
+# is checked against, and how a ctypes caller of the library names the fields.
 class _Rotary(ctypes.Structure):
     _fields_ = [
         ("position", ctypes.c_void_p),

@@ -294,8 +294,9 @@ __device__ __forceinline__ void qk_finalize(const QkWs &ws, float scale, float *
     const int slot0 = keys ? ws.cut.q_slots : 0, slots = keys ? ws.cut.slots - ws.cut.q_slots : ws.cut.q_slots;
     constexpr int kShares = CTAS * kFinalWarps * 4;
     const int64_t per = (ws.groups + kShares - 1) / kShares;
-    // (few groups: one a warp, so that cut ones are not added up one after the other; 1,140 tokens whose 142 groups are
-    // all cut, 33 partial sums each: 26 us with four a warp)
+    // (few groups: one a warp, so that cut ones are not added up one after the other; all groups cut, this way and four a
+    // warp: 200 tokens of 59+7 heads of 128 12 and 20 us, 504 of 60+3 of 8 18 and 55; above 128 groups it loses a little,
+    // 1,140 of 59+7 of 128 10.8 and 8.4)
     const int64_t g0 = ((lane >> 3) * (CTAS * kFinalWarps) + int(blockIdx.y) * kFinalWarps + warp) * per;
     const int64_t g1 = g0 + per < ws.groups ? g0 + per : ws.groups;
     const bool check = blockIdx.x == 0, have = col < ws.D;

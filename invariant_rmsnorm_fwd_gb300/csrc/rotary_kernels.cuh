@@ -28,7 +28,7 @@
 
 namespace rbi {
 
-constexpr int kChunkHeads = 8;                           // heads of a usual chunk
+constexpr int kChunkHeads = 8;                           // most heads of a warp of the rotation alone; QkGroups reckons with chunks of as many
 constexpr int kMostGroup = 10;                           // most logical tokens of a group of the weight gradients' order
 constexpr int kBusyWarps = 2432;                         // warps that fill the GPU: 16 on each of 152 SMs
 constexpr uint64_t kQkMagic = 0x3149422d4b514e52ull;
@@ -50,8 +50,9 @@ struct QkTeams {
 // (tokens, heads, D) alone: as many as a warp has teams, or, fewer than 5 teams, a multiple up to
 // 8: each team takes a share of consecutive tokens, from the first to the last, then
 // the shares are added likewise.  The multiple is halved while the groups' chunks of heads
-// are too few for a round and a half of warps (644 tokens of 60 heads of 192: 42 us in groups of 8, 33 of 4, 25 of
-// 2; 17,620 of 17 of 256: 99, 101, 114).  More than 10 teams (heads up to 32 columns) have groups of 8.
+// are too few for a round and a half of warps, the chunks taken to be of 8 heads (644 tokens of 60 heads of 192: 41 us
+// in groups of 8, 32 of 4, 27 of 2; 17,620 of 17 of 256, permuted: 97, 95, 103).  More than 10 teams (heads up to 32
+// columns) have groups of 8.
 struct QkGroups {
     int group, share;
     int64_t groups;
@@ -367,8 +368,8 @@ __device__ __forceinline__ void lane_weights(uint32_t from, f2_t (&f)[8]) {
 // 1/8 turn either way, y = rest in radians.  sin y and cos y are their Taylor polynomials
 // of degree 9 and 10: what is left out is below (pi/4)^11 / 11! = 1.8e-9 and
 // (pi/4)^12 / 12! = 1.2e-10.  FINE (FP32 heads): y is formed with what the float of the
-// rest loses, and enters as y + d: sin + d cos, cos - d sin; without that the angle is
-// off by up to 1.7 times 2^-24 more.  (One pair at a time: constants are operands of its
+// rest loses, and enters as y + d: sin + d cos, cos - d sin.  In units of 2^-24, over all
+// 2^30 rests, sine and cosine are off by at most 1.16 and 1.38, without FINE 1.52 and 1.71.  (One pair at a time: constants are operands of its
 // instructions, in registers of two they are moves.  1+1 heads of 128, 270,100 tokens, with
 // the norm: 70 -> 67 us.)
 template <bool FINE>
@@ -824,8 +825,10 @@ inline int qk_bwd_smem(int ring_bytes, bool grads, bool straddles) {
 // over a token's heads of one kind, in shared memory over a team's tokens of the run, and
 // leave as one partial sum a run.  It holds x, g, g w, a token's angles and the sums: 128
 // registers for 16 warps an SM (12 warps at 168 registers: 183 us where 16 take 169; in
-// pieces, heads of 72, 82 and 73; FP32, which would spill, has 12).  Left on the table: about 330 instructions a
-// warp for 4 rows of 128, of which some 20 % are addresses and copies.
+// pieces, heads of 72, 82 and 73; FP32, which needs more than 128, has 12).  A few registers spill in two forms:
+// neighbours of 16 bits whose team is known only when the kernel runs (16 bytes stored, 28 loaded a thread) and FP32
+// pieces of four columns (8 to 12, 12 to 20).  Left on the table: about 330 instructions a warp for 4 rows of 128, of
+// which some 20 % are addresses and copies.
 // With ws.hdr == NULL there are no gradients: every active slot is one on its own.
 template <class E, int PAIRS, int TEAM>
 __global__ void __launch_bounds__(kQkWarps * 32, sizeof(E) == 4 ? 3 : 4) qk_bwd_kernel(const __grid_constant__ RotaryParams p, int straddles) {
